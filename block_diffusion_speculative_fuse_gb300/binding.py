@@ -51,6 +51,20 @@ class DflashKV(ctypes.Structure):
                 ("scales", ctypes.c_void_p)]
 
 
+class DflashHeads(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_terms", ctypes.c_int32)]
+
+
+class DflashRope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_double), ("inv_freq", ctypes.c_double * 64)]
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "dflash_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -108,6 +122,29 @@ EXPORTS = {
     "dflash_lm_head_argmax": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_size_t, ctypes.c_void_p]),
+    "dflash_rope_init": (ctypes.c_int, [ctypes.POINTER(DflashRope), ctypes.c_int32,
+                                        ctypes.c_int32, ctypes.c_double, ctypes.c_int32,
+                                        ctypes.c_double, ctypes.c_int32, ctypes.c_double,
+                                        ctypes.c_double]),
+    "dflash_kv_rope_append": (ctypes.c_int, [ctypes.POINTER(DflashHeads),
+                                             ctypes.POINTER(DflashRope), ctypes.c_int32] +
+                              [ctypes.c_void_p, ctypes.c_int64] * 3 +
+                              [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
+                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                               ctypes.c_int64, ctypes.POINTER(DflashKV), ctypes.c_void_p,
+                               ctypes.c_size_t, ctypes.c_void_p]),
+    "dflash_attention_prefix_bytes": (ctypes.c_size_t, [ctypes.POINTER(DflashHeads),
+                                                        ctypes.c_int32, ctypes.c_int32,
+                                                        ctypes.c_int32]),
+    "dflash_attention_prefix": (ctypes.c_int, [ctypes.POINTER(DflashHeads), ctypes.c_int32,
+                                               ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                               ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                               ctypes.POINTER(DflashKV)] + [ctypes.c_void_p] * 5 +
+                                [ctypes.c_size_t, ctypes.c_void_p]),
+    "dflash_sample_filtered_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "dflash_sample_filtered": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                              ctypes.c_int32] + [ctypes.c_void_p] * 9 +
+                               [ctypes.c_size_t, ctypes.c_void_p]),
     "dflash_synth_target": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64,
                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
@@ -290,3 +327,119 @@ def dflash_ctx_fuse_noalloc(h, taps, T, ctx, stream=None):
     device memory; its scratch is a fixed array inside the library."""
     return _check("dflash_ctx_fuse_noalloc", load().dflash_ctx_fuse_noalloc(
         h, ptr(taps), T, ptr(ctx), stream_handle(stream)))
+
+
+# ------------------------------------------------------- serving operators
+def _tensor(fn, t, dtype, shape, strides=None, optional=False):
+    """Checks a tensor argument against what the library will read or write:
+    on the current CUDA device, dtype, shape, and dense (or the strides given,
+    None standing for any)."""
+    if t is None:
+        if optional:
+            return
+        raise DflashError(fn, -1)
+    if not t.is_cuda or t.device.index != torch.cuda.current_device() or t.dtype != dtype or \
+            tuple(t.shape) != shape:
+        raise DflashError(fn, -1)
+    if strides is None:
+        if not t.is_contiguous():
+            raise DflashError(fn, -1)
+    elif any(w is not None and n > 1 and s != w for s, w, n in zip(t.stride(), strides, shape)):
+        raise DflashError(fn, -1)
+
+
+def _workspace_arg(fn, ws):
+    if ws is None or not ws.is_cuda or ws.device.index != torch.cuda.current_device() or \
+            not ws.is_contiguous():
+        raise DflashError(fn, -1)
+    return ptr(ws), ws.numel() * ws.element_size()
+
+
+def dflash_rope_init(rot_dim, interleaved=False, base=1e6, scaling="none", factor=1.0,
+                     orig_ctx=0, beta_fast=32.0, beta_slow=1.0) -> DflashRope:
+    """Rotation plan; ``scaling`` is one of ``ROPE_SCALINGS``."""
+    if scaling not in ROPE_SCALINGS:
+        raise DflashError("dflash_rope_init", -1)
+    r = DflashRope()
+    _check("dflash_rope_init", load().dflash_rope_init(
+        ctypes.byref(r), int(rot_dim), 1 if interleaved else 0, float(base),
+        ROPE_SCALINGS[scaling], float(factor), int(orig_ctx), float(beta_fast), float(beta_slow)))
+    return r
+
+
+def dflash_kv_rope_append(heads: DflashHeads, rope: DflashRope, layer, q, k, v, row_req, row_pos,
+                          T, q_out, kv: DflashKV, ws, q_norm=None, k_norm=None, eps=1e-6,
+                          stream=None):
+    """q [T][hq][d], k, v [T][hkv][d] (bf16 or fp32; rows may be strided, a
+    row's heads are dense); q and q_out may both be None."""
+    fn = "dflash_kv_rope_append"
+    hq, hkv, d = heads.n_q_heads, heads.n_kv_heads, heads.head_dim
+    if k is None or k.dtype not in (torch.bfloat16, torch.float32):
+        raise DflashError(fn, -1)
+    _tensor(fn, k, k.dtype, (T, hkv, d), (None, d, 1))
+    _tensor(fn, v, k.dtype, (T, hkv, d), (None, d, 1))
+    _tensor(fn, q, k.dtype, (T, hq, d), (None, d, 1), optional=True)
+    _tensor(fn, q_out, torch.bfloat16, (T, hq, d), (None, d, 1), optional=True)
+    _tensor(fn, q_norm, torch.bfloat16, (d,), optional=True)
+    _tensor(fn, k_norm, torch.bfloat16, (d,), optional=True)
+    _tensor(fn, row_req, torch.int32, (T,))
+    _tensor(fn, row_pos, torch.int32, (T,))
+    w, wn = _workspace_arg(fn, ws)
+
+    def ld(t, dense):
+        return 0 if t is None else t.stride(0) if t.shape[0] > 1 else dense
+    return _check(fn, load().dflash_kv_rope_append(
+        ctypes.byref(heads), ctypes.byref(rope), layer, ptr(q), ld(q, hq * d), ptr(k),
+        ld(k, hkv * d), ptr(v), ld(v, hkv * d), 0 if k.dtype == torch.bfloat16 else 1,
+        ptr(q_norm), ptr(k_norm), float(eps), ptr(row_req), ptr(row_pos), T, ptr(q_out),
+        ld(q_out, hq * d), ctypes.byref(kv), w, wn, stream_handle(stream)))
+
+
+def dflash_attention_prefix_bytes(heads: DflashHeads, batch, n, group) -> int:
+    size = load().dflash_attention_prefix_bytes(ctypes.byref(heads), batch, n, group)
+    if size == 0:
+        raise DflashError("dflash_attention_prefix_bytes", -1)
+    return int(size)
+
+
+def dflash_attention_prefix(heads: DflashHeads, layer, q, batch, n, group, causal, scale,
+                            kv: DflashKV, ctx_len, prefix_len, out, lse, ws, stream=None):
+    fn = "dflash_attention_prefix"
+    if batch < 1 or group < 1 or batch % group:
+        raise DflashError(fn, -1)
+    shape = (batch, n, heads.n_q_heads, heads.head_dim)
+    _tensor(fn, q, torch.bfloat16, shape)
+    _tensor(fn, out, torch.bfloat16, shape)
+    _tensor(fn, lse, torch.float32, shape[:3], optional=True)
+    _tensor(fn, ctx_len, torch.int32, (batch,))
+    _tensor(fn, prefix_len, torch.int32, (batch // group,))
+    w, wn = _workspace_arg(fn, ws)
+    return _check(fn, load().dflash_attention_prefix(
+        ctypes.byref(heads), layer, ptr(q), batch, n, group, 1 if causal else 0, float(scale),
+        ctypes.byref(kv), ptr(ctx_len), ptr(prefix_len), ptr(out), ptr(lse), w, wn,
+        stream_handle(stream)))
+
+
+def dflash_sample_filtered_bytes(rows, vocab) -> int:
+    size = load().dflash_sample_filtered_bytes(rows, vocab)
+    if size == 0:
+        raise DflashError("dflash_sample_filtered_bytes", -1)
+    return int(size)
+
+
+def dflash_sample_filtered(logits, rows, vocab, temperature, top_k, top_p, min_p, a, token,
+                           n_kept, logprob, ws, stream=None):
+    """logits fp32 [rows][vocab] (rows may be strided); top_k, top_p, min_p,
+    n_kept and logprob may be None."""
+    fn = "dflash_sample_filtered"
+    _tensor(fn, logits, torch.float32, (rows, vocab), (None, 1))
+    for t, dt, opt in ((temperature, torch.float32, False), (top_k, torch.int32, True),
+                       (top_p, torch.float32, True), (min_p, torch.float32, True),
+                       (a, torch.float64, False), (token, torch.int32, False),
+                       (n_kept, torch.int32, True), (logprob, torch.float32, True)):
+        _tensor(fn, t, dt, (rows,), optional=opt)
+    w, wn = _workspace_arg(fn, ws)
+    return _check(fn, load().dflash_sample_filtered(
+        ptr(logits), logits.stride(0) if rows > 1 else vocab, rows, vocab, ptr(temperature),
+        ptr(top_k), ptr(top_p), ptr(min_p), ptr(a), ptr(token), ptr(n_kept), ptr(logprob), w, wn,
+        stream_handle(stream)))

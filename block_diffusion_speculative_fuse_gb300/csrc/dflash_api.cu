@@ -660,6 +660,8 @@ int check_cfg(const dflash_config* c, bool draft) {
 }  // namespace
 
 namespace dflash {
+int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
 // Argument and capacity checks of dflash_ctx_fuse (nothing is launched).
 int ctx_fuse_check(const dflash_model_s* m, const void* taps, int32_t T, const void* ctx,
                    const void* ws, size_t ws_bytes) {

@@ -238,4 +238,48 @@ cudaError_t sample_rows_launch(const float* rows, int n_used, int block, int ski
 cudaError_t wait_selftest_launch(int arrive, uint64_t limit_ns, int* status, int64_t* waited_ns,
                                  cudaStream_t s);
 
+// Rotation and append (rope_append.cu): one CTA per row.
+struct RopeAppendParams {
+  const void *q, *k, *v;       // bf16 or fp32 rows; q may be null
+  int64_t ld_q, ld_k, ld_v;    // row strides (elements)
+  const uint16_t *q_norm, *k_norm;  // [d] gains or null
+  const int32_t *row_req, *row_pos;
+  uint16_t* q_out;
+  int64_t ld_qo;
+  uint16_t* pool;              // layer base (bf16 caches)
+  uint8_t* pool8;              // layer base (E4M3 caches) or null
+  float* scales8;
+  const int32_t* page_table;
+  int32_t* status;
+  int T, hq, hkv, rot_dim, interleaved, kv_terms, max_pages, n_pages, n_req;
+  float eps, mscale;
+  unsigned long long turns[kMaxRopePairs];  // inv_freq / 2pi as a 64-bit fraction of a turn
+};
+cudaError_t rope_append_launch(const RopeAppendParams& p, int d, bool fp32, cudaStream_t s);
+
+// Filtered sampling (sample_filtered.cu).
+struct SampleFilteredParams {
+  const float* logits;
+  int64_t ld;
+  int rows, vocab;
+  const float* temperature;
+  const int32_t* top_k;        // the four settings, uniforms: [rows] (top_k, top_p, min_p may be null)
+  const float *top_p, *min_p;
+  const double* a;
+  int32_t *token, *n_kept;
+  float* logprob;
+  int32_t* status;
+};
+cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s);
+constexpr int kMaxSampleVocab = 393216;
+
+// Prefix attention (prefix_attention.cuh): row tiles and workers from the
+// sizes, then the launches (d = head_dim).
+struct PrefixParams;
+void prefix_attention_shape(PrefixParams* p);
+cudaError_t prefix_attention_launch(const PrefixParams& p, int d, cudaStream_t s);
+
+// Records the error for dflash_last_cuda_error and returns DFLASH_ERR_CUDA.
+int record_cuda_error(cudaError_t e);
+
 }  // namespace dflash

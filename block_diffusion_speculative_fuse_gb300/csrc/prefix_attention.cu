@@ -1,0 +1,402 @@
+// Attention over the paged cache for batches whose requests share a prefix:
+// the small-tile kernel and the join of the partial results.
+//
+//   s_j = scale q.k_j, o = sum_j exp(s_j) v_j / sum_j exp(s_j)
+//
+// over the keys a row sees, with a running maximum and sum per row (in the
+// exp2 domain, fp32).  See prefix_attention.cuh for how the work is cut up.
+//
+// Small tiles (mma.sync, 16 rows).  With one token per request a unit has at
+// most 16 rows, 16 flop per key byte: the bound is bytes, and the many short
+// ranges favour independent workers over large tiles.  A worker is one warp:
+// a page (16 keys) is a step of two m16n8 score tiles and one k16 step of the
+// product with V, fed by the warp's own ring of pages through cp.async, with
+// no barrier between warps.
+#include "attention.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "prefix_attention.cuh"
+
+namespace dflash {
+
+namespace {
+
+constexpr int kSmallWarps = 8;
+constexpr int kSmallCtas = 152;    // one per SM
+constexpr int kSmallRows = 16;
+
+template <int D>
+struct SmallCfg {
+  static constexpr int PAGE = 16 * D * 2;          // bytes of one page of K or V
+  static constexpr int STAGES = D == 128 ? 3 : 6;  // pages in flight per warp
+  static constexpr int RING = STAGES * 2 * PAGE;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Row `i` of a tile: the request and the row of q/out ([batch][n][hq]) it
+// stands for; false past the entity's rows.
+struct RowMap {
+  int e, ng, group, n, G, hq, kvh, rows;
+  __device__ RowMap(const PrefixParams& p, int entity, int kv_head)
+      : e(entity), ng(p.ng), group(p.group), n(p.n), G(p.hq / p.hkv), hq(p.hq), kvh(kv_head),
+        rows((entity < p.ng ? p.group : 1) * p.n * (p.hq / p.hkv)) {}
+  __device__ bool at(int row, int* req, int* i, size_t* vec) const {
+    if (row >= rows) return false;
+    const int h = row % G, bi = row / G;
+    *i = bi % n;
+    *req = e < ng ? e * group + bi / n : e - ng;
+    *vec = (static_cast<size_t>(*req) * n + *i) * hq + kvh * G + h;
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const PrefixParams p) {
+  using C = SmallCfg<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const PrefixList& L = p.list[0];
+  const int ne = p.ng + p.batch;
+  int* off = reinterpret_cast<int*>(smem + kSmallWarps * C::RING);
+  int* cut = off + ne + 1;
+  int* live = cut + p.ng;
+  int* scratch = live + p.ng;
+  griddep_launch_dependents();
+  griddep_wait();
+  prefix_plan(p, L, cut, live, off, scratch);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int worker = blockIdx.x * kSmallWarps + warp;
+  const int total = off[ne];
+  const int per = chunks_per_worker(total, L.workers);
+  int c = worker * per;
+  const int c_end = min(total, c + per);
+  uint8_t* ring = smem + warp * C::RING;
+  const uint32_t ring_a = smem_u32(ring);
+  const size_t head_elems = 16 * D;
+  const size_t page_elems = static_cast<size_t>(2) * p.hkv * head_elems;
+  const int tq = lane % 4, tg = lane / 4;
+
+  int e = c < c_end ? find_entity(off, ne, c) : 0;
+  while (c < c_end) {
+    while (off[e + 1] <= c) ++e;
+    // ---- the segment: unit (e, kvh, tile), its pages [pg0, pg1)
+    const int tiles = entity_tiles(p, L, e);
+    const int nch = (off[e + 1] - off[e]) / (p.hkv * tiles);  // pages of one unit
+    const int in_e = c - off[e];
+    const int ul = in_e / nch;
+    const int pg0 = in_e - ul * nch;
+    const int pg1 = min(nch, pg0 + (c_end - c));
+    const int kvh = ul / tiles, tile = ul % tiles;
+    const int slot = units_before(p, L, e) + ul + worker;
+    const bool pre = e < p.ng;
+    const int req_t = pre ? live[e] : e - p.ng;               // whose table row
+    const int page0 = pre ? 0 : cut[(e - p.ng) / p.group] / 16;
+    const int ctx = pre ? cut[e] : clamped_ctx(p, e - p.ng);  // keys at or past it take no part
+    const int32_t* table = p.page_table + static_cast<size_t>(req_t) * p.max_pages + page0;
+    const RowMap map(p, e, kvh);
+
+    // ---- query fragments (rows tg, tg + 8 of the tile) and their limits
+    uint32_t qf[D / 16][4];
+    int lim[2];
+    {
+      const uint16_t* qp[2];
+      bool ok[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int req = 0, i = 0;
+        size_t vec = 0;
+        ok[h] = map.at(tile * kSmallRows + tg + 8 * h, &req, &i, &vec);
+        qp[h] = p.q + vec * D;
+        lim[h] = !ok[h] ? 0 : pre ? INT_MAX : p.causal ? ctx - p.n + i + 1 : ctx;
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int col = kk * 16 + tq * 2;
+        qf[kk][0] = ok[0] ? __ldcg(reinterpret_cast<const unsigned*>(qp[0] + col)) : 0u;
+        qf[kk][1] = ok[1] ? __ldcg(reinterpret_cast<const unsigned*>(qp[1] + col)) : 0u;
+        qf[kk][2] = ok[0] ? __ldcg(reinterpret_cast<const unsigned*>(qp[0] + col + 8)) : 0u;
+        qf[kk][3] = ok[1] ? __ldcg(reinterpret_cast<const unsigned*>(qp[1] + col + 8)) : 0u;
+      }
+    }
+
+    // ---- page ids, 32 at a time, one per lane
+    int ids = -1, ids_at = -1;
+    auto page_id = [&](int pg) {
+      if (pg / 32 != ids_at) {
+        ids_at = pg / 32;
+        const int j = ids_at * 32 + lane;
+        ids = j >= pg0 && j < pg1 ? __ldcg(table + j) : 0;
+        if (j >= pg0 && j < pg1 && (ids < 0 || ids >= p.n_pages)) {
+          raise_status(p.status, DFLASH_ERR_CAPACITY, 521);
+          ids = -1;
+        }
+      }
+      return __shfl_sync(0xffffffffu, ids, pg % 32);
+    };
+    auto load_page = [&](int pg) {
+      const int id = page_id(pg);
+      const uint16_t* k = p.pool + (id < 0 ? 0 : id) * page_elems + kvh * head_elems;
+      const uint16_t* v = k + p.hkv * head_elems;
+      const uint32_t st = ring_a + (pg % C::STAGES) * 2 * C::PAGE;
+      const int bytes = id < 0 ? 0 : 16;
+#pragma unroll
+      for (int i = 0; i < C::PAGE / 512; ++i) {
+        const int pc = i * 32 + lane;                 // 16-byte piece of the page
+        const uint32_t o = swz<D>(pc / (D / 8), pc % (D / 8));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + o), "l"(k + pc * 8), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + C::PAGE + o), "l"(v + pc * 8), "r"(bytes) : "memory");
+      }
+    };
+
+    float o[D / 8][4];
+    float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+      if (pg0 + s < pg1) load_page(pg0 + s);
+      cp_async_commit();
+    }
+    for (int pg = pg0; pg < pg1; ++pg) {
+      if (pg + C::STAGES - 1 < pg1) load_page(pg + C::STAGES - 1);
+      cp_async_commit();
+      cp_async_wait<C::STAGES - 1>();
+      __syncwarp();
+      const uint32_t kb = ring_a + (pg % C::STAGES) * 2 * C::PAGE;
+      const uint32_t vb = kb + C::PAGE;
+      const int key0 = (page0 + pg) * 16;
+      const bool last = key0 + 16 > ctx;
+      if (last) {
+        // rows at or past the context hold whatever was there: 0 * V must be 0
+        for (int i = lane; i < 16 * (D / 8); i += 32)
+          if (key0 + i / (D / 8) >= ctx) st_shared_u4(vb + swz<D>(i / (D / 8), i % (D / 8)), make_uint4(0u, 0u, 0u, 0u));
+        __syncwarp();
+      }
+      // S = Q K^T: keys 0-7 and 8-15
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(kb + swz<D>((lane & 7) + (lane >> 4) * 8, kk * 2 + ((lane >> 3) & 1)), b0, b1, b2, b3);
+        mma16816(s[0], qf[kk], b0, b1);
+        mma16816(s[1], qf[kk], b2, b3);
+      }
+      // scale, mask, running maximum of rows tg and tg + 8
+      uint32_t a[4];
+      float alpha[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = key0 + (j / 2) * 8 + tq * 2 + j % 2;
+          x[j] = key < lim[h] && key < ctx ? s[j / 2][2 * h + j % 2] * p.scale_log2 : -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m_r[h], mx);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        alpha[h] = ex2(m_r[h] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = ex2(x[j] - ref);
+          sum += x[j];
+        }
+        l_r[h] = l_r[h] * alpha[h] + sum;  // this thread's keys only
+        m_r[h] = m_new;
+        a[h] = pack_bf2(x[0], x[1]);
+        a[2 + h] = pack_bf2(x[2], x[3]);
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int nd = 0; nd < D / 8; nd += 2) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_t(vb + swz<D>((lane & 7) + ((lane >> 3) & 1) * 8, nd + (lane >> 4)), b0, b1, b2, b3);
+        mma16816(o[nd], a, b0, b1);
+        mma16816(o[nd + 1], a, b2, b3);
+      }
+      __syncwarp();  // all lanes are done with the stage before it is refilled
+    }
+
+    // ---- partial of the segment
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float l = l_r[h];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const int row = tile * kSmallRows + tg + 8 * h;
+      if (row < map.rows) {
+        const size_t ps = static_cast<size_t>(slot) * kSmallRows + tg + 8 * h;
+        float* dst = L.part_o + ps * D;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(dst + i * 8 + tq * 2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        if (tq == 0) *reinterpret_cast<float2*>(L.part_ml + ps * 2) = make_float2(m_r[h], l);
+      }
+    }
+    c += pg1 - pg0;
+  }
+}
+
+// Joins the partials of each (row, query head): WPV warps per vector, each
+// taking every WPV-th partial, in a fixed order.
+template <int D, int WPV>
+__global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) {
+  constexpr int VEC = D / 32;
+  __shared__ float so[8][D];
+  __shared__ float sml[8][2];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int vec = blockIdx.x * (8 / WPV) + warp / WPV, sub = warp % WPV;
+  const int vecs = p.batch * p.n * p.hq;
+  const bool on = vec < vecs;
+  const int ne = p.ng + p.batch;
+  const int G = p.hq / p.hkv;
+  float m = -INFINITY, l = 0.f, acc[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+  bool sees = false;
+  if (on) {
+    const int h = vec % p.hq, i = vec / p.hq % p.n, req = vec / p.hq / p.n;
+    const int kvh = h / G;
+    const int ctx = clamped_ctx(p, req);
+    sees = (p.causal ? ctx - p.n + i + 1 : ctx) > 0;
+    if (sees) {
+      int turn = 0;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const int e = part == 0 ? req / p.group : p.ng + req;
+        const int row = part == 0 ? ((req % p.group) * p.n + i) * G + h % G : i * G + h % G;
+        const PrefixList& L = (part == 0 ? p.list[0].prefix_tiles : p.list[0].suffix_tiles) > 0 ? p.list[0] : p.list[1];
+        const int tiles = entity_tiles(p, L, e);
+        if (tiles == 0) continue;
+        const int c_lo = __ldcg(L.off + e), c_hi = __ldcg(L.off + e + 1);
+        if (c_hi == c_lo) continue;
+        const int nch = (c_hi - c_lo) / (p.hkv * tiles);
+        const int per = chunks_per_worker(__ldcg(L.off + ne), L.workers);
+        const int ul = kvh * tiles + row / L.tile_rows;
+        const int c0 = c_lo + ul * nch;
+        const int w0 = c0 / per, w1 = (c0 + nch - 1) / per;
+        const int unit = units_before(p, L, e) + ul;
+        for (int w = w0; w <= w1; ++w, ++turn) {
+          if (turn % WPV != sub) continue;
+          const size_t ps = static_cast<size_t>(unit + w) * L.tile_rows + row % L.tile_rows;
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(L.part_ml + ps * 2));
+          float v[VEC];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) v[j] = __ldcg(L.part_o + ps * D + j * 32 + lane);
+          if (ml.x == -INFINITY) continue;   // the row saw none of the segment's keys
+          const float mn = fmaxf(m, ml.x);
+          const float f0 = exp2f(m - mn), f1 = exp2f(ml.x - mn);
+          l = l * f0 + ml.y * f1;
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) acc[j] = acc[j] * f0 + v[j] * f1;
+          m = mn;
+        }
+      }
+    }
+  }
+  if (WPV > 1) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) so[warp][j * 32 + lane] = acc[j];
+    if (lane == 0) {
+      sml[warp][0] = m;
+      sml[warp][1] = l;
+    }
+    __syncthreads();
+    if (sub != 0 || !on) return;
+    for (int w = 1; w < WPV; ++w) {
+      const float mw = sml[warp + w][0];
+      if (mw == -INFINITY) continue;
+      const float mn = fmaxf(m, mw);
+      const float f0 = exp2f(m - mn), f1 = exp2f(mw - mn);
+      l = l * f0 + sml[warp + w][1] * f1;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc[j] = acc[j] * f0 + so[warp + w][j * 32 + lane] * f1;
+      m = mn;
+    }
+  }
+  if (!on) return;
+  const float inv = sees ? 1.f / l : 0.f;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) p.out[static_cast<size_t>(vec) * D + j * 32 + lane] = f2bf(acc[j] * inv);
+  if (p.lse != nullptr && lane == 0)
+    p.lse[vec] = sees ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+}
+
+cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, void** args, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <int D>
+cudaError_t run(const PrefixParams& p, cudaStream_t s) {
+  const int ne = p.ng + p.batch;
+  void* args[] = {const_cast<PrefixParams*>(&p)};
+  {
+    const size_t smem = kSmallWarps * SmallCfg<D>::RING + (ne + 1 + 2 * p.ng + 33) * sizeof(int);
+    const void* fn = reinterpret_cast<const void*>(prefix_small_kernel<D>);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(fn, kSmallCtas, kSmallWarps * 32, smem, args, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int vecs = p.batch * p.n * p.hq;
+  // few vectors have many partials each: more warps per vector
+  if (vecs >= 4096)
+    return launch_pdl(reinterpret_cast<const void*>(prefix_join_kernel<D, 1>), (vecs + 7) / 8, 256, 0, args, s);
+  return launch_pdl(reinterpret_cast<const void*>(prefix_join_kernel<D, 8>), vecs, 256, 0, args, s);
+}
+
+}  // namespace
+
+// Row tiles and workers of the two lists.
+void prefix_attention_shape(PrefixParams* p) {
+  const int G = p->hq / p->hkv;
+  const int rows_p = p->group * p->n * G, rows_s = p->n * G;
+  p->ng = p->batch / p->group;
+  PrefixList& S = p->list[0];
+  S.chunk_keys = 16;
+  S.tile_rows = kSmallRows;
+  S.workers = kSmallCtas * kSmallWarps;
+  S.prefix_tiles = (rows_p + kSmallRows - 1) / kSmallRows;
+  S.suffix_tiles = (rows_s + kSmallRows - 1) / kSmallRows;
+  PrefixList& T = p->list[1];
+  T = S;
+  T.workers = 0;
+  T.prefix_tiles = T.suffix_tiles = 0;
+}
+
+cudaError_t prefix_attention_launch(const PrefixParams& p, int d, cudaStream_t s) {
+  return d == 128 ? run<128>(p, s) : run<64>(p, s);
+}
+
+}  // namespace dflash

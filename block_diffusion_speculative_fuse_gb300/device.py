@@ -123,6 +123,37 @@ class PagedKV:
         B.dflash_kv_quantize(model.handle, self.struct, q.struct)
         return q
 
+    def heads(self, n_q_heads: int):
+        """The cache's geometry for the serving operators, read by queries of
+        n_q_heads heads."""
+        L, _, planes, hkv, page, d = self.pool.shape
+        return B.DflashHeads(n_layers=L, n_q_heads=n_q_heads, n_kv_heads=hkv, head_dim=d,
+                             page_size=page, kv_terms=planes // 2)
+
+    def append_rotated(self, rope, layer: int, q, k, v, row_req, row_pos, ws, q_out=None,
+                       q_norm=None, k_norm=None, eps=1e-6, stream=None):
+        """Rotate q [T][hq][d] into q_out and k by their positions and store
+        k, v [T][hkv][d] at position row_pos of request row_req
+        (dflash_kv_rope_append); q and q_out may both be None."""
+        hq = q.shape[1] if q is not None else self.pool.shape[3]
+        B.dflash_kv_rope_append(self.heads(hq), rope, layer, q, k, v, row_req, row_pos,
+                                k.shape[0], q_out, self.struct, ws, q_norm, k_norm, eps, stream)
+
+    def attention_workspace(self, n_q_heads: int, batch: int, n: int, group: int):
+        """An initialised workspace for attend_prefix calls of these sizes."""
+        size = B.dflash_attention_prefix_bytes(self.heads(n_q_heads), batch, n, group)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.pool.device)
+        B.dflash_workspace_init(ws)
+        return ws
+
+    def attend_prefix(self, layer: int, q, ctx_len, prefix_len, group: int, out, ws, lse=None,
+                      causal=True, scale=0.0, stream=None):
+        """Attention of q [batch][n][hq][d] to the cache, each group of
+        requests sharing its first prefix_len positions (dflash_attention_prefix)."""
+        b, n, hq, _ = q.shape
+        B.dflash_attention_prefix(self.heads(hq), layer, q, b, n, group, causal, scale,
+                                  self.struct, ctx_len, prefix_len, out, lse, ws, stream)
+
     def read_codes(self, layer: int, req: int, n: int):
         """E4M3 cache: codes [n][2][hkv][d] (uint8) and scales [n][2][hkv] of
         one request's logical positions 0..n-1, on the host."""

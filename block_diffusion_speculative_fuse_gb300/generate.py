@@ -84,6 +84,41 @@ def ar_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int):
     return torch.cat(res, dim=1).cpu().numpy()
 
 
+def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u: np.ndarray,
+                    temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, keep_logits=None):
+    """Autoregressive decoding with filtered sampling (dflash_sample_filtered),
+    one target forward per token.  u [batch][n_tokens]: the draws' uniforms in
+    [0, 1).  The settings are numbers or one value per request.  keep_logits:
+    a list that receives each step's logits (host)."""
+    b, P = prompts.shape
+    dev, vocab = runner.device, runner.shape.vocab
+
+    def per_request(x, dtype):
+        return torch.as_tensor(np.broadcast_to(np.asarray(x), (b,)).copy()).to(dev, dtype)
+    settings = (per_request(temperature, torch.float32), per_request(top_k, torch.int32),
+                per_request(top_p, torch.float32), per_request(min_p, torch.float32))
+    uniforms = torch.as_tensor(np.ascontiguousarray(np.asarray(u, np.float64).T)).to(dev)
+    logits = torch.empty((b, vocab), dtype=torch.float32, device=dev)
+    ws = torch.empty(B.dflash_sample_filtered_bytes(b, vocab), dtype=torch.uint8, device=dev)
+    B.dflash_workspace_init(ws)
+    res = torch.empty((n_tokens, b), dtype=torch.int32, device=dev)
+    if P > 1:
+        runner.forward(i32(prompts[:, :-1], dev), i32(np.zeros(b), dev), P - 1)
+    tok = i32(prompts[:, -1:], dev)
+    pos = torch.full((b,), P - 1, dtype=torch.int32, device=dev)
+    for i in range(n_tokens):
+        runner.forward(tok, pos, 1, logits=logits)
+        B.dflash_sample_filtered(logits, b, vocab, *settings, uniforms[i], res[i], None, None, ws)
+        if keep_logits is not None:
+            keep_logits.append(logits.cpu().numpy())
+        tok = res[i].view(b, 1)
+        pos += 1
+    status, site = B.dflash_get_status(ws)
+    if status != 0:
+        raise B.DflashError(f"dflash_sample_filtered (site {site})", status)
+    return res.T.contiguous().cpu().numpy()
+
+
 class SpecDecoder:
     def __init__(self, target: DeviceModel, drafter: DeviceModel, tap_layers, batch: int,
                  max_len: int, device="cuda"):

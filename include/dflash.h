@@ -318,6 +318,147 @@ int dflash_sample_rows(const float* logits, int32_t n_blocks, int32_t block, int
                        int32_t vocab, double temperature, const double* a, int32_t* out,
                        void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------ serving operators */
+/* A decode step over a paged cache for callers that bring their own
+ * projections: append rotated K/V (dflash_kv_rope_append), attend to them
+ * with a prefix shared by many requests read once (dflash_attention_prefix),
+ * draw the next tokens from the logits (dflash_sample_filtered).  None needs a
+ * model handle.  They share the conventions above: device pointers, caller's
+ * workspace, asynchronous on `stream`, nothing launched on an argument error.
+ * All of a call's device memory belongs to the current device. */
+
+/* Heads and cache geometry (as in dflash_config).  Supported: head_dim 64 or
+ * 128, page_size 16, kv_terms 1 or 2 (0 is read as 1), n_q_heads a multiple
+ * of n_kv_heads with a quotient of at most 16. */
+typedef struct {
+  int32_t n_layers;
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t kv_terms;
+} dflash_heads;
+
+#define DFLASH_ROPE_NONE 0   /* f_p = base^(-2p/rot_dim)                             */
+#define DFLASH_ROPE_LINEAR 1 /* f_p / factor (position interpolation)                */
+#define DFLASH_ROPE_NTK 2    /* base replaced by base * factor^(rot_dim/(rot_dim-2)) */
+#define DFLASH_ROPE_YARN 3   /* f_p / factor for slow pairs, f_p for fast ones, a ramp
+                              * between the pairs that turn beta_slow and beta_fast
+                              * times in orig_ctx positions; mscale = 0.1 ln(factor) + 1
+                              * ("YaRN: Efficient Context Window Extension of Large
+                              * Language Models")                                     */
+
+/* A rotation of the first rot_dim components of a head; the others pass
+ * through.  Pair p turns by the angle pos * inv_freq[p] and is scaled by
+ * mscale; pairs are (p, p + rot_dim/2), or (2p, 2p+1) when interleaved.
+ * rot_dim is a multiple of 16 up to the head's size (0: no rotation).  The
+ * fields may be set directly (finite, inv_freq >= 0). */
+typedef struct {
+  int32_t rot_dim;
+  int32_t interleaved;
+  double mscale;
+  double inv_freq[64];
+} dflash_rope;
+
+/* Fills *rope on the host.  base > 1; factor >= 1 (not read with NONE);
+ * orig_ctx >= 1 and beta_fast > beta_slow > 0 with YARN (not read otherwise). */
+int dflash_rope_init(dflash_rope* rope, int32_t rot_dim, int32_t interleaved, double base,
+                     int32_t scaling, double factor, int32_t orig_ctx, double beta_fast,
+                     double beta_slow);
+
+/* For T rows: q and k get an optional per-head RMSNorm (gains q_norm, k_norm:
+ * bf16 [head_dim], or NULL) and the rotation at position row_pos[t]; k and v
+ * are stored in layer `layer` of the cache at that position of request
+ * row_req[t], q goes to q_out (bf16).
+ * q [T][n_q_heads][head_dim], k, v [T][n_kv_heads][head_dim]: in_dtype 0 =
+ * bf16, 1 = fp32; rows ld_q, ld_k, ld_v elements apart (so they can be columns
+ * of one fused projection), the heads of a row dense; row strides and base
+ * pointers 16-byte aligned.  q and q_out may both be NULL (keys and values
+ * only); q_out rows are ld_qo elements apart, and q_out == q is allowed for
+ * bf16 input with ld_qo == ld_q (no other overlap of inputs and outputs).
+ * The cache may be bf16 with one or two terms, or E4M3 (dflash_kv); values
+ * are rounded to bf16 first, as the library's own projections do.
+ * Rows with row_pos[t] < 0 are skipped (their q_out rows too).  A row whose
+ * request, page-table column or page id is out of range is recorded as
+ * DFLASH_ERR_CAPACITY (site 501) and its K/V are dropped; its q_out row is
+ * written.  The (request, position) pairs of one call must be distinct.
+ * ws: an initialised workspace of at least 64 KiB; only its status word is
+ * used.  The angle is formed modulo one turn in 64-bit fixed point, so far
+ * positions lose nothing; norms and rotations are fp32. */
+int dflash_kv_rope_append(const dflash_heads* heads, const dflash_rope* rope, int32_t layer,
+                          const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                          int64_t ld_v, int32_t in_dtype, const void* q_norm, const void* k_norm,
+                          float eps, const int32_t* row_req, const int32_t* row_pos, int32_t T,
+                          void* q_out, int64_t ld_qo, const dflash_kv* kv, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* Attention of `batch` requests x n query rows to one layer of a bf16
+ * one-term cache, for batches in which requests share a long prefix:
+ * consecutive groups of `group` requests (group divides batch) whose first
+ * prefix_len[g] positions hold the same tokens, and whose page-table rows name
+ * the same pages for the prefix_len[g] / 16 whole pages of it.  Those pages
+ * are read once per group, for all its rows together; the rest request by
+ * request.  The result does not depend on where the prefix is said to end
+ * (up to rounding); group 1 or prefix_len 0 is ordinary paged attention.
+ *   q    bf16 [batch][n][n_q_heads][head_dim], dense
+ *   out  bf16, same shape;  lse fp32 [batch][n][n_q_heads] or NULL
+ *   ctx_len int32 [batch]: cached positions of each request, the n query rows'
+ *   own included; prefix_len int32 [batch/group], both on the device.
+ * Row i of request r sees positions [0, ctx_len[r]) or, causal, [0,
+ * ctx_len[r] - n + i].  A row that sees none gives out = 0, lse = -inf.
+ *   out = sum_j p_j v_j, p = softmax_j(scale * q . k_j), lse = ln sum_j
+ *   exp(scale * q . k_j); scale 0 stands for 1/sqrt(head_dim).
+ * Pages are read by whole 16-position pages up to the one ctx_len ends in; a
+ * page id out of range there reads as zeros and is recorded as
+ * DFLASH_ERR_CAPACITY (site 521), and so is a ctx_len beyond the page table
+ * (site 522; the table's capacity is used).  Positions at or past ctx_len
+ * never take part, whatever their pages hold.  K and V of the visible
+ * positions must be finite.  batch <= 1024 and <= kv->n_rows, 1 <= n <= 32.
+ * Scores, softmax statistics and accumulators are fp32; probabilities are
+ * rounded to bf16 for the product with V.  Deterministic.
+ * ws: initialised, dflash_attention_prefix_bytes(heads, batch, n, group)
+ * bytes (0: unsupported sizes). */
+size_t dflash_attention_prefix_bytes(const dflash_heads* heads, int32_t batch, int32_t n,
+                                     int32_t group);
+int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void* q, int32_t batch,
+                            int32_t n, int32_t group, int32_t causal, float scale,
+                            const dflash_kv* kv, const int32_t* ctx_len,
+                            const int32_t* prefix_len, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* One draw per row of logits (fp32 [rows][vocab], rows ld elements apart)
+ * under per-row settings, device arrays [rows]:
+ *   w_i = exp((z_i - max z) / temperature), tokens ordered by (z descending,
+ *   index ascending);
+ *   K = the first top_k tokens (top_k NULL or <= 0: all);
+ *   P = the shortest prefix of K with mass >= top_p * mass(K) (top_p NULL or
+ *   >= 1: all of K; at least one token);
+ *   M = the tokens with (z_i - max z) / temperature >= ln min_p (min_p NULL or
+ *   <= 0: all; above 1 it counts as 1);
+ *   kept = the tokens in K, P and M.
+ * The draw is that of dflash_sample_rows over the kept tokens: the smallest
+ * index with a * S < C (C the running sum of the kept w in index order, S
+ * their total, a fp64 [rows] in [0, 1)).  temperature 0 takes the largest
+ * logit (lowest index) alone; one below 1e-30 counts as 1e-30.
+ * Outputs: token int32; optional n_kept int32 and logprob fp32 (ln of the
+ * drawn token's probability among the kept).  Tokens with z = -inf are never
+ * kept.  A row without a finite maximum (all -inf, a NaN or +inf in it) or
+ * with a setting that is NaN, a temperature that is negative or infinite, or
+ * a outside [0, 1) gives token -1, n_kept 0, logprob 0 and records
+ * DFLASH_ERR_INVALID_ARG (site 541); the other rows are drawn as usual.
+ * Weights and sums are fixed point with 45 fractional bits (44 above 2^18
+ * tokens), summed exactly, so the result does not depend on any order; a
+ * weight below 2^-46 of the largest counts as zero mass.  A decision can
+ * differ from exact arithmetic only when its border is met within about 1e-11
+ * (relative, 1e-9 where nearly all tokens are about that far below the
+ * largest).  1 <= vocab <= 393216 (else DFLASH_ERR_UNSUPPORTED), ld >= vocab.
+ * ws: initialised, dflash_sample_filtered_bytes(rows, vocab) bytes. */
+size_t dflash_sample_filtered_bytes(int32_t rows, int32_t vocab);
+int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_t vocab,
+                           const float* temperature, const int32_t* top_k, const float* top_p,
+                           const float* min_p, const double* a, int32_t* token, int32_t* n_kept,
+                           float* logprob, void* ws, size_t ws_bytes, void* stream);
+
 /* ----------------------------------------------- end-to-end loop helpers */
 
 /* Causal target forward over `batch` requests x `n` consecutive rows

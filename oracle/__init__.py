@@ -31,6 +31,10 @@ checks of losslessness (tests/test_oracle_sampling.py).
 fp8 context K/V cache and the study of its effect on the draft logits,
 pinned against the format's table and PyTorch's float8 cast
 (tests/test_oracle_fp8.py).
+
+``oracle.serving`` holds the serving operators (rotation of q and k,
+attention of query rows to cached keys, filtered sampling), pinned in
+tests/test_oracle_serving.py.
 """
 from .dflash_oracle import *  # noqa: F401,F403
-from . import fp8, sampling  # noqa: F401,E402
+from . import fp8, sampling, serving  # noqa: F401,E402
