@@ -662,6 +662,22 @@ int check_cfg(const dflash_config* c, bool draft) {
 namespace dflash {
 int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
+int encode_kv_pages(CUtensorMap* map, const void* base, uint64_t groups, uint32_t d) {
+  const int rc = load_encode();
+  if (rc) return rc;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) != 0 || (d != 64 && d != 128))
+    return DFLASH_ERR_INVALID_ARG;
+  cuuint64_t dims[4] = {64, 8, d / 64, groups};
+  cuuint64_t strides[3] = {d * 2ull, 128ull, 8 * d * 2ull};
+  cuuint32_t box[4] = {64, 8, d / 64, 2};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_ERR_INVALID_ARG;
+}
+
 // Argument and capacity checks of dflash_ctx_fuse (nothing is launched).
 int ctx_fuse_check(const dflash_model_s* m, const void* taps, int32_t T, const void* ctx,
                    const void* ws, size_t ws_bytes) {

@@ -277,7 +277,14 @@ constexpr int kMaxSampleVocab = 393216;
 // sizes, then the launches (d = head_dim).
 struct PrefixParams;
 void prefix_attention_shape(PrefixParams* p);
-cudaError_t prefix_attention_launch(const PrefixParams& p, int d, cudaStream_t s);
+// map: encode_kv_pages over the pool (only when a list has large tiles);
+// group0: 8-row group of the layer's first page, oob_group: one past the end.
+cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,
+                                    int oob_group, cudaStream_t s);
+// 4-D map over `groups` groups of 8 rows of d bf16: box (64 columns, 8 rows,
+// d/64 column halves, 2 groups), one 16-row page as [group][half][8][128 B],
+// 128-byte swizzled, zero fill out of bounds.  A DFLASH_* code.
+int encode_kv_pages(CUtensorMap* map, const void* base, uint64_t groups, uint32_t d);
 
 // Records the error for dflash_last_cuda_error and returns DFLASH_ERR_CUDA.
 int record_cuda_error(cudaError_t e);

@@ -12,6 +12,8 @@
 // a page (16 keys) is a step of two m16n8 score tiles and one k16 step of the
 // product with V, fed by the warp's own ring of pages through cp.async, with
 // no barrier between warps.
+#include <climits>
+
 #include "attention.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -24,35 +26,13 @@ namespace {
 constexpr int kSmallWarps = 8;
 constexpr int kSmallCtas = 152;    // one per SM
 constexpr int kSmallRows = 16;
+constexpr int kTcMinRows = 32;     // an entity with more rows goes to the large tiles
 
 template <int D>
 struct SmallCfg {
   static constexpr int PAGE = 16 * D * 2;          // bytes of one page of K or V
   static constexpr int STAGES = D == 128 ? 3 : 6;  // pages in flight per warp
   static constexpr int RING = STAGES * 2 * PAGE;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Row `i` of a tile: the request and the row of q/out ([batch][n][hq]) it
-// stands for; false past the entity's rows.
-struct RowMap {
-  int e, ng, group, n, G, hq, kvh, rows;
-  __device__ RowMap(const PrefixParams& p, int entity, int kv_head)
-      : e(entity), ng(p.ng), group(p.group), n(p.n), G(p.hq / p.hkv), hq(p.hq), kvh(kv_head),
-        rows((entity < p.ng ? p.group : 1) * p.n * (p.hq / p.hkv)) {}
-  __device__ bool at(int row, int* req, int* i, size_t* vec) const {
-    if (row >= rows) return false;
-    const int h = row % G, bi = row / G;
-    *i = bi % n;
-    *req = e < ng ? e * group + bi / n : e - ng;
-    *vec = (static_cast<size_t>(*req) * n + *i) * hq + kvh * G + h;
-    return true;
-  }
 };
 
 template <int D>
@@ -71,28 +51,19 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int worker = blockIdx.x * kSmallWarps + warp;
-  const int total = off[ne];
-  const int per = chunks_per_worker(total, L.workers);
-  int c = worker * per;
-  const int c_end = min(total, c + per);
   uint8_t* ring = smem + warp * C::RING;
   const uint32_t ring_a = smem_u32(ring);
   const size_t head_elems = 16 * D;
   const size_t page_elems = static_cast<size_t>(2) * p.hkv * head_elems;
   const int tq = lane % 4, tg = lane / 4;
 
-  int e = c < c_end ? find_entity(off, ne, c) : 0;
-  while (c < c_end) {
-    while (off[e + 1] <= c) ++e;
+  Segments seg(L, off, ne, worker);
+  while (seg.next(p, L, off)) {
     // ---- the segment: unit (e, kvh, tile), its pages [pg0, pg1)
+    const int e = seg.e, pg0 = seg.chunk0, pg1 = seg.chunk1;
     const int tiles = entity_tiles(p, L, e);
-    const int nch = (off[e + 1] - off[e]) / (p.hkv * tiles);  // pages of one unit
-    const int in_e = c - off[e];
-    const int ul = in_e / nch;
-    const int pg0 = in_e - ul * nch;
-    const int pg1 = min(nch, pg0 + (c_end - c));
-    const int kvh = ul / tiles, tile = ul % tiles;
-    const int slot = units_before(p, L, e) + ul + worker;
+    const int kvh = seg.ul / tiles, tile = seg.ul % tiles;
+    const int slot = units_before(p, L, e) + seg.ul + worker;
     const bool pre = e < p.ng;
     const int req_t = pre ? live[e] : e - p.ng;               // whose table row
     const int page0 = pre ? 0 : cut[(e - p.ng) / p.group] / 16;
@@ -250,7 +221,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
         if (tq == 0) *reinterpret_cast<float2*>(L.part_ml + ps * 2) = make_float2(m_r[h], l);
       }
     }
-    c += pg1 - pg0;
   }
 }
 
@@ -289,15 +259,16 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
         if (tiles == 0) continue;
         const int c_lo = __ldcg(L.off + e), c_hi = __ldcg(L.off + e + 1);
         if (c_hi == c_lo) continue;
-        const int nch = (c_hi - c_lo) / (p.hkv * tiles);
-        const int per = chunks_per_worker(__ldcg(L.off + ne), L.workers);
         const int ul = kvh * tiles + row / L.tile_rows;
-        const int c0 = c_lo + ul * nch;
-        const int w0 = c0 / per, w1 = (c0 + nch - 1) / per;
+        int w0, w1;
+        unit_workers(p, L, e, ul, c_lo, c_hi, __ldcg(L.off + ne), &w0, &w1);
         const int unit = units_before(p, L, e) + ul;
-        for (int w = w0; w <= w1; ++w, ++turn) {
+        const bool two = part == 0 ? L.prefix_split : L.suffix_split;
+        for (int i2 = w0 * (two ? 2 : 1), last = w1 * (two ? 2 : 1) + (two ? 1 : 0); i2 <= last; ++i2, ++turn) {
           if (turn % WPV != sub) continue;
-          const size_t ps = static_cast<size_t>(unit + w) * L.tile_rows + row % L.tile_rows;
+          const int w = two ? i2 / 2 : i2;
+          const size_t ps = static_cast<size_t>(unit + w) * L.tile_rows + row % L.tile_rows +
+                            (two && i2 % 2 ? L.tile_rows / 2 : 0);
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(L.part_ml + ps * 2));
           float v[VEC];
 #pragma unroll
@@ -357,18 +328,18 @@ cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, void** 
 }
 
 template <int D>
-cudaError_t run(const PrefixParams& p, cudaStream_t s) {
+cudaError_t run_small(const PrefixParams& p, void** args, cudaStream_t s) {
   const int ne = p.ng + p.batch;
-  void* args[] = {const_cast<PrefixParams*>(&p)};
-  {
-    const size_t smem = kSmallWarps * SmallCfg<D>::RING + (ne + 1 + 2 * p.ng + 33) * sizeof(int);
-    const void* fn = reinterpret_cast<const void*>(prefix_small_kernel<D>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(fn, kSmallCtas, kSmallWarps * 32, smem, args, s);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = kSmallWarps * SmallCfg<D>::RING + (ne + 1 + 2 * p.ng + 33) * sizeof(int);
+  const void* fn = reinterpret_cast<const void*>(prefix_small_kernel<D>);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, kSmallCtas, kSmallWarps * 32, smem, args, s);
+}
+
+template <int D>
+cudaError_t run_join(const PrefixParams& p, void** args, cudaStream_t s) {
   const int vecs = p.batch * p.n * p.hq;
   // few vectors have many partials each: more warps per vector
   if (vecs >= 4096)
@@ -383,20 +354,36 @@ void prefix_attention_shape(PrefixParams* p) {
   const int G = p->hq / p->hkv;
   const int rows_p = p->group * p->n * G, rows_s = p->n * G;
   p->ng = p->batch / p->group;
+  const bool tc_p = p->group > 1 && rows_p > kTcMinRows, tc_s = rows_s > kTcMinRows;
   PrefixList& S = p->list[0];
   S.chunk_keys = 16;
   S.tile_rows = kSmallRows;
-  S.workers = kSmallCtas * kSmallWarps;
-  S.prefix_tiles = (rows_p + kSmallRows - 1) / kSmallRows;
-  S.suffix_tiles = (rows_s + kSmallRows - 1) / kSmallRows;
+  S.prefix_tiles = tc_p || p->group == 1 ? 0 : (rows_p + kSmallRows - 1) / kSmallRows;
+  S.suffix_tiles = tc_s ? 0 : (rows_s + kSmallRows - 1) / kSmallRows;
+  S.workers = S.prefix_tiles + S.suffix_tiles > 0 ? kSmallCtas * kSmallWarps : 0;
+  S.prefix_cost = S.suffix_cost = 1;
   PrefixList& T = p->list[1];
-  T = S;
-  T.workers = 0;
-  T.prefix_tiles = T.suffix_tiles = 0;
+  T.chunk_keys = 128;
+  T.tile_rows = 256;
+  T.prefix_tiles = tc_p ? (rows_p + 255) / 256 : 0;
+  T.suffix_tiles = tc_s ? (rows_s + 255) / 256 : 0;
+  T.workers = T.prefix_tiles + T.suffix_tiles > 0 ? kTcCtas : 0;
+  // up to 128 rows leave half of a tile's tensor work to do
+  T.prefix_split = rows_p <= 128;
+  T.suffix_split = rows_s <= 128;
+  T.prefix_cost = T.prefix_split ? 1 : 2;
+  T.suffix_cost = T.suffix_split ? 1 : 2;
+  T.unit_cost = 2;
 }
 
-cudaError_t prefix_attention_launch(const PrefixParams& p, int d, cudaStream_t s) {
-  return d == 128 ? run<128>(p, s) : run<64>(p, s);
+cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,
+                                    int oob_group, cudaStream_t s) {
+  void* args[] = {const_cast<PrefixParams*>(&p)};
+  cudaError_t e = cudaSuccess;
+  if (p.list[1].workers > 0) e = prefix_tc_launch(*map, group0, oob_group, p, d, s);
+  if (e == cudaSuccess && p.list[0].workers > 0) e = d == 128 ? run_small<128>(p, args, s) : run_small<64>(p, args, s);
+  if (e != cudaSuccess) return e;
+  return d == 128 ? run_join<128>(p, args, s) : run_join<64>(p, args, s);
 }
 
 }  // namespace dflash

@@ -9,12 +9,13 @@
 // (entity, KV head, row tile) is a unit.
 //
 // The lengths are on the device, so the host cannot deal out the keys.  Every
-// worker of a kernel derives the same list from them: all chunks of all units
-// in order, cut into equal ranges, one per worker, wherever a unit ends.  A
-// unit's part in one range is a segment; each leaves a partial (O, m, l) for
-// the unit's rows.  Segment number = unit + worker is unique and below units +
-// workers, which fixes its slot.  A last kernel joins the partials of each
-// row in order.
+// worker of a kernel derives the same list from them: all units in order, each
+// with a cost of unit_cost plus chunk_cost for every chunk, cut into ranges of
+// equal cost, one per worker; a chunk belongs to the worker in whose range its
+// cost starts.  A unit's part in one range is a segment; each leaves a partial
+// (O, m, l) for the unit's rows.  Unit + worker is unique per segment and below
+// units + workers, which fixes its slot.  A last kernel joins the partials of
+// each row in order.
 //
 // A prefix is cut short to whole pages that every row of the group sees
 // (causal rows near its end, short requests), so prefix chunks need no mask.
@@ -32,7 +33,11 @@ struct PrefixList {            // one kernel's share of the work
   int workers;
   int prefix_tiles;            // row tiles of a prefix (0: not this kernel's)
   int suffix_tiles;            // row tiles of a request (0: not this kernel's)
-  int* off;                    // [entities + 1] first chunk of each entity (written for the merge)
+  int unit_cost;               // see above; a range is at least one chunk's cost
+  int prefix_cost, suffix_cost;  // of a chunk
+  int prefix_split, suffix_split;  // 1: even and odd chunks of a segment leave partials of their
+                               // own, in rows [0, tile_rows/2) and [tile_rows/2, tile_rows)
+  int* off;                    // [entities + 1] cost before each entity (written for the join)
   float* part_o;               // [units + workers][tile_rows][d]
   float* part_ml;              // [units + workers][tile_rows][2]
 };
@@ -48,7 +53,7 @@ struct PrefixParams {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int* cut;                    // [ng] prefix keys used (written for the merge)
+  int* cut;                    // [ng] prefix keys used (written for the join)
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
 };
 
@@ -61,6 +66,10 @@ __device__ __forceinline__ int units_before(const PrefixParams& p, const PrefixL
 }
 __device__ __forceinline__ int entity_tiles(const PrefixParams& p, const PrefixList& L, int e) {
   return e < p.ng ? L.prefix_tiles : L.suffix_tiles;
+}
+
+__device__ __forceinline__ int chunk_cost(const PrefixParams& p, const PrefixList& L, int e) {
+  return e < p.ng ? L.prefix_cost : L.suffix_cost;
 }
 
 // The list, by all threads of a CTA: cut[ng] (keys of each group's prefix),
@@ -86,10 +95,10 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, const PrefixL
   __syncthreads();
   for (int g = tid; g < p.ng; g += nt) cut[g] = live[g] < p.batch ? cut[g] & ~15 : 0;
   __syncthreads();
-  // exclusive scan of the entities' chunks, thread t taking a run of them
+  // exclusive scan of the entities' costs, thread t taking a run of them
   const int ne = p.ng + p.batch;
   const int per = (ne + nt - 1) / nt;
-  auto chunks = [&](int e) {
+  auto cost = [&](int e) {
     int keys;
     if (e < p.ng) {
       keys = cut[e];
@@ -97,11 +106,12 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, const PrefixL
       const int c = clamped_ctx(p, e - p.ng);
       keys = max(0, c - cut[(e - p.ng) / p.group]);
     }
-    return (keys + L.chunk_keys - 1) / L.chunk_keys * p.hkv * entity_tiles(p, L, e);
+    const int n = (keys + L.chunk_keys - 1) / L.chunk_keys;
+    return n > 0 ? (L.unit_cost + n * chunk_cost(p, L, e)) * p.hkv * entity_tiles(p, L, e) : 0;
   };
   const int e0 = min(ne, tid * per), e1 = min(ne, e0 + per);
   int sum = 0;
-  for (int e = e0; e < e1; ++e) sum += chunks(e);
+  for (int e = e0; e < e1; ++e) sum += cost(e);
   int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -114,7 +124,7 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, const PrefixL
   for (int w = 0; w < tid / 32; ++w) run += scratch[w];
   for (int e = e0; e < e1; ++e) {
     off[e] = run;
-    run += chunks(e);
+    run += cost(e);
   }
   if (tid == nt - 1) off[ne] = run;  // the last thread's run ends at the total
   __syncthreads();
@@ -124,11 +134,11 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, const PrefixL
   }
 }
 
-__device__ __forceinline__ int chunks_per_worker(int total, int workers) {
-  return max(1, (total + workers - 1) / workers);
+__device__ __forceinline__ int cost_per_worker(const PrefixList& L, int total) {
+  return max(max(L.prefix_cost, L.suffix_cost), (total + L.workers - 1) / L.workers);
 }
 
-// The entity that holds chunk c (off[e] <= c < off[e + 1]).
+// The entity in whose cost c lies (off[e] <= c < off[e + 1]).
 __device__ __forceinline__ int find_entity(const int* off, int ne, int c) {
   int lo = 0, hi = ne;
   while (hi - lo > 1) {
@@ -138,5 +148,78 @@ __device__ __forceinline__ int find_entity(const int* off, int ne, int c) {
   }
   return lo;
 }
+
+// A worker's segments, one after the other.
+struct Segments {
+  int c, end;          // cost still to do
+  int e;               // entity
+  int ul;              // unit of the entity: head * tiles + tile
+  int chunk0, chunk1;  // the segment's chunks
+  int nch;             // the unit's
+  __device__ Segments(const PrefixList& L, const int* off, int ne, int worker) {
+    const int total = off[ne];
+    const int per = cost_per_worker(L, total);
+    const long long lo = static_cast<long long>(worker) * per;
+    c = lo < total ? static_cast<int>(lo) : total;
+    end = min(total - c, per) + c;
+    e = c < end ? find_entity(off, ne, c) : 0;
+  }
+  __device__ bool next(const PrefixParams& p, const PrefixList& L, const int* off) {
+    while (c < end) {
+      while (off[e + 1] <= c) ++e;
+      const int cw = chunk_cost(p, L, e);
+      const int units = p.hkv * entity_tiles(p, L, e);
+      const int unit = (off[e + 1] - off[e]) / units;  // cost of one
+      nch = (unit - L.unit_cost) / cw;
+      ul = (c - off[e]) / unit;
+      const int first = off[e] + ul * unit + L.unit_cost;  // where its chunks start
+      // chunks whose start lies in [c, end)
+      chunk0 = c > first ? (c - first + cw - 1) / cw : 0;
+      chunk1 = end > first ? min(nch, (end - first + cw - 1) / cw) : 0;
+      c = first - L.unit_cost + unit;
+      if (chunk0 < chunk1) return true;
+    }
+    return false;
+  }
+};
+
+// The workers [w0, w1] that have chunks of unit ul of entity e.
+__device__ __forceinline__ void unit_workers(const PrefixParams& p, const PrefixList& L, int e, int ul,
+                                             int off_e, int off_e1, int total, int* w0, int* w1) {
+  const int unit = (off_e1 - off_e) / (p.hkv * entity_tiles(p, L, e));
+  const int per = cost_per_worker(L, total);
+  const int first = off_e + ul * unit + L.unit_cost;
+  *w0 = first / per;
+  *w1 = (off_e + (ul + 1) * unit - chunk_cost(p, L, e)) / per;
+}
+
+// Row `row` of an entity: its request, block row, and vector of q and out
+// ([batch][n][hq]); false past the entity's rows.
+struct RowMap {
+  int e, ng, group, n, G, hq, kvh, rows;
+  __device__ RowMap(const PrefixParams& p, int entity, int kv_head)
+      : e(entity), ng(p.ng), group(p.group), n(p.n), G(p.hq / p.hkv), hq(p.hq), kvh(kv_head),
+        rows((entity < p.ng ? p.group : 1) * p.n * (p.hq / p.hkv)) {}
+  __device__ bool at(int row, int* req, int* i, size_t* vec) const {
+    if (row >= rows) return false;
+    const int h = row % G, bi = row / G;
+    *i = bi % n;
+    *req = e < ng ? e * group + bi / n : e - ng;
+    *vec = (static_cast<size_t>(*req) * n + *i) * hq + kvh * G + h;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Large tiles (prefix_attention_tc05.cu).  map: the pool as [rows / 8][d / 64][8
+// rows][64 columns], box one 16-row page.
+constexpr int kTcCtas = 152;
+cudaError_t prefix_tc_launch(const CUtensorMap& map, int group0, int oob_group, const PrefixParams& p,
+                             int d, cudaStream_t s);
 
 }  // namespace dflash

@@ -1,0 +1,495 @@
+// Attention over the paged cache for batches whose requests share a prefix:
+// the large-tile kernel (tcgen05), for entities of more than 32 rows per KV
+// head (prefixes of a batch, block verifies).
+//
+// One persistent CTA per SM works through its segments (prefix_attention.cuh).
+// A unit is 256 rows in two tiles of 128, A and B, which read the same keys,
+// 128 a chunk: per chunk and tile
+//   S = Q K^T   (M = 128, N = 128, K = d)   TMEM, 128 columns
+//   O += P V    (M = 128, N = d, K = 128)   TMEM, d columns
+// issued in the order S_A S_B | PV_A S_A' PV_B S_B' | ..., so that the tensor
+// cores work on one tile while the other's warps form P = exp2(S - m).  P
+// replaces S in TMEM (bf16, the A operand of the second product).  An entity of
+// at most 128 rows has no second tile: there A takes the even chunks and B the
+// odd ones, over the same Q, and both leave a partial result.
+//
+// Softmax: a thread per row (warps 0-3 tile A, 4-7 tile B), no exchange
+// between threads.  The row's reference maximum is raised, and O rescaled,
+// only when a chunk exceeds it by more than 2^8, which after the first chunks
+// is rare; P then stays below 2^8, exact enough in bf16 (relative rounding),
+// and l is summed in fp32.
+//
+// Keys arrive by TMA, one 4 KB box per page and plane, as [8-row group][column
+// half][8 rows][128 B]: the 8-row groups of a 128-key plane then lie at one
+// distance, which is what both the K-major (K) and the MN-major (V)
+// descriptors need; a box per column half would double the boxes, and the SM's
+// TMA unit spends a fixed time on each.  K and V planes of 32 KB (d = 128) go
+// through one ring in the order in which the MMAs use them, each released by
+// the MMA that read it last.
+#include "common.cuh"
+#include "kernels.h"
+#include "prefix_attention.cuh"
+
+namespace dflash {
+
+namespace {
+
+constexpr int kTcThreads = 320;   // warps 0-7 softmax, 8 TMA, 9 MMA
+constexpr int kChunk = 128;
+constexpr float kRaise = 8.f;     // log2
+
+template <int D>
+struct TcCfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int PAGE = 16 * D * 2;
+  static constexpr int PLANE = kChunk * D * 2;           // K or V of a chunk
+  static constexpr int Q_TILE = 128 * D * 2;             // [HALVES][128 rows][128 B]
+  static constexpr int MAX_SLOTS = D == 128 ? 5 : 10;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;      // two tiles each: + 128 * tile
+};
+
+// tcgen05.mma with the A operand in TMEM (lane = row, two bf16 of K per column)
+__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// K-major operand, 128-byte swizzle, 8-row groups `sbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr, uint32_t sbo) {
+  return (umma_desc_sw128(addr) & ~(0x3FFFull << 32)) | (static_cast<uint64_t>(sbo >> 4) << 32);
+}
+// 4-D tiled load (coordinates innermost first).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int w, uint64_t* bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Place of a segment's planes in the ring's order (n chunks): two tiles per
+// chunk K0 V0 K1 V1 ...; split K0 K1 V0 K2 V1 K3 ...
+__device__ __forceinline__ int place_k(bool split, int c) { return split ? c + max(0, c - 1) : 2 * c; }
+__device__ __forceinline__ int place_v(bool split, int c, int n) {
+  return split ? c + min(n, c + 2) : 2 * c + 1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PrefixParams p,
+                     int group0, int oob_group, int slots) {
+  using C = TcCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = sm + 2 * C::Q_TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + slots * C::PLANE);
+  uint64_t* empty = full + C::MAX_SLOTS;
+  uint64_t* s_full = empty + C::MAX_SLOTS;  // [2] S of a tile is complete (and the PV before it)
+  uint64_t* p_full = s_full + 2;            // [2] P of a tile is in TMEM
+  uint64_t* q_full = p_full + 2;            // Q of the segment is in shared memory
+  uint64_t* o_full = q_full + 1;            // all of the segment's products are complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const PrefixList& L = p.list[1];
+  const int ne = p.ng + p.batch;
+  int* off = reinterpret_cast<int*>(tmem_slot + 2);
+  int* cut = off + ne + 1;
+  int* live = cut + p.ng;
+  int* scratch = live + p.ng;
+
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (tid == 0) {
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(o_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map);
+  }
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  griddep_wait();
+  griddep_launch_dependents();
+  prefix_plan(p, L, cut, live, off, scratch);  // ends with a barrier
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int worker = blockIdx.x;
+  Segments seg(L, off, ne, worker);
+
+  if (warp == 8) {
+    // ------------------------------------------------ TMA producer
+    const uint64_t pol = l2_policy_evict_last();  // a prefix is read again by other row tiles
+    int at = 0;                                   // planes requested so far
+    bool ok = true;
+    while (ok && seg.next(p, L, off)) {
+      const int e = seg.e, n = seg.chunk1 - seg.chunk0;
+      const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
+      const int kvh = seg.ul / entity_tiles(p, L, e);
+      const int page0 = (pre ? 0 : cut[(e - p.ng) / p.group] / 16) + seg.chunk0 * 8;
+      const int pages_end = pre ? cut[e] / 16 : (clamped_ctx(p, e - p.ng) + 15) / 16;
+      const int npg = min(n * 8, pages_end - page0);
+      const int32_t* table = p.page_table + static_cast<size_t>(pre ? live[e] : e - p.ng) * p.max_pages + page0;
+      // lane -> 8-row group of its page's K plane in the map, 32 pages a time,
+      // the next 32 requested ahead
+      auto ids_of = [&](int b) {
+        const int j = b * 32 + lane;
+        return j < npg ? max(__ldcg(table + j), -1) : -2;  // -2: past the segment
+      };
+      auto check = [&](int id) {
+        if (id >= 0 && id < p.n_pages) return group0 + (id * 2 * p.hkv + kvh) * 2;
+        if (id != -2) raise_status(p.status, DFLASH_ERR_CAPACITY, 521);
+        return oob_group;
+      };
+      int kb = 0, vb = 0;  // 32-page batch held for K, for V
+      int next_id = ids_of(1);
+      int kg = check(ids_of(0)), vg = kg;
+      int k = 0, v = 0;
+      for (int i = 0; i < 2 * n; ++i, ++at) {
+        const bool is_k = k < n && place_k(split, k) == i;
+        const int c = is_k ? k++ : v++;
+        if (is_k) {
+          if (c / 4 != kb) {  // K runs ahead: V's batch is the previous one until it follows
+            kb = c / 4;
+            kg = check(next_id);
+            next_id = ids_of(kb + 1);
+          }
+        } else if (c / 4 != vb) {
+          vb = c / 4;
+          vg = kg;
+        }
+        // V's batch may lag one behind K's; K is at most two chunks ahead
+        const int grp = __shfl_sync(0xffffffffu, is_k ? kg : vg, (c % 4) * 8 + lane % 8);
+        const int st = at % slots;
+        int go = 1;
+        if (lane == 0) {
+          if (at >= slots && !mbar_wait(&empty[st], (at / slots - 1) & 1, abort_flag)) {
+            *abort_flag = 1;
+            raise_status(p.status, DFLASH_ERR_TIMEOUT, 523);
+            go = 0;
+          } else {
+            mbar_arrive_expect_tx(&full[st], C::PLANE);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, go, 0)) {
+          ok = false;
+          break;
+        }
+        if (lane < 8) {
+          const int y = grp == oob_group || is_k ? grp : grp + p.hkv * 2;
+          tma_load_4d(smem_u32(ring + st * C::PLANE + lane * C::PAGE), &map, y, &full[st], pol);
+        }
+      }
+    }
+    // copies still in flight after an abort land before the CTA exits
+    if (lane == 0)
+      for (int i = max(0, at - slots); i < at; ++i) mbar_wait(&full[i % slots], (i / slots) & 1, nullptr);
+  } else if (warp == 9) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D) | (1u << 16);  // V MN-major
+      constexpr uint32_t GS = C::HALVES * 1024;  // between 8-row groups of a plane
+      const uint32_t q_addr = smem_u32(sm), ring_addr = smem_u32(ring);
+      int at = 0, segs = 0;
+      int np[2] = {0, 0};  // P tiles consumed
+      bool ok = true;
+      auto wait_plane = [&](int i) { return mbar_wait(&full[i % slots], (i / slots) & 1, abort_flag); };
+      auto issue_s = [&](int tile, int q_tile, int i) {
+        const uint32_t kb = ring_addr + (i % slots) * C::PLANE;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          umma_bf16(tmem + C::S_COL + tile * 128,
+                    umma_desc_sw128(q_addr + q_tile * C::Q_TILE + (k / 4) * (128 * 128) + (k % 4) * 32),
+                    desc_k(kb + (k / 4) * 1024 + (k % 4) * 32, GS), idesc_s, k > 0 ? 1u : 0u);
+        umma_commit(&s_full[tile]);
+      };
+      auto issue_pv = [&](int tile, int i, bool accumulate) {
+        const uint32_t vb = ring_addr + (i % slots) * C::PLANE;
+#pragma unroll
+        for (int k = 0; k < kChunk / 16; ++k)
+          umma_bf16_ta(tmem + C::O_COL + tile * 128, tmem + C::S_COL + tile * 128 + k * 8,
+                       umma_desc_sw128_mn(vb + k * C::PAGE, 1024, GS), idesc_pv,
+                       accumulate || k > 0 ? 1u : 0u);
+      };
+      auto wait_p = [&](int tile) {
+        const bool r = mbar_wait(&p_full[tile], np[tile]++ & 1, abort_flag);
+        tc_fence_after();
+        return r;
+      };
+      while (ok && seg.next(p, L, off)) {
+        const int n = seg.chunk1 - seg.chunk0;
+        const bool split = seg.e < p.ng ? L.prefix_split : L.suffix_split;
+        ok = mbar_wait(q_full, segs++ & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (split) {
+          for (int c = 0; ok && c < min(2, n); ++c) {
+            const int ik = at + place_k(true, c);
+            ok = wait_plane(ik);
+            if (ok) {
+              issue_s(c, 0, ik);
+              umma_commit(&empty[ik % slots]);
+            }
+          }
+          for (int c = 0; ok && c < n; ++c) {
+            const int iv = at + place_v(true, c, n), t = c & 1;
+            ok = wait_plane(iv) && wait_p(t);
+            if (!ok) break;
+            issue_pv(t, iv, c >= 2);
+            umma_commit(&empty[iv % slots]);
+            if (c + 2 < n) {
+              const int ik = at + place_k(true, c + 2);
+              ok = wait_plane(ik);
+              if (ok) {
+                issue_s(t, 0, ik);
+                umma_commit(&empty[ik % slots]);
+              }
+            }
+          }
+        } else {
+          ok = wait_plane(at);
+          if (ok) {
+            issue_s(0, 0, at);
+            issue_s(1, 1, at);
+            umma_commit(&empty[at % slots]);
+          }
+          for (int c = 0; ok && c < n; ++c) {
+            const int iv = at + 2 * c + 1, ik = iv + 1;
+            const bool more = c + 1 < n;
+            ok = wait_plane(iv) && wait_p(0);
+            if (!ok) break;
+            issue_pv(0, iv, c > 0);
+            if (more) {
+              ok = wait_plane(ik);
+              if (!ok) break;
+              issue_s(0, 0, ik);
+            }
+            ok = wait_p(1);
+            if (!ok) break;
+            issue_pv(1, iv, c > 0);
+            umma_commit(&empty[iv % slots]);
+            if (more) {
+              issue_s(1, 1, ik);
+              umma_commit(&empty[ik % slots]);
+            }
+          }
+        }
+        if (ok) umma_commit(o_full);
+        at += 2 * n;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        raise_status(p.status, DFLASH_ERR_TIMEOUT, 524);
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax: a thread per row
+    const int tile = warp / 4;
+    const int r128 = (warp % 4) * 32 + lane;  // row of the tile, TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t s_addr = lane_base + C::S_COL + tile * 128;
+    const uint32_t o_addr = lane_base + C::O_COL + tile * 128;
+    int at = 0, segs = 0, ns = 0;
+    bool ok = true;
+    while (ok && seg.next(p, L, off)) {
+      const int e = seg.e, n = seg.chunk1 - seg.chunk0;
+      const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
+      const int tiles = entity_tiles(p, L, e);
+      const int kvh = seg.ul / tiles, row0 = seg.ul % tiles * L.tile_rows;
+      const RowMap rows(p, e, kvh);
+      // ---- Q of the segment (split: A's warps load it for both)
+      if (tile == 0 || !split) {
+        constexpr int CH = D / 8;
+        for (int i = (tid % 128); i < 128 * CH; i += 128) {
+          const int r = i / CH, c = i % CH;
+          int rq, ri;
+          size_t vec;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (rows.at(row0 + tile * 128 + r, &rq, &ri, &vec))
+            x = __ldcg(reinterpret_cast<const uint4*>(p.q + vec * D + c * 8));
+          *reinterpret_cast<uint4*>(sm + tile * C::Q_TILE + (c / 8) * (128 * 128) + r * 128 +
+                                    (((c % 8) ^ (r & 7)) << 4)) = x;
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      // keys this row sees, from the segment's first
+      const int my_row = row0 + (split ? r128 : tile * 128 + r128);
+      int lim = 0, stale = 0x7FFFFFFF;  // stale: keys from here on hold no data of the request
+      {
+        int rq, ri;
+        size_t vec;
+        const bool real = rows.at(my_row, &rq, &ri, &vec);
+        const int base = (pre ? 0 : cut[(e - p.ng) / p.group]) + seg.chunk0 * kChunk;
+        const int ctx = pre ? cut[e] : clamped_ctx(p, e - p.ng);
+        lim = (real && !pre && p.causal ? ctx - p.n + ri + 1 : ctx) - base;
+        if (ctx % 16) stale = ctx - base;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int c = split ? tile : 0; c < n; c += split ? 2 : 1) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[tile], ns++ & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld32_nowait(s_addr + j * 32, s[j]);
+        tmem_wait_ld(s[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) tmem_regs_ready(s[j]);
+        if (__any_sync(0xffffffffu, (c + 1) * kChunk > lim)) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (c * kChunk + j >= lim) s[j / 32][j % 32] = 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mx[j] = __uint_as_float(s[j][0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) mx[j] = fmaxf(mx[j], __uint_as_float(s[j][i]));
+        }
+        const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool raise = mc > m + kRaise;
+        const bool rescale = raise && m != -INFINITY;
+        if (__any_sync(0xffffffffu, rescale)) {
+          // S is complete, so the PV before it is too: O may be read
+          const float alpha = rescale ? ex2(m - mc) : 1.f;
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32_nowait(o_addr + q * 32, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st32(o_addr + q * 32, o);
+            tmem_wait_st();
+          }
+          l *= alpha;
+        }
+        if (raise) m = mc;
+        const float neg = m == -INFINITY ? 0.f : -m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[2 * h + j / 16][2 * j % 32]), p.scale_log2, neg));
+            const float p1 = ex2(fmaf(__uint_as_float(s[2 * h + j / 16][2 * j % 32 + 1]), p.scale_log2, neg));
+            ls[j & 3] += p0 + p1;
+            pk[j] = pack_bf2(p0, p1);
+          }
+          tmem_st32(s_addr + h * 32, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        if ((c + 1) * kChunk > stale) {
+          // the page the context ends in holds whatever was there past it: 0 * V must be 0
+          const int iv = at + place_v(split, c, n);
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[iv % slots], (iv / slots) & 1, abort_flag))) {
+            ok = false;
+            break;
+          }
+          uint8_t* vp = ring + (iv % slots) * C::PLANE;
+          for (int i = tid % 128; i < 16 * C::HALVES * 8; i += 128) {
+            const int key = (stale - c * kChunk) / 16 * 16 + i / (C::HALVES * 8);
+            const int hf = i / 8 % C::HALVES, c16 = i % 8;
+            if (key >= stale - c * kChunk && key < kChunk)
+              *reinterpret_cast<uint4*>(vp + (key / 8) * (C::HALVES * 1024) + hf * 1024 + (key % 8) * 128 +
+                                        ((c16 ^ (key & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[tile]);
+      }
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) ok = false;
+      ++segs;
+      if (!ok) break;
+      tc_fence_after();
+      // ---- partial of the segment
+      const bool have = !split || tile < n;     // split: this tile had a chunk
+      const size_t ps = static_cast<size_t>(units_before(p, L, e) + seg.ul + worker) * L.tile_rows +
+                        tile * 128 + r128;
+      const bool mine = my_row < rows.rows;
+      if (have) {
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32_nowait(o_addr + q * 32, o);
+          tmem_wait_ld(o);
+          if (mine) {
+            float* dst = L.part_o + ps * D + q * 32;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+      }
+      if (mine)
+        *reinterpret_cast<float2*>(L.part_ml + ps * 2) = make_float2(have ? m : -INFINITY, l);
+      tc_fence_before();
+      at += 2 * n;
+    }
+    if (!ok) {
+      *abort_flag = 1;
+      if (lane == 0) raise_status(p.status, DFLASH_ERR_TIMEOUT, 525);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& map, int group0, int oob_group, const PrefixParams& p, cudaStream_t s) {
+  using C = TcCfg<D>;
+  constexpr int kMax = 227 * 1024;
+  const int ne = p.ng + p.batch;
+  // barriers and flags, the lists, slack for the alignment
+  const int fixed = (2 * C::MAX_SLOTS + 6) * 8 + 8 + (ne + 1 + 2 * p.ng + 33) * 4 + 1024;
+  int slots = (kMax - fixed - 2 * C::Q_TILE) / C::PLANE;
+  if (slots > C::MAX_SLOTS) slots = C::MAX_SLOTS;
+  const int smem = fixed + 2 * C::Q_TILE + slots * C::PLANE;
+  cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kTcCtas);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, prefix_tc_kernel<D>, map, p, group0, oob_group, slots);
+}
+
+}  // namespace
+
+cudaError_t prefix_tc_launch(const CUtensorMap& map, int group0, int oob_group, const PrefixParams& p,
+                             int d, cudaStream_t s) {
+  return d == 128 ? launch<128>(map, group0, oob_group, p, s) : launch<64>(map, group0, oob_group, p, s);
+}
+
+}  // namespace dflash

@@ -230,12 +230,13 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
   if (kv->dtype != 0 || terms_of(heads) != 1) return DFLASH_ERR_UNSUPPORTED;
   if (batch > kv->n_rows) return DFLASH_ERR_CAPACITY;
   const int d = heads->head_dim;
-  // chunks are counted in 32 bits
+  // costs are counted in 32 bits
   for (const PrefixList& L : p.list) {
     const double units = static_cast<double>(p.hkv) *
                          (static_cast<double>(p.ng) * L.prefix_tiles + static_cast<double>(batch) * L.suffix_tiles);
-    if (units * (static_cast<double>(kv->max_pages) * 16 / L.chunk_keys + 1) >= 2147483648.0)
-      return DFLASH_ERR_UNSUPPORTED;
+    const double cost = std::max(L.prefix_cost, L.suffix_cost) *
+                        (static_cast<double>(kv->max_pages) * 16 / L.chunk_keys + 1) + L.unit_cost;
+    if (units * cost >= 2147483648.0) return DFLASH_ERR_UNSUPPORTED;
   }
   rc = check_ws(ws, ws_bytes, layout_prefix(&p, d, static_cast<uint8_t*>(ws)));
   if (rc) return rc;
@@ -252,7 +253,17 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.status = static_cast<int32_t*>(ws);
-  const cudaError_t e = prefix_attention_launch(p, d, static_cast<cudaStream_t>(stream));
+  CUtensorMap map;
+  const uint64_t layer_groups = static_cast<uint64_t>(kv->n_pages) * 2 * heads->n_kv_heads * 2;
+  const uint64_t groups = layer_groups * heads->n_layers;
+  if (p.list[1].workers > 0) {
+    // TMA coordinates are 32 bits
+    if (groups >= (1ull << 31) - 2) return DFLASH_ERR_UNSUPPORTED;
+    rc = encode_kv_pages(&map, kv->pool, groups, d);
+    if (rc) return rc;
+  }
+  const cudaError_t e = prefix_attention_launch(p, d, &map, static_cast<int>(layer_groups * layer),
+                                                static_cast<int>(groups), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
 }
 

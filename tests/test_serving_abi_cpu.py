@@ -100,7 +100,8 @@ def test_attention_refuses(lib):
                      (dict(out=ctypes.c_void_p(0x1008)), -1), (dict(ctx=None), -1), (dict(pre=None), -1),
                      (dict(layer=2), -1), (dict(kv=cache(n_rows=3)), -3),
                      (dict(kv=cache(dtype=1, scales=0x1000)), -2), (dict(hd=heads(kv_terms=2)), -2),
-                     (dict(hd=heads(head_dim=96)), -2), (dict(kv=cache(max_pages=1 << 26), n=32), -2),
+                     (dict(hd=heads(head_dim=96)), -2),
+                     (dict(kv=cache(max_pages=1 << 26, n_rows=1024), batch=1024, n=1), -2),
                      (dict(ws=ctypes.c_void_p((1 << 20) + 128)), -1), (dict(size=WS_N), -3)):
         assert attend(lib, **kw) == code, kw
     hd = heads()
