@@ -52,6 +52,12 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return static_cast<uint32_t>(f2bf(lo)) | (static_cast<uint32_t>(f2bf(hi)) << 16);
 }
 
+// The same in one conversion instruction.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
 // E4M3 codes of two floats (bits 0-7 from lo, 8-15 from hi): round to
 // nearest, ties to even, finite values beyond 448 saturate.
 __device__ __forceinline__ uint16_t e4m3x2_encode(float lo, float hi) {

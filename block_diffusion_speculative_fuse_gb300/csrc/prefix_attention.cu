@@ -26,7 +26,8 @@ namespace {
 constexpr int kSmallWarps = 8;
 constexpr int kSmallCtas = 152;    // one per SM
 constexpr int kSmallRows = 16;
-constexpr int kTcMinRows = 32;     // an entity with more rows goes to the large tiles
+constexpr int kTcMinRows = 32;     // an entity with more rows may go to the large tiles:
+constexpr int kTcMinKeys = 1024;   // every prefix, and a request's own keys from here on
 
 template <int D>
 struct SmallCfg {
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
   int* scratch = live + p.ng;
   griddep_launch_dependents();
   griddep_wait();
-  prefix_plan(p, L, cut, live, off, scratch);
+  prefix_plan(p, 0, cut, live, off, scratch);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int worker = blockIdx.x * kSmallWarps + warp;
@@ -183,8 +184,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
         }
         l_r[h] = l_r[h] * alpha[h] + sum;  // this thread's keys only
         m_r[h] = m_new;
-        a[h] = pack_bf2(x[0], x[1]);
-        a[2 + h] = pack_bf2(x[2], x[3]);
+        a[h] = bf16x2(x[0], x[1]);
+        a[2 + h] = bf16x2(x[2], x[3]);
       }
       if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
@@ -224,92 +225,149 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
   }
 }
 
-// Joins the partials of each (row, query head): WPV warps per vector, each
-// taking every WPV-th partial, in a fixed order.
+// Joins the partials of each vector (row, query head): WPV warps per vector,
+// warp `sub` taking the partials sub, sub + WPV, ...; the order is fixed.  The
+// bound is the latency of a few dependent loads, so each level of them (the
+// list's offsets, all (m, l), then eight O rows at a time) is issued at once.
 template <int D, int WPV>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) {
-  constexpr int VEC = D / 32;
+  constexpr int VEC = D / 32;  // columns per lane
   __shared__ float so[8][D];
   __shared__ float sml[8][2];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int vec = blockIdx.x * (8 / WPV) + warp / WPV, sub = warp % WPV;
-  const int vecs = p.batch * p.n * p.hq;
-  const bool on = vec < vecs;
+  const bool on = vec < p.batch * p.n * p.hq;
   const int ne = p.ng + p.batch;
   const int G = p.hq / p.hkv;
   float m = -INFINITY, l = 0.f, acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-  bool sees = false;
   if (on) {
     const int h = vec % p.hq, i = vec / p.hq % p.n, req = vec / p.hq / p.n;
-    const int kvh = h / G;
+    const int kvh = h / G, gi = req / p.group, se = p.ng + req;
+    const int pl = p.list[0].prefix_tiles > 0 ? 0 : 1;
+    const PrefixList& P = p.list[pl];
+    int offs[2][2], tot[2], po[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool used = p.list[j].workers > 0;
+      offs[j][0] = used ? __ldcg(p.list[j].off + se) : 0;
+      offs[j][1] = used ? __ldcg(p.list[j].off + se + 1) : 0;
+      tot[j] = used ? __ldcg(p.list[j].off + ne) : 0;
+    }
+    if (P.prefix_tiles > 0) {
+      po[0] = __ldcg(P.off + gi);
+      po[1] = __ldcg(P.off + gi + 1);
+    }
     const int ctx = clamped_ctx(p, req);
-    sees = (p.causal ? ctx - p.n + i + 1 : ctx) > 0;
-    if (sees) {
-      int turn = 0;
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        const int e = part == 0 ? req / p.group : p.ng + req;
-        const int row = part == 0 ? ((req % p.group) * p.n + i) * G + h % G : i * G + h % G;
-        const PrefixList& L = (part == 0 ? p.list[0].prefix_tiles : p.list[0].suffix_tiles) > 0 ? p.list[0] : p.list[1];
-        const int tiles = entity_tiles(p, L, e);
-        if (tiles == 0) continue;
-        const int c_lo = __ldcg(L.off + e), c_hi = __ldcg(L.off + e + 1);
-        if (c_hi == c_lo) continue;
-        const int ul = kvh * tiles + row / L.tile_rows;
-        int w0, w1;
-        unit_workers(p, L, e, ul, c_lo, c_hi, __ldcg(L.off + ne), &w0, &w1);
-        const int unit = units_before(p, L, e) + ul;
-        const bool two = part == 0 ? L.prefix_split : L.suffix_split;
-        for (int i2 = w0 * (two ? 2 : 1), last = w1 * (two ? 2 : 1) + (two ? 1 : 0); i2 <= last; ++i2, ++turn) {
-          if (turn % WPV != sub) continue;
-          const int w = two ? i2 / 2 : i2;
-          const size_t ps = static_cast<size_t>(unit + w) * L.tile_rows + row % L.tile_rows +
-                            (two && i2 % 2 ? L.tile_rows / 2 : 0);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(L.part_ml + ps * 2));
-          float v[VEC];
+    const bool sees = (p.causal ? ctx - p.n + i + 1 : ctx) > 0;
+    // a request's own keys are in one of the lists
+    const int sl = offs[1][1] > offs[1][0] ? 1 : 0;
+    const PrefixList& S = p.list[sl];
+    int pw0 = 0, np = 0, sw0 = 0, nsu = 0;
+    size_t p_at = 0, s_at = 0;  // partial row of worker 0
+    if (sees && po[1] > po[0]) {
+      const int row = ((req % p.group) * p.n + i) * G + h % G;
+      const int ul = kvh * P.prefix_tiles + row / P.tile_rows;
+      int w1;
+      unit_workers(p, P, gi, ul, po[0], po[1], tot[pl], &pw0, &w1);
+      np = w1 - pw0 + 1;
+      p_at = static_cast<size_t>(units_before(p, P, gi) + ul + pw0) * P.tile_rows + row % P.tile_rows;
+    }
+    if (sees && offs[sl][1] > offs[sl][0]) {
+      const int row = i * G + h % G;
+      const int ul = kvh * S.suffix_tiles + row / S.tile_rows;
+      int w1;
+      unit_workers(p, S, se, ul, offs[sl][0], offs[sl][1], tot[sl], &sw0, &w1);
+      nsu = w1 - sw0 + 1;
+      s_at = static_cast<size_t>(units_before(p, S, se) + ul + sw0) * S.tile_rows + row % S.tile_rows;
+    }
+    const int parts = np + nsu;
+    for (int b = sub; b < parts; b += 32 * WPV) {
+      const int mine = b + lane * WPV;  // this lane's partial
+      const int cnt = min(32, (parts - b + WPV - 1) / WPV);
+      const float* o = nullptr;
+      float ms = -INFINITY, ls = 0.f;
+      if (mine < parts) {
+        const bool pre = mine < np;
+        const PrefixList& L = pre ? P : S;
+        const size_t ps = pre ? p_at + static_cast<size_t>(mine) * P.tile_rows
+                              : s_at + static_cast<size_t>(mine - np) * S.tile_rows;
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(L.part_ml + ps * 2));
+        o = L.part_o + ps * D;
+        ms = v.x;
+        ls = v.y;
+      }
+      // -inf: the row saw none of that segment's keys, and no O was written
+      const float mn = fmaxf(m, warp_max(ms));
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float w = ms == -INFINITY ? 0.f : exp2f(ms - ref);
+      const float f0 = exp2f(m - ref);
+      l = l * f0 + warp_sum(ls * w);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] = __ldcg(L.part_o + ps * D + j * 32 + lane);
-          if (ml.x == -INFINITY) continue;   // the row saw none of the segment's keys
-          const float mn = fmaxf(m, ml.x);
-          const float f0 = exp2f(m - mn), f1 = exp2f(ml.x - mn);
-          l = l * f0 + ml.y * f1;
+      for (int j = 0; j < VEC; ++j) acc[j] *= f0;
+      m = mn;
+      for (int j0 = 0; j0 < cnt; j0 += 8) {
+        float v[8][VEC], wj[8];
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) acc[j] = acc[j] * f0 + v[j] * f1;
-          m = mn;
+        for (int j = 0; j < 8; ++j) {
+          const float* src = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (j0 + j) & 31));
+          wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+          const bool use = j0 + j < cnt && wj[j] > 0.f;
+          if (!use) wj[j] = 0.f;
+          if constexpr (VEC == 4) {
+            const float4 x = use ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+          } else {
+            const float2 x = use ? __ldcg(reinterpret_cast<const float2*>(src) + lane) : make_float2(0.f, 0.f);
+            v[j][0] = x.x, v[j][1] = x.y;
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int t = 0; t < VEC; ++t) acc[t] = fmaf(v[j][t], wj[j], acc[t]);
       }
     }
   }
   if (WPV > 1) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) so[warp][j * 32 + lane] = acc[j];
+    for (int j = 0; j < VEC; ++j) so[warp][lane * VEC + j] = acc[j];
     if (lane == 0) {
       sml[warp][0] = m;
       sml[warp][1] = l;
     }
     __syncthreads();
     if (sub != 0 || !on) return;
-    for (int w = 1; w < WPV; ++w) {
-      const float mw = sml[warp + w][0];
-      if (mw == -INFINITY) continue;
-      const float mn = fmaxf(m, mw);
-      const float f0 = exp2f(m - mn), f1 = exp2f(mw - mn);
-      l = l * f0 + sml[warp + w][1] * f1;
+    float mn = m;
+    for (int w = 1; w < WPV; ++w) mn = fmaxf(mn, sml[warp + w][0]);
+    if (mn > -INFINITY) {
+      const float f0 = exp2f(m - mn);
+      l *= f0;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) acc[j] = acc[j] * f0 + so[warp + w][j * 32 + lane] * f1;
+      for (int j = 0; j < VEC; ++j) acc[j] *= f0;
+      for (int w = 1; w < WPV; ++w) {
+        const float f1 = exp2f(sml[warp + w][0] - mn);
+        l = fmaf(sml[warp + w][1], f1, l);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] = fmaf(so[warp + w][lane * VEC + j], f1, acc[j]);
+      }
       m = mn;
     }
   }
   if (!on) return;
-  const float inv = sees ? 1.f / l : 0.f;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) p.out[static_cast<size_t>(vec) * D + j * 32 + lane] = f2bf(acc[j] * inv);
+  const bool any = m > -INFINITY;
+  const float inv = any ? 1.f / l : 0.f;
+  uint16_t* dst = p.out + static_cast<size_t>(vec) * D + lane * VEC;
+  if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = bf16x2(acc[0] * inv, acc[1] * inv);
   if (p.lse != nullptr && lane == 0)
-    p.lse[vec] = sees ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+    p.lse[vec] = any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
 cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, void** args, cudaStream_t s) {
@@ -359,7 +417,7 @@ void prefix_attention_shape(PrefixParams* p) {
   S.chunk_keys = 16;
   S.tile_rows = kSmallRows;
   S.prefix_tiles = tc_p || p->group == 1 ? 0 : (rows_p + kSmallRows - 1) / kSmallRows;
-  S.suffix_tiles = tc_s ? 0 : (rows_s + kSmallRows - 1) / kSmallRows;
+  S.suffix_tiles = (rows_s + kSmallRows - 1) / kSmallRows;
   S.workers = S.prefix_tiles + S.suffix_tiles > 0 ? kSmallCtas * kSmallWarps : 0;
   S.prefix_cost = S.suffix_cost = 1;
   PrefixList& T = p->list[1];
@@ -374,6 +432,7 @@ void prefix_attention_shape(PrefixParams* p) {
   T.prefix_cost = T.prefix_split ? 1 : 2;
   T.suffix_cost = T.suffix_split ? 1 : 2;
   T.unit_cost = 2;
+  p->large_keys = kTcMinKeys;
 }
 
 cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,

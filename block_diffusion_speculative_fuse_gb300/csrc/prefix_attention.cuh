@@ -35,8 +35,7 @@ struct PrefixList {            // one kernel's share of the work
   int suffix_tiles;            // row tiles of a request (0: not this kernel's)
   int unit_cost;               // see above; a range is at least one chunk's cost
   int prefix_cost, suffix_cost;  // of a chunk
-  int prefix_split, suffix_split;  // 1: even and odd chunks of a segment leave partials of their
-                               // own, in rows [0, tile_rows/2) and [tile_rows/2, tile_rows)
+  int prefix_split, suffix_split;  // large tiles: at most 128 rows (see there)
   int* off;                    // [entities + 1] cost before each entity (written for the join)
   float* part_o;               // [units + workers][tile_rows][d]
   float* part_ml;              // [units + workers][tile_rows][2]
@@ -54,6 +53,8 @@ struct PrefixParams {
   float* lse;
   int32_t* status;
   int* cut;                    // [ng] prefix keys used (written for the join)
+  int large_keys;              // a request with this many keys past the prefix is the large
+                               // tiles' where they take requests at all
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
 };
 
@@ -68,6 +69,11 @@ __device__ __forceinline__ int entity_tiles(const PrefixParams& p, const PrefixL
   return e < p.ng ? L.prefix_tiles : L.suffix_tiles;
 }
 
+// Whether a list takes what follows the prefix of a request, of `keys` keys.
+__device__ __forceinline__ bool takes_suffix(const PrefixParams& p, int list, int keys) {
+  const bool large = p.list[1].suffix_tiles > 0 && (keys >= p.large_keys || p.list[0].suffix_tiles == 0);
+  return (list == 1) == large;
+}
 __device__ __forceinline__ int chunk_cost(const PrefixParams& p, const PrefixList& L, int e) {
   return e < p.ng ? L.prefix_cost : L.suffix_cost;
 }
@@ -75,8 +81,9 @@ __device__ __forceinline__ int chunk_cost(const PrefixParams& p, const PrefixLis
 // The list, by all threads of a CTA: cut[ng] (keys of each group's prefix),
 // live[ng] (a request of the group whose table is read for it), off[ne + 1].
 // scratch: 33 ints.
-__device__ __forceinline__ void prefix_plan(const PrefixParams& p, const PrefixList& L, int* cut,
-                                            int* live, int* off, int* scratch) {
+__device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, int* cut, int* live,
+                                            int* off, int* scratch) {
+  const PrefixList& L = p.list[list];
   const int tid = threadIdx.x, nt = blockDim.x;
   for (int g = tid; g < p.ng; g += nt) {
     cut[g] = p.group > 1 ? min(max(__ldcg(p.prefix_len + g), 0), p.max_pages * 16) : 0;
@@ -105,6 +112,7 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, const PrefixL
     } else {
       const int c = clamped_ctx(p, e - p.ng);
       keys = max(0, c - cut[(e - p.ng) / p.group]);
+      if (!takes_suffix(p, list, keys)) keys = 0;
     }
     const int n = (keys + L.chunk_keys - 1) / L.chunk_keys;
     return n > 0 ? (L.unit_cost + n * chunk_cost(p, L, e)) * p.hkv * entity_tiles(p, L, e) : 0;

@@ -11,7 +11,7 @@
 // cores work on one tile while the other's warps form P = exp2(S - m).  P
 // replaces S in TMEM (bf16, the A operand of the second product).  An entity of
 // at most 128 rows has no second tile: there A takes the even chunks and B the
-// odd ones, over the same Q, and both leave a partial result.
+// odd ones, over the same Q, and the two states are joined at the end.
 //
 // Softmax: a thread per row (warps 0-3 tile A, 4-7 tile B), no exchange
 // between threads.  The row's reference maximum is raised, and O rescaled,
@@ -48,19 +48,52 @@ struct TcCfg {
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // two tiles each: + 128 * tile
 };
 
-// tcgen05.mma with the A operand in TMEM (lane = row, two bf16 of K per column)
-__device__ __forceinline__ void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// One thread issues the products, and an M = N = 128, K = 16 step takes the
+// tensor pipe 64 cycles: building both 64-bit descriptors anew for each step
+// took that thread 150.  Only the address field changes from step to step, so
+// the steps add constants to a low word (address >> 4, leading offset) and join
+// it with a constant high word (stride between 8-row groups, version, swizzle).
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t group_stride) {
+  return (group_stride >> 4) | (1u << 14) | (2u << 29);  // bits 32-45, 46, 61-63: SWIZZLE_128B
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading) {
+  return (addr >> 4) | ((leading >> 4) << 16);
+}
+// A and B in shared memory
+__device__ __forceinline__ void umma_ss(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// K-major operand, 128-byte swizzle, 8-row groups `sbo` bytes apart.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr, uint32_t sbo) {
-  return (umma_desc_sw128(addr) & ~(0x3FFFull << 32)) | (static_cast<uint64_t>(sbo >> 4) << 32);
+// A in TMEM (lane = row, two bf16 of K per column)
+__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
 }
 // 4-D tiled load (coordinates innermost first).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int w, uint64_t* bar,
@@ -122,7 +155,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   griddep_wait();
   griddep_launch_dependents();
-  prefix_plan(p, L, cut, live, off, scratch);  // ends with a barrier
+  prefix_plan(p, 1, cut, live, off, scratch);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -209,21 +242,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       auto wait_plane = [&](int i) { return mbar_wait(&full[i % slots], (i / slots) & 1, abort_flag); };
       auto issue_s = [&](int tile, int q_tile, int i) {
-        const uint32_t kb = ring_addr + (i % slots) * C::PLANE;
+        const uint32_t q = desc_lo(q_addr + q_tile * C::Q_TILE, 16);
+        const uint32_t k = desc_lo(ring_addr + (i % slots) * C::PLANE, 16);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_bf16(tmem + C::S_COL + tile * 128,
-                    umma_desc_sw128(q_addr + q_tile * C::Q_TILE + (k / 4) * (128 * 128) + (k % 4) * 32),
-                    desc_k(kb + (k / 4) * 1024 + (k % 4) * 32, GS), idesc_s, k > 0 ? 1u : 0u);
+        for (int j = 0; j < D / 16; ++j)
+          umma_ss(tmem + C::S_COL + tile * 128, desc_of(q + (j / 4) * (128 * 128 / 16) + (j % 4) * 2, desc_hi(1024)),
+                  desc_of(k + (j / 4) * (1024 / 16) + (j % 4) * 2, desc_hi(GS)), idesc_s, j > 0 ? 1u : 0u);
         umma_commit(&s_full[tile]);
       };
       auto issue_pv = [&](int tile, int i, bool accumulate) {
-        const uint32_t vb = ring_addr + (i % slots) * C::PLANE;
+        const uint32_t v = desc_lo(ring_addr + (i % slots) * C::PLANE, 1024);
+        const uint32_t o = tmem + C::O_COL + tile * 128, pa = tmem + C::S_COL + tile * 128;
 #pragma unroll
-        for (int k = 0; k < kChunk / 16; ++k)
-          umma_bf16_ta(tmem + C::O_COL + tile * 128, tmem + C::S_COL + tile * 128 + k * 8,
-                       umma_desc_sw128_mn(vb + k * C::PAGE, 1024, GS), idesc_pv,
-                       accumulate || k > 0 ? 1u : 0u);
+        for (int j = 0; j < kChunk / 16; ++j)
+          umma_ts(o, pa + j * 8, desc_of(v + j * (C::PAGE / 16), desc_hi(GS)), idesc_pv,
+                  j > 0 ? 1u : accumulate ? 1u : 0u);
       };
       auto wait_p = [&](int tile) {
         const bool r = mbar_wait(&p_full[tile], np[tile]++ & 1, abort_flag);
@@ -303,9 +336,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
     const uint32_t s_addr = lane_base + C::S_COL + tile * 128;
     const uint32_t o_addr = lane_base + C::O_COL + tile * 128;
+    // After a wait that gave up, a warp goes on through the segments without
+    // waiting, so that all warps meet at the same named barriers; the results
+    // are void (the status word says so).
     int at = 0, segs = 0, ns = 0;
     bool ok = true;
-    while (ok && seg.next(p, L, off)) {
+    while (seg.next(p, L, off)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
       const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
       const int tiles = entity_tiles(p, L, e);
@@ -341,31 +377,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (ctx % 16) stale = ctx - base;
       }
       float m = -INFINITY, l = 0.f;
-      for (int c = split ? tile : 0; c < n; c += split ? 2 : 1) {
+      for (int c = split ? tile : 0; ok && c < n; c += split ? 2 : 1) {
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[tile], ns++ & 1, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t s[4][32];
+        // the row's maximum; in a chunk that ends past this row's keys the
+        // scores beyond them become -inf, here and in TMEM
+        const bool masked = __any_sync(0xffffffffu, (c + 1) * kChunk > lim);
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[32], b[32];
+          tmem_ld32_nowait(s_addr + h * 64, a);
+          tmem_ld32_nowait(s_addr + h * 64 + 32, b);
+          tmem_wait_ld(a);
+          tmem_regs_ready(b);
+          if (masked) {
+            const int left = lim - c * kChunk - h * 64;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32_nowait(s_addr + j * 32, s[j]);
-        tmem_wait_ld(s[0]);
+            for (int j = 0; j < 32; ++j) {
+              if (j >= left) a[j] = 0xFF800000u;
+              if (j + 32 >= left) b[j] = 0xFF800000u;
+            }
+            tmem_st32(s_addr + h * 64, a);
+            tmem_st32(s_addr + h * 64 + 32, b);
+          }
+          float m0 = mx, m1 = mx;
 #pragma unroll
-        for (int j = 1; j < 4; ++j) tmem_regs_ready(s[j]);
-        if (__any_sync(0xffffffffu, (c + 1) * kChunk > lim)) {
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (c * kChunk + j >= lim) s[j / 32][j % 32] = 0xFF800000u;
+          for (int j = 0; j < 32; j += 2) {
+            m0 = fmaxf(m0, fmaxf(__uint_as_float(a[j]), __uint_as_float(a[j + 1])));
+            m1 = fmaxf(m1, fmaxf(__uint_as_float(b[j]), __uint_as_float(b[j + 1])));
+          }
+          mx = fmaxf(m0, m1);
         }
-        float mx[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mx[j] = __uint_as_float(s[j][0]);
-#pragma unroll
-          for (int i = 1; i < 32; ++i) mx[j] = fmaxf(mx[j], __uint_as_float(s[j][i]));
-        }
-        const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (masked) tmem_wait_st();
+        const float mc = mx * p.scale_log2;
         const bool raise = mc > m + kRaise;
         const bool rescale = raise && m != -INFINITY;
         if (__any_sync(0xffffffffu, rescale)) {
@@ -384,21 +432,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l *= alpha;
         }
         if (raise) m = mc;
+        // P = exp2(scale S - m) in bf16 over S, 32 columns at a time, the next
+        // 32 on their way
         const float neg = m == -INFINITY ? 0.f : -m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(neg, neg);
+        float2 la = make_float2(0.f, 0.f), lb = la;
+        auto form = [&](const uint32_t (&x)[32], uint32_t* pk) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 t = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc2, neg2);
+            t.x = ex2(t.x);
+            t.y = ex2(t.y);
+            if (j & 1) lb = add2(lb, t);
+            else la = add2(la, t);
+            pk[j] = bf16x2(t.x, t.y);
+          }
+        };
+        uint32_t x0[32], x1[32];
+        tmem_ld32_nowait(s_addr, x0);
+        tmem_wait_ld(x0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[2 * h + j / 16][2 * j % 32]), p.scale_log2, neg));
-            const float p1 = ex2(fmaf(__uint_as_float(s[2 * h + j / 16][2 * j % 32 + 1]), p.scale_log2, neg));
-            ls[j & 3] += p0 + p1;
-            pk[j] = pack_bf2(p0, p1);
-          }
+          tmem_ld32_nowait(s_addr + h * 64 + 32, x1);
+          form(x0, pk);
+          tmem_wait_ld(x1);
+          if (h == 0) tmem_ld32_nowait(s_addr + 64, x0);
+          form(x1, pk + 16);
+          if (h == 0) tmem_wait_ld(x0);
           tmem_st32(s_addr + h * 32, pk);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += (la.x + la.y) + (lb.x + lb.y);
         if ((c + 1) * kChunk > stale) {
           // the page the context ends in holds whatever was there past it: 0 * V must be 0
           const int iv = at + place_v(split, c, n);
@@ -423,29 +487,88 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) ok = false;
       ++segs;
-      if (!ok) break;
       tc_fence_after();
-      // ---- partial of the segment
-      const bool have = !split || tile < n;     // split: this tile had a chunk
-      const size_t ps = static_cast<size_t>(units_before(p, L, e) + seg.ul + worker) * L.tile_rows +
-                        tile * 128 + r128;
-      const bool mine = my_row < rows.rows;
-      if (have) {
+      // ---- partial of the segment.  O goes through shared memory (the Q
+      // tiles are free now: a quarter of one for each warp's 32 rows, half a row
+      // at a time) so that rows are written to global memory whole.  Split: B
+      // hands its state to A's warp with the same rows, which joins the two.
+      constexpr int COLS = D / 2, PIECES = COLS / 4;  // half a row; its 16-byte pieces
+      constexpr int STAGE = 32 * COLS * 4;
+      static_assert(8 * STAGE <= 2 * C::Q_TILE, "stages fit the Q tiles");
+      const bool have = !split || tile < n;  // split: this tile had a chunk
+      uint8_t* stage = sm + warp * STAGE;
+      uint8_t* stage_b = sm + (4 + warp % 4) * STAGE;
+      auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + warp % 4) : "memory"); };
+      float wa = 1.f, wb = 0.f;
+      if (split) {
+        if (tile == 1) *reinterpret_cast<float2*>(stage + lane * 8) = make_float2(have ? m : -INFINITY, l);
+        pair_sync();
+        if (tile == 0) {
+          const float2 b = *reinterpret_cast<const float2*>(stage_b + lane * 8);
+          const float mn = fmaxf(m, b.x);
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          wa = ex2(m - ref);
+          wb = ex2(b.x - ref);
+          l = l * wa + b.y * wb;
+          m = mn;
+        }
+        pair_sync();
+      }
+      const size_t slot_row = static_cast<size_t>(units_before(p, L, e) + seg.ul + worker) * L.tile_rows;
+      const int first = (split ? 0 : tile * 128) + (warp % 4) * 32;  // the warp's first row in the unit
+      const int rows_here = min(32, rows.rows - row0 - first);
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld32_nowait(o_addr + q * 32, o);
-          tmem_wait_ld(o);
-          if (mine) {
-            float* dst = L.part_o + ps * D + q * 32;
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[COLS / 32][32];
+        if (have) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int j = 0; j < COLS / 32; ++j) tmem_ld32_nowait(o_addr + half * COLS + j * 32, o[j]);
+          tmem_wait_ld(o[0]);
+#pragma unroll
+          for (int j = 1; j < COLS / 32; ++j) tmem_regs_ready(o[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) o[j / 32][j % 32] = 0u;
+        }
+        auto at16 = [&](uint8_t* base, int r, int piece) {
+          return reinterpret_cast<uint4*>(base + r * (COLS * 4) + ((piece ^ (r & (PIECES - 1))) << 4));
+        };
+        auto put = [&]() {
+#pragma unroll
+          for (int j = 0; j < PIECES; ++j)
+            *at16(stage, lane, j) = make_uint4(o[j / 8][j % 8 * 4], o[j / 8][j % 8 * 4 + 1], o[j / 8][j % 8 * 4 + 2],
+                                               o[j / 8][j % 8 * 4 + 3]);
+        };
+        if (split) {
+          if (tile == 1) put();
+          pair_sync();
+          if (tile == 0) {
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+              const uint4 b = *at16(stage_b, lane, j);
+              const uint32_t x[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                uint32_t& y = o[j / 8][j % 8 * 4 + t];
+                y = __float_as_uint(__uint_as_float(y) * wa + __uint_as_float(x[t]) * wb);
+              }
+            }
           }
+          pair_sync();  // B may put its next half
+        }
+        if (tile == 0 || !split) {
+          put();
+          __syncwarp();
+          for (int r = lane / PIECES; r < rows_here; r += 32 / PIECES)
+            *reinterpret_cast<uint4*>(L.part_o + (slot_row + first + r) * D + half * COLS + (lane % PIECES) * 4) =
+                *at16(stage, r, lane % PIECES);
+          __syncwarp();
         }
       }
-      if (mine)
-        *reinterpret_cast<float2*>(L.part_ml + ps * 2) = make_float2(have ? m : -INFINITY, l);
+      if ((tile == 0 || !split) && lane < rows_here)
+        *reinterpret_cast<float2*>(L.part_ml + (slot_row + first + lane) * 2) = make_float2(m, l);
+      // the next Q overwrites the stages: all of the tiles' warps are done
+      asm volatile("bar.sync 5, 256;" ::: "memory");
       tc_fence_before();
       at += 2 * n;
     }

@@ -45,8 +45,8 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]),
-                                            pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+  *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]),
+                                            bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
 }
 // the low terms bf16(x - bf16(x))
 __device__ __forceinline__ void store8_lo(uint16_t* p, const float (&x)[8]) {
