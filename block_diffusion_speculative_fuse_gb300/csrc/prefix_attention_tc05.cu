@@ -349,16 +349,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const RowMap rows(p, e, kvh);
       // ---- Q of the segment (split: A's warps load it for both)
       if (tile == 0 || !split) {
-        constexpr int CH = D / 8;
-        for (int i = (tid % 128); i < 128 * CH; i += 128) {
-          const int r = i / CH, c = i % CH;
-          int rq, ri;
-          size_t vec;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (rows.at(row0 + tile * 128 + r, &rq, &ri, &vec))
-            x = __ldcg(reinterpret_cast<const uint4*>(p.q + vec * D + c * 8));
-          *reinterpret_cast<uint4*>(sm + tile * C::Q_TILE + (c / 8) * (128 * 128) + r * 128 +
-                                    (((c % 8) ^ (r & 7)) << 4)) = x;
+        // piece c of rows r0, r0 + RS, ...; eight loads in flight
+        constexpr int CH = D / 8, RS = 128 / CH;
+        const int c = tid % CH, r0 = tid % 128 / CH;
+#pragma unroll 1
+        for (int b = 0; b < 128; b += 8 * RS) {
+          uint4 x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            int rq, ri;
+            size_t vec;
+            x[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (rows.at(row0 + tile * 128 + b + j * RS + r0, &rq, &ri, &vec))
+              x[j] = __ldcg(reinterpret_cast<const uint4*>(p.q + vec * D + c * 8));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = b + j * RS + r0;
+            *reinterpret_cast<uint4*>(sm + tile * C::Q_TILE + (c / 8) * (128 * 128) + r * 128 +
+                                      (((c % 8) ^ (r & 7)) << 4)) = x[j];
+          }
         }
         fence_proxy_async_smem();
       }
