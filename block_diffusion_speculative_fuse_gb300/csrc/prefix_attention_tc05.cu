@@ -105,6 +105,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Position in the ring: the slot and the parity of its present round.  (Slot
+// numbers by division cost the issuing thread 600 cycles a chunk.)
+struct Cursor {
+  int slot = 0, parity = 0;
+  __device__ __forceinline__ void advance(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // Place of a segment's planes in the ring's order (n chunks): two tiles per
 // chunk K0 V0 K1 V1 ...; split K0 K1 V0 K2 V1 K3 ...
 __device__ __forceinline__ int place_k(bool split, int c) { return split ? c + max(0, c - 1) : 2 * c; }
@@ -167,6 +179,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------ TMA producer
     const uint64_t pol = l2_policy_evict_last();  // a prefix is read again by other row tiles
     int at = 0;                                   // planes requested so far
+    Cursor cur;
     bool ok = true;
     while (ok && seg.next(p, L, off)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int next_id = ids_of(1);
       int kg = check(ids_of(0)), vg = kg;
       int k = 0, v = 0;
-      for (int i = 0; i < 2 * n; ++i, ++at) {
+      for (int i = 0; i < 2 * n; ++i, ++at, cur.advance(slots)) {
         const bool is_k = k < n && place_k(split, k) == i;
         const int c = is_k ? k++ : v++;
         if (is_k) {
@@ -206,10 +219,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // V's batch may lag one behind K's; K is at most two chunks ahead
         const int grp = __shfl_sync(0xffffffffu, is_k ? kg : vg, (c % 4) * 8 + lane % 8);
-        const int st = at % slots;
+        const int st = cur.slot;
         int go = 1;
         if (lane == 0) {
-          if (at >= slots && !mbar_wait(&empty[st], (at / slots - 1) & 1, abort_flag)) {
+          if (at >= slots && !mbar_wait(&empty[st], cur.parity ^ 1, abort_flag)) {
             *abort_flag = 1;
             raise_status(p.status, DFLASH_ERR_TIMEOUT, 523);
             go = 0;
@@ -237,21 +250,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D) | (1u << 16);  // V MN-major
       constexpr uint32_t GS = C::HALVES * 1024;  // between 8-row groups of a plane
       const uint32_t q_addr = smem_u32(sm), ring_addr = smem_u32(ring);
-      int at = 0, segs = 0;
-      int np[2] = {0, 0};  // P tiles consumed
+      int segs = 0;
+      int np[2] = {0, 0};  // parity of the next P of each tile
       bool ok = true;
-      auto wait_plane = [&](int i) { return mbar_wait(&full[i % slots], (i / slots) & 1, abort_flag); };
-      auto issue_s = [&](int tile, int q_tile, int i) {
+      Cursor cur;          // the next plane: they are used in the order they arrive
+      // waits for the next plane and takes it: its slot, or -1
+      auto take = [&]() {
+        const int st = cur.slot;
+        const bool r = mbar_wait(&full[st], cur.parity, abort_flag);
+        cur.advance(slots);
+        return r ? st : -1;
+      };
+      auto issue_s = [&](int tile, int q_tile, int st) {
         const uint32_t q = desc_lo(q_addr + q_tile * C::Q_TILE, 16);
-        const uint32_t k = desc_lo(ring_addr + (i % slots) * C::PLANE, 16);
+        const uint32_t k = desc_lo(ring_addr + st * C::PLANE, 16);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
           umma_ss(tmem + C::S_COL + tile * 128, desc_of(q + (j / 4) * (128 * 128 / 16) + (j % 4) * 2, desc_hi(1024)),
                   desc_of(k + (j / 4) * (1024 / 16) + (j % 4) * 2, desc_hi(GS)), idesc_s, j > 0 ? 1u : 0u);
         umma_commit(&s_full[tile]);
       };
-      auto issue_pv = [&](int tile, int i, bool accumulate) {
-        const uint32_t v = desc_lo(ring_addr + (i % slots) * C::PLANE, 1024);
+      auto issue_pv = [&](int tile, int st, bool accumulate) {
+        const uint32_t v = desc_lo(ring_addr + st * C::PLANE, 1024);
         const uint32_t o = tmem + C::O_COL + tile * 128, pa = tmem + C::S_COL + tile * 128;
 #pragma unroll
         for (int j = 0; j < kChunk / 16; ++j)
@@ -259,7 +279,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   j > 0 ? 1u : accumulate ? 1u : 0u);
       };
       auto wait_p = [&](int tile) {
-        const bool r = mbar_wait(&p_full[tile], np[tile]++ & 1, abort_flag);
+        const bool r = mbar_wait(&p_full[tile], np[tile], abort_flag);
+        np[tile] ^= 1;
         tc_fence_after();
         return r;
       };
@@ -271,58 +292,57 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         if (split) {
           for (int c = 0; ok && c < min(2, n); ++c) {
-            const int ik = at + place_k(true, c);
-            ok = wait_plane(ik);
-            if (ok) {
-              issue_s(c, 0, ik);
-              umma_commit(&empty[ik % slots]);
-            }
+            const int ik = take();
+            ok = ik >= 0;
+            if (!ok) break;
+            issue_s(c, 0, ik);
+            umma_commit(&empty[ik]);
           }
           for (int c = 0; ok && c < n; ++c) {
-            const int iv = at + place_v(true, c, n), t = c & 1;
-            ok = wait_plane(iv) && wait_p(t);
+            const int t = c & 1, iv = take();
+            ok = iv >= 0 && wait_p(t);
             if (!ok) break;
             issue_pv(t, iv, c >= 2);
-            umma_commit(&empty[iv % slots]);
+            umma_commit(&empty[iv]);
             if (c + 2 < n) {
-              const int ik = at + place_k(true, c + 2);
-              ok = wait_plane(ik);
-              if (ok) {
-                issue_s(t, 0, ik);
-                umma_commit(&empty[ik % slots]);
-              }
+              const int ik = take();
+              ok = ik >= 0;
+              if (!ok) break;
+              issue_s(t, 0, ik);
+              umma_commit(&empty[ik]);
             }
           }
         } else {
-          ok = wait_plane(at);
+          int ik = take();
+          ok = ik >= 0;
           if (ok) {
-            issue_s(0, 0, at);
-            issue_s(1, 1, at);
-            umma_commit(&empty[at % slots]);
+            issue_s(0, 0, ik);
+            issue_s(1, 1, ik);
+            umma_commit(&empty[ik]);
           }
           for (int c = 0; ok && c < n; ++c) {
-            const int iv = at + 2 * c + 1, ik = iv + 1;
             const bool more = c + 1 < n;
-            ok = wait_plane(iv) && wait_p(0);
+            const int iv = take();
+            ok = iv >= 0 && wait_p(0);
             if (!ok) break;
             issue_pv(0, iv, c > 0);
             if (more) {
-              ok = wait_plane(ik);
+              ik = take();
+              ok = ik >= 0;
               if (!ok) break;
               issue_s(0, 0, ik);
             }
             ok = wait_p(1);
             if (!ok) break;
             issue_pv(1, iv, c > 0);
-            umma_commit(&empty[iv % slots]);
+            umma_commit(&empty[iv]);
             if (more) {
               issue_s(1, 1, ik);
-              umma_commit(&empty[ik % slots]);
+              umma_commit(&empty[ik]);
             }
           }
         }
         if (ok) umma_commit(o_full);
-        at += 2 * n;
       }
       if (!ok) {
         *abort_flag = 1;
