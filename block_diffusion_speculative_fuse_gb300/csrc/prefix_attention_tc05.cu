@@ -45,7 +45,8 @@ struct TcCfg {
   static constexpr int PLANE = kChunk * D * 2;           // K or V of a chunk
   static constexpr int Q_TILE = 128 * D * 2;             // [HALVES][128 rows][128 B]
   static constexpr int MAX_SLOTS = D == 128 ? 5 : 10;
-  static constexpr uint32_t S_COL = 0, O_COL = 256;      // two tiles each: + 128 * tile
+  // two tiles each: + 128 * tile; P (64 columns) takes the upper half of S
+  static constexpr uint32_t S_COL = 0, P_COL = 64, O_COL = 256;
 };
 
 // One thread issues the products, and an M = N = 128, K = 16 step takes the
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + slots * C::PLANE);
   uint64_t* empty = full + C::MAX_SLOTS;
   uint64_t* s_full = empty + C::MAX_SLOTS;  // [2] S of a tile is complete (and the PV before it)
-  uint64_t* p_full = s_full + 2;            // [2] P of a tile is in TMEM
-  uint64_t* q_full = p_full + 2;            // Q of the segment is in shared memory
+  uint64_t* p_full = s_full + 2;            // [2][2] P of a tile is in TMEM: upper, lower 64 keys
+  uint64_t* q_full = p_full + 4;            // Q of the segment is in shared memory
   uint64_t* o_full = q_full + 1;            // all of the segment's products are complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
     }
     mbar_init(q_full, 8);
     mbar_init(o_full, 1);
@@ -270,19 +272,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   desc_of(k + (j / 4) * (1024 / 16) + (j % 4) * 2, desc_hi(GS)), idesc_s, j > 0 ? 1u : 0u);
         umma_commit(&s_full[tile]);
       };
+      // waits for the tile's P, half by half, and issues O += P V
       auto issue_pv = [&](int tile, int st, bool accumulate) {
         const uint32_t v = desc_lo(ring_addr + st * C::PLANE, 1024);
-        const uint32_t o = tmem + C::O_COL + tile * 128, pa = tmem + C::S_COL + tile * 128;
+        const uint32_t o = tmem + C::O_COL + tile * 128, pa = tmem + C::P_COL + tile * 128;
 #pragma unroll
-        for (int j = 0; j < kChunk / 16; ++j)
-          umma_ts(o, pa + j * 8, desc_of(v + j * (C::PAGE / 16), desc_hi(GS)), idesc_pv,
-                  j > 0 ? 1u : accumulate ? 1u : 0u);
-      };
-      auto wait_p = [&](int tile) {
-        const bool r = mbar_wait(&p_full[tile], np[tile], abort_flag);
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(&p_full[2 * tile + h], np[tile], abort_flag)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = (1 - h) * 4 + i;  // the upper keys first
+            umma_ts(o, pa + j * 8, desc_of(v + j * (C::PAGE / 16), desc_hi(GS)), idesc_pv,
+                    h + i > 0 ? 1u : accumulate ? 1u : 0u);
+          }
+        }
         np[tile] ^= 1;
-        tc_fence_after();
-        return r;
+        return true;
       };
       while (ok && seg.next(p, L, off)) {
         const int n = seg.chunk1 - seg.chunk0;
@@ -300,9 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           for (int c = 0; ok && c < n; ++c) {
             const int t = c & 1, iv = take();
-            ok = iv >= 0 && wait_p(t);
+            ok = iv >= 0 && issue_pv(t, iv, c >= 2);
             if (!ok) break;
-            issue_pv(t, iv, c >= 2);
             umma_commit(&empty[iv]);
             if (c + 2 < n) {
               const int ik = take();
@@ -323,18 +328,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; ok && c < n; ++c) {
             const bool more = c + 1 < n;
             const int iv = take();
-            ok = iv >= 0 && wait_p(0);
+            ok = iv >= 0 && issue_pv(0, iv, c > 0);
             if (!ok) break;
-            issue_pv(0, iv, c > 0);
             if (more) {
               ik = take();
               ok = ik >= 0;
               if (!ok) break;
               issue_s(0, 0, ik);
             }
-            ok = wait_p(1);
+            ok = issue_pv(1, iv, c > 0);
             if (!ok) break;
-            issue_pv(1, iv, c > 0);
             umma_commit(&empty[iv]);
             if (more) {
               issue_s(1, 1, ik);
@@ -416,33 +419,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the row's maximum; in a chunk that ends past this row's keys the
         // scores beyond them become -inf, here and in TMEM
         const bool masked = __any_sync(0xffffffffu, (c + 1) * kChunk > lim);
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t a[32], b[32];
-          tmem_ld32_nowait(s_addr + h * 64, a);
-          tmem_ld32_nowait(s_addr + h * 64 + 32, b);
-          tmem_wait_ld(a);
-          tmem_regs_ready(b);
-          if (masked) {
-            const int left = lim - c * kChunk - h * 64;
+        uint32_t x[4][32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (j >= left) a[j] = 0xFF800000u;
-              if (j + 32 >= left) b[j] = 0xFF800000u;
-            }
-            tmem_st32(s_addr + h * 64, a);
-            tmem_st32(s_addr + h * 64 + 32, b);
-          }
-          float m0 = mx, m1 = mx;
+        for (int j = 0; j < 4; ++j) tmem_ld32_nowait(s_addr + j * 32, x[j]);
+        tmem_wait_ld(x[0]);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            m0 = fmaxf(m0, fmaxf(__uint_as_float(a[j]), __uint_as_float(a[j + 1])));
-            m1 = fmaxf(m1, fmaxf(__uint_as_float(b[j]), __uint_as_float(b[j + 1])));
-          }
-          mx = fmaxf(m0, m1);
+        for (int j = 1; j < 4; ++j) tmem_regs_ready(x[j]);
+        if (masked) {
+          const int left = lim - c * kChunk;
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j >= left) x[j / 32][j % 32] = 0xFF800000u;
+          tmem_st32(s_addr, x[0]);
+          tmem_st32(s_addr + 32, x[1]);
+          tmem_wait_st();
         }
-        if (masked) tmem_wait_st();
+        float mx4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mx4[j] = fmaxf(__uint_as_float(x[j][0]), __uint_as_float(x[j][1]));
+#pragma unroll
+          for (int i = 2; i < 32; i += 2)
+            mx4[j] = fmaxf(mx4[j], fmaxf(__uint_as_float(x[j][i]), __uint_as_float(x[j][i + 1])));
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const float mc = mx * p.scale_log2;
         const bool raise = mc > m + kRaise;
         const bool rescale = raise && m != -INFINITY;
@@ -462,37 +462,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l *= alpha;
         }
         if (raise) m = mc;
-        // P = exp2(scale S - m) in bf16 over S, 32 columns at a time, the next
-        // 32 on their way
-        const float neg = m == -INFINITY ? 0.f : -m;
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(neg, neg);
-        float2 la = make_float2(0.f, 0.f), lb = la;
-        auto form = [&](const uint32_t (&x)[32], uint32_t* pk) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float2 t = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc2, neg2);
-            t.x = ex2(t.x);
-            t.y = ex2(t.y);
-            if (j & 1) lb = add2(lb, t);
-            else la = add2(la, t);
-            pk[j] = bf16x2(t.x, t.y);
-          }
-        };
-        uint32_t x0[32], x1[32];
-        tmem_ld32_nowait(s_addr, x0);
-        tmem_wait_ld(x0);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-          tmem_ld32_nowait(s_addr + h * 64 + 32, x1);
-          form(x0, pk);
-          tmem_wait_ld(x1);
-          if (h == 0) tmem_ld32_nowait(s_addr + 64, x0);
-          form(x1, pk + 16);
-          if (h == 0) tmem_wait_ld(x0);
-          tmem_st32(s_addr + h * 32, pk);
-        }
-        l += (la.x + la.y) + (lb.x + lb.y);
         if ((c + 1) * kChunk > stale) {
           // the page the context ends in holds whatever was there past it: 0 * V must be 0
           const int iv = at + place_v(split, c, n);
@@ -510,10 +479,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tile]);
+        // P = exp2(scale S - m) in bf16.  The upper 64 keys first, still in
+        // registers: the product with V starts on them while the lower 64,
+        // read again from TMEM, are formed.
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(neg, neg);
+        float2 la = make_float2(0.f, 0.f), lb = la;
+        auto form = [&](const uint32_t (&y)[32], uint32_t* pk) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 t = fma2(make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), sc2, neg2);
+            t.x = ex2(t.x);
+            t.y = ex2(t.y);
+            if (j & 1) lb = add2(lb, t);
+            else la = add2(la, t);
+            pk[j] = bf16x2(t.x, t.y);
+          }
+        };
+        const uint32_t p_addr = lane_base + C::P_COL + tile * 128;
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          uint32_t pk[32];
+          if (h == 0) {
+            tmem_wait_ld(x[0]);
+            tmem_regs_ready(x[1]);
+          }
+          form(x[2 * h], pk);
+          form(x[2 * h + 1], pk + 16);
+          tmem_st32(p_addr + h * 32, pk);
+          if (h == 1) {
+            tmem_ld32_nowait(s_addr, x[0]);
+            tmem_ld32_nowait(s_addr + 32, x[1]);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * tile + 1 - h]);
+        }
+        l += (la.x + la.y) + (lb.x + lb.y);
       }
       if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) ok = false;
       ++segs;
@@ -618,7 +621,7 @@ cudaError_t launch(const CUtensorMap& map, int group0, int oob_group, const Pref
   constexpr int kMax = 227 * 1024;
   const int ne = p.ng + p.batch;
   // barriers and flags, the lists, slack for the alignment
-  const int fixed = (2 * C::MAX_SLOTS + 6) * 8 + 8 + (ne + 1 + 2 * p.ng + 33) * 4 + 1024;
+  const int fixed = (2 * C::MAX_SLOTS + 8) * 8 + 8 + (ne + 1 + 2 * p.ng + 33) * 4 + 1024;
   int slots = (kMax - fixed - 2 * C::Q_TILE) / C::PLANE;
   if (slots > C::MAX_SLOTS) slots = C::MAX_SLOTS;
   const int smem = fixed + 2 * C::Q_TILE + slots * C::PLANE;
