@@ -330,29 +330,45 @@ def dflash_ctx_fuse_noalloc(h, taps, T, ctx, stream=None):
 
 
 # ------------------------------------------------------- serving operators
-def _tensor(fn, t, dtype, shape, strides=None, optional=False):
-    """Checks a tensor argument against what the library will read or write:
-    on the current CUDA device, dtype, shape, and dense (or the strides given,
-    None standing for any)."""
-    if t is None:
-        if optional:
-            return
-        raise DflashError(fn, -1)
-    if not t.is_cuda or t.device.index != torch.cuda.current_device() or t.dtype != dtype or \
-            tuple(t.shape) != shape:
-        raise DflashError(fn, -1)
-    if strides is None:
-        if not t.is_contiguous():
-            raise DflashError(fn, -1)
-    elif any(w is not None and n > 1 and s != w for s, w, n in zip(t.stride(), strides, shape)):
-        raise DflashError(fn, -1)
+# A call of these is a few microseconds of device work at decode sizes, so
+# their checks are few and plain: each tensor's device, dtype and shape, and
+# that it is dense (or strided where the library takes a stride).
+_BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
 
 
-def _workspace_arg(fn, ws):
-    if ws is None or not ws.is_cuda or ws.device.index != torch.cuda.current_device() or \
-            not ws.is_contiguous():
+def _dense(fn, dev, t, dtype, shape):
+    """Address of a dense tensor of this device, dtype and shape."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
+            not t.is_contiguous():
         raise DflashError(fn, -1)
-    return ptr(ws), ws.numel() * ws.element_size()
+    return t.data_ptr()
+
+
+def _rows(fn, dev, t, dtype, T, h, d):
+    """Address and row stride of a [T][h][d] tensor whose rows are dense."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != (T, h, d):
+        raise DflashError(fn, -1)
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and h > 1):
+        raise DflashError(fn, -1)
+    return t.data_ptr(), s0 if T > 1 else h * d
+
+
+def _space(fn, dev, ws):
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous():
+        raise DflashError(fn, -1)
+    return ws.data_ptr(), ws.nbytes
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _device(fn, t):
+    """The current CUDA device, which a call's first tensor must be on."""
+    if t is None or not t.is_cuda:
+        raise DflashError(fn, -1)
+    return torch.cuda.current_device()
 
 
 def dflash_rope_init(rot_dim, interleaved=False, base=1e6, scaling="none", factor=1.0,
@@ -373,26 +389,23 @@ def dflash_kv_rope_append(heads: DflashHeads, rope: DflashRope, layer, q, k, v, 
     """q [T][hq][d], k, v [T][hkv][d] (bf16 or fp32; rows may be strided, a
     row's heads are dense); q and q_out may both be None."""
     fn = "dflash_kv_rope_append"
+    dev = _device(fn, k)
     hq, hkv, d = heads.n_q_heads, heads.n_kv_heads, heads.head_dim
-    if k is None or k.dtype not in (torch.bfloat16, torch.float32):
+    dt = k.dtype
+    if dt is not _BF16 and dt is not _F32:
         raise DflashError(fn, -1)
-    _tensor(fn, k, k.dtype, (T, hkv, d), (None, d, 1))
-    _tensor(fn, v, k.dtype, (T, hkv, d), (None, d, 1))
-    _tensor(fn, q, k.dtype, (T, hq, d), (None, d, 1), optional=True)
-    _tensor(fn, q_out, torch.bfloat16, (T, hq, d), (None, d, 1), optional=True)
-    _tensor(fn, q_norm, torch.bfloat16, (d,), optional=True)
-    _tensor(fn, k_norm, torch.bfloat16, (d,), optional=True)
-    _tensor(fn, row_req, torch.int32, (T,))
-    _tensor(fn, row_pos, torch.int32, (T,))
-    w, wn = _workspace_arg(fn, ws)
-
-    def ld(t, dense):
-        return 0 if t is None else t.stride(0) if t.shape[0] > 1 else dense
+    kp, ldk = _rows(fn, dev, k, dt, T, hkv, d)
+    vp, ldv = _rows(fn, dev, v, dt, T, hkv, d)
+    qp, ldq = _rows(fn, dev, q, dt, T, hq, d) if q is not None else (None, 0)
+    op, ldo = _rows(fn, dev, q_out, _BF16, T, hq, d) if q_out is not None else (None, 0)
+    qn = _dense(fn, dev, q_norm, _BF16, (d,)) if q_norm is not None else None
+    kn = _dense(fn, dev, k_norm, _BF16, (d,)) if k_norm is not None else None
+    w, wn = _space(fn, dev, ws)
     return _check(fn, load().dflash_kv_rope_append(
-        ctypes.byref(heads), ctypes.byref(rope), layer, ptr(q), ld(q, hq * d), ptr(k),
-        ld(k, hkv * d), ptr(v), ld(v, hkv * d), 0 if k.dtype == torch.bfloat16 else 1,
-        ptr(q_norm), ptr(k_norm), float(eps), ptr(row_req), ptr(row_pos), T, ptr(q_out),
-        ld(q_out, hq * d), ctypes.byref(kv), w, wn, stream_handle(stream)))
+        ctypes.byref(heads), ctypes.byref(rope), layer, qp, ldq, kp, ldk, vp, ldv,
+        0 if dt is _BF16 else 1, qn, kn, eps, _dense(fn, dev, row_req, _I32, (T,)),
+        _dense(fn, dev, row_pos, _I32, (T,)), T, op, ldo, ctypes.byref(kv), w, wn,
+        _stream(stream)))
 
 
 def dflash_attention_prefix_bytes(heads: DflashHeads, batch, n, group) -> int:
@@ -404,20 +417,20 @@ def dflash_attention_prefix_bytes(heads: DflashHeads, batch, n, group) -> int:
 
 def dflash_attention_prefix(heads: DflashHeads, layer, q, batch, n, group, causal, scale,
                             kv: DflashKV, ctx_len, prefix_len, out, lse, ws, stream=None):
+    """q, out bf16 [batch][n][hq][d]; lse fp32 [batch][n][hq] or None."""
     fn = "dflash_attention_prefix"
+    dev = _device(fn, q)
     if batch < 1 or group < 1 or batch % group:
         raise DflashError(fn, -1)
-    shape = (batch, n, heads.n_q_heads, heads.head_dim)
-    _tensor(fn, q, torch.bfloat16, shape)
-    _tensor(fn, out, torch.bfloat16, shape)
-    _tensor(fn, lse, torch.float32, shape[:3], optional=True)
-    _tensor(fn, ctx_len, torch.int32, (batch,))
-    _tensor(fn, prefix_len, torch.int32, (batch // group,))
-    w, wn = _workspace_arg(fn, ws)
+    hq = heads.n_q_heads
+    shape = (batch, n, hq, heads.head_dim)
+    w, wn = _space(fn, dev, ws)
     return _check(fn, load().dflash_attention_prefix(
-        ctypes.byref(heads), layer, ptr(q), batch, n, group, 1 if causal else 0, float(scale),
-        ctypes.byref(kv), ptr(ctx_len), ptr(prefix_len), ptr(out), ptr(lse), w, wn,
-        stream_handle(stream)))
+        ctypes.byref(heads), layer, _dense(fn, dev, q, _BF16, shape), batch, n, group,
+        1 if causal else 0, scale, ctypes.byref(kv), _dense(fn, dev, ctx_len, _I32, (batch,)),
+        _dense(fn, dev, prefix_len, _I32, (batch // group,)), _dense(fn, dev, out, _BF16, shape),
+        _dense(fn, dev, lse, _F32, (batch, n, hq)) if lse is not None else None, w, wn,
+        _stream(stream)))
 
 
 def dflash_sample_filtered_bytes(rows, vocab) -> int:
@@ -432,14 +445,21 @@ def dflash_sample_filtered(logits, rows, vocab, temperature, top_k, top_p, min_p
     """logits fp32 [rows][vocab] (rows may be strided); top_k, top_p, min_p,
     n_kept and logprob may be None."""
     fn = "dflash_sample_filtered"
-    _tensor(fn, logits, torch.float32, (rows, vocab), (None, 1))
-    for t, dt, opt in ((temperature, torch.float32, False), (top_k, torch.int32, True),
-                       (top_p, torch.float32, True), (min_p, torch.float32, True),
-                       (a, torch.float64, False), (token, torch.int32, False),
-                       (n_kept, torch.int32, True), (logprob, torch.float32, True)):
-        _tensor(fn, t, dt, (rows,), optional=opt)
-    w, wn = _workspace_arg(fn, ws)
+    dev = _device(fn, logits)
+    if logits.dtype is not _F32 or logits.get_device() != dev or logits.shape != (rows, vocab):
+        raise DflashError(fn, -1)
+    ld, s1 = logits.stride()
+    if s1 != 1 and vocab > 1:
+        raise DflashError(fn, -1)
+    one = (rows,)
+    w, wn = _space(fn, dev, ws)
     return _check(fn, load().dflash_sample_filtered(
-        ptr(logits), logits.stride(0) if rows > 1 else vocab, rows, vocab, ptr(temperature),
-        ptr(top_k), ptr(top_p), ptr(min_p), ptr(a), ptr(token), ptr(n_kept), ptr(logprob), w, wn,
-        stream_handle(stream)))
+        logits.data_ptr(), ld if rows > 1 else vocab, rows, vocab,
+        _dense(fn, dev, temperature, _F32, one),
+        _dense(fn, dev, top_k, _I32, one) if top_k is not None else None,
+        _dense(fn, dev, top_p, _F32, one) if top_p is not None else None,
+        _dense(fn, dev, min_p, _F32, one) if min_p is not None else None,
+        _dense(fn, dev, a, _F64, one), _dense(fn, dev, token, _I32, one),
+        _dense(fn, dev, n_kept, _I32, one) if n_kept is not None else None,
+        _dense(fn, dev, logprob, _F32, one) if logprob is not None else None, w, wn,
+        _stream(stream)))

@@ -286,6 +286,17 @@ cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensor
 // 128-byte swizzled, zero fill out of bounds.  A DFLASH_* code.
 int encode_kv_pages(CUtensorMap* map, const void* base, uint64_t groups, uint32_t d);
 
+// Allows `bytes` of dynamic shared memory for a kernel, once per device and
+// host thread (`done`: a thread_local of the caller, -1 at first).
+inline cudaError_t allow_smem(const void* fn, int bytes, int* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || *done == dev) return e;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) *done = dev;
+  return e;
+}
+
 // Records the error for dflash_last_cuda_error and returns DFLASH_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
 

@@ -390,8 +390,8 @@ cudaError_t run_small(const PrefixParams& p, void** args, cudaStream_t s) {
   const int ne = p.ng + p.batch;
   const size_t smem = kSmallWarps * SmallCfg<D>::RING + (ne + 1 + 2 * p.ng + 33) * sizeof(int);
   const void* fn = reinterpret_cast<const void*>(prefix_small_kernel<D>);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4);
+  static thread_local int allowed = -1;
+  const cudaError_t e = allow_smem(fn, kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4, &allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(fn, kSmallCtas, kSmallWarps * 32, smem, args, s);
 }

@@ -625,7 +625,8 @@ cudaError_t launch(const CUtensorMap& map, int group0, int oob_group, const Pref
   int slots = (kMax - fixed - 2 * C::Q_TILE) / C::PLANE;
   if (slots > C::MAX_SLOTS) slots = C::MAX_SLOTS;
   const int smem = fixed + 2 * C::Q_TILE + slots * C::PLANE;
-  cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+  static thread_local int allowed = -1;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(prefix_tc_kernel<D>), kMax, &allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -630,13 +630,18 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
 }  // namespace
 
 cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s) {
+  // CTAs per row: a slice of at most kSlice logits, so that two CTAs fit an SM;
+  // more (down to kMinSlice logits) while the rows leave SMs without work
+  constexpr int kSlice = 24576, kMinSlice = 4096, kResident = 2 * 152;
   int nc = 1;
-  while (nc < kMaxCluster && (p.vocab + nc - 1) / nc > kMaxSlice) nc *= 2;
+  while (nc < kMaxCluster && ((p.vocab + nc - 1) / nc > kSlice ||
+                              (2 * nc * p.rows <= kResident && p.vocab / (2 * nc) >= kMinSlice)))
+    nc *= 2;
   const int slice = ((p.vocab + nc - 1) / nc + 3) / 4 * 4;
   const int cs = (slice + kWarps * 128 - 1) / (kWarps * 128) * 128;
   const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(kWarps) * cs * 4;
-  cudaError_t e = cudaFuncSetAttribute(sample_filtered_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static thread_local int allowed = -1;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sample_filtered_kernel), 227 * 1024, &allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
