@@ -21,11 +21,18 @@
 // Selection without a sort.  A histogram of counts over 1023 equal steps of t
 // in [0, 46) (one shared-memory atomic per logit) bounds the mass of every
 // prefix within 3 %, which leaves a few bins that can hold the border of top-p
-// (one bin for top-k).  Only their tokens are then split by their exact
-// 32-bit key, ten bits a pass, with the exact masses; a border that falls on
-// equal logits is settled by counting them in index order.
+// (one bin for top-k).  Their tokens, the candidates, go to a list if they are
+// few, where each counts what precedes it; otherwise they are first split by
+// their exact 32-bit key, ten bits a pass, with the exact masses.  A border that
+// falls on many equal logits is settled by counting them in index order.
+//
+// Bound: for a batch of rows instruction issue (about 45 instructions per
+// weight, evaluated once per token of K), for a few rows the latency of about
+// ten passes, each ending in a cluster barrier.
 #include <cfloat>
 #include <climits>
+#include <cmath>
+#include <cstring>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -36,26 +43,38 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;           // two CTAs per SM
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;          // one per thread; the last is the tail (t >= 46)
+constexpr int kBins = 1024;          // two per thread; the last is the tail (t >= 46)
+constexpr int kList = 256;           // candidates settled in a list
 constexpr float kMaxLog2 = 46.f;     // weights below 2^-46 count as 0
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSlice = 49152;     // logits per CTA (192 KB)
+static_assert(kMaxSampleVocab / kMaxCluster * 4 + 16384 <= 227 * 1024, "a slice fits shared memory");
 
 struct Shared {
   float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(45-j/64) in two words
-  u64 mass[kBins];
+  u64 mass[kBins];                   // also the candidates' list: kList orders, kList weights
   unsigned hist[kBins];
-  u64 xch[2][kMaxCluster][4];        // exchanged values, one row per rank of the cluster
-  u64 wred[kWarps][4];
-  u64 blk[4];
+  u64 xch[2][kMaxCluster][2];        // exchanged values, one row per rank of the cluster
+  unsigned xch32[2][kMaxCluster][2];
+  u64 wred[kWarps][2];
+  u64 wscan[kWarps];
+  unsigned wred32[kWarps][2];
   float f0[kWarps], f1[kWarps];
   float ch, cl, scale;               // log2(e)/T as a float pair; bins per unit of z
   unsigned key_m;                    // smallest key that min_p keeps
   int b_lo, b_hi;
   int found;
+  unsigned found_n;
   u64 before;
+  unsigned list_n;                   // rank 0: candidates listed
+  unsigned border_key;               // the list's answer
+  int border_index;
+};
+
+// 2^(-j/64) for the kernel, made on the host
+struct WeightTable {
+  float4 e[64];
 };
 
 struct Weights {
@@ -133,16 +152,30 @@ __device__ __forceinline__ unsigned ld_cluster_u32(const void* smem, uint32_t ra
   return v;
 }
 
-enum Op { kSum, kMax, kMin };
-template <Op op>
-__device__ __forceinline__ u64 combine(u64 a, u64 b) {
-  return op == kSum ? a + b : op == kMax ? (a > b ? a : b) : (a < b ? a : b);
+__device__ __forceinline__ void st_cluster_u32(const void* smem, uint32_t rank, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_map(smem_u32(smem), rank)), "r"(v) : "memory");
 }
+__device__ __forceinline__ unsigned add_cluster_u32(const void* smem, uint32_t rank, unsigned v) {
+  unsigned r;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(dsmem_map(smem_u32(smem), rank)), "r"(v) : "memory");
+  return r;
+}
+
+// (key, index) as one number that orders tokens: larger key first, then lower
+// index.
+__device__ __forceinline__ u64 order_of(unsigned key, int i) {
+  return (static_cast<u64>(~key) << 32) | static_cast<unsigned>(i);
+}
+
+struct Border {
+  unsigned key;
+  int index;  // tokens with this key are in up to this index
+};
 
 // The row's work, shared by all threads of the cluster.
 struct Row {
   Shared* sh;
-  const float* vals;   // this CTA's slice, padded with -inf to 32 * cs
+  const float* vals;   // this CTA's slice, padded with -inf to kWarps * cs
   int cs;              // logits per warp (a multiple of 128)
   int base;            // index of the slice's first logit
   int nc, rank;        // CTAs of the cluster, this one's rank
@@ -154,46 +187,62 @@ struct Row {
     else __syncthreads();
   }
 
-  // Reduces one value per thread over the cluster.  The CTAs' own values stay
-  // in sh->xch[buffer][rank][slot]; the buffer alternates, and the barrier of
-  // the exchange in between separates its uses.
-  template <Op op0, Op op1>
-  __device__ void reduce2(u64& v0, u64& v1) {
+  // Sums of two values and the least and largest of two keys, over the
+  // cluster.  The CTAs' own sums stay in sh->xch[buffer][rank], the warps' in
+  // sh->wred; the buffer alternates, and the barrier of the reduction in
+  // between separates its uses.
+  __device__ void reduce(u64& s0, u64& s1, unsigned& lo, unsigned& hi) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      v0 = combine<op0>(v0, shfl_xor64(v0, o));
-      v1 = combine<op1>(v1, shfl_xor64(v1, o));
+      s0 += shfl_xor64(s0, o);
+      s1 += shfl_xor64(s1, o);
     }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
-      sh->wred[warp][0] = v0;
-      sh->wred[warp][1] = v1;
+      sh->wred[warp][0] = s0;
+      sh->wred[warp][1] = s1;
+      sh->wred32[warp][0] = lo;
+      sh->wred32[warp][1] = hi;
     }
     __syncthreads();
     if (warp == 0) {
-      v0 = sh->wred[lane][0];
-      v1 = sh->wred[lane][1];
+      const bool in = lane < kWarps;
+      s0 = in ? sh->wred[lane][0] : 0;
+      s1 = in ? sh->wred[lane][1] : 0;
+      lo = in ? sh->wred32[lane][0] : ~0u;
+      hi = in ? sh->wred32[lane][1] : 0u;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
-        v0 = combine<op0>(v0, shfl_xor64(v0, o));
-        v1 = combine<op1>(v1, shfl_xor64(v1, o));
+        s0 += shfl_xor64(s0, o);
+        s1 += shfl_xor64(s1, o);
       }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
       if (lane < nc) {
         if (nc > 1) {
-          st_cluster_u64(&sh->xch[par][rank][0], lane, v0);
-          st_cluster_u64(&sh->xch[par][rank][1], lane, v1);
+          st_cluster_u64(&sh->xch[par][rank][0], lane, s0);
+          st_cluster_u64(&sh->xch[par][rank][1], lane, s1);
+          st_cluster_u32(&sh->xch32[par][rank][0], lane, lo);
+          st_cluster_u32(&sh->xch32[par][rank][1], lane, hi);
         } else {
-          sh->xch[par][0][0] = v0;
-          sh->xch[par][0][1] = v1;
+          sh->xch[par][0][0] = s0;
+          sh->xch[par][0][1] = s1;
+          sh->xch32[par][0][0] = lo;
+          sh->xch32[par][0][1] = hi;
         }
       }
     }
     barrier();
-    v0 = sh->xch[par][0][0];
-    v1 = sh->xch[par][0][1];
-    for (int r = 1; r < nc; ++r) {
-      v0 = combine<op0>(v0, sh->xch[par][r][0]);
-      v1 = combine<op1>(v1, sh->xch[par][r][1]);
+    s0 = s1 = 0;
+    lo = ~0u;
+    hi = 0;
+    for (int r = 0; r < nc; ++r) {
+      s0 += sh->xch[par][r][0];
+      s1 += sh->xch[par][r][1];
+      lo = min(lo, sh->xch32[par][r][0]);
+      hi = max(hi, sh->xch32[par][r][1]);
     }
     par ^= 1;
   }
@@ -219,21 +268,13 @@ struct Row {
       const u64 x = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += x;
     }
-    if (lane == 31) sh->wred[warp][2] = v;
+    if (lane == 31) sh->wscan[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-      u64 x = sh->wred[lane][2];
+    u64 x = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      sh->wred[lane][2] = x;
-    }
+    for (int i = 0; i < kWarps; ++i) x += i < warp ? sh->wscan[i] : 0;
     __syncthreads();
-    if (warp > 0) v += sh->wred[warp - 1][2];
-    __syncthreads();
-    return v;
+    return v + x;
   }
   __device__ void scan2f(float& a, float& b) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -253,7 +294,7 @@ struct Row {
 
   // Where, in index order, the running sum of value(z, index) reaches `need`
   // (1 <= need <= the total).  The caller has just reduced the threads' sums as
-  // reduce2's first value through buffer `buf`; returns true on one thread of
+  // reduce()'s first value through buffer `buf`; returns true on one thread of
   // the cluster, with the index and its logit.
   template <typename F>
   __device__ bool locate(int buf, u64 need, F value, int* index, float* logit) {
@@ -303,83 +344,177 @@ struct Row {
     return false;
   }
 
-  // Border search by key.  The candidates are the logits with keys in [lo,
-  // hi] that in(z, index) admits; `base_sum` is what lies above them.  Finds
-  // the key at which the running sum (of counts, or of masses) in descending
-  // key order reaches `need`; *sum_above = the sum strictly above that key.
-  template <bool MASS, typename In>
-  __device__ unsigned border_key(unsigned lo, unsigned hi, u64 need, u64 base_sum, In in,
-                                 u64* sum_above) {
-    while (lo < hi) {
-      const int shift = max(0, 32 - __clz(hi - lo) - 10);
-      sh->mass[threadIdx.x] = 0;
-      sh->hist[threadIdx.x] = 0;
-      if (threadIdx.x == 0) sh->found = -1;
-      __syncthreads();
-      each([&](float z, int i) {
-        const unsigned k = key_of(z);
-        if (k < lo || k > hi || !in(z, i)) return;
-        const unsigned b = (hi - k) >> shift;
-        if (MASS) atomicAdd(&sh->mass[b], weight_of(w, z));
-        else atomicAdd(&sh->hist[b], 1u);
-      });
-      barrier();
-      u64 v = 0;
-      for (int r = 0; r < nc; ++r) {
-        if (MASS) v += nc > 1 ? ld_cluster_u64(&sh->mass[threadIdx.x], r) : sh->mass[threadIdx.x];
-        else v += nc > 1 ? ld_cluster_u32(&sh->hist[threadIdx.x], r) : sh->hist[threadIdx.x];
-      }
-      const u64 inc = base_sum + scan(v);
-      if (v > 0 && need <= inc && inc - v < need) {
-        sh->found = threadIdx.x;
-        sh->before = inc - v;
-      }
-      barrier();  // also: the bins may be cleared again
-      const int b = sh->found;
-      const u64 before = sh->before;
-      __syncthreads();
-      if (b < 0) break;  // the sums end below `need`: all candidates
-      base_sum = before;
-      hi -= static_cast<unsigned>(b) << shift;
-      const unsigned span = (1u << shift) - 1;
-      lo = hi - lo > span ? hi - span : lo;
-    }
-    *sum_above = base_sum;
-    return lo;
-  }
-
   // Of the admitted logits with this key, the index of the c-th in index
   // order (INT_MAX if there are no more than c).
   template <typename In>
   __device__ int border_index(unsigned key, u64 c, In in) {
     const float z = of_key(key);
     auto tie = [&](float x, int i) -> u64 { return x == z && in(x, i) ? 1 : 0; };
-    u64 mine = 0, none = 0;
-    each([&](float x, int i) { mine += tie(x, i); });
+    u64 all = 0, none = 0;
+    unsigned lo = 0, hi = 0;
+    each([&](float x, int i) { all += tie(x, i); });
     const int buf = par;
-    u64 all = mine;
-    reduce2<kSum, kSum>(all, none);
+    reduce(all, none, lo, hi);
     if (c >= all) {
       __syncthreads();
       return INT_MAX;
     }
     int idx;
     float dummy;
-    u64 cut = ~0ull, zero = 0;
-    if (locate(buf, c, tie, &idx, &dummy)) cut = static_cast<u64>(idx);
+    unsigned cut = 0x7FFFFFFFu;
+    if (locate(buf, c, tie, &idx, &dummy)) cut = static_cast<unsigned>(idx);
     __syncthreads();
-    reduce2<kMin, kSum>(cut, zero);
+    u64 z0 = 0, z1 = 0;
+    unsigned top = 0;
+    reduce(z0, z1, cut, top);
     return static_cast<int>(cut);
+  }
+
+  // The border of a prefix in (key descending, index ascending) order: the
+  // token at which the running sum (of counts, or of masses) reaches `need`,
+  // among the n candidates, the logits whose t lies in bins [b_lo, b_hi] and
+  // that in(z, index) admits; `above` is the sum before them.  [lo, hi] bounds
+  // their keys where have_keys says so.
+  template <bool MASS, typename In>
+  __device__ Border border(int b_lo, int b_hi, unsigned n, bool have_keys, unsigned lo, unsigned hi, u64 need,
+                           u64 above, In in) {
+    const int tid = threadIdx.x;
+    if (n > kList && !have_keys) {
+      lo = ~0u;
+      hi = 0;
+      each([&](float z, int i) {
+        const int b = bin_of(w, z);
+        if (b < b_lo || b > b_hi || !in(z, i)) return;
+        const unsigned key = key_of(z);
+        lo = min(lo, key);
+        hi = max(hi, key);
+      });
+      u64 z0 = 0, z1 = 0;
+      reduce(z0, z1, lo, hi);
+      have_keys = true;
+    }
+    while (n > kList && lo < hi) {
+      const int shift = max(0, 32 - __clz(hi - lo) - 10);
+      for (int j = tid; j < kBins; j += kThreads) {
+        sh->mass[j] = 0;
+        sh->hist[j] = 0;
+      }
+      if (tid == 0) sh->found = -1;
+      __syncthreads();
+      each([&](float z, int i) {
+        const unsigned k = key_of(z);
+        if (k < lo || k > hi || !in(z, i)) return;
+        const unsigned b = (hi - k) >> shift;
+        if (MASS) atomicAdd(&sh->mass[b], weight_of(w, z));
+        atomicAdd(&sh->hist[b], 1u);
+      });
+      barrier();
+      u64 v[2] = {0, 0};
+      unsigned cn[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        for (int r = 0; r < nc; ++r) {
+          cn[j] += nc > 1 ? ld_cluster_u32(&sh->hist[2 * tid + j], r) : sh->hist[2 * tid + j];
+          if (MASS) v[j] += nc > 1 ? ld_cluster_u64(&sh->mass[2 * tid + j], r) : sh->mass[2 * tid + j];
+        }
+      if (!MASS) v[0] = cn[0], v[1] = cn[1];
+      const u64 inc1 = above + scan(v[0] + v[1]), inc0 = inc1 - v[1];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u64 inc = j ? inc1 : inc0;
+        if (v[j] > 0 && need <= inc && inc - v[j] < need) {
+          sh->found = 2 * tid + j;
+          sh->found_n = cn[j];
+          sh->before = inc - v[j];
+        }
+      }
+      barrier();  // also: the bins may be cleared again
+      const int b = sh->found;
+      const u64 before = sh->before;
+      const unsigned bn = sh->found_n;
+      __syncthreads();
+      if (b < 0) return Border{lo, INT_MAX};  // the sums end below `need`: all candidates
+      above = before;
+      n = bn;
+      hi -= static_cast<unsigned>(b) << shift;
+      const unsigned span = (1u << shift) - 1;
+      lo = hi - lo > span ? hi - span : lo;
+    }
+    if (n > kList) {  // one key
+      const u64 wk = MASS ? max(weight_of(w, of_key(lo)), 1ull) : 1;
+      return Border{lo, border_index(lo, need > above ? (need - above + wk - 1) / wk : 1, in)};
+    }
+    // ---- the list, in rank 0's shared memory
+    u64* orders = sh->mass;
+    u64* weights = sh->mass + kList;
+    each([&](float z, int i) {
+      const unsigned key = key_of(z);
+      if (have_keys) {
+        if (key < lo || key > hi) return;
+      } else {
+        const int b = bin_of(w, z);
+        if (b < b_lo || b > b_hi) return;
+      }
+      if (!in(z, i)) return;
+      const u64 x = MASS ? weight_of(w, z) : 1;
+      if (nc > 1) {
+        const unsigned at = add_cluster_u32(&sh->list_n, 0, 1);
+        if (at < kList) {
+          st_cluster_u64(&orders[at], 0, order_of(key, i));
+          st_cluster_u64(&weights[at], 0, x);
+        }
+      } else {
+        const unsigned at = atomicAdd(&sh->list_n, 1u);
+        if (at < kList) {
+          orders[at] = order_of(key, i);
+          weights[at] = x;
+        }
+      }
+    });
+    barrier();
+    if (rank == 0) {
+      // two threads per candidate, each summing half of what precedes it
+      static_assert(kThreads == 2 * kList, "two threads per candidate");
+      const unsigned cnt = min(sh->list_n, static_cast<unsigned>(kList));
+      const int c = tid / 2;
+      const bool on = c < static_cast<int>(cnt);
+      const u64 mine = on ? orders[c] : 0, wm = on ? weights[c] : 0;
+      u64 before = 0, all = 0;
+      for (unsigned j = tid % 2; j < cnt; j += 2) {
+        const u64 x = weights[j];
+        all += x;
+        before += orders[j] < mine ? x : 0;
+      }
+      before += shfl_xor64(before, 1);
+      all += shfl_xor64(all, 1);
+      // the first to reach `need`, or the last of all
+      if (on && tid % 2 == 0 && above + before < need && (above + before + wm >= need || before + wm == all)) {
+        const unsigned bk = ~static_cast<unsigned>(mine >> 32), bi = static_cast<unsigned>(mine);
+        for (int r = 0; r < nc; ++r) {
+          if (nc > 1) {
+            st_cluster_u32(&sh->border_key, r, bk);
+            st_cluster_u32(&sh->border_index, r, bi);
+          } else {
+            sh->border_key = bk;
+            sh->border_index = static_cast<int>(bi);
+          }
+        }
+      }
+      __syncthreads();
+      if (tid == 0) sh->list_n = 0;  // for the next border
+    }
+    barrier();
+    return Border{sh->border_key, sh->border_index};
   }
 };
 
-__global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleFilteredParams p,
-                                                                   int nc, int slice, int cs) {
+__global__ void __launch_bounds__(kThreads, 2)
+    sample_filtered_kernel(const __grid_constant__ SampleFilteredParams p,
+                           const __grid_constant__ WeightTable table, int nc, int slice, int cs) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared* sh = reinterpret_cast<Shared*>(smem);
   float* vals = reinterpret_cast<float*>(smem + (sizeof(Shared) + 15) / 16 * 16);
   griddep_launch_dependents();
-  griddep_wait();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int row = blockIdx.x / nc, rank = blockIdx.x % nc;
   const int V = p.vocab;
@@ -392,16 +527,17 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
   R.nc = nc;
   R.rank = rank;
   R.par = 0;
+  if (tid < 64) sh->tab[tid] = table.e[tid];
+  if (tid == 0) sh->list_n = 0;
+  griddep_wait();
 
-  if (tid < 64) {
-    // 2^(-j/64) in 64 bits (64 threads, once)
-    const double t = exp2(-tid / 64.0);
-    const float hi = static_cast<float>(t);
-    const u64 fix = static_cast<u64>(t * 0x1p45 + 0.5);
-    sh->tab[tid] = make_float4(hi, static_cast<float>(t - static_cast<double>(hi)),
-                               __uint_as_float(static_cast<unsigned>(fix)),
-                               __uint_as_float(static_cast<unsigned>(fix >> 32)));
-  }
+  // ---- settings (used after the first reduction)
+  const float T = p.temperature[row];
+  const int k = p.top_k != nullptr ? p.top_k[row] : 0;
+  const float tp = p.top_p != nullptr ? p.top_p[row] : 1.f;
+  const float mp = p.min_p != nullptr ? p.min_p[row] : 0.f;
+  const double a = p.a[row];
+
   // ---- the slice to shared memory; -0 becomes +0, so that the zeros tie
   const int n_loc = max(0, min(slice, V - rank * slice));
   const float* src = p.logits + row * p.ld + static_cast<int64_t>(rank) * slice;
@@ -409,7 +545,14 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
   float mx = -INFINITY;
   unsigned finite = 0;
   bool bad = false;
-  for (int o = warp * cs + lane * 4; o < (warp + 1) * cs; o += 128) {
+  auto put = [&](int o, float4 v) {
+    v.x += 0.f, v.y += 0.f, v.z += 0.f, v.w += 0.f;
+    *reinterpret_cast<float4*>(vals + o) = v;
+    bad |= !(v.x <= FLT_MAX && v.y <= FLT_MAX && v.z <= FLT_MAX && v.w <= FLT_MAX);
+    mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+    finite += (v.x > -INFINITY) + (v.y > -INFINITY) + (v.z > -INFINITY) + (v.w > -INFINITY);
+  };
+  auto get = [&](int o) {
     float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     if (vec && o + 3 < n_loc) {
       v = __ldcs(reinterpret_cast<const float4*>(src + o));
@@ -419,25 +562,37 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
       if (o + 2 < n_loc) v.z = __ldcs(src + o + 2);
       if (o + 3 < n_loc) v.w = __ldcs(src + o + 3);
     }
-    v.x += 0.f, v.y += 0.f, v.z += 0.f, v.w += 0.f;
-    *reinterpret_cast<float4*>(vals + o) = v;
-    bad |= !(v.x <= FLT_MAX && v.y <= FLT_MAX && v.z <= FLT_MAX && v.w <= FLT_MAX);
-    mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-    finite += (v.x > -INFINITY) + (v.y > -INFINITY) + (v.z > -INFINITY) + (v.w > -INFINITY);
+    return v;
+  };
+  {
+    const int end = (warp + 1) * cs;
+    int o = warp * cs + lane * 4;
+    for (; o + 3 * 128 < end; o += 4 * 128) {  // four loads in flight
+      const float4 v0 = get(o), v1 = get(o + 128), v2 = get(o + 256), v3 = get(o + 384);
+      put(o, v0);
+      put(o + 128, v1);
+      put(o + 256, v2);
+      put(o + 384, v3);
+    }
+    for (; o < end; o += 128) put(o, get(o));
+  }
+  if (tid == 0) {
+    // log2(e)/T as a float pair: the quotient, then that of its remainder
+    const float t = fmaxf(T, 1e-30f);
+    constexpr double L2E = 1.44269504088896340736;
+    constexpr float LH = static_cast<float>(L2E), LL = static_cast<float>(L2E - static_cast<double>(LH));
+    const float ch = LH / t;
+    sh->ch = ch;
+    sh->cl = (fmaf(-ch, t, LH) + LL) / t;
+    sh->scale = ch * ((kBins - 1) / kMaxLog2);
   }
   R.barrier();  // every CTA of the cluster runs before its shared memory is written
-  u64 top = key_of(mx), n_fin = finite + (bad ? 1ull << 40 : 0);
-  R.reduce2<kMax, kSum>(top, n_fin);
-  const float m = of_key(static_cast<unsigned>(top));
+  u64 n_fin = finite, n_bad = bad ? 1 : 0;
+  unsigned least = 0, top = key_of(mx);
+  R.reduce(n_fin, n_bad, least, top);
+  const float m = of_key(top);
 
-  // ---- settings
-  const float T = p.temperature[row];
-  const int k = p.top_k != nullptr ? p.top_k[row] : 0;
-  const float tp = p.top_p != nullptr ? p.top_p[row] : 1.f;
-  const float mp = p.min_p != nullptr ? p.min_p[row] : 0.f;
-  const double a = p.a[row];
-  if (!(T >= 0.f && T <= FLT_MAX) || tp != tp || mp != mp || !(a >= 0.0 && a < 1.0) || n_fin == 0 ||
-      n_fin >> 40) {
+  if (!(T >= 0.f && T <= FLT_MAX) || tp != tp || mp != mp || !(a >= 0.0 && a < 1.0) || n_fin == 0 || n_bad != 0) {
     if (rank == 0 && tid == 0) {
       p.token[row] = -1;
       if (p.n_kept != nullptr) p.n_kept[row] = 0;
@@ -447,11 +602,12 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
     return;  // the whole cluster
   }
   if (T == 0.f) {
-    u64 first = ~0ull, none = 0;
+    unsigned first = ~0u, none = 0;
+    u64 z0 = 0, z1 = 0;
     R.each([&](float z, int i) {
-      if (z == m && static_cast<u64>(i) < first) first = i;
+      if (z == m) first = min(first, static_cast<unsigned>(i));
     });
-    R.reduce2<kMin, kSum>(first, none);
+    R.reduce(z0, z1, first, none);
     if (rank == 0 && tid == 0) {
       p.token[row] = static_cast<int32_t>(first);
       if (p.n_kept != nullptr) p.n_kept[row] = 1;
@@ -459,27 +615,20 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
     }
     return;
   }
-  const double Td = fmax(static_cast<double>(T), 1e-30);
-  if (tid == 0) {
-    const double c = 1.44269504088896340736 / Td;
-    sh->ch = static_cast<float>(c);
-    sh->cl = static_cast<float>(c - static_cast<double>(sh->ch));
-    sh->scale = static_cast<float>(c * ((kBins - 1) / static_cast<double>(kMaxLog2)));
-    // smallest float z with (z - m) / T >= ln min_p
-    unsigned km = 0;
-    if (mp > 0.f) {
-      const double lim = log(static_cast<double>(mp)), md = m;
-      float z = static_cast<float>(fmin(fmax(md + Td * lim, -static_cast<double>(FLT_MAX)), md));
+  if (mp > 0.f) {
+    if (tid == 0) {
+      // smallest float z with (z - m) / T >= ln min_p
+      const double Td = fmax(static_cast<double>(T), 1e-30);
+      const double lim = log(fmin(static_cast<double>(mp), 1.0)), md = m;
       auto ok = [&](float x) { return (static_cast<double>(x) - md) / Td >= lim; };
-      unsigned kz = key_of(z);
-      const unsigned kmax = key_of(m), kmin = key_of(-FLT_MAX);
+      unsigned kz = key_of(static_cast<float>(fmax(md + Td * lim, -static_cast<double>(FLT_MAX))));
+      const unsigned kmax = top, kmin = key_of(-FLT_MAX);
       while (kz < kmax && !ok(of_key(kz))) ++kz;
       while (kz > kmin && ok(of_key(kz - 1))) --kz;
-      km = kz;
+      sh->key_m = kz;
     }
-    sh->key_m = km;
+    __syncthreads();
   }
-  __syncthreads();
   R.w.tab = sh->tab;
   R.w.m = m;
   R.w.ch = sh->ch;
@@ -487,112 +636,135 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
   R.w.scale = sh->scale;
   R.w.extra = V > (1 << 18) ? 1 : 0;
 
-  // the kept set: keys above v, and key v up to index i
-  unsigned v = sh->key_m;
+  // the kept set: keys above v, and key v up to index vi
+  unsigned v = mp > 0.f ? sh->key_m : 0;
   int vi = INT_MAX;
+  auto narrow = [&](const Border& b) {
+    if (b.key > v || (b.key == v && b.index < vi)) {
+      v = b.key;
+      vi = b.index;
+      return true;
+    }
+    return false;
+  };
   const bool use_k = k > 0 && static_cast<u64>(k) < n_fin;
   const bool use_p = tp < 1.f;
+  // a top-p border that decides: the mass of what this thread keeps for sure,
+  // and the bins that hold the rest
+  u64 sure = 0;
+  int p_lo = kBins, p_hi = -1;
   if (use_k || use_p) {
     // ---- counts by t
-    sh->hist[tid] = 0;
+    for (int j = tid; j < kBins; j += kThreads) sh->hist[j] = 0;
     __syncthreads();
     R.each([&](float z, int) {
       const int b = bin_of(R.w, z);
       if (b < kBins - 1) atomicAdd(&sh->hist[b], 1u);
     });
     R.barrier();
-    u64 cnt = 0;
-    for (int r = 0; r < nc; ++r) cnt += nc > 1 ? ld_cluster_u32(&sh->hist[tid], r) : sh->hist[tid];
-    const u64 cum = R.scan(cnt);
+    unsigned cnt[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      for (int r = 0; r < nc; ++r)
+        cnt[j] += nc > 1 ? ld_cluster_u32(&sh->hist[2 * tid + j], r) : sh->hist[2 * tid + j];
+    unsigned cum[2];
+    cum[1] = static_cast<unsigned>(R.scan(cnt[0] + cnt[1]));
+    cum[0] = cum[1] - cnt[1];
     if (tid == 0) sh->found = -1;
-    R.barrier();
+    R.barrier();  // the bins may be cleared again
 
     // ---- top-k
-    unsigned vk = 0;
-    int ik = INT_MAX, bk = kBins - 1;  // bin of K's border (kBins - 1: in the tail, or none)
+    Border bk = {0, INT_MAX};
+    int k_bin = kBins - 1;  // bin of K's border (kBins - 1: in the tail, or none)
     if (use_k) {
-      if (cnt > 0 && cum >= static_cast<u64>(k) && cum - cnt < static_cast<u64>(k)) {
-        sh->found = tid;
-        sh->before = cum - cnt;
-      }
+      const unsigned ku = k;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (cnt[j] > 0 && cum[j] >= ku && cum[j] - cnt[j] < ku) {
+          sh->found = 2 * tid + j;
+          sh->found_n = cnt[j];
+          sh->before = cum[j] - cnt[j];
+        }
       __syncthreads();
-      bk = sh->found < 0 ? kBins - 1 : sh->found;
+      const int f = sh->found;
+      const unsigned fn = sh->found_n;
       const u64 before = sh->before;
       __syncthreads();
-      if (bk < kBins - 1) {
-        u64 lo = ~0ull, hi = 0;
-        R.each([&](float z, int) {
-          if (bin_of(R.w, z) == bk) {
-            const u64 key = key_of(z);
-            lo = key < lo ? key : lo;
-            hi = key > hi ? key : hi;
-          }
-        });
-        R.reduce2<kMin, kMax>(lo, hi);
-        auto any = [](float, int) { return true; };
-        u64 above;
-        vk = R.border_key<false>(static_cast<unsigned>(lo), static_cast<unsigned>(hi), k, before, any, &above);
-        ik = R.border_index(vk, k - above, any);
+      if (f >= 0) {
+        k_bin = f;
+        bk = R.border<false>(f, f, fn, false, 0, 0, ku, before, [](float, int) { return true; });
       }
     }
     auto in_k = [&](float z, int i) {
       const unsigned key = key_of(z);
-      return key > vk || (key == vk && i <= ik);
+      return key > bk.key || (key == bk.key && i <= bk.index);
     };
-    if (vk > v || (vk == v && ik < vi)) v = vk, vi = ik;
+    narrow(bk);
 
     // ---- top-p
     if (use_p) {
       // bounds of every prefix's mass from the counts (K's last bin in part)
       constexpr float step = kMaxLog2 / (kBins - 1);
-      u64 part = cnt;
-      if (bk < kBins - 1) part = tid < bk ? cnt : tid == bk ? k - (cum - cnt) : 0;
-      if (tid == kBins - 1) part = 0;
-      const float c = static_cast<float>(part);
-      float low = c * exp2f(-(tid + 1) * step * 1.0001f), high = c * exp2f(-tid * step * 0.9999f);
-      R.scan2f(low, high);
+      float low[2], high[2];
+      unsigned part[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * tid + j;
+        part[j] = b < k_bin ? cnt[j] : b == k_bin && b < kBins - 1 ? k - (cum[j] - cnt[j]) : 0;
+        low[j] = part[j] * exp2f(-(b + 1) * step * 1.0001f);
+        high[j] = part[j] * exp2f(-b * step * 0.9999f);
+      }
+      float li = low[0] + low[1], hi_ = high[0] + high[1];
+      R.scan2f(li, hi_);
       if (tid == kThreads - 1) {
-        sh->f0[0] = low;
-        sh->f1[0] = high;
+        sh->f0[0] = li;
+        sh->f1[0] = hi_;
         sh->b_lo = sh->b_hi = kBins - 2;
       }
       __syncthreads();
       const float q = fmaxf(tp, 0.f);
-      if (part > 0 && high >= q * sh->f0[0] * 0.999f) atomicMin(&sh->b_lo, tid);
-      if (part > 0 && low >= q * sh->f1[0] * 1.001f) atomicMin(&sh->b_hi, tid);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float l = j ? li : li - low[1], h = j ? hi_ : hi_ - high[1];
+        if (part[j] > 0 && h * 1.001f >= q * sh->f0[0]) atomicMin(&sh->b_lo, 2 * tid + j);
+        if (part[j] > 0 && l >= q * sh->f1[0] * 1.001f) atomicMin(&sh->b_hi, 2 * tid + j);
+      }
+      if (tid == 0) sh->found_n = 0;
       __syncthreads();
-      const int b_lo = sh->b_lo, b_hi = sh->b_hi;
+      p_lo = sh->b_lo;
+      p_hi = sh->b_hi;
+      // the candidates, by count
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (2 * tid + j >= p_lo && 2 * tid + j <= p_hi && part[j] > 0) atomicAdd(&sh->found_n, part[j]);
+      __syncthreads();
+      const unsigned n_cand = sh->found_n;
       __syncthreads();
       // K's mass, and the mass above the bins in question
-      u64 M = 0, A = 0, lo = ~0ull, hi = 0;
+      u64 M = 0, A = 0;
+      unsigned lo = ~0u, hi = 0;
       R.each([&](float z, int i) {
         const int b = bin_of(R.w, z);
         if (b >= kBins - 1 || !in_k(z, i)) return;
         const u64 x = weight_of(R.w, z);
         M += x;
-        if (b < b_lo) A += x;
-        else if (b <= b_hi) {
-          const u64 key = key_of(z);
-          lo = key < lo ? key : lo;
-          hi = key > hi ? key : hi;
+        if (b < p_lo) {
+          A += x;
+        } else if (b <= p_hi) {
+          const unsigned key = key_of(z);
+          lo = min(lo, key);
+          hi = max(hi, key);
         }
       });
-      R.reduce2<kSum, kSum>(M, A);
-      R.reduce2<kMin, kMax>(lo, hi);
-      const double want = ceil(static_cast<double>(q) * static_cast<double>(M));
-      u64 need = static_cast<u64>(want);
+      sure = A;
+      R.reduce(M, A, lo, hi);
+      u64 need = static_cast<u64>(ceil(static_cast<double>(q) * static_cast<double>(M)));
       if (need > M) need = M;
       if (need <= A) need = A + 1;
-      u64 above;
-      const unsigned vp = R.border_key<true>(static_cast<unsigned>(lo), static_cast<unsigned>(hi), need, A,
-                                             in_k, &above);
-      const u64 wp = weight_of(R.w, of_key(vp));
-      const u64 c_ties = need > above ? (need - above + wp - 1) / max(wp, 1ull) : 1;
-      const int ip = R.border_index(vp, c_ties, in_k);
-      // a tie cut by K and not by P stays cut by K
-      if (vp > v || (vp == v && ip < vi)) v = vp, vi = ip;
+      if (!narrow(R.border<true>(p_lo, p_hi, n_cand, true, lo, hi, need, A, in_k))) p_lo = kBins;
     }
   }
+  const bool by_p = p_lo < kBins;  // top-p's border is the kept set's
 
   // ---- the draw
   auto value = [&](float z, int i) -> u64 {
@@ -600,17 +772,20 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
     if (key < v || (key == v && i > vi) || bin_of(R.w, z) >= kBins - 1) return 0;
     return weight_of(R.w, z);
   };
-  u64 mine = 0, kept = 0;
+  u64 mine = by_p ? sure : 0, kept = 0;
   R.each([&](float z, int i) {
     const unsigned key = key_of(z);
     if (z > -INFINITY && (key > v || (key == v && i <= vi))) {
       ++kept;
-      if (bin_of(R.w, z) < kBins - 1) mine += weight_of(R.w, z);
+      const int b = bin_of(R.w, z);
+      // by_p: what lies above p_lo is in `sure` already, nothing below p_hi is kept
+      if (b < kBins - 1 && (!by_p || b >= p_lo)) mine += weight_of(R.w, z);
     }
   });
   const int buf = R.par;
   u64 S = mine;
-  R.reduce2<kSum, kSum>(S, kept);
+  unsigned none0 = 0, none1 = 0;
+  R.reduce(S, kept, none0, none1);
   u64 need = static_cast<u64>(a * static_cast<double>(S)) + 1;
   if (need > S) need = S;
   int idx;
@@ -621,10 +796,29 @@ __global__ void __launch_bounds__(kThreads) sample_filtered_kernel(const SampleF
       if (k > 0 && kept > static_cast<u64>(k)) kept = k;  // K's border lies in the tail
       p.n_kept[row] = static_cast<int32_t>(kept);
     }
-    if (p.logprob != nullptr)
+    if (p.logprob != nullptr) {
+      const double Td = fmax(static_cast<double>(T), 1e-30);
       p.logprob[row] = static_cast<float>((static_cast<double>(z) - static_cast<double>(m)) / Td -
                                           log(ldexp(static_cast<double>(S), R.w.extra - 45)));
+    }
   }
+}
+
+const WeightTable& weight_table() {
+  static const WeightTable t = [] {
+    WeightTable x;
+    for (int j = 0; j < 64; ++j) {
+      const double e = std::exp2(-j / 64.0);
+      const float hi = static_cast<float>(e);
+      const u64 fix = static_cast<u64>(e * 0x1p45 + 0.5);
+      const uint32_t w[2] = {static_cast<uint32_t>(fix), static_cast<uint32_t>(fix >> 32)};
+      float f[2];
+      std::memcpy(f, w, sizeof(f));
+      x.e[j] = make_float4(hi, static_cast<float>(e - static_cast<double>(hi)), f[0], f[1]);
+    }
+    return x;
+  }();
+  return t;
 }
 
 }  // namespace
@@ -658,7 +852,7 @@ cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, sample_filtered_kernel, p, nc, slice, cs);
+  return cudaLaunchKernelEx(&cfg, sample_filtered_kernel, p, weight_table(), nc, slice, cs);
 }
 
 }  // namespace dflash
