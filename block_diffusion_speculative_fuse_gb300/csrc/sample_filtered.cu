@@ -13,7 +13,7 @@
 // (45 fractional bits): t as an unevaluated float pair, t = j/64 + r with a
 // table of 2^(-j/64) (P. T. P. Tang's table-driven scheme) and the Taylor
 // series of exp(-r ln 2), the parts added in fixed point; relative error
-// 2^-35 per weight and without bias, so a row's sum is good to about 1e-12.
+// 2^-34 per weight and without bias, so a row's sum is good to about 1e-12.
 // fp64 would do, but its rate here is a sixty-fourth of fp32's.  Integer sums
 // are exact: results do not depend on how the row is split or in which order
 // atomics arrive.
@@ -53,8 +53,9 @@ static_assert(kMaxSampleVocab / kMaxCluster * 4 + 16384 <= 227 * 1024, "a slice 
 
 struct Shared {
   float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(45-j/64) in two words
-  u64 mass[kBins];                   // also the candidates' list: kList orders, kList weights
+  u64 list[2 * kList];               // candidates: orders, weights
   unsigned hist[kBins];
+  unsigned mass[3][kBins];           // in limbs of 16 bits (a slice has fewer than 2^16 logits)
   u64 xch[2][kMaxCluster][2];        // exchanged values, one row per rank of the cluster
   unsigned xch32[2][kMaxCluster][2];
   u64 wred[kWarps][2];
@@ -92,9 +93,18 @@ __device__ __forceinline__ float of_key(unsigned k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
+// Roundings to an integer are made by adding 1.5 * 2^23 (for magnitudes below
+// 2^22): the conversion instructions run at an eighth of the rate of an add and
+// set the pace otherwise.
+constexpr float kMagic = 12582912.f;
+__device__ __forceinline__ int magic_int(float x_plus_magic) {
+  return __float_as_int(x_plus_magic) - 0x4B400000;
+}
+
+// Steps of t nearest to the logit's, non-decreasing as z falls.
 __device__ __forceinline__ int bin_of(const Weights& w, float z) {
   const float x = (w.m - z) * w.scale;
-  return x < static_cast<float>(kBins - 1) ? static_cast<int>(x) : kBins - 1;
+  return x < kBins - 1.5f ? magic_int(x + kMagic) : kBins - 1;
 }
 
 // the weight of logit z <= m, not in the tail
@@ -107,30 +117,31 @@ __device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
   float e = fmaf(dh, w.ch, -t);
   e = fmaf(dh, w.cl, e);
   e = fmaf(dl, w.ch, e);
-  const float k64 = rintf(t * 64.f);
-  const int k = static_cast<int>(k64);
-  const float r = fmaf(k64, -1.f / 64.f, t);
-  // u = -(r + e) ln 2 = -(uh + ul)
-  constexpr float LH = 0.693147180559945309f;
-  constexpr float LL = static_cast<float>(0.693147180559945309 - static_cast<double>(LH));
-  float uh = r * LH;
+  const float kx = fmaf(t, 64.f, kMagic);
+  const int k = magic_int(kx);
+  const float r = fmaf(kx - kMagic, -1.f / 64.f, t);
+  // u = -(r + e) ln 2 = uh + ul
+  constexpr double LN2 = 0.693147180559945309;
+  constexpr float LH = static_cast<float>(-LN2);
+  constexpr float LL = static_cast<float>(-LN2 - static_cast<double>(LH));
+  const float uh = r * LH;
   float ul = fmaf(r, LH, -uh);
   ul = fmaf(r, LL, ul);
   ul = fmaf(e, LH, ul);
-  uh = -uh;
-  ul = -ul;
   const float s = (uh * uh) * fmaf(uh, fmaf(uh, 1.f / 24.f, 1.f / 6.f), 0.5f);
   const float tail = s + fmaf(uh, ul, ul);  // exp(u) - 1 = uh + tail
   const float4 tj = w.tab[k & 63];
   const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
-  const float ph = tj.x * uh;
+  const float ph = tj.x * uh;               // below 2^-7
   float low = fmaf(tj.x, uh, -ph);
   low = fmaf(tj.y, uh, low);
-  low = fmaf(tj.x, tail, low);
-  const float a = rintf(ph * 0x1p30f);
-  low += fmaf(a, -0x1p-30f, ph);
-  const long long R = static_cast<long long>(fix) + (static_cast<long long>(static_cast<int>(a)) << 15) +
-                      __float2int_rn(low * 0x1p45f);
+  low = fmaf(tj.x, tail, low);              // below 2^-15
+  // to integers: ph in units of 2^-29 (what that leaves goes to low), low of 2^-37
+  const float ax = fmaf(ph, 0x1p29f, kMagic);
+  low += fmaf(ax - kMagic, -0x1p-29f, ph);
+  const int bx = magic_int(fmaf(low, 0x1p37f, kMagic));
+  const long long R = static_cast<long long>(fix) + (static_cast<long long>(magic_int(ax)) << 16) +
+                      static_cast<long long>(bx * 256);
   const int n = (k >> 6) + w.extra;
   return (static_cast<u64>(R) + ((1ull << n) >> 1)) >> n;
 }
@@ -140,11 +151,6 @@ __device__ __forceinline__ u64 shfl_xor64(u64 v, int o) { return __shfl_xor_sync
 __device__ __forceinline__ void st_cluster_u64(const void* smem, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dsmem_map(smem_u32(smem), rank)), "l"(v)
                : "memory");
-}
-__device__ __forceinline__ u64 ld_cluster_u64(const void* smem, uint32_t rank) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(dsmem_map(smem_u32(smem), rank)) : "memory");
-  return v;
 }
 __device__ __forceinline__ unsigned ld_cluster_u32(const void* smem, uint32_t rank) {
   unsigned v;
@@ -395,18 +401,20 @@ struct Row {
     }
     while (n > kList && lo < hi) {
       const int shift = max(0, 32 - __clz(hi - lo) - 10);
-      for (int j = tid; j < kBins; j += kThreads) {
-        sh->mass[j] = 0;
-        sh->hist[j] = 0;
-      }
+      for (int j = tid; j < kBins; j += kThreads) sh->hist[j] = sh->mass[0][j] = sh->mass[1][j] = sh->mass[2][j] = 0;
       if (tid == 0) sh->found = -1;
       __syncthreads();
       each([&](float z, int i) {
         const unsigned k = key_of(z);
         if (k < lo || k > hi || !in(z, i)) return;
         const unsigned b = (hi - k) >> shift;
-        if (MASS) atomicAdd(&sh->mass[b], weight_of(w, z));
         atomicAdd(&sh->hist[b], 1u);
+        if (MASS) {
+          const u64 x = weight_of(w, z);
+          atomicAdd(&sh->mass[0][b], static_cast<unsigned>(x) & 0xFFFFu);
+          atomicAdd(&sh->mass[1][b], static_cast<unsigned>(x) >> 16);
+          atomicAdd(&sh->mass[2][b], static_cast<unsigned>(x >> 32));
+        }
       });
       barrier();
       u64 v[2] = {0, 0};
@@ -415,7 +423,12 @@ struct Row {
       for (int j = 0; j < 2; ++j)
         for (int r = 0; r < nc; ++r) {
           cn[j] += nc > 1 ? ld_cluster_u32(&sh->hist[2 * tid + j], r) : sh->hist[2 * tid + j];
-          if (MASS) v[j] += nc > 1 ? ld_cluster_u64(&sh->mass[2 * tid + j], r) : sh->mass[2 * tid + j];
+          if (MASS)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const unsigned* at = &sh->mass[i][2 * tid + j];
+              v[j] += static_cast<u64>(nc > 1 ? ld_cluster_u32(at, r) : *at) << (16 * i);
+            }
         }
       if (!MASS) v[0] = cn[0], v[1] = cn[1];
       const u64 inc1 = above + scan(v[0] + v[1]), inc0 = inc1 - v[1];
@@ -445,8 +458,8 @@ struct Row {
       return Border{lo, border_index(lo, need > above ? (need - above + wk - 1) / wk : 1, in)};
     }
     // ---- the list, in rank 0's shared memory
-    u64* orders = sh->mass;
-    u64* weights = sh->mass + kList;
+    u64* orders = sh->list;
+    u64* weights = sh->list + kList;
     each([&](float z, int i) {
       const unsigned key = key_of(z);
       if (have_keys) {
@@ -711,8 +724,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < 2; ++j) {
         const int b = 2 * tid + j;
         part[j] = b < k_bin ? cnt[j] : b == k_bin && b < kBins - 1 ? k - (cum[j] - cnt[j]) : 0;
-        low[j] = part[j] * exp2f(-(b + 1) * step * 1.0001f);
-        high[j] = part[j] * exp2f(-b * step * 0.9999f);
+        low[j] = part[j] * exp2f(-(b + 0.5f) * step * 1.0001f);
+        high[j] = part[j] * exp2f(-(b - 0.5f) * step * 0.9999f);
       }
       float li = low[0] + low[1], hi_ = high[0] + high[1];
       R.scan2f(li, hi_);
