@@ -18,13 +18,16 @@
 // are exact: results do not depend on how the row is split or in which order
 // atomics arrive.
 //
-// Selection without a sort.  A histogram of counts over 1023 equal steps of t
-// in [0, 46) (one shared-memory atomic per logit) bounds the mass of every
-// prefix within 3 %, which leaves a few bins that can hold the border of top-p
-// (one bin for top-k).  Their tokens, the candidates, go to a list if they are
-// few, where each counts what precedes it; otherwise they are first split by
-// their exact 32-bit key, ten bits a pass, with the exact masses.  A border that
-// falls on many equal logits is settled by counting them in index order.
+// Selection without a sort.  Over 1023 equal steps of t in [0, 46) the tokens
+// are counted, and their distances from the step's middle summed (two shared-
+// memory atomics per logit): to first order that is the step's mass, so every
+// prefix's mass is known within 2e-4, which leaves one or two steps that can hold
+// the border of top-p (one for top-k).  (From the counts alone it would be 3 %:
+// on flat logits a quarter of all tokens.)  Those steps' tokens, the candidates,
+// go to a list if they are few, where each counts what precedes it; otherwise
+// they are first split by their exact 32-bit key, eight bits a pass, with the
+// exact masses.  A border that falls on many equal logits is settled by
+// counting them in index order.
 //
 // Bound: for a batch of rows instruction issue (about 45 instructions per
 // weight, evaluated once per token of K), for a few rows the latency of about
@@ -47,6 +50,7 @@ constexpr int kThreads = 512;           // two CTAs per SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;          // two per thread; the last is the tail (t >= 46)
 constexpr int kList = 256;           // candidates settled in a list
+constexpr int kKeyBins = 256;        // of a pass over the candidates' keys
 constexpr float kMaxLog2 = 46.f;     // weights below 2^-46 count as 0
 constexpr int kMaxCluster = 8;
 static_assert(kMaxSampleVocab / kMaxCluster * 4 + 16384 <= 227 * 1024, "a slice fits shared memory");
@@ -55,7 +59,8 @@ struct Shared {
   float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(45-j/64) in two words
   u64 list[2 * kList];               // candidates: orders, weights
   unsigned hist[kBins];
-  unsigned mass[3][kBins];           // in limbs of 16 bits (a slice has fewer than 2^16 logits)
+  unsigned dist[kBins];              // sums of (distance + 1/2) * 2^14
+  unsigned keys[4][kKeyBins];        // counts; masses in limbs of 16 bits (a slice has fewer than 2^16 logits)
   u64 xch[2][kMaxCluster][2];        // exchanged values, one row per rank of the cluster
   unsigned xch32[2][kMaxCluster][2];
   u64 wred[kWarps][2];
@@ -101,10 +106,17 @@ __device__ __forceinline__ int magic_int(float x_plus_magic) {
   return __float_as_int(x_plus_magic) - 0x4B400000;
 }
 
-// Steps of t nearest to the logit's, non-decreasing as z falls.
-__device__ __forceinline__ int bin_of(const Weights& w, float z) {
+// The step of t nearest to the logit's, non-decreasing as z falls; *dist = how
+// far past the step's middle, in steps.
+__device__ __forceinline__ int bin_of(const Weights& w, float z, float* dist) {
   const float x = (w.m - z) * w.scale;
-  return x < kBins - 1.5f ? magic_int(x + kMagic) : kBins - 1;
+  const float k = x + kMagic;
+  *dist = x - (k - kMagic);
+  return x < kBins - 1.5f ? magic_int(k) : kBins - 1;
+}
+__device__ __forceinline__ int bin_of(const Weights& w, float z) {
+  float dist;
+  return bin_of(w, z, &dist);
 }
 
 // the weight of logit z <= m, not in the tail
@@ -151,6 +163,11 @@ __device__ __forceinline__ u64 shfl_xor64(u64 v, int o) { return __shfl_xor_sync
 __device__ __forceinline__ void st_cluster_u64(const void* smem, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dsmem_map(smem_u32(smem), rank)), "l"(v)
                : "memory");
+}
+__device__ __forceinline__ u64 ld_cluster_u64(const void* smem, uint32_t rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(dsmem_map(smem_u32(smem), rank)) : "memory");
+  return v;
 }
 __device__ __forceinline__ unsigned ld_cluster_u32(const void* smem, uint32_t rank) {
   unsigned v;
@@ -400,46 +417,40 @@ struct Row {
       have_keys = true;
     }
     while (n > kList && lo < hi) {
-      const int shift = max(0, 32 - __clz(hi - lo) - 10);
-      for (int j = tid; j < kBins; j += kThreads) sh->hist[j] = sh->mass[0][j] = sh->mass[1][j] = sh->mass[2][j] = 0;
+      const int shift = max(0, 32 - __clz(hi - lo) - 8);
+      if (tid < kKeyBins) sh->keys[0][tid] = sh->keys[1][tid] = sh->keys[2][tid] = sh->keys[3][tid] = 0;
       if (tid == 0) sh->found = -1;
       __syncthreads();
       each([&](float z, int i) {
         const unsigned k = key_of(z);
         if (k < lo || k > hi || !in(z, i)) return;
         const unsigned b = (hi - k) >> shift;
-        atomicAdd(&sh->hist[b], 1u);
+        atomicAdd(&sh->keys[0][b], 1u);
         if (MASS) {
           const u64 x = weight_of(w, z);
-          atomicAdd(&sh->mass[0][b], static_cast<unsigned>(x) & 0xFFFFu);
-          atomicAdd(&sh->mass[1][b], static_cast<unsigned>(x) >> 16);
-          atomicAdd(&sh->mass[2][b], static_cast<unsigned>(x >> 32));
+          atomicAdd(&sh->keys[1][b], static_cast<unsigned>(x) & 0xFFFFu);
+          atomicAdd(&sh->keys[2][b], static_cast<unsigned>(x) >> 16);
+          atomicAdd(&sh->keys[3][b], static_cast<unsigned>(x >> 32));
         }
       });
       barrier();
-      u64 v[2] = {0, 0};
-      unsigned cn[2] = {0, 0};
+      u64 v = 0;
+      unsigned cn = 0;
+      if (tid < kKeyBins) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        for (int r = 0; r < nc; ++r) {
-          cn[j] += nc > 1 ? ld_cluster_u32(&sh->hist[2 * tid + j], r) : sh->hist[2 * tid + j];
-          if (MASS)
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              const unsigned* at = &sh->mass[i][2 * tid + j];
-              v[j] += static_cast<u64>(nc > 1 ? ld_cluster_u32(at, r) : *at) << (16 * i);
-            }
+        for (int j = 0; j < (MASS ? 4 : 1); ++j) {
+          u64 x = 0;
+          for (int r = 0; r < nc; ++r) x += nc > 1 ? ld_cluster_u32(&sh->keys[j][tid], r) : sh->keys[j][tid];
+          if (j == 0) cn = static_cast<unsigned>(x);
+          else v += x << (16 * (j - 1));
         }
-      if (!MASS) v[0] = cn[0], v[1] = cn[1];
-      const u64 inc1 = above + scan(v[0] + v[1]), inc0 = inc1 - v[1];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u64 inc = j ? inc1 : inc0;
-        if (v[j] > 0 && need <= inc && inc - v[j] < need) {
-          sh->found = 2 * tid + j;
-          sh->found_n = cn[j];
-          sh->before = inc - v[j];
-        }
+        if (!MASS) v = cn;
+      }
+      const u64 inc = above + scan(v);
+      if (v > 0 && need <= inc && inc - v < need) {
+        sh->found = tid;
+        sh->found_n = cn;
+        sh->before = inc - v;
       }
       barrier();  // also: the bins may be cleared again
       const int b = sh->found;
@@ -668,23 +679,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   int p_lo = kBins, p_hi = -1;
   if (use_k || use_p) {
     // ---- counts by t
-    for (int j = tid; j < kBins; j += kThreads) sh->hist[j] = 0;
+    for (int j = tid; j < kBins; j += kThreads) sh->hist[j] = sh->dist[j] = 0;
     __syncthreads();
     R.each([&](float z, int) {
-      const int b = bin_of(R.w, z);
-      if (b < kBins - 1) atomicAdd(&sh->hist[b], 1u);
+      float d;
+      const int b = bin_of(R.w, z, &d);
+      if (b < kBins - 1) {
+        atomicAdd(&sh->hist[b], 1u);
+        if (use_p) atomicAdd(&sh->dist[b], static_cast<unsigned>(magic_int(fmaf(d, 16384.f, kMagic + 8192.f))));
+      }
     });
     R.barrier();
     unsigned cnt[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      for (int r = 0; r < nc; ++r)
-        cnt[j] += nc > 1 ? ld_cluster_u32(&sh->hist[2 * tid + j], r) : sh->hist[2 * tid + j];
+    float dist[2] = {0.f, 0.f};
+    for (int r = 0; r < nc; ++r) {
+      const u64 c = nc > 1 ? ld_cluster_u64(&sh->hist[2 * tid], r) : *reinterpret_cast<const u64*>(&sh->hist[2 * tid]);
+      const u64 d = nc > 1 ? ld_cluster_u64(&sh->dist[2 * tid], r) : *reinterpret_cast<const u64*>(&sh->dist[2 * tid]);
+      cnt[0] += static_cast<unsigned>(c);
+      cnt[1] += static_cast<unsigned>(c >> 32);
+      dist[0] += static_cast<float>(static_cast<unsigned>(d));
+      dist[1] += static_cast<float>(static_cast<unsigned>(d >> 32));
+    }
     unsigned cum[2];
     cum[1] = static_cast<unsigned>(R.scan(cnt[0] + cnt[1]));
     cum[0] = cum[1] - cnt[1];
     if (tid == 0) sh->found = -1;
-    R.barrier();  // the bins may be cleared again
+    __syncthreads();
 
     // ---- top-k
     Border bk = {0, INT_MAX};
@@ -716,16 +736,26 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // ---- top-p
     if (use_p) {
-      // bounds of every prefix's mass from the counts (K's last bin in part)
-      constexpr float step = kMaxLog2 / (kBins - 1);
+      // bounds of every prefix's mass.  A step's mass relative to its middle is
+      // sum exp(-c d), c = step ln 2, |d| <= 1/2: n - c sum d, and more by at most
+      // n (c/2)^2 / 2 = 1.2e-4 n; the sum's quantisation and fp32 are far below.
+      // K's last step, of which only a part counts, by its edges.
+      constexpr float step = kMaxLog2 / (kBins - 1), c = step * 0.69314718f;
       float low[2], high[2];
       unsigned part[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int b = 2 * tid + j;
-        part[j] = b < k_bin ? cnt[j] : b == k_bin && b < kBins - 1 ? k - (cum[j] - cnt[j]) : 0;
-        low[j] = part[j] * exp2f(-(b + 0.5f) * step * 1.0001f);
-        high[j] = part[j] * exp2f(-(b - 0.5f) * step * 0.9999f);
+        const float mid = exp2f(-b * step);
+        part[j] = b < k_bin ? cnt[j] : 0;
+        low[j] = fmaf(-c, dist[j] * (1.f / 16384.f) - 0.5f * cnt[j], static_cast<float>(cnt[j])) * mid * (1.f - 3e-5f);
+        high[j] = low[j] * (1.f + 2e-4f);
+        if (b >= k_bin || part[j] == 0) low[j] = high[j] = 0.f;
+        if (b == k_bin && b < kBins - 1) {
+          part[j] = k - (cum[j] - cnt[j]);
+          low[j] = part[j] * mid * (1.f - 0.5f * c);
+          high[j] = part[j] * mid * (1.f + 0.51f * c);
+        }
       }
       float li = low[0] + low[1], hi_ = high[0] + high[1];
       R.scan2f(li, hi_);
@@ -739,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float l = j ? li : li - low[1], h = j ? hi_ : hi_ - high[1];
-        if (part[j] > 0 && h * 1.001f >= q * sh->f0[0]) atomicMin(&sh->b_lo, 2 * tid + j);
-        if (part[j] > 0 && l >= q * sh->f1[0] * 1.001f) atomicMin(&sh->b_hi, 2 * tid + j);
+        if (part[j] > 0 && h * (1.f + 1e-5f) >= q * sh->f0[0]) atomicMin(&sh->b_lo, 2 * tid + j);
+        if (part[j] > 0 && l >= q * sh->f1[0] * (1.f + 1e-5f)) atomicMin(&sh->b_hi, 2 * tid + j);
       }
       if (tid == 0) sh->found_n = 0;
       __syncthreads();
