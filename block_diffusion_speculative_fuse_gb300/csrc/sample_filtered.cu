@@ -6,8 +6,11 @@
 //   kept set is {z > v} plus the tokens with z = v up to an index.  The token
 //   is the smallest index with a * S < C over the kept weights in index order.
 //
-// One thread-block cluster per row; each CTA keeps its slice of the logits in
-// shared memory, so the row is read from HBM once however many passes follow.
+// A few rows, or rows that fit: one thread-block cluster per row, each CTA with
+// its slice of the logits in shared memory, so the row is read from memory once
+// however many passes follow.  Many long rows: one CTA per row, which reads the
+// row again in every pass (the rows in flight fit L2); that saves the cluster's
+// barriers, which cost a row as much as its arithmetic.
 //
 // Weights.  2^-t with t = (m - z) log2(e) / T is evaluated as a 46-bit integer
 // (45 fractional bits): t as an unevaluated float pair, t = j/64 + r with a
@@ -46,14 +49,13 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 512;           // two CTAs per SM
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;          // two per thread; the last is the tail (t >= 46)
-constexpr int kList = 256;           // candidates settled in a list
+constexpr int kBins = 1024;          // the last is the tail (t >= 46)
+constexpr int kList = 256;           // candidates settled in the list
+constexpr int kMaxWarps = 32;
 constexpr int kKeyBins = 256;        // of a pass over the candidates' keys
 constexpr float kMaxLog2 = 46.f;     // weights below 2^-46 count as 0
 constexpr int kMaxCluster = 8;
-static_assert(kMaxSampleVocab / kMaxCluster * 4 + 16384 <= 227 * 1024, "a slice fits shared memory");
+static_assert(kMaxSampleVocab / kMaxCluster * 4 + 28672 <= 227 * 1024, "a slice fits shared memory");
 
 struct Shared {
   float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(45-j/64) in two words
@@ -63,10 +65,12 @@ struct Shared {
   unsigned keys[4][kKeyBins];        // counts; masses in limbs of 16 bits (a slice has fewer than 2^16 logits)
   u64 xch[2][kMaxCluster][2];        // exchanged values, one row per rank of the cluster
   unsigned xch32[2][kMaxCluster][2];
-  u64 wred[kWarps][2];
-  u64 wscan[kWarps];
-  unsigned wred32[kWarps][2];
-  float f0[kWarps], f1[kWarps];
+  u64 wred[kMaxWarps][2];
+  u64 wscan[kMaxWarps];
+  u64 wadd[kMaxWarps];               // kept candidates' mass, by the warp that owns their index
+  unsigned wred32[kMaxWarps][2];
+  float f0[kMaxWarps], f1[kMaxWarps];
+  float tot0, tot1;
   float ch, cl, scale;               // log2(e)/T as a float pair; bins per unit of z
   unsigned key_m;                    // smallest key that min_p keeps
   int b_lo, b_hi;
@@ -74,6 +78,8 @@ struct Shared {
   unsigned found_n;
   u64 before;
   unsigned list_n;                   // rank 0: candidates listed
+  unsigned cand_n;                   // candidates kept aside
+  unsigned above_n;                  // tokens of K above them
   unsigned border_key;               // the list's answer
   int border_index;
 };
@@ -109,8 +115,8 @@ __device__ __forceinline__ int magic_int(float x_plus_magic) {
 // The step of t nearest to the logit's, non-decreasing as z falls; *dist = how
 // far past the step's middle, in steps.
 __device__ __forceinline__ int bin_of(const Weights& w, float z, float* dist) {
-  const float x = (w.m - z) * w.scale;
-  const float k = x + kMagic;
+  const float x = __fmul_rn(w.m - z, w.scale);  // (never contracted: every pass has the same steps)
+  const float k = __fadd_rn(x, kMagic);
   *dist = x - (k - kMagic);
   return x < kBins - 1.5f ? magic_int(k) : kBins - 1;
 }
@@ -119,13 +125,14 @@ __device__ __forceinline__ int bin_of(const Weights& w, float z) {
   return bin_of(w, z, &dist);
 }
 
-// the weight of logit z <= m, not in the tail
+// the weight of logit z <= m, not in the tail (no product is contracted with a
+// sum: weight_of2 gives the same bits)
 __device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
   // m - z = dh + dl exactly
   const float dh = w.m - z;
   const float bb = dh - w.m;
   const float dl = (w.m - (dh - bb)) + (-z - bb);
-  const float t = dh * w.ch;
+  const float t = __fmul_rn(dh, w.ch);
   float e = fmaf(dh, w.ch, -t);
   e = fmaf(dh, w.cl, e);
   e = fmaf(dl, w.ch, e);
@@ -136,15 +143,15 @@ __device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
   constexpr double LN2 = 0.693147180559945309;
   constexpr float LH = static_cast<float>(-LN2);
   constexpr float LL = static_cast<float>(-LN2 - static_cast<double>(LH));
-  const float uh = r * LH;
+  const float uh = __fmul_rn(r, LH);
   float ul = fmaf(r, LH, -uh);
   ul = fmaf(r, LL, ul);
   ul = fmaf(e, LH, ul);
-  const float s = (uh * uh) * fmaf(uh, fmaf(uh, 1.f / 24.f, 1.f / 6.f), 0.5f);
-  const float tail = s + fmaf(uh, ul, ul);  // exp(u) - 1 = uh + tail
+  const float s = __fmul_rn(__fmul_rn(uh, uh), fmaf(uh, fmaf(uh, 1.f / 24.f, 1.f / 6.f), 0.5f));
+  const float tail = __fadd_rn(s, fmaf(uh, ul, ul));  // exp(u) - 1 = uh + tail
   const float4 tj = w.tab[k & 63];
   const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
-  const float ph = tj.x * uh;               // below 2^-7
+  const float ph = __fmul_rn(tj.x, uh);               // below 2^-7
   float low = fmaf(tj.x, uh, -ph);
   low = fmaf(tj.y, uh, low);
   low = fmaf(tj.x, tail, low);              // below 2^-15
@@ -156,6 +163,81 @@ __device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
                       static_cast<long long>(bx * 256);
   const int n = (k >> 6) + w.extra;
   return (static_cast<u64>(R) + ((1ull << n) >> 1)) >> n;
+}
+
+// Two fp32 operations in one instruction.
+struct F2 {
+  u64 v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void un2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// weight_of for two logits, operation by operation the same
+__device__ __forceinline__ void weight_of2(const Weights& w, float z0, float z1, u64* w0, u64* w1) {
+  const F2 neg = f2(-1.f, -1.f), m = f2(w.m, w.m), z = f2(z0, z1), ch = f2(w.ch, w.ch), cl = f2(w.cl, w.cl);
+  const F2 magic = f2(kMagic, kMagic), unmagic = f2(-kMagic, -kMagic);
+  const F2 dh = fma(z, neg, m);
+  const F2 bb = fma(m, neg, dh);
+  const F2 dl = add(fma(fma(bb, neg, dh), neg, m), mul(add(z, bb), neg));
+  const F2 t = mul(dh, ch);
+  F2 e = fma(dh, ch, mul(t, neg));
+  e = fma(dh, cl, e);
+  e = fma(dl, ch, e);
+  const F2 kx = fma(t, f2(64.f, 64.f), magic);
+  const F2 r = fma(add(kx, unmagic), f2(-1.f / 64.f, -1.f / 64.f), t);
+  constexpr double LN2 = 0.693147180559945309;
+  constexpr float LH = static_cast<float>(-LN2);
+  constexpr float LL = static_cast<float>(-LN2 - static_cast<double>(LH));
+  const F2 lh = f2(LH, LH);
+  const F2 uh = mul(r, lh);
+  F2 ul = fma(r, lh, mul(uh, neg));
+  ul = fma(r, f2(LL, LL), ul);
+  ul = fma(e, lh, ul);
+  const F2 s = mul(mul(uh, uh), fma(uh, fma(uh, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f)));
+  const F2 tail = add(s, fma(uh, ul, ul));
+  float k0, k1;
+  un2(kx, k0, k1);
+  const int ka = magic_int(k0), kb = magic_int(k1);
+  const float4 ta = w.tab[ka & 63], tb = w.tab[kb & 63];
+  const F2 th = f2(ta.x, tb.x);
+  const F2 ph = mul(th, uh);
+  F2 low = fma(th, uh, mul(ph, neg));
+  low = fma(f2(ta.y, tb.y), uh, low);
+  low = fma(th, tail, low);
+  const F2 ax = fma(ph, f2(0x1p29f, 0x1p29f), magic);
+  low = add(low, fma(add(ax, unmagic), f2(-0x1p-29f, -0x1p-29f), ph));
+  const F2 bx = fma(low, f2(0x1p37f, 0x1p37f), magic);
+  float a0, a1, b0, b1;
+  un2(ax, a0, a1);
+  un2(bx, b0, b1);
+  auto join = [&](const float4& tj, float a, float b, int k) {
+    const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
+    const long long R = static_cast<long long>(fix) + (static_cast<long long>(magic_int(a)) << 16) +
+                        static_cast<long long>(magic_int(b) * 256);
+    const int n = (k >> 6) + w.extra;
+    return (static_cast<u64>(R) + ((1ull << n) >> 1)) >> n;
+  };
+  *w0 = join(ta, a0, b0, ka);
+  *w1 = join(tb, a1, b1, kb);
 }
 
 __device__ __forceinline__ u64 shfl_xor64(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
@@ -195,10 +277,18 @@ struct Border {
   int index;  // tokens with this key are in up to this index
 };
 
-// The row's work, shared by all threads of the cluster.
+// The row's work, shared by all threads of the cluster.  HELD: the slice is in
+// shared memory; otherwise (one CTA per row) it is read from the logits.
+template <int kThreads, bool HELD>
 struct Row {
+  [[maybe_unused]] static constexpr int kWarps = kThreads / 32;
+  [[maybe_unused]] static constexpr int BPT = kBins / kThreads;  // steps of t per thread
+  [[maybe_unused]] static constexpr unsigned kCand = HELD ? 512 : 4096;  // candidates a CTA keeps aside
   Shared* sh;
-  const float* vals;   // this CTA's slice, padded with -inf to kWarps * cs
+  u64 *cand_order, *cand_w;  // [kCand]
+  const float* vals;   // this CTA's slice (HELD: padded with -inf to kWarps * cs)
+  int n_loc;           // its logits
+  bool vec;            // its address is 16-byte aligned
   int cs;              // logits per warp (a multiple of 128)
   int base;            // index of the slice's first logit
   int nc, rank;        // CTAs of the cluster, this one's rank
@@ -206,8 +296,24 @@ struct Row {
   Weights w;
 
   __device__ void barrier() const {
-    if (nc > 1) cluster_sync();
+    if (HELD && nc > 1) cluster_sync();
     else __syncthreads();
+  }
+
+  // Four logits from slice offset o on; -0 as +0, so that the zeros tie.
+  __device__ __forceinline__ float4 four(int o) const {
+    if constexpr (HELD) return *reinterpret_cast<const float4*>(vals + o);
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (vec && o + 3 < n_loc) {
+      v = __ldg(reinterpret_cast<const float4*>(vals + o));
+    } else {
+      if (o < n_loc) v.x = __ldg(vals + o);
+      if (o + 1 < n_loc) v.y = __ldg(vals + o + 1);
+      if (o + 2 < n_loc) v.z = __ldg(vals + o + 2);
+      if (o + 3 < n_loc) v.w = __ldg(vals + o + 3);
+    }
+    v.x += 0.f, v.y += 0.f, v.z += 0.f, v.w += 0.f;
+    return v;
   }
 
   // Sums of two values and the least and largest of two keys, over the
@@ -270,17 +376,35 @@ struct Row {
     par ^= 1;
   }
 
-  // Calls f(z, index) for this thread's logits; a warp's 128 logits at a time.
+  // Calls f(four logits, index of the first) for this thread's logits; a warp's
+  // 128 at a time, the next on their way.
+  template <typename F>
+  __device__ __forceinline__ void each4(F f) const {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int end = (warp + 1) * cs;
+    int o = warp * cs + lane * 4;
+    if constexpr (HELD) {
+      for (; o < end; o += 128) f(four(o), base + o);
+    } else {
+      for (; o + 3 * 128 < end; o += 4 * 128) {
+        const float4 v0 = four(o), v1 = four(o + 128), v2 = four(o + 256), v3 = four(o + 384);
+        f(v0, base + o);
+        f(v1, base + o + 128);
+        f(v2, base + o + 256);
+        f(v3, base + o + 384);
+      }
+      for (; o < end; o += 128) f(four(o), base + o);
+    }
+  }
+  // Calls f(z, index) for each of them.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int o = warp * cs + lane * 4; o < (warp + 1) * cs; o += 128) {
-      const float4 v = *reinterpret_cast<const float4*>(vals + o);
-      f(v.x, base + o);
-      f(v.y, base + o + 1);
-      f(v.z, base + o + 2);
-      f(v.w, base + o + 3);
-    }
+    each4([&](const float4& v, int i) {
+      f(v.x, i);
+      f(v.y, i + 1);
+      f(v.z, i + 2);
+      f(v.w, i + 3);
+    });
   }
 
   // Inclusive scan over the threads of the CTA.
@@ -336,7 +460,7 @@ struct Row {
     if (need > sh->wred[warp][0]) return false;
     // this warp's: 128 logits at a time
     for (int o = warp * cs + lane * 4; o < (warp + 1) * cs; o += 128) {
-      const float4 v = *reinterpret_cast<const float4*>(vals + o);
+      const float4 v = four(o);
       const float zs[4] = {v.x, v.y, v.z, v.w};
       u64 x[4], sum = 0;
 #pragma unroll
@@ -395,39 +519,37 @@ struct Row {
 
   // The border of a prefix in (key descending, index ascending) order: the
   // token at which the running sum (of counts, or of masses) reaches `need`,
-  // among the n candidates, the logits whose t lies in bins [b_lo, b_hi] and
-  // that in(z, index) admits; `above` is the sum before them.  [lo, hi] bounds
-  // their keys where have_keys says so.
+  // among n candidates; `above` is the sum before them.  The candidates are the
+  // logits with keys in [lo, hi] that in(z, index) admits, or, `aside`, what the
+  // CTAs hold in cand_order, cand_w (masses only).
   template <bool MASS, typename In>
-  __device__ Border border(int b_lo, int b_hi, unsigned n, bool have_keys, unsigned lo, unsigned hi, u64 need,
-                           u64 above, In in) {
+  __device__ Border border(unsigned n, unsigned lo, unsigned hi, u64 need, u64 above, bool aside, In in) {
     const int tid = threadIdx.x;
-    if (n > kList && !have_keys) {
-      lo = ~0u;
-      hi = 0;
-      each([&](float z, int i) {
-        const int b = bin_of(w, z);
-        if (b < b_lo || b > b_hi || !in(z, i)) return;
-        const unsigned key = key_of(z);
-        lo = min(lo, key);
-        hi = max(hi, key);
-      });
-      u64 z0 = 0, z1 = 0;
-      reduce(z0, z1, lo, hi);
-      have_keys = true;
-    }
+    // f(order, weight) for this CTA's candidates with keys in [lo, hi]
+    auto candidates = [&](auto f) {
+      if (aside) {
+        for (unsigned j = tid; j < sh->cand_n; j += kThreads) {
+          const u64 o = cand_order[j];
+          const unsigned key = ~static_cast<unsigned>(o >> 32);
+          if (key >= lo && key <= hi) f(o, cand_w[j]);
+        }
+      } else {
+        each([&](float z, int i) {
+          const unsigned key = key_of(z);
+          if (key < lo || key > hi || !in(z, i)) return;
+          f(order_of(key, i), MASS ? weight_of(w, z) : 1ull);
+        });
+      }
+    };
     while (n > kList && lo < hi) {
       const int shift = max(0, 32 - __clz(hi - lo) - 8);
       if (tid < kKeyBins) sh->keys[0][tid] = sh->keys[1][tid] = sh->keys[2][tid] = sh->keys[3][tid] = 0;
       if (tid == 0) sh->found = -1;
       __syncthreads();
-      each([&](float z, int i) {
-        const unsigned k = key_of(z);
-        if (k < lo || k > hi || !in(z, i)) return;
-        const unsigned b = (hi - k) >> shift;
+      candidates([&](u64 o, u64 x) {
+        const unsigned b = (hi - ~static_cast<unsigned>(o >> 32)) >> shift;
         atomicAdd(&sh->keys[0][b], 1u);
         if (MASS) {
-          const u64 x = weight_of(w, z);
           atomicAdd(&sh->keys[1][b], static_cast<unsigned>(x) & 0xFFFFu);
           atomicAdd(&sh->keys[2][b], static_cast<unsigned>(x) >> 16);
           atomicAdd(&sh->keys[3][b], static_cast<unsigned>(x >> 32));
@@ -471,48 +593,42 @@ struct Row {
     // ---- the list, in rank 0's shared memory
     u64* orders = sh->list;
     u64* weights = sh->list + kList;
-    each([&](float z, int i) {
-      const unsigned key = key_of(z);
-      if (have_keys) {
-        if (key < lo || key > hi) return;
-      } else {
-        const int b = bin_of(w, z);
-        if (b < b_lo || b > b_hi) return;
-      }
-      if (!in(z, i)) return;
-      const u64 x = MASS ? weight_of(w, z) : 1;
+    candidates([&](u64 o, u64 x) {
       if (nc > 1) {
         const unsigned at = add_cluster_u32(&sh->list_n, 0, 1);
         if (at < kList) {
-          st_cluster_u64(&orders[at], 0, order_of(key, i));
+          st_cluster_u64(&orders[at], 0, o);
           st_cluster_u64(&weights[at], 0, x);
         }
       } else {
         const unsigned at = atomicAdd(&sh->list_n, 1u);
         if (at < kList) {
-          orders[at] = order_of(key, i);
+          orders[at] = o;
           weights[at] = x;
         }
       }
     });
     barrier();
     if (rank == 0) {
-      // two threads per candidate, each summing half of what precedes it
-      static_assert(kThreads == 2 * kList, "two threads per candidate");
+      // TPC threads per candidate, each summing a part of what precedes it
+      constexpr int TPC = kThreads / kList;
       const unsigned cnt = min(sh->list_n, static_cast<unsigned>(kList));
-      const int c = tid / 2;
+      const int c = tid / TPC;
       const bool on = c < static_cast<int>(cnt);
       const u64 mine = on ? orders[c] : 0, wm = on ? weights[c] : 0;
       u64 before = 0, all = 0;
-      for (unsigned j = tid % 2; j < cnt; j += 2) {
+      for (unsigned j = tid % TPC; j < cnt; j += TPC) {
         const u64 x = weights[j];
         all += x;
         before += orders[j] < mine ? x : 0;
       }
-      before += shfl_xor64(before, 1);
-      all += shfl_xor64(all, 1);
+#pragma unroll
+      for (int o = TPC / 2; o > 0; o >>= 1) {
+        before += shfl_xor64(before, o);
+        all += shfl_xor64(all, o);
+      }
       // the first to reach `need`, or the last of all
-      if (on && tid % 2 == 0 && above + before < need && (above + before + wm >= need || before + wm == all)) {
+      if (on && tid % TPC == 0 && above + before < need && (above + before + wm >= need || before + wm == all)) {
         const unsigned bk = ~static_cast<unsigned>(mine >> 32), bi = static_cast<unsigned>(mine);
         for (int r = 0; r < nc; ++r) {
           if (nc > 1) {
@@ -532,20 +648,24 @@ struct Row {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kThreads, bool HELD>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     sample_filtered_kernel(const __grid_constant__ SampleFilteredParams p,
                            const __grid_constant__ WeightTable table, int nc, int slice, int cs) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared* sh = reinterpret_cast<Shared*>(smem);
-  float* vals = reinterpret_cast<float*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+  u64* cand = reinterpret_cast<u64*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+  float* vals = reinterpret_cast<float*>(cand + 2 * Row<kThreads, HELD>::kCand);
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int row = blockIdx.x / nc, rank = blockIdx.x % nc;
   const int V = p.vocab;
 
-  Row R;
+  Row<kThreads, HELD> R;
+  constexpr int BPT = Row<kThreads, HELD>::BPT;
   R.sh = sh;
-  R.vals = vals;
+  R.cand_order = cand;
+  R.cand_w = cand + R.kCand;
   R.cs = cs;
   R.base = rank * slice;
   R.nc = nc;
@@ -553,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   R.par = 0;
   if (tid < 64) sh->tab[tid] = table.e[tid];
   if (tid == 0) sh->list_n = 0;
+  if (tid < kMaxWarps) sh->wadd[tid] = 0;
   griddep_wait();
 
   // ---- settings (used after the first reduction)
@@ -562,44 +683,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float mp = p.min_p != nullptr ? p.min_p[row] : 0.f;
   const double a = p.a[row];
 
-  // ---- the slice to shared memory; -0 becomes +0, so that the zeros tie
-  const int n_loc = max(0, min(slice, V - rank * slice));
-  const float* src = p.logits + row * p.ld + static_cast<int64_t>(rank) * slice;
-  const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  // ---- the logits' maximum, and the slice to shared memory
+  R.n_loc = max(0, min(slice, V - rank * slice));
+  R.vals = p.logits + row * p.ld + static_cast<int64_t>(rank) * slice;
+  R.vec = (reinterpret_cast<uintptr_t>(R.vals) & 15) == 0;
   float mx = -INFINITY;
   unsigned finite = 0;
   bool bad = false;
-  auto put = [&](int o, float4 v) {
-    v.x += 0.f, v.y += 0.f, v.z += 0.f, v.w += 0.f;
-    *reinterpret_cast<float4*>(vals + o) = v;
+  Row<kThreads, false> src;
+  src.vals = R.vals;
+  src.n_loc = R.n_loc;
+  src.vec = R.vec;
+  src.cs = cs;
+  src.base = 0;
+  src.each4([&](const float4& v, int o) {
+    if constexpr (HELD) *reinterpret_cast<float4*>(vals + o) = v;
     bad |= !(v.x <= FLT_MAX && v.y <= FLT_MAX && v.z <= FLT_MAX && v.w <= FLT_MAX);
     mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
     finite += (v.x > -INFINITY) + (v.y > -INFINITY) + (v.z > -INFINITY) + (v.w > -INFINITY);
-  };
-  auto get = [&](int o) {
-    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (vec && o + 3 < n_loc) {
-      v = __ldcs(reinterpret_cast<const float4*>(src + o));
-    } else {
-      if (o < n_loc) v.x = __ldcs(src + o);
-      if (o + 1 < n_loc) v.y = __ldcs(src + o + 1);
-      if (o + 2 < n_loc) v.z = __ldcs(src + o + 2);
-      if (o + 3 < n_loc) v.w = __ldcs(src + o + 3);
-    }
-    return v;
-  };
-  {
-    const int end = (warp + 1) * cs;
-    int o = warp * cs + lane * 4;
-    for (; o + 3 * 128 < end; o += 4 * 128) {  // four loads in flight
-      const float4 v0 = get(o), v1 = get(o + 128), v2 = get(o + 256), v3 = get(o + 384);
-      put(o, v0);
-      put(o + 128, v1);
-      put(o + 256, v2);
-      put(o + 384, v3);
-    }
-    for (; o < end; o += 128) put(o, get(o));
-  }
+  });
+  if constexpr (HELD) R.vals = vals;
   if (tid == 0) {
     // log2(e)/T as a float pair: the quotient, then that of its remainder
     const float t = fmaxf(T, 1e-30f);
@@ -676,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // a top-p border that decides: the mass of what this thread keeps for sure,
   // and the bins that hold the rest
   u64 sure = 0;
+  bool aside = true;
   int p_lo = kBins, p_hi = -1;
   if (use_k || use_p) {
     // ---- counts by t
@@ -690,19 +794,30 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     });
     R.barrier();
-    unsigned cnt[2] = {0, 0};
-    float dist[2] = {0.f, 0.f};
-    for (int r = 0; r < nc; ++r) {
-      const u64 c = nc > 1 ? ld_cluster_u64(&sh->hist[2 * tid], r) : *reinterpret_cast<const u64*>(&sh->hist[2 * tid]);
-      const u64 d = nc > 1 ? ld_cluster_u64(&sh->dist[2 * tid], r) : *reinterpret_cast<const u64*>(&sh->dist[2 * tid]);
-      cnt[0] += static_cast<unsigned>(c);
-      cnt[1] += static_cast<unsigned>(c >> 32);
-      dist[0] += static_cast<float>(static_cast<unsigned>(d));
-      dist[1] += static_cast<float>(static_cast<unsigned>(d >> 32));
+    unsigned cnt[BPT], cum[BPT];
+    float dist[BPT];
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+      cnt[j] = 0;
+      dist[j] = 0.f;
     }
-    unsigned cum[2];
-    cum[1] = static_cast<unsigned>(R.scan(cnt[0] + cnt[1]));
-    cum[0] = cum[1] - cnt[1];
+    if constexpr (BPT == 2) {
+      for (int r = 0; r < nc; ++r) {
+        const u64 c = nc > 1 ? ld_cluster_u64(&sh->hist[2 * tid], r) : *reinterpret_cast<const u64*>(&sh->hist[2 * tid]);
+        const u64 d = nc > 1 ? ld_cluster_u64(&sh->dist[2 * tid], r) : *reinterpret_cast<const u64*>(&sh->dist[2 * tid]);
+        cnt[0] += static_cast<unsigned>(c);
+        cnt[1] += static_cast<unsigned>(c >> 32);
+        dist[0] += static_cast<float>(static_cast<unsigned>(d));
+        dist[1] += static_cast<float>(static_cast<unsigned>(d >> 32));
+      }
+    } else {
+      cnt[0] = sh->hist[tid];
+      dist[0] = static_cast<float>(sh->dist[tid]);
+    }
+    unsigned all = cnt[0];
+    if constexpr (BPT == 2) all += cnt[1];
+    cum[BPT - 1] = static_cast<unsigned>(R.scan(all));
+    if constexpr (BPT == 2) cum[0] = cum[1] - cnt[1];
     if (tid == 0) sh->found = -1;
     __syncthreads();
 
@@ -712,9 +827,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (use_k) {
       const unsigned ku = k;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < BPT; ++j)
         if (cnt[j] > 0 && cum[j] >= ku && cum[j] - cnt[j] < ku) {
-          sh->found = 2 * tid + j;
+          sh->found = BPT * tid + j;
           sh->found_n = cnt[j];
           sh->before = cum[j] - cnt[j];
         }
@@ -725,7 +840,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       if (f >= 0) {
         k_bin = f;
-        bk = R.border<false>(f, f, fn, false, 0, 0, ku, before, [](float, int) { return true; });
+        // the keys of its tokens
+        unsigned lo = ~0u, hi = 0;
+        R.each([&](float z, int) {
+          if (bin_of(R.w, z) != f) return;
+          lo = min(lo, key_of(z));
+          hi = max(hi, key_of(z));
+        });
+        u64 z0 = 0, z1 = 0;
+        R.reduce(z0, z1, lo, hi);
+        bk = R.template border<false>(fn, lo, hi, ku, before, false, [](float, int) { return true; });
       }
     }
     auto in_k = [&](float z, int i) {
@@ -741,11 +865,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       // n (c/2)^2 / 2 = 1.2e-4 n; the sum's quantisation and fp32 are far below.
       // K's last step, of which only a part counts, by its edges.
       constexpr float step = kMaxLog2 / (kBins - 1), c = step * 0.69314718f;
-      float low[2], high[2];
-      unsigned part[2];
+      float low[BPT], high[BPT], li = 0.f, hi_ = 0.f;
+      unsigned part[BPT];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = 2 * tid + j;
+      for (int j = 0; j < BPT; ++j) {
+        const int b = BPT * tid + j;
         const float mid = exp2f(-b * step);
         part[j] = b < k_bin ? cnt[j] : 0;
         low[j] = fmaf(-c, dist[j] * (1.f / 16384.f) - 0.5f * cnt[j], static_cast<float>(cnt[j])) * mid * (1.f - 3e-5f);
@@ -756,40 +880,44 @@ __global__ void __launch_bounds__(kThreads, 2)
           low[j] = part[j] * mid * (1.f - 0.5f * c);
           high[j] = part[j] * mid * (1.f + 0.51f * c);
         }
+        li += low[j];
+        hi_ += high[j];
       }
-      float li = low[0] + low[1], hi_ = high[0] + high[1];
       R.scan2f(li, hi_);
       if (tid == kThreads - 1) {
-        sh->f0[0] = li;
-        sh->f1[0] = hi_;
+        sh->tot0 = li;
+        sh->tot1 = hi_;
         sh->b_lo = sh->b_hi = kBins - 2;
+        sh->found_n = 0;
+        sh->cand_n = 0;
       }
       __syncthreads();
       const float q = fmaxf(tp, 0.f);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float l = j ? li : li - low[1], h = j ? hi_ : hi_ - high[1];
-        if (part[j] > 0 && h * (1.f + 1e-5f) >= q * sh->f0[0]) atomicMin(&sh->b_lo, 2 * tid + j);
-        if (part[j] > 0 && l >= q * sh->f1[0] * (1.f + 1e-5f)) atomicMin(&sh->b_hi, 2 * tid + j);
+      for (int j = BPT - 1; j >= 0; --j) {
+        if (part[j] > 0 && hi_ * (1.f + 1e-5f) >= q * sh->tot0) atomicMin(&sh->b_lo, BPT * tid + j);
+        if (part[j] > 0 && li >= q * sh->tot1 * (1.f + 1e-5f)) atomicMin(&sh->b_hi, BPT * tid + j);
+        li -= low[j];
+        hi_ -= high[j];
       }
-      if (tid == 0) sh->found_n = 0;
       __syncthreads();
       p_lo = sh->b_lo;
       p_hi = sh->b_hi;
-      // the candidates, by count
+      // the candidates, by count, and the tokens above them
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (2 * tid + j >= p_lo && 2 * tid + j <= p_hi && part[j] > 0) atomicAdd(&sh->found_n, part[j]);
+      for (int j = 0; j < BPT; ++j) {
+        const int b = BPT * tid + j;
+        if (b >= p_lo && b <= p_hi && part[j] > 0) atomicAdd(&sh->found_n, part[j]);
+        if (b == p_lo) sh->above_n = cum[j] - cnt[j];
+      }
       __syncthreads();
       const unsigned n_cand = sh->found_n;
       __syncthreads();
-      // K's mass, and the mass above the bins in question
+      // K's mass, and the mass above the steps in question; their tokens go aside
       u64 M = 0, A = 0;
       unsigned lo = ~0u, hi = 0;
-      R.each([&](float z, int i) {
-        const int b = bin_of(R.w, z);
-        if (b >= kBins - 1 || !in_k(z, i)) return;
-        const u64 x = weight_of(R.w, z);
+      bool overflow = false;
+      auto take = [&](float z, int i, int b, u64 x) {
         M += x;
         if (b < p_lo) {
           A += x;
@@ -797,14 +925,40 @@ __global__ void __launch_bounds__(kThreads, 2)
           const unsigned key = key_of(z);
           lo = min(lo, key);
           hi = max(hi, key);
+          const unsigned at = atomicAdd(&sh->cand_n, 1u);
+          if (at < R.kCand) {
+            R.cand_order[at] = order_of(key, i);
+            R.cand_w[at] = x;
+          } else {
+            overflow = true;
+          }
         }
+      };
+      auto pair = [&](float z0, float z1, int i) {
+        const int b0 = bin_of(R.w, z0), b1 = bin_of(R.w, z1);
+        const bool t0 = b0 < kBins - 1 && in_k(z0, i), t1 = b1 < kBins - 1 && in_k(z1, i + 1);
+        if (!t0 && !t1) return;
+        u64 x0, x1;
+        weight_of2(R.w, t0 ? z0 : m, t1 ? z1 : m, &x0, &x1);
+        if (t0) take(z0, i, b0, x0);
+        if (t1) take(z1, i + 1, b1, x1);
+      };
+      R.each4([&](const float4& v4, int i) {
+        pair(v4.x, v4.y, i);
+        pair(v4.z, v4.w, i + 2);
       });
       sure = A;
       R.reduce(M, A, lo, hi);
+      if (n_cand > R.kCand) {  // some CTA may have had more than it can keep aside
+        u64 spilt = overflow ? 1 : 0, zero = 0;
+        unsigned none_lo = 0, none_hi = 0;
+        R.reduce(spilt, zero, none_lo, none_hi);
+        aside = spilt == 0;
+      }
       u64 need = static_cast<u64>(ceil(static_cast<double>(q) * static_cast<double>(M)));
       if (need > M) need = M;
       if (need <= A) need = A + 1;
-      if (!narrow(R.border<true>(p_lo, p_hi, n_cand, true, lo, hi, need, A, in_k))) p_lo = kBins;
+      if (!narrow(R.template border<true>(n_cand, lo, hi, need, A, aside, in_k))) p_lo = kBins;
     }
   }
   const bool by_p = p_lo < kBins;  // top-p's border is the kept set's
@@ -816,15 +970,42 @@ __global__ void __launch_bounds__(kThreads, 2)
     return weight_of(R.w, z);
   };
   u64 mine = by_p ? sure : 0, kept = 0;
-  R.each([&](float z, int i) {
-    const unsigned key = key_of(z);
-    if (z > -INFINITY && (key > v || (key == v && i <= vi))) {
-      ++kept;
-      const int b = bin_of(R.w, z);
-      // by_p: what lies above p_lo is in `sure` already, nothing below p_hi is kept
-      if (b < kBins - 1 && (!by_p || b >= p_lo)) mine += weight_of(R.w, z);
+  if (by_p && aside) {
+    // what lies above p_lo is in `sure` already, nothing below p_hi is kept, and
+    // the rest is aside
+    if (rank == 0 && tid == 0) kept = sh->above_n;
+    for (unsigned j = tid; j < sh->cand_n; j += kThreads) {
+      const u64 o = R.cand_order[j];
+      const unsigned key = ~static_cast<unsigned>(o >> 32);
+      const int i = static_cast<int>(static_cast<unsigned>(o));
+      if (key > v || (key == v && i <= vi)) {
+        ++kept;
+        atomicAdd(&sh->wadd[(i - R.base) / cs], R.cand_w[j]);
+      }
     }
-  });
+    __syncthreads();
+    if (lane == 0) mine += sh->wadd[warp];
+  } else {
+    R.each4([&](const float4& v4, int i) {
+      const float zs[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        bool take[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const unsigned key = key_of(zs[j + t]);
+          const bool in = zs[j + t] > -INFINITY && (key > v || (key == v && i + j + t <= vi));
+          kept += in;
+          const int b = bin_of(R.w, zs[j + t]);
+          take[t] = in && b < kBins - 1 && (!by_p || b >= p_lo);
+        }
+        if (!take[0] && !take[1]) continue;
+        u64 x0, x1;
+        weight_of2(R.w, take[0] ? zs[j] : m, take[1] ? zs[j + 1] : m, &x0, &x1);
+        mine += (take[0] ? x0 : 0) + (take[1] ? x1 : 0);
+      }
+    });
+  }
   const int buf = R.par;
   u64 S = mine;
   unsigned none0 = 0, none1 = 0;
@@ -866,19 +1047,16 @@ const WeightTable& weight_table() {
 
 }  // namespace
 
-cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s) {
-  // CTAs per row: a slice of at most kSlice logits, so that two CTAs fit an SM;
-  // more (down to kMinSlice logits) while the rows leave SMs without work
-  constexpr int kSlice = 24576, kMinSlice = 4096, kResident = 2 * 152;
-  int nc = 1;
-  while (nc < kMaxCluster && ((p.vocab + nc - 1) / nc > kSlice ||
-                              (2 * nc * p.rows <= kResident && p.vocab / (2 * nc) >= kMinSlice)))
-    nc *= 2;
+template <int kThreads, bool HELD>
+static cudaError_t launch_sample(const SampleFilteredParams& p, int nc, cudaStream_t s) {
+  constexpr int kWarps = kThreads / 32;
   const int slice = ((p.vocab + nc - 1) / nc + 3) / 4 * 4;
   const int cs = (slice + kWarps * 128 - 1) / (kWarps * 128) * 128;
-  const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(kWarps) * cs * 4;
+  const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + 16 * Row<kThreads, HELD>::kCand +
+                      (HELD ? static_cast<size_t>(kWarps) * cs * 4 : 0);
   static thread_local int allowed = -1;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sample_filtered_kernel), 227 * 1024, &allowed);
+  const cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(sample_filtered_kernel<kThreads, HELD>), 227 * 1024, &allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -895,7 +1073,20 @@ cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, sample_filtered_kernel, p, weight_table(), nc, slice, cs);
+  return cudaLaunchKernelEx(&cfg, sample_filtered_kernel<kThreads, HELD>, p, weight_table(), nc, slice, cs);
+}
+
+cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s) {
+  // CTAs per row: a slice of at most kSlice logits, so that two CTAs fit an SM;
+  // more (down to kMinSlice logits) while the rows leave SMs without work
+  constexpr int kSlice = 20480, kMinSlice = 4096, kResident = 2 * 152;
+  int nc = 1;
+  while (nc < kMaxCluster && ((p.vocab + nc - 1) / nc > kSlice ||
+                              (2 * nc * p.rows <= kResident && p.vocab / (2 * nc) >= kMinSlice)))
+    nc *= 2;
+  // more clusters than fit at once: see above
+  if (nc > 1 && nc * p.rows > kResident) return launch_sample<1024, false>(p, 1, s);
+  return launch_sample<512, true>(p, nc, s);
 }
 
 }  // namespace dflash
