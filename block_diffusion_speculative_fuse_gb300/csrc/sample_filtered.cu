@@ -58,7 +58,7 @@ constexpr int kMaxCluster = 8;
 static_assert(kMaxSampleVocab / kMaxCluster * 4 + 28672 <= 227 * 1024, "a slice fits shared memory");
 
 struct Shared {
-  float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(45-j/64) in two words
+  float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(46-j/64) in two words
   u64 list[2 * kList];               // candidates: orders, weights
   unsigned hist[kBins];
   unsigned dist[kBins];              // sums of (distance + 1/2) * 2^14
@@ -95,9 +95,9 @@ struct Weights {
   int extra;                         // 1: 44 fractional bits
 };
 
-// increasing integer key of a float (no NaN)
+// increasing integer key of a float (no NaN); -0 and +0 share one
 __device__ __forceinline__ unsigned key_of(float z) {
-  const unsigned u = __float_as_uint(z);
+  const unsigned u = __float_as_uint(z + 0.f);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float of_key(unsigned k) {
@@ -112,17 +112,37 @@ __device__ __forceinline__ int magic_int(float x_plus_magic) {
   return __float_as_int(x_plus_magic) - 0x4B400000;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kLastStep = kMagic + (kBins - 2);
 // The step of t nearest to the logit's, non-decreasing as z falls; *dist = how
 // far past the step's middle, in steps.
 __device__ __forceinline__ int bin_of(const Weights& w, float z, float* dist) {
-  const float x = __fmul_rn(w.m - z, w.scale);  // (never contracted: every pass has the same steps)
-  const float k = __fadd_rn(x, kMagic);
-  *dist = x - (k - kMagic);
-  return x < kBins - 1.5f ? magic_int(k) : kBins - 1;
+  const float dh = w.m - z;
+  const float k = fmaf(dh, w.scale, kMagic);  // one rounding: every pass has the same steps
+  *dist = fmaf(dh, w.scale, kMagic - k);
+  return k <= kLastStep ? magic_int(k) : kBins - 1;
 }
 __device__ __forceinline__ int bin_of(const Weights& w, float z) {
   float dist;
   return bin_of(w, z, &dist);
+}
+
+__device__ __forceinline__ long long mad_wide(int a, int b, long long c) {
+  long long r;
+  asm("mad.wide.s32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(b), "l"(c));
+  return r;
+}
+// The table's 46-bit integer plus the two corrections (as magic sums, of units
+// 2^-29 and 2^-37), times 2^-n, rounded to 45 fractional bits.
+__device__ __forceinline__ u64 join_weight(const float4& tj, float ax, float bx, int n) {
+  const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
+  const long long R = mad_wide(magic_int(bx), 1 << 9, mad_wide(magic_int(ax), 1 << 17, static_cast<long long>(fix)));
+  return ((static_cast<u64>(R) >> n) + 1) >> 1;
 }
 
 // the weight of logit z <= m, not in the tail (no product is contracted with a
@@ -147,10 +167,9 @@ __device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
   float ul = fmaf(r, LH, -uh);
   ul = fmaf(r, LL, ul);
   ul = fmaf(e, LH, ul);
-  const float s = __fmul_rn(__fmul_rn(uh, uh), fmaf(uh, fmaf(uh, 1.f / 24.f, 1.f / 6.f), 0.5f));
-  const float tail = __fadd_rn(s, fmaf(uh, ul, ul));  // exp(u) - 1 = uh + tail
+  const float tail = fmaf(__fmul_rn(uh, uh), fmaf(uh, fmaf(uh, 1.f / 24.f, 1.f / 6.f), 0.5f),
+                          fmaf(uh, ul, ul));  // exp(u) - 1 = uh + tail
   const float4 tj = w.tab[k & 63];
-  const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
   const float ph = __fmul_rn(tj.x, uh);               // below 2^-7
   float low = fmaf(tj.x, uh, -ph);
   low = fmaf(tj.y, uh, low);
@@ -158,11 +177,7 @@ __device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
   // to integers: ph in units of 2^-29 (what that leaves goes to low), low of 2^-37
   const float ax = fmaf(ph, 0x1p29f, kMagic);
   low += fmaf(ax - kMagic, -0x1p-29f, ph);
-  const int bx = magic_int(fmaf(low, 0x1p37f, kMagic));
-  const long long R = static_cast<long long>(fix) + (static_cast<long long>(magic_int(ax)) << 16) +
-                      static_cast<long long>(bx * 256);
-  const int n = (k >> 6) + w.extra;
-  return (static_cast<u64>(R) + ((1ull << n) >> 1)) >> n;
+  return join_weight(tj, ax, fmaf(low, 0x1p37f, kMagic), (k >> 6) + w.extra);
 }
 
 // Two fp32 operations in one instruction.
@@ -191,7 +206,9 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// weight_of for two logits, operation by operation the same
+// weight_of for two logits, to the same bits: a packed product that only a sum
+// uses is fused with it by the compiler, so where that would round differently
+// both write the fma.
 __device__ __forceinline__ void weight_of2(const Weights& w, float z0, float z1, u64* w0, u64* w1) {
   const F2 neg = f2(-1.f, -1.f), m = f2(w.m, w.m), z = f2(z0, z1), ch = f2(w.ch, w.ch), cl = f2(w.cl, w.cl);
   const F2 magic = f2(kMagic, kMagic), unmagic = f2(-kMagic, -kMagic);
@@ -212,8 +229,8 @@ __device__ __forceinline__ void weight_of2(const Weights& w, float z0, float z1,
   F2 ul = fma(r, lh, mul(uh, neg));
   ul = fma(r, f2(LL, LL), ul);
   ul = fma(e, lh, ul);
-  const F2 s = mul(mul(uh, uh), fma(uh, fma(uh, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f)));
-  const F2 tail = add(s, fma(uh, ul, ul));
+  const F2 tail = fma(mul(uh, uh), fma(uh, fma(uh, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f)),
+                      fma(uh, ul, ul));
   float k0, k1;
   un2(kx, k0, k1);
   const int ka = magic_int(k0), kb = magic_int(k1);
@@ -229,15 +246,8 @@ __device__ __forceinline__ void weight_of2(const Weights& w, float z0, float z1,
   float a0, a1, b0, b1;
   un2(ax, a0, a1);
   un2(bx, b0, b1);
-  auto join = [&](const float4& tj, float a, float b, int k) {
-    const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
-    const long long R = static_cast<long long>(fix) + (static_cast<long long>(magic_int(a)) << 16) +
-                        static_cast<long long>(magic_int(b) * 256);
-    const int n = (k >> 6) + w.extra;
-    return (static_cast<u64>(R) + ((1ull << n) >> 1)) >> n;
-  };
-  *w0 = join(ta, a0, b0, ka);
-  *w1 = join(tb, a1, b1, kb);
+  *w0 = join_weight(ta, a0, b0, (ka >> 6) + w.extra);
+  *w1 = join_weight(tb, a1, b1, (kb >> 6) + w.extra);
 }
 
 __device__ __forceinline__ u64 shfl_xor64(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
@@ -300,7 +310,7 @@ struct Row {
     else __syncthreads();
   }
 
-  // Four logits from slice offset o on; -0 as +0, so that the zeros tie.
+  // Four logits from slice offset o on.
   __device__ __forceinline__ float4 four(int o) const {
     if constexpr (HELD) return *reinterpret_cast<const float4*>(vals + o);
     float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
@@ -312,7 +322,6 @@ struct Row {
       if (o + 2 < n_loc) v.z = __ldg(vals + o + 2);
       if (o + 3 < n_loc) v.w = __ldg(vals + o + 3);
     }
-    v.x += 0.f, v.y += 0.f, v.z += 0.f, v.w += 0.f;
     return v;
   }
 
@@ -687,9 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   R.n_loc = max(0, min(slice, V - rank * slice));
   R.vals = p.logits + row * p.ld + static_cast<int64_t>(rank) * slice;
   R.vec = (reinterpret_cast<uintptr_t>(R.vals) & 15) == 0;
-  float mx = -INFINITY;
-  unsigned finite = 0;
-  bool bad = false;
+  float mx = -INFINITY;  // NaN as soon as one logit is
   Row<kThreads, false> src;
   src.vals = R.vals;
   src.n_loc = R.n_loc;
@@ -698,9 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   src.base = 0;
   src.each4([&](const float4& v, int o) {
     if constexpr (HELD) *reinterpret_cast<float4*>(vals + o) = v;
-    bad |= !(v.x <= FLT_MAX && v.y <= FLT_MAX && v.z <= FLT_MAX && v.w <= FLT_MAX);
-    mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-    finite += (v.x > -INFINITY) + (v.y > -INFINITY) + (v.z > -INFINITY) + (v.w > -INFINITY);
+    mx = max_nan(mx, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
   });
   if constexpr (HELD) R.vals = vals;
   if (tid == 0) {
@@ -714,12 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     sh->scale = ch * ((kBins - 1) / kMaxLog2);
   }
   R.barrier();  // every CTA of the cluster runs before its shared memory is written
-  u64 n_fin = finite, n_bad = bad ? 1 : 0;
-  unsigned least = 0, top = key_of(mx);
-  R.reduce(n_fin, n_bad, least, top);
+  u64 nans = mx != mx ? 1 : 0, none = 0;
+  unsigned least = 0, top = mx != mx ? 0 : key_of(mx);
+  R.reduce(nans, none, least, top);
   const float m = of_key(top);
 
-  if (!(T >= 0.f && T <= FLT_MAX) || tp != tp || mp != mp || !(a >= 0.0 && a < 1.0) || n_fin == 0 || n_bad != 0) {
+  if (!(T >= 0.f && T <= FLT_MAX) || tp != tp || mp != mp || !(a >= 0.0 && a < 1.0) || nans != 0 ||
+      !(m >= -FLT_MAX && m <= FLT_MAX)) {
     if (rank == 0 && tid == 0) {
       p.token[row] = -1;
       if (p.n_kept != nullptr) p.n_kept[row] = 0;
@@ -774,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
     return false;
   };
-  const bool use_k = k > 0 && static_cast<u64>(k) < n_fin;
+  const bool use_k = k > 0 && k < V;
   const bool use_p = tp < 1.f;
   // a top-p border that decides: the mass of what this thread keeps for sure,
   // and the bins that hold the rest
@@ -917,31 +923,42 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       u64 M = 0, A = 0;
       unsigned lo = ~0u, hi = 0;
       bool overflow = false;
-      auto take = [&](float z, int i, int b, u64 x) {
-        M += x;
-        if (b < p_lo) {
-          A += x;
-        } else if (b <= p_hi) {
-          const unsigned key = key_of(z);
-          lo = min(lo, key);
-          hi = max(hi, key);
-          const unsigned at = atomicAdd(&sh->cand_n, 1u);
-          if (at < R.kCand) {
-            R.cand_order[at] = order_of(key, i);
-            R.cand_w[at] = x;
-          } else {
-            overflow = true;
-          }
+      // steps as bin_of's magic sums, two at a time
+      const float f_lo = kMagic + p_lo, f_hi = kMagic + p_hi;
+      const F2 neg = f2(-1.f, -1.f), m2 = f2(m, m), sc2 = f2(R.w.scale, R.w.scale), magic = f2(kMagic, kMagic);
+      auto put_aside = [&](float z, int i, u64 x) {
+        const unsigned key = key_of(z);
+        lo = min(lo, key);
+        hi = max(hi, key);
+        const unsigned at = atomicAdd(&sh->cand_n, 1u);
+        if (at < R.kCand) {
+          R.cand_order[at] = order_of(key, i);
+          R.cand_w[at] = x;
+        } else {
+          overflow = true;
         }
       };
       auto pair = [&](float z0, float z1, int i) {
-        const int b0 = bin_of(R.w, z0), b1 = bin_of(R.w, z1);
-        const bool t0 = b0 < kBins - 1 && in_k(z0, i), t1 = b1 < kBins - 1 && in_k(z1, i + 1);
+        float f0, f1;
+        un2(fma(fma(f2(z0, z1), neg, m2), sc2, magic), f0, f1);
+        bool t0 = f0 <= kLastStep, t1 = f1 <= kLastStep;
+        if (use_k) {
+          t0 = t0 && in_k(z0, i);
+          t1 = t1 && in_k(z1, i + 1);
+        }
         if (!t0 && !t1) return;
         u64 x0, x1;
         weight_of2(R.w, t0 ? z0 : m, t1 ? z1 : m, &x0, &x1);
-        if (t0) take(z0, i, b0, x0);
-        if (t1) take(z1, i + 1, b1, x1);
+        x0 = t0 ? x0 : 0;
+        x1 = t1 ? x1 : 0;
+        M += x0 + x1;
+        A += (f0 < f_lo ? x0 : 0) + (f1 < f_lo ? x1 : 0);
+        // (rarely) a candidate
+        const bool c0 = t0 && f0 >= f_lo && f0 <= f_hi, c1 = t1 && f1 >= f_lo && f1 <= f_hi;
+        if (c0 || c1) {
+          if (c0) put_aside(z0, i, x0);
+          if (c1) put_aside(z1, i + 1, x1);
+        }
       };
       R.each4([&](const float4& v4, int i) {
         pair(v4.x, v4.y, i);
@@ -1034,7 +1051,7 @@ const WeightTable& weight_table() {
     for (int j = 0; j < 64; ++j) {
       const double e = std::exp2(-j / 64.0);
       const float hi = static_cast<float>(e);
-      const u64 fix = static_cast<u64>(e * 0x1p45 + 0.5);
+      const u64 fix = static_cast<u64>(e * 0x1p46 + 0.5);
       const uint32_t w[2] = {static_cast<uint32_t>(fix), static_cast<uint32_t>(fix >> 32)};
       float f[2];
       std::memcpy(f, w, sizeof(f));
