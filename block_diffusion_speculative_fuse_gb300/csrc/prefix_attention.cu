@@ -57,6 +57,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
   const size_t head_elems = 16 * D;
   const size_t page_elems = static_cast<size_t>(2) * p.hkv * head_elems;
   const int tq = lane % 4, tg = lane / 4;
+  // Shared-memory offsets of a lane.  A page row's 16-byte pieces are permuted by
+  // XOR with the row's low bits; an even step along a row, or whole rows, then
+  // only flips bits of the first offset, or adds to it.
+  constexpr int RPI = 32 / (D / 8);  // rows of a page that one load instruction covers
+  const uint32_t ld_off = swz<D>(lane / (D / 8), lane % (D / 8));
+  const uint32_t k_off = swz<D>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+  const uint32_t v_off = swz<D>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
 
   Segments seg(L, off, ne, worker);
   while (seg.next(p, L, off)) {
@@ -97,31 +104,34 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
     }
 
     // ---- page ids, 32 at a time, one per lane
-    int ids = -1, ids_at = -1;
-    auto page_id = [&](int pg) {
-      if (pg / 32 != ids_at) {
-        ids_at = pg / 32;
-        const int j = ids_at * 32 + lane;
-        ids = j >= pg0 && j < pg1 ? __ldcg(table + j) : 0;
-        if (j >= pg0 && j < pg1 && (ids < 0 || ids >= p.n_pages)) {
+    int ids = 0, left = 0;  // ids not yet used: lanes [32 - left, 32)
+    int pg_ids = pg0;
+    auto page_id = [&]() {
+      if (left == 0) {
+        const int j = pg_ids + lane;
+        ids = j < pg1 ? __ldcg(table + j) : 0;
+        if (ids < 0 || ids >= p.n_pages) {
           raise_status(p.status, DFLASH_ERR_CAPACITY, 521);
           ids = -1;
         }
+        pg_ids += 32;
+        left = 32;
       }
-      return __shfl_sync(0xffffffffu, ids, pg % 32);
+      return __shfl_sync(0xffffffffu, ids, 32 - left--);
     };
-    auto load_page = [&](int pg) {
-      const int id = page_id(pg);
-      const uint16_t* k = p.pool + (id < 0 ? 0 : id) * page_elems + kvh * head_elems;
+    int st_load = 0, st_use = 0;  // ring positions
+    auto load_page = [&]() {
+      const int id = page_id();
+      const uint16_t* k = p.pool + (id < 0 ? 0 : id) * page_elems + kvh * head_elems + lane * 8;
       const uint16_t* v = k + p.hkv * head_elems;
-      const uint32_t st = ring_a + (pg % C::STAGES) * 2 * C::PAGE;
+      const uint32_t st = ring_a + st_load * (2 * C::PAGE);
+      st_load = st_load == C::STAGES - 1 ? 0 : st_load + 1;
       const int bytes = id < 0 ? 0 : 16;
 #pragma unroll
-      for (int i = 0; i < C::PAGE / 512; ++i) {
-        const int pc = i * 32 + lane;                 // 16-byte piece of the page
-        const uint32_t o = swz<D>(pc / (D / 8), pc % (D / 8));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + o), "l"(k + pc * 8), "r"(bytes) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + C::PAGE + o), "l"(v + pc * 8), "r"(bytes) : "memory");
+      for (int i = 0; i < C::PAGE / 512; ++i) {  // 16-byte piece i * 32 + lane of the page
+        const uint32_t o = st + (ld_off ^ ((i * RPI & 7) << 4)) + i * 512;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(o), "l"(k + i * 256), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(o + C::PAGE), "l"(v + i * 256), "r"(bytes) : "memory");
       }
     };
 
@@ -129,77 +139,98 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    // keys that both of this thread's rows see without a mask
+    const int clear = min(min(lim[0], lim[1]), ctx);
 
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) {
-      if (pg0 + s < pg1) load_page(pg0 + s);
+      if (pg0 + s < pg1) load_page();
       cp_async_commit();
     }
     for (int pg = pg0; pg < pg1; ++pg) {
-      if (pg + C::STAGES - 1 < pg1) load_page(pg + C::STAGES - 1);
+      if (pg + C::STAGES - 1 < pg1) load_page();
       cp_async_commit();
       cp_async_wait<C::STAGES - 1>();
       __syncwarp();
-      const uint32_t kb = ring_a + (pg % C::STAGES) * 2 * C::PAGE;
+      const uint32_t kb = ring_a + st_use * (2 * C::PAGE);
       const uint32_t vb = kb + C::PAGE;
+      st_use = st_use == C::STAGES - 1 ? 0 : st_use + 1;
       const int key0 = (page0 + pg) * 16;
-      const bool last = key0 + 16 > ctx;
-      if (last) {
+      if (key0 + 16 > ctx) {
         // rows at or past the context hold whatever was there: 0 * V must be 0
         for (int i = lane; i < 16 * (D / 8); i += 32)
           if (key0 + i / (D / 8) >= ctx) st_shared_u4(vb + swz<D>(i / (D / 8), i % (D / 8)), make_uint4(0u, 0u, 0u, 0u));
         __syncwarp();
       }
-      // S = Q K^T: keys 0-7 and 8-15
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      // S = Q K^T: keys 0-7 and 8-15, each in two independent sums
+      float s[2][2][4];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i / 8][i / 4 % 2][i % 4] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t b0, b1, b2, b3;
-        ldsm_x4(kb + swz<D>((lane & 7) + (lane >> 4) * 8, kk * 2 + ((lane >> 3) & 1)), b0, b1, b2, b3);
-        mma16816(s[0], qf[kk], b0, b1);
-        mma16816(s[1], qf[kk], b2, b3);
+        ldsm_x4(kb + (k_off ^ (kk << 5)), b0, b1, b2, b3);
+        mma16816(s[kk & 1][0], qf[kk], b0, b1);
+        mma16816(s[kk & 1][1], qf[kk], b2, b3);
       }
-      // scale, mask, running maximum of rows tg and tg + 8
-      uint32_t a[4];
-      float alpha[2];
+      // scale, mask, maximum of rows tg and tg + 8
+      float x[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[h][j] = (s[0][j / 2][2 * h + j % 2] + s[1][j / 2][2 * h + j % 2]) * p.scale_log2;
+      if (__any_sync(0xffffffffu, key0 + 16 > clear)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = key0 + (j / 2) * 8 + tq * 2 + j % 2;
+            if (key >= lim[h] || key >= ctx) x[h][j] = -INFINITY;
+          }
+      }
+      float mx[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x[4];
+        mx[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      }
+      // the reference maximum moves, and O and l with it, only when exceeded by
+      // 2^8 (P stays below 2^8; its rounding to bf16 is relative)
+      const bool up0 = mx[0] > m_r[0] + 8.f, up1 = mx[1] > m_r[1] + 8.f;
+      if (__any_sync(0xffffffffu, up0 || up1)) {
+        const float f0 = up0 ? ex2(m_r[0] - mx[0]) : 1.f, f1 = up1 ? ex2(m_r[1] - mx[1]) : 1.f;
+        if (up0) m_r[0] = mx[0];
+        if (up1) m_r[1] = mx[1];
+        l_r[0] *= f0;
+        l_r[1] *= f1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = key0 + (j / 2) * 8 + tq * 2 + j % 2;
-          x[j] = key < lim[h] && key < ctx ? s[j / 2][2 * h + j % 2] * p.scale_log2 : -INFINITY;
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= f0;
+          o[i][1] *= f0;
+          o[i][2] *= f1;
+          o[i][3] *= f1;
         }
-        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m_r[h], mx);
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
-        alpha[h] = ex2(m_r[h] - ref);
+      }
+      uint32_t a[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float ref = m_r[h] == -INFINITY ? 0.f : m_r[h];
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[j] = ex2(x[j] - ref);
-          sum += x[j];
+          x[h][j] = ex2(x[h][j] - ref);
+          sum += x[h][j];
         }
-        l_r[h] = l_r[h] * alpha[h] + sum;  // this thread's keys only
-        m_r[h] = m_new;
-        a[h] = bf16x2(x[0], x[1]);
-        a[2 + h] = bf16x2(x[2], x[3]);
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
-        }
+        l_r[h] += sum;  // this thread's keys only
+        a[h] = bf16x2(x[h][0], x[h][1]);
+        a[2 + h] = bf16x2(x[h][2], x[h][3]);
       }
 #pragma unroll
       for (int nd = 0; nd < D / 8; nd += 2) {
         uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(vb + swz<D>((lane & 7) + ((lane >> 3) & 1) * 8, nd + (lane >> 4)), b0, b1, b2, b3);
+        ldsm_x4_t(vb + (v_off ^ (nd << 4)), b0, b1, b2, b3);
         mma16816(o[nd], a, b0, b1);
         mma16816(o[nd + 1], a, b2, b3);
       }
@@ -228,9 +259,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
 // Joins the partials of each vector (row, query head): WPV warps per vector,
 // warp `sub` taking the partials sub, sub + WPV, ...; the order is fixed.  The
 // bound is the latency of a few dependent loads, so each level of them (the
-// list's offsets, all (m, l), then eight O rows at a time) is issued at once.
+// list's offsets, all (m, l), then four O rows at a time) is issued at once.
 template <int D, int WPV>
-__global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams p) {
   constexpr int VEC = D / 32;  // columns per lane
   __shared__ float so[8][D];
   __shared__ float sml[8][2];
@@ -309,10 +340,10 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[j] *= f0;
       m = mn;
-      for (int j0 = 0; j0 < cnt; j0 += 8) {
-        float v[8][VEC], wj[8];
+      for (int j0 = 0; j0 < cnt; j0 += 4) {
+        float v[4][VEC], wj[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float* src = reinterpret_cast<const float*>(
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (j0 + j) & 31));
           wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
@@ -327,7 +358,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int t = 0; t < VEC; ++t) acc[t] = fmaf(v[j][t], wj[j], acc[t]);
       }

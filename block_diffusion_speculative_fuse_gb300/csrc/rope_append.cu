@@ -13,12 +13,13 @@
 // bits, as a float in half turns, go to sincospif.  The error (2e-7 rad) is
 // that of the conversion to float at any position.
 //
-// Bound: bytes.  Each thread owns two 16-byte pieces (of bf16) of one head
+// Bound: bytes.  Each thread owns two 16-byte pieces (of bf16) of a head
 // vector, chosen so that both members of its eight pairs are its own: no
 // exchange but the row sums of the norm (and the maximum for an E4M3 scale)
-// among the head's D/16 threads.  The row's sines and cosines are computed
-// once per CTA and shared by all heads through shared memory, while the
-// vectors' loads are in flight.
+// among the head's D/16 threads.  One CTA of 128 threads per row; a thread's
+// loads, for up to four head vectors, are all issued before anything else, so
+// that some 100 KB per SM are in flight; the row's sines and cosines are made
+// meanwhile, once for all heads, and passed through shared memory.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -26,23 +27,40 @@ namespace dflash {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kThreads = 128;
 
-// 8 consecutive elements as floats
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 consecutive elements, as loaded and as floats
+template <typename In>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = __uint_as_float(w[j] << 16);
-    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  Raw8<uint16_t> r;
+  r.v = __ldg(reinterpret_cast<const uint4*>(p));
+  r.get(x);
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]),
@@ -56,177 +74,200 @@ __device__ __forceinline__ void store8_lo(uint16_t* p, const float (&x)[8]) {
   store8(p, y);
 }
 
-template <int D, typename In>
-__global__ void __launch_bounds__(kMaxThreads) rope_append_kernel(const RopeAppendParams p) {
-  constexpr int TPH = D / 16;  // threads per head vector
+// NI: head vectors per thread and round.
+template <int D, typename In, int NI>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+  constexpr int TPH = D / 16;          // threads per head vector
+  constexpr int HPR = kThreads / TPH;  // head vectors per round and NI
   __shared__ float2 cs[64];
   griddep_launch_dependents();
   griddep_wait();
   const int t = blockIdx.x;
-  const int pos = p.row_pos[t];
-  if (pos < 0) return;  // the whole CTA
   const int rot = p.rot_dim, half = rot / 2;
-
-  // where the row's K and V go
-  const int req = p.row_req[t];
-  long long page = -1;
-  if (req >= 0 && req < p.n_req && pos / 16 < p.max_pages)
-    page = p.page_table[static_cast<size_t>(req) * p.max_pages + pos / 16];
-  const bool kept = page >= 0 && page < p.n_pages;
-  if (!kept && threadIdx.x == 0) raise_status(p.status, DFLASH_ERR_CAPACITY, 501);
-
   const int heads_q = p.q != nullptr ? p.hq : 0;
-  const int items = (heads_q + 2 * p.hkv) * TPH;
+  const int heads = heads_q + 2 * p.hkv;
   // the two 8-element pieces of this thread: a rotated pair of pieces, or two
   // neighbours (interleaved pairs, and everything past rot_dim)
   const int sub = threadIdx.x % TPH;
   const bool split = !p.interleaved && sub < rot / 16;
-  const int c0 = split ? sub : 2 * sub;
-  const int c1 = split ? sub + rot / 16 : 2 * sub + 1;
+  const int c0 = (split ? sub : 2 * sub) * 8;
+  const int c1 = split ? c0 + half : c0 + 8;
+  const int pos = __ldg(p.row_pos + t), req = __ldg(p.row_req + t);
 
-  bool table = false;
+  bool first = true;
+  long long page = -1;
   // all threads of the CTA run the same number of rounds (barrier, shuffles)
-  for (int it0 = 0; it0 < items; it0 += blockDim.x) {
-    const int it = it0 + threadIdx.x;
-    const bool on = it < items;
-    const int head = on ? it / TPH : 0;
-    const bool is_q = head < heads_q;
-    const int hk = head - heads_q;
-    const bool is_v = on && !is_q && hk >= p.hkv;
-    const int h = is_q ? head : is_v ? hk - p.hkv : hk;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      const In* src = is_q ? static_cast<const In*>(p.q) + t * p.ld_q
-                           : is_v ? static_cast<const In*>(p.v) + t * p.ld_v
-                                  : static_cast<const In*>(p.k) + t * p.ld_k;
-      load8(src + h * D + c0 * 8, x);
-      load8(src + h * D + c1 * 8, y);
+  for (int h0 = 0; h0 < heads; h0 += NI * HPR) {
+    Raw8<In> r0[NI], r1[NI];
+#pragma unroll
+    for (int u = 0; u < NI; ++u) {
+      const int head = h0 + u * HPR + threadIdx.x / TPH;
+      if (head < heads) {
+        const bool is_q = head < heads_q;
+        const int hk = head - heads_q;
+        const In* src = is_q ? static_cast<const In*>(p.q) + t * p.ld_q + head * D
+                        : hk < p.hkv ? static_cast<const In*>(p.k) + t * p.ld_k + hk * D
+                                     : static_cast<const In*>(p.v) + t * p.ld_v + (hk - p.hkv) * D;
+        r0[u].load(src + c0);
+        r1[u].load(src + c1);
+      }
     }
-    if (!table) {
-      table = true;
-      for (int j = threadIdx.x; j < half; j += blockDim.x) {
-        const unsigned long long phase = static_cast<unsigned long long>(pos) * p.turns[j];
+    if (first) {
+      first = false;
+      if (pos < 0) return;  // the whole CTA
+      // where the row's K and V go
+      if (req >= 0 && req < p.n_req && pos / 16 < p.max_pages)
+        page = __ldg(p.page_table + static_cast<size_t>(req) * p.max_pages + pos / 16);
+      if (page >= p.n_pages) page = -1;
+      if (page < 0 && threadIdx.x == 0) raise_status(p.status, DFLASH_ERR_CAPACITY, 501);
+      if (threadIdx.x < half) {
+        const unsigned long long phase = static_cast<unsigned long long>(pos) * p.turns[threadIdx.x];
         float s, c;
         sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);
-        cs[j] = make_float2(c * p.mscale, s * p.mscale);
+        cs[threadIdx.x] = make_float2(c * p.mscale, s * p.mscale);
       }
       __syncthreads();
     }
-    const uint16_t* gain = is_v ? nullptr : is_q ? p.q_norm : p.k_norm;
-    {
-      float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+    for (int u = 0; u < NI; ++u) {
+      const int head = h0 + u * HPR + threadIdx.x / TPH;
+      const bool on = head < heads;
+      const bool is_q = head < heads_q;
+      const int hk = head - heads_q;
+      const bool is_v = !is_q && hk >= p.hkv;
+      const int h = is_q ? head : is_v ? hk - p.hkv : hk;
+      float x[8], y[8];
 #pragma unroll
-      for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (gain != nullptr) {
-        const float r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-        float g0[8], g1[8];
-        load8(gain + c0 * 8, g0);
-        load8(gain + c1 * 8, g1);
+      for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
+      if (on) {
+        r0[u].get(x);
+        r1[u].get(y);
+      }
+      const uint16_t* gain = is_v ? nullptr : is_q ? p.q_norm : p.k_norm;
+      if (p.q_norm != nullptr || p.k_norm != nullptr) {
+        float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] = x[j] * r * g0[j];
-          y[j] = y[j] * r * g1[j];
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+#pragma unroll
+        for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (gain != nullptr) {
+          const float r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+          float g0[8], g1[8];
+          load8(gain + c0, g0);
+          load8(gain + c1, g1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[j] = x[j] * r * g0[j];
+            y[j] = y[j] * r * g1[j];
+          }
         }
       }
-    }
-    if (!is_v) {
-      if (split) {
+      if (!is_v) {
+        if (split) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 w = cs[c0 * 8 + j];
-          const float a = x[j], b = y[j];
-          x[j] = a * w.x - b * w.y;
-          y[j] = fmaf(a, w.y, b * w.x);
-        }
-      } else if (p.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          if (c0 * 8 + j < rot) {
-            const float2 w = cs[(c0 * 8 + j) / 2];
-            const float a = x[j], b = x[j + 1];
+          for (int j = 0; j < 8; ++j) {
+            const float2 w = cs[c0 + j];
+            const float a = x[j], b = y[j];
             x[j] = a * w.x - b * w.y;
-            x[j + 1] = fmaf(a, w.y, b * w.x);
+            y[j] = fmaf(a, w.y, b * w.x);
           }
-          if (c1 * 8 + j < rot) {
-            const float2 w = cs[(c1 * 8 + j) / 2];
-            const float a = y[j], b = y[j + 1];
-            y[j] = a * w.x - b * w.y;
-            y[j + 1] = fmaf(a, w.y, b * w.x);
+        } else if (p.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            if (c0 + j < rot) {
+              const float2 w = cs[(c0 + j) / 2];
+              const float a = x[j], b = x[j + 1];
+              x[j] = a * w.x - b * w.y;
+              x[j + 1] = fmaf(a, w.y, b * w.x);
+            }
+            if (c1 + j < rot) {
+              const float2 w = cs[(c1 + j) / 2];
+              const float a = y[j], b = y[j + 1];
+              y[j] = a * w.x - b * w.y;
+              y[j + 1] = fmaf(a, w.y, b * w.x);
+            }
           }
         }
       }
-    }
-    if (on && is_q) {
-      uint16_t* o = p.q_out + t * p.ld_qo + h * D;
-      store8(o + c0 * 8, x);
-      store8(o + c1 * 8, y);
-    }
-    if (p.pool8 != nullptr) {
-      // E4M3 codes of the bf16-rounded vector, scale = amax / 448 (1 for a
-      // zero vector), the code decided from the fp32 quotient
-      float am = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = bf2f(f2bf(x[j]));
-        y[j] = bf2f(f2bf(y[j]));
-        am = fmaxf(am, fmaxf(fabsf(x[j]), fabsf(y[j])));
+      if (on && is_q) {
+        uint16_t* o = p.q_out + t * p.ld_qo + h * D;
+        store8(o + c0, x);
+        store8(o + c1, y);
       }
+      if (p.pool8 != nullptr) {
+        // E4M3 codes of the bf16-rounded vector, scale = amax / 448 (1 for a
+        // zero vector), the code decided from the fp32 quotient
+        float am = 0.f;
 #pragma unroll
-      for (int o = TPH / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-      if (on && !is_q && kept) {
-        const float scale = am > 0.f ? am / 448.f : 1.f;
-        const size_t vec = ((static_cast<size_t>(page) * 2 + (is_v ? 1 : 0)) * p.hkv + h) * 16 + pos % 16;
-        uint32_t a[2], b[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          a[j] = e4m3x2_encode(x[4 * j] / scale, x[4 * j + 1] / scale) |
-                 (static_cast<uint32_t>(e4m3x2_encode(x[4 * j + 2] / scale, x[4 * j + 3] / scale)) << 16);
-          b[j] = e4m3x2_encode(y[4 * j] / scale, y[4 * j + 1] / scale) |
-                 (static_cast<uint32_t>(e4m3x2_encode(y[4 * j + 2] / scale, y[4 * j + 3] / scale)) << 16);
+        for (int j = 0; j < 8; ++j) {
+          x[j] = bf2f(f2bf(x[j]));
+          y[j] = bf2f(f2bf(y[j]));
+          am = fmaxf(am, fmaxf(fabsf(x[j]), fabsf(y[j])));
         }
-        *reinterpret_cast<uint2*>(p.pool8 + vec * D + c0 * 8) = make_uint2(a[0], a[1]);
-        *reinterpret_cast<uint2*>(p.pool8 + vec * D + c1 * 8) = make_uint2(b[0], b[1]);
-        if (sub == 0) p.scales8[vec] = scale;
-      }
-    } else if (on && !is_q && kept) {
-      const int planes = 2 * p.kv_terms;
-      uint16_t* o = p.pool + (((static_cast<size_t>(page) * planes + (is_v ? 1 : 0)) * p.hkv + h) * 16 +
-                              pos % 16) * D;
-      store8(o + c0 * 8, x);
-      store8(o + c1 * 8, y);
-      if (p.kv_terms == 2) {
-        o += static_cast<size_t>(2) * p.hkv * 16 * D;
-        store8_lo(o + c0 * 8, x);
-        store8_lo(o + c1 * 8, y);
+#pragma unroll
+        for (int o = TPH / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        if (on && !is_q && page >= 0) {
+          const float scale = am > 0.f ? am / 448.f : 1.f;
+          const size_t vec = ((static_cast<size_t>(page) * 2 + (is_v ? 1 : 0)) * p.hkv + h) * 16 + pos % 16;
+          uint32_t a[2], b[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            a[j] = e4m3x2_encode(x[4 * j] / scale, x[4 * j + 1] / scale) |
+                   (static_cast<uint32_t>(e4m3x2_encode(x[4 * j + 2] / scale, x[4 * j + 3] / scale)) << 16);
+            b[j] = e4m3x2_encode(y[4 * j] / scale, y[4 * j + 1] / scale) |
+                   (static_cast<uint32_t>(e4m3x2_encode(y[4 * j + 2] / scale, y[4 * j + 3] / scale)) << 16);
+          }
+          *reinterpret_cast<uint2*>(p.pool8 + vec * D + c0) = make_uint2(a[0], a[1]);
+          *reinterpret_cast<uint2*>(p.pool8 + vec * D + c1) = make_uint2(b[0], b[1]);
+          if (sub == 0) p.scales8[vec] = scale;
+        }
+      } else if (on && !is_q && page >= 0) {
+        const int planes = 2 * p.kv_terms;
+        uint16_t* o = p.pool + (((static_cast<size_t>(page) * planes + (is_v ? 1 : 0)) * p.hkv + h) * 16 +
+                                pos % 16) * D;
+        store8(o + c0, x);
+        store8(o + c1, y);
+        if (p.kv_terms == 2) {
+          o += static_cast<size_t>(2) * p.hkv * 16 * D;
+          store8_lo(o + c0, x);
+          store8_lo(o + c1, y);
+        }
       }
     }
   }
 }
 
-template <int D, typename In>
+template <int D, typename In, int NI>
 cudaError_t launch_append(const RopeAppendParams& p, cudaStream_t s) {
-  const int items = ((p.q != nullptr ? p.hq : 0) + 2 * p.hkv) * (D / 16);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.T);
-  cfg.blockDim = dim3(items >= kMaxThreads ? kMaxThreads : (items + 31) / 32 * 32);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, In>, p);
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<D, In, NI>, p);
+}
+
+// Head vectors per thread: what one round needs, four at most.
+template <int D, typename In>
+cudaError_t choose(const RopeAppendParams& p, cudaStream_t s) {
+  const int heads = (p.q != nullptr ? p.hq : 0) + 2 * p.hkv;
+  const int rounds = (heads * (D / 16) + kThreads - 1) / kThreads;
+  if (rounds <= 1) return launch_append<D, In, 1>(p, s);
+  if (rounds <= 2) return launch_append<D, In, 2>(p, s);
+  if (rounds == 3) return launch_append<D, In, 3>(p, s);
+  return launch_append<D, In, 4>(p, s);
 }
 
 }  // namespace
 
 cudaError_t rope_append_launch(const RopeAppendParams& p, int d, bool fp32, cudaStream_t s) {
-  if (d == 128)
-    return fp32 ? launch_append<128, float>(p, s) : launch_append<128, uint16_t>(p, s);
-  return fp32 ? launch_append<64, float>(p, s) : launch_append<64, uint16_t>(p, s);
+  if (d == 128) return fp32 ? choose<128, float>(p, s) : choose<128, uint16_t>(p, s);
+  return fp32 ? choose<64, float>(p, s) : choose<64, uint16_t>(p, s);
 }
 
 }  // namespace dflash
