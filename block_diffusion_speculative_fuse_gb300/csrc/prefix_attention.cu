@@ -268,52 +268,55 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int vec = blockIdx.x * (8 / WPV) + warp / WPV, sub = warp % WPV;
-  const bool on = vec < p.batch * p.n * p.hq;
+  const int row_q = blockIdx.y;  // request * n + block row
+  const int h = blockIdx.x * (8 / WPV) + warp / WPV, sub = warp % WPV;
+  const bool on = h < p.hq;
+  const int vec = row_q * p.hq + h;
   const int ne = p.ng + p.batch;
-  const int G = p.hq / p.hkv;
   float m = -INFINITY, l = 0.f, acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
   if (on) {
-    const int h = vec % p.hq, i = vec / p.hq % p.n, req = vec / p.hq / p.n;
-    const int kvh = h / G, gi = req / p.group, se = p.ng + req;
+    const int req = row_q / p.n, i = row_q - req * p.n;
+    const int gi = req / p.group, se = p.ng + req;
+    const int G = p.hq / p.hkv;
+    const int kvh = h / G, g = h - kvh * G;
     const int pl = p.list[0].prefix_tiles > 0 ? 0 : 1;
     const PrefixList& P = p.list[pl];
-    int offs[2][2], tot[2], po[2] = {0, 0};
+    int so_[2], su[2], per[2], po = 0, pu = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const bool used = p.list[j].workers > 0;
-      offs[j][0] = used ? __ldcg(p.list[j].off + se) : 0;
-      offs[j][1] = used ? __ldcg(p.list[j].off + se + 1) : 0;
-      tot[j] = used ? __ldcg(p.list[j].off + ne) : 0;
+      so_[j] = used ? __ldcg(p.list[j].off + se) : 0;
+      su[j] = used ? __ldcg(p.list[j].unit + se) : 0;
+      per[j] = used ? __ldcg(p.list[j].unit + ne) : 1;
     }
     if (P.prefix_tiles > 0) {
-      po[0] = __ldcg(P.off + gi);
-      po[1] = __ldcg(P.off + gi + 1);
+      po = __ldcg(P.off + gi);
+      pu = __ldcg(P.unit + gi);
     }
     const int ctx = clamped_ctx(p, req);
     const bool sees = (p.causal ? ctx - p.n + i + 1 : ctx) > 0;
     // a request's own keys are in one of the lists
-    const int sl = offs[1][1] > offs[1][0] ? 1 : 0;
+    const int sl = su[1] > 0 ? 1 : 0;
     const PrefixList& S = p.list[sl];
-    int pw0 = 0, np = 0, sw0 = 0, nsu = 0;
-    size_t p_at = 0, s_at = 0;  // partial row of worker 0
-    if (sees && po[1] > po[0]) {
-      const int row = ((req % p.group) * p.n + i) * G + h % G;
-      const int ul = kvh * P.prefix_tiles + row / P.tile_rows;
-      int w1;
-      unit_workers(p, P, gi, ul, po[0], po[1], tot[pl], &pw0, &w1);
-      np = w1 - pw0 + 1;
-      p_at = static_cast<size_t>(units_before(p, P, gi) + ul + pw0) * P.tile_rows + row % P.tile_rows;
+    int np = 0, nsu = 0;
+    size_t p_at = 0, s_at = 0;  // partial rows of the first worker
+    if (sees && pu > 0) {
+      const int row = ((req - gi * p.group) * p.n + i) * G + g;
+      const int tile = row / P.tile_rows, ul = kvh * P.prefix_tiles + tile;
+      int w0, w1;
+      unit_workers(p, P, gi, ul, po, pu, per[pl], &w0, &w1);
+      np = w1 - w0 + 1;
+      p_at = static_cast<size_t>(units_before(p, P, gi) + ul + w0) * P.tile_rows + row - tile * P.tile_rows;
     }
-    if (sees && offs[sl][1] > offs[sl][0]) {
-      const int row = i * G + h % G;
-      const int ul = kvh * S.suffix_tiles + row / S.tile_rows;
-      int w1;
-      unit_workers(p, S, se, ul, offs[sl][0], offs[sl][1], tot[sl], &sw0, &w1);
-      nsu = w1 - sw0 + 1;
-      s_at = static_cast<size_t>(units_before(p, S, se) + ul + sw0) * S.tile_rows + row % S.tile_rows;
+    if (sees && su[sl] > 0) {
+      const int row = i * G + g;
+      const int tile = row / S.tile_rows, ul = kvh * S.suffix_tiles + tile;
+      int w0, w1;
+      unit_workers(p, S, se, ul, so_[sl], su[sl], per[sl], &w0, &w1);
+      nsu = w1 - w0 + 1;
+      s_at = static_cast<size_t>(units_before(p, S, se) + ul + w0) * S.tile_rows + row - tile * S.tile_rows;
     }
     const int parts = np + nsu;
     for (int b = sub; b < parts; b += 32 * WPV) {
@@ -401,12 +404,12 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
     p.lse[vec] = any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
-cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, void** args, cudaStream_t s) {
+cudaError_t launch_pdl(const void* fn, dim3 grid, int block, size_t smem, void** args, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -424,16 +427,16 @@ cudaError_t run_small(const PrefixParams& p, void** args, cudaStream_t s) {
   static thread_local int allowed = -1;
   const cudaError_t e = allow_smem(fn, kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, kSmallCtas, kSmallWarps * 32, smem, args, s);
+  return launch_pdl(fn, dim3(kSmallCtas), kSmallWarps * 32, smem, args, s);
 }
 
 template <int D>
 cudaError_t run_join(const PrefixParams& p, void** args, cudaStream_t s) {
-  const int vecs = p.batch * p.n * p.hq;
+  const int rows = p.batch * p.n;
   // few vectors have many partials each: more warps per vector
-  if (vecs >= 4096)
-    return launch_pdl(reinterpret_cast<const void*>(prefix_join_kernel<D, 1>), (vecs + 7) / 8, 256, 0, args, s);
-  return launch_pdl(reinterpret_cast<const void*>(prefix_join_kernel<D, 8>), vecs, 256, 0, args, s);
+  if (rows * p.hq >= 4096)
+    return launch_pdl(reinterpret_cast<const void*>(prefix_join_kernel<D, 1>), dim3((p.hq + 7) / 8, rows), 256, 0, args, s);
+  return launch_pdl(reinterpret_cast<const void*>(prefix_join_kernel<D, 4>), dim3((p.hq + 1) / 2, rows), 256, 0, args, s);
 }
 
 }  // namespace

@@ -37,6 +37,7 @@ struct PrefixList {            // one kernel's share of the work
   int prefix_cost, suffix_cost;  // of a chunk
   int prefix_split, suffix_split;  // large tiles: at most 128 rows (see there)
   int* off;                    // [entities + 1] cost before each entity (written for the join)
+  int* unit;                   // [entities + 1] cost of one of its units; last: of a worker's range
   float* part_o;               // [units + workers][tile_rows][d]
   float* part_ml;              // [units + workers][tile_rows][2]
 };
@@ -78,6 +79,10 @@ __device__ __forceinline__ int chunk_cost(const PrefixParams& p, const PrefixLis
   return e < p.ng ? L.prefix_cost : L.suffix_cost;
 }
 
+__device__ __forceinline__ int cost_per_worker(const PrefixList& L, int total) {
+  return max(max(L.prefix_cost, L.suffix_cost), (total + L.workers - 1) / L.workers);
+}
+
 // The list, by all threads of a CTA: cut[ng] (keys of each group's prefix),
 // live[ng] (a request of the group whose table is read for it), off[ne + 1].
 // scratch: 33 ints.
@@ -105,7 +110,7 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, int
   // exclusive scan of the entities' costs, thread t taking a run of them
   const int ne = p.ng + p.batch;
   const int per = (ne + nt - 1) / nt;
-  auto cost = [&](int e) {
+  auto unit_of = [&](int e) {
     int keys;
     if (e < p.ng) {
       keys = cut[e];
@@ -115,8 +120,9 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, int
       if (!takes_suffix(p, list, keys)) keys = 0;
     }
     const int n = (keys + L.chunk_keys - 1) / L.chunk_keys;
-    return n > 0 ? (L.unit_cost + n * chunk_cost(p, L, e)) * p.hkv * entity_tiles(p, L, e) : 0;
+    return n > 0 ? L.unit_cost + n * chunk_cost(p, L, e) : 0;
   };
+  auto cost = [&](int e) { return unit_of(e) * p.hkv * entity_tiles(p, L, e); };
   const int e0 = min(ne, tid * per), e1 = min(ne, e0 + per);
   int sum = 0;
   for (int e = e0; e < e1; ++e) sum += cost(e);
@@ -137,13 +143,12 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, int
   if (tid == nt - 1) off[ne] = run;  // the last thread's run ends at the total
   __syncthreads();
   if (blockIdx.x == 0) {
-    for (int e = tid; e <= ne; e += nt) L.off[e] = off[e];
+    for (int e = tid; e <= ne; e += nt) {
+      L.off[e] = off[e];
+      L.unit[e] = e < ne ? unit_of(e) : cost_per_worker(L, off[ne]);
+    }
     for (int g = tid; g < p.ng; g += nt) p.cut[g] = cut[g];
   }
-}
-
-__device__ __forceinline__ int cost_per_worker(const PrefixList& L, int total) {
-  return max(max(L.prefix_cost, L.suffix_cost), (total + L.workers - 1) / L.workers);
 }
 
 // The entity in whose cost c lies (off[e] <= c < off[e + 1]).
@@ -191,14 +196,22 @@ struct Segments {
   }
 };
 
-// The workers [w0, w1] that have chunks of unit ul of entity e.
-__device__ __forceinline__ void unit_workers(const PrefixParams& p, const PrefixList& L, int e, int ul,
-                                             int off_e, int off_e1, int total, int* w0, int* w1) {
-  const int unit = (off_e1 - off_e) / (p.hkv * entity_tiles(p, L, e));
-  const int per = cost_per_worker(L, total);
-  const int first = off_e + ul * unit + L.unit_cost;
-  *w0 = first / per;
-  *w1 = (off_e + (ul + 1) * unit - chunk_cost(p, L, e)) / per;
+// a / b for 0 <= a, 0 < b and a quotient below 2^20, by way of a float quotient
+// that is off by one at most.
+__device__ __forceinline__ int small_div(int a, int b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  const int r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
+}
+
+// The workers [w0, w1] that have chunks of unit ul of entity e (off_e: the cost
+// before the entity, unit: of one unit, per: of a worker's range).
+__device__ __forceinline__ void unit_workers(const PrefixParams& p, const PrefixList& L, int e, int ul, int off_e,
+                                             int unit, int per, int* w0, int* w1) {
+  *w0 = small_div(off_e + ul * unit + L.unit_cost, per);
+  *w1 = small_div(off_e + (ul + 1) * unit - chunk_cost(p, L, e), per);
 }
 
 // Row `row` of an entity: its request, block row, and vector of q and out
