@@ -36,19 +36,22 @@ struct SmallCfg {
   static constexpr int RING = STAGES * 2 * PAGE;
 };
 
+// 16 bytes global -> shared (zeros when bytes is 0) under an L2 policy.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy)
+               : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const PrefixParams p) {
   using C = SmallCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   const PrefixList& L = p.list[0];
   const int ne = p.ng + p.batch;
-  int* off = reinterpret_cast<int*>(smem + kSmallWarps * C::RING);
-  int* cut = off + ne + 1;
-  int* live = cut + p.ng;
-  int* scratch = live + p.ng;
+  const PrefixPlan pl(reinterpret_cast<int*>(smem + kSmallWarps * C::RING), p.batch, p.ng);
   griddep_launch_dependents();
   griddep_wait();
-  prefix_plan(p, 0, cut, live, off, scratch);
+  prefix_plan(p, 0, pl);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int worker = blockIdx.x * kSmallWarps + warp;
@@ -64,42 +67,44 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
   const uint32_t ld_off = swz<D>(lane / (D / 8), lane % (D / 8));
   const uint32_t k_off = swz<D>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
   const uint32_t v_off = swz<D>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+  const uint32_t q_off = v_off;
+  const uint64_t pol = l2_policy_evict_first();  // keys are read once, or by neighbouring workers at once
 
-  Segments seg(L, off, ne, worker);
-  while (seg.next(p, L, off)) {
+  Segments seg(L, pl.off, ne, worker);
+  while (seg.next(p, L, pl.off)) {
     // ---- the segment: unit (e, kvh, tile), its pages [pg0, pg1)
     const int e = seg.e, pg0 = seg.chunk0, pg1 = seg.chunk1;
     const int tiles = entity_tiles(p, L, e);
     const int kvh = seg.ul / tiles, tile = seg.ul % tiles;
     const int slot = units_before(p, L, e) + seg.ul + worker;
     const bool pre = e < p.ng;
-    const int req_t = pre ? live[e] : e - p.ng;               // whose table row
-    const int page0 = pre ? 0 : cut[(e - p.ng) / p.group] / 16;
-    const int ctx = pre ? cut[e] : clamped_ctx(p, e - p.ng);  // keys at or past it take no part
+    const int req_t = pre ? pl.live[e] : e - p.ng;               // whose table row
+    const int page0 = pre ? 0 : pl.cut[(e - p.ng) / p.group] / 16;
+    const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];  // keys at or past it take no part
     const int32_t* table = p.page_table + static_cast<size_t>(req_t) * p.max_pages + page0;
     const RowMap map(p, e, kvh);
 
-    // ---- query fragments (rows tg, tg + 8 of the tile) and their limits
-    uint32_t qf[D / 16][4];
+    // ---- the query rows to the ring's last stage (free until the second page
+    // is done), and the limits of rows tg, tg + 8 of the tile
     int lim[2];
     {
-      const uint16_t* qp[2];
-      bool ok[2];
+      const uint32_t qs = ring_a + (C::STAGES - 1) * (2 * C::PAGE);
+#pragma unroll
+      for (int i = 0; i < C::PAGE / 512; ++i) {
+        int req, bi;
+        size_t vec = 0;
+        const bool ok = map.at(tile * kSmallRows + i * RPI + lane / (D / 8), &req, &bi, &vec);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + (ld_off ^ ((i * RPI & 7) << 4)) + i * 512),
+                     "l"(p.q + (ok ? vec : 0) * D + lane % (D / 8) * 8), "r"(ok ? 16 : 0)
+                     : "memory");
+      }
+      cp_async_commit();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        int req = 0, i = 0;
-        size_t vec = 0;
-        ok[h] = map.at(tile * kSmallRows + tg + 8 * h, &req, &i, &vec);
-        qp[h] = p.q + vec * D;
-        lim[h] = !ok[h] ? 0 : pre ? INT_MAX : p.causal ? ctx - p.n + i + 1 : ctx;
-      }
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const int col = kk * 16 + tq * 2;
-        qf[kk][0] = ok[0] ? __ldcg(reinterpret_cast<const unsigned*>(qp[0] + col)) : 0u;
-        qf[kk][1] = ok[1] ? __ldcg(reinterpret_cast<const unsigned*>(qp[1] + col)) : 0u;
-        qf[kk][2] = ok[0] ? __ldcg(reinterpret_cast<const unsigned*>(qp[0] + col + 8)) : 0u;
-        qf[kk][3] = ok[1] ? __ldcg(reinterpret_cast<const unsigned*>(qp[1] + col + 8)) : 0u;
+        int req, i = 0;
+        size_t vec;
+        const bool ok = map.at(tile * kSmallRows + tg + 8 * h, &req, &i, &vec);
+        lim[h] = !ok ? 0 : pre ? INT_MAX : p.causal ? ctx - p.n + i + 1 : ctx;
       }
     }
 
@@ -130,8 +135,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
 #pragma unroll
       for (int i = 0; i < C::PAGE / 512; ++i) {  // 16-byte piece i * 32 + lane of the page
         const uint32_t o = st + (ld_off ^ ((i * RPI & 7) << 4)) + i * 512;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(o), "l"(k + i * 256), "r"(bytes) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(o + C::PAGE), "l"(v + i * 256), "r"(bytes) : "memory");
+        copy16(o, k + i * 256, bytes, pol);
+        copy16(o + C::PAGE, v + i * 256, bytes, pol);
       }
     };
 
@@ -147,6 +152,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
       if (pg0 + s < pg1) load_page();
       cp_async_commit();
     }
+    uint32_t qf[D / 16][4];
+    cp_async_wait<C::STAGES - 1>();
+    __syncwarp();
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      ldsm_x4(ring_a + (C::STAGES - 1) * (2 * C::PAGE) + (q_off ^ (kk << 5)), qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3]);
+    __syncwarp();
     for (int pg = pg0; pg < pg1; ++pg) {
       if (pg + C::STAGES - 1 < pg1) load_page();
       cp_async_commit();
@@ -281,8 +293,8 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
     const int gi = req / p.group, se = p.ng + req;
     const int G = p.hq / p.hkv;
     const int kvh = h / G, g = h - kvh * G;
-    const int pl = p.list[0].prefix_tiles > 0 ? 0 : 1;
-    const PrefixList& P = p.list[pl];
+    const int li = p.list[0].prefix_tiles > 0 ? 0 : 1;
+    const PrefixList& P = p.list[li];
     int so_[2], su[2], per[2], po = 0, pu = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -306,7 +318,7 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
       const int row = ((req - gi * p.group) * p.n + i) * G + g;
       const int tile = row / P.tile_rows, ul = kvh * P.prefix_tiles + tile;
       int w0, w1;
-      unit_workers(p, P, gi, ul, po, pu, per[pl], &w0, &w1);
+      unit_workers(p, P, gi, ul, po, pu, per[li], &w0, &w1);
       np = w1 - w0 + 1;
       p_at = static_cast<size_t>(units_before(p, P, gi) + ul + w0) * P.tile_rows + row - tile * P.tile_rows;
     }
@@ -421,11 +433,10 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, int block, size_t smem, void**
 
 template <int D>
 cudaError_t run_small(const PrefixParams& p, void** args, cudaStream_t s) {
-  const int ne = p.ng + p.batch;
-  const size_t smem = kSmallWarps * SmallCfg<D>::RING + (ne + 1 + 2 * p.ng + 33) * sizeof(int);
+  const size_t smem = kSmallWarps * SmallCfg<D>::RING + PrefixPlan::ints(p.batch, p.ng) * sizeof(int);
   const void* fn = reinterpret_cast<const void*>(prefix_small_kernel<D>);
   static thread_local int allowed = -1;
-  const cudaError_t e = allow_smem(fn, kSmallWarps * SmallCfg<D>::RING + (4 * kMaxPrefixBatch + 34) * 4, &allowed);
+  const cudaError_t e = allow_smem(fn, kSmallWarps * SmallCfg<D>::RING + PrefixPlan::ints(kMaxPrefixBatch, kMaxPrefixBatch) * 4, &allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(fn, dim3(kSmallCtas), kSmallWarps * 32, smem, args, s);
 }

@@ -53,7 +53,6 @@ struct PrefixParams {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int* cut;                    // [ng] prefix keys used (written for the join)
   int large_keys;              // a request with this many keys past the prefix is the large
                                // tiles' where they take requests at all
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
@@ -83,40 +82,54 @@ __device__ __forceinline__ int cost_per_worker(const PrefixList& L, int total) {
   return max(max(L.prefix_cost, L.suffix_cost), (total + L.workers - 1) / L.workers);
 }
 
-// The list, by all threads of a CTA: cut[ng] (keys of each group's prefix),
-// live[ng] (a request of the group whose table is read for it), off[ne + 1].
-// scratch: 33 ints.
-__device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, int* cut, int* live,
-                                            int* off, int* scratch) {
+// What every CTA works out first, in shared memory.
+struct PrefixPlan {
+  int* ctx;      // [batch] context lengths, within the page table
+  int* cut;      // [ng] keys of each group's prefix
+  int* live;     // [ng] a request of the group whose page-table row is read for it
+  int* off;      // [entities + 1] cost before each entity
+  int* scratch;  // [32]
+  __host__ __device__ static int ints(int batch, int ng) { return 2 * batch + 3 * ng + 33; }
+  __device__ PrefixPlan(int* mem, int batch, int ng)
+      : ctx(mem), cut(ctx + batch), live(cut + ng), off(live + ng), scratch(off + ng + batch + 1) {}
+};
+
+// The list, by all threads of a CTA.
+__device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, const PrefixPlan& pl) {
   const PrefixList& L = p.list[list];
   const int tid = threadIdx.x, nt = blockDim.x;
-  for (int g = tid; g < p.ng; g += nt) {
-    cut[g] = p.group > 1 ? min(max(__ldcg(p.prefix_len + g), 0), p.max_pages * 16) : 0;
-    live[g] = p.batch;
-  }
-  __syncthreads();
+  const int cap = p.max_pages * 16;
   for (int r = tid; r < p.batch; r += nt) {
     const int raw = __ldcg(p.ctx_len + r);
-    if (raw > p.max_pages * 16 && blockIdx.x == 0) raise_status(p.status, DFLASH_ERR_CAPACITY, 522);
-    const int c = clamped_ctx(p, r);
-    if (c > 0) {
-      atomicMin(&cut[r / p.group], p.causal ? max(0, c - p.n + 1) : c);
-      atomicMin(&live[r / p.group], r);
-    }
+    if (raw > cap && blockIdx.x == 0) raise_status(p.status, DFLASH_ERR_CAPACITY, 522);
+    pl.ctx[r] = min(max(raw, 0), cap);
+  }
+  for (int g = tid; g < p.ng; g += nt) {
+    pl.cut[g] = p.group > 1 ? min(max(__ldcg(p.prefix_len + g), 0), cap) : 0;
+    pl.live[g] = p.batch;
   }
   __syncthreads();
-  for (int g = tid; g < p.ng; g += nt) cut[g] = live[g] < p.batch ? cut[g] & ~15 : 0;
-  __syncthreads();
+  if (p.group > 1) {
+    for (int r = tid; r < p.batch; r += nt) {
+      const int c = pl.ctx[r], g = r / p.group;
+      if (c > 0) {
+        atomicMin(&pl.cut[g], p.causal ? max(0, c - p.n + 1) : c);
+        atomicMin(&pl.live[g], r);
+      }
+    }
+    __syncthreads();
+    for (int g = tid; g < p.ng; g += nt) pl.cut[g] = pl.live[g] < p.batch ? pl.cut[g] & ~15 : 0;
+    __syncthreads();
+  }
   // exclusive scan of the entities' costs, thread t taking a run of them
   const int ne = p.ng + p.batch;
   const int per = (ne + nt - 1) / nt;
   auto unit_of = [&](int e) {
     int keys;
     if (e < p.ng) {
-      keys = cut[e];
+      keys = pl.cut[e];
     } else {
-      const int c = clamped_ctx(p, e - p.ng);
-      keys = max(0, c - cut[(e - p.ng) / p.group]);
+      keys = max(0, pl.ctx[e - p.ng] - pl.cut[(e - p.ng) / p.group]);
       if (!takes_suffix(p, list, keys)) keys = 0;
     }
     const int n = (keys + L.chunk_keys - 1) / L.chunk_keys;
@@ -132,22 +145,21 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, int
     const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (tid % 32 >= o) inc += x;
   }
-  if (tid % 32 == 31) scratch[tid / 32] = inc;
+  if (tid % 32 == 31) pl.scratch[tid / 32] = inc;
   __syncthreads();
   int run = inc - sum;
-  for (int w = 0; w < tid / 32; ++w) run += scratch[w];
+  for (int w = 0; w < tid / 32; ++w) run += pl.scratch[w];
   for (int e = e0; e < e1; ++e) {
-    off[e] = run;
+    pl.off[e] = run;
     run += cost(e);
   }
-  if (tid == nt - 1) off[ne] = run;  // the last thread's run ends at the total
+  if (tid == nt - 1) pl.off[ne] = run;  // the last thread's run ends at the total
   __syncthreads();
   if (blockIdx.x == 0) {
     for (int e = tid; e <= ne; e += nt) {
-      L.off[e] = off[e];
-      L.unit[e] = e < ne ? unit_of(e) : cost_per_worker(L, off[ne]);
+      L.off[e] = pl.off[e];
+      L.unit[e] = e < ne ? unit_of(e) : cost_per_worker(L, pl.off[ne]);
     }
-    for (int g = tid; g < p.ng; g += nt) p.cut[g] = cut[g];
   }
 }
 

@@ -144,10 +144,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const PrefixList& L = p.list[1];
   const int ne = p.ng + p.batch;
-  int* off = reinterpret_cast<int*>(tmem_slot + 2);
-  int* cut = off + ne + 1;
-  int* live = cut + p.ng;
-  int* scratch = live + p.ng;
+  const PrefixPlan pl(reinterpret_cast<int*>(tmem_slot + 2), p.batch, p.ng);
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
@@ -169,28 +166,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   griddep_wait();
   griddep_launch_dependents();
-  prefix_plan(p, 1, cut, live, off, scratch);  // ends with a barrier
+  prefix_plan(p, 1, pl);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int worker = blockIdx.x;
-  Segments seg(L, off, ne, worker);
+  Segments seg(L, pl.off, ne, worker);
 
   if (warp == 8) {
     // ------------------------------------------------ TMA producer
-    const uint64_t pol = l2_policy_evict_last();  // a prefix is read again by other row tiles
+    // keys that other row tiles read too stay as they may; those read once leave
+    // first (kept, they pushed the next kernels' code out of L2: 8 us a call)
+    const uint64_t pol = L.prefix_tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
     int at = 0;                                   // planes requested so far
     Cursor cur;
     bool ok = true;
-    while (ok && seg.next(p, L, off)) {
+    while (ok && seg.next(p, L, pl.off)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
       const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
       const int kvh = seg.ul / entity_tiles(p, L, e);
-      const int page0 = (pre ? 0 : cut[(e - p.ng) / p.group] / 16) + seg.chunk0 * 8;
-      const int pages_end = pre ? cut[e] / 16 : (clamped_ctx(p, e - p.ng) + 15) / 16;
+      const int page0 = (pre ? 0 : pl.cut[(e - p.ng) / p.group] / 16) + seg.chunk0 * 8;
+      const int pages_end = pre ? pl.cut[e] / 16 : (pl.ctx[e - p.ng] + 15) / 16;
       const int npg = min(n * 8, pages_end - page0);
-      const int32_t* table = p.page_table + static_cast<size_t>(pre ? live[e] : e - p.ng) * p.max_pages + page0;
+      const int32_t* table = p.page_table + static_cast<size_t>(pre ? pl.live[e] : e - p.ng) * p.max_pages + page0;
       // lane -> 8-row group of its page's K plane in the map, 32 pages a time,
       // the next 32 requested ahead
       auto ids_of = [&](int b) {
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         np[tile] ^= 1;
         return true;
       };
-      while (ok && seg.next(p, L, off)) {
+      while (ok && seg.next(p, L, pl.off)) {
         const int n = seg.chunk1 - seg.chunk0;
         const bool split = seg.e < p.ng ? L.prefix_split : L.suffix_split;
         ok = mbar_wait(q_full, segs++ & 1, abort_flag);
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // are void (the status word says so).
     int at = 0, segs = 0, ns = 0;
     bool ok = true;
-    while (seg.next(p, L, off)) {
+    while (seg.next(p, L, pl.off)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
       const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
       const int tiles = entity_tiles(p, L, e);
@@ -404,8 +403,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int rq, ri;
         size_t vec;
         const bool real = rows.at(my_row, &rq, &ri, &vec);
-        const int base = (pre ? 0 : cut[(e - p.ng) / p.group]) + seg.chunk0 * kChunk;
-        const int ctx = pre ? cut[e] : clamped_ctx(p, e - p.ng);
+        const int base = (pre ? 0 : pl.cut[(e - p.ng) / p.group]) + seg.chunk0 * kChunk;
+        const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];
         lim = (real && !pre && p.causal ? ctx - p.n + ri + 1 : ctx) - base;
         if (ctx % 16) stale = ctx - base;
       }
@@ -619,9 +618,8 @@ template <int D>
 cudaError_t launch(const CUtensorMap& map, int group0, int oob_group, const PrefixParams& p, cudaStream_t s) {
   using C = TcCfg<D>;
   constexpr int kMax = 227 * 1024;
-  const int ne = p.ng + p.batch;
-  // barriers and flags, the lists, slack for the alignment
-  const int fixed = (2 * C::MAX_SLOTS + 8) * 8 + 8 + (ne + 1 + 2 * p.ng + 33) * 4 + 1024;
+  // barriers and flags, the plan, slack for the alignment
+  const int fixed = (2 * C::MAX_SLOTS + 8) * 8 + 8 + PrefixPlan::ints(p.batch, p.ng) * 4 + 1024;
   int slots = (kMax - fixed - 2 * C::Q_TILE) / C::PLANE;
   if (slots > C::MAX_SLOTS) slots = C::MAX_SLOTS;
   const int smem = fixed + 2 * C::Q_TILE + slots * C::PLANE;

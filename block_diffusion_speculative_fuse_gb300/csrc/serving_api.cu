@@ -61,7 +61,6 @@ size_t layout_prefix(PrefixParams* p, int d, uint8_t* base) {
     off = al256(off + bytes);
     return q;
   };
-  p->cut = reinterpret_cast<int*>(take(p->ng * sizeof(int)));
   for (PrefixList& L : p->list) {
     const size_t units = static_cast<size_t>(p->hkv) *
                          (static_cast<size_t>(p->ng) * L.prefix_tiles + static_cast<size_t>(p->batch) * L.suffix_tiles);
