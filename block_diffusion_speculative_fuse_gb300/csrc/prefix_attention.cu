@@ -26,8 +26,7 @@ namespace {
 constexpr int kSmallWarps = 8;
 constexpr int kSmallCtas = 152;    // one per SM
 constexpr int kSmallRows = 16;
-constexpr int kTcMinRows = 32;     // an entity with more rows may go to the large tiles:
-constexpr int kTcMinKeys = 1024;   // every prefix, and a request's own keys from here on
+constexpr int kTcMinRows = 32;     // an entity with more rows goes to the large tiles
 
 template <int D>
 struct SmallCfg {
@@ -91,9 +90,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
       const uint32_t qs = ring_a + (C::STAGES - 1) * (2 * C::PAGE);
 #pragma unroll
       for (int i = 0; i < C::PAGE / 512; ++i) {
-        int req, bi;
+        int bi;
         size_t vec = 0;
-        const bool ok = map.at(tile * kSmallRows + i * RPI + lane / (D / 8), &req, &bi, &vec);
+        const bool ok = map.at(tile * kSmallRows + i * RPI + lane / (D / 8), &bi, &vec);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qs + (ld_off ^ ((i * RPI & 7) << 4)) + i * 512),
                      "l"(p.q + (ok ? vec : 0) * D + lane % (D / 8) * 8), "r"(ok ? 16 : 0)
                      : "memory");
@@ -101,9 +100,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
       cp_async_commit();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        int req, i = 0;
+        int i = 0;
         size_t vec;
-        const bool ok = map.at(tile * kSmallRows + tg + 8 * h, &req, &i, &vec);
+        const bool ok = map.at(tile * kSmallRows + tg + 8 * h, &i, &vec);
         lim[h] = !ok ? 0 : pre ? INT_MAX : p.causal ? ctx - p.n + i + 1 : ctx;
       }
     }
@@ -293,40 +292,32 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
     const int gi = req / p.group, se = p.ng + req;
     const int G = p.hq / p.hkv;
     const int kvh = h / G, g = h - kvh * G;
-    const int li = p.list[0].prefix_tiles > 0 ? 0 : 1;
-    const PrefixList& P = p.list[li];
-    int so_[2], su[2], per[2], po = 0, pu = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool used = p.list[j].workers > 0;
-      so_[j] = used ? __ldcg(p.list[j].off + se) : 0;
-      su[j] = used ? __ldcg(p.list[j].unit + se) : 0;
-      per[j] = used ? __ldcg(p.list[j].unit + ne) : 1;
-    }
+    const PrefixList& P = p.list[p.list[0].prefix_tiles > 0 ? 0 : 1];
+    const PrefixList& S = p.list[p.list[0].suffix_tiles > 0 ? 0 : 1];
+    const int so_ = __ldcg(S.off + se), su = __ldcg(S.unit + se), sper = __ldcg(S.unit + ne);
+    int po = 0, pu = 0, pper = 1;
     if (P.prefix_tiles > 0) {
       po = __ldcg(P.off + gi);
       pu = __ldcg(P.unit + gi);
+      pper = __ldcg(P.unit + ne);
     }
     const int ctx = clamped_ctx(p, req);
     const bool sees = (p.causal ? ctx - p.n + i + 1 : ctx) > 0;
-    // a request's own keys are in one of the lists
-    const int sl = su[1] > 0 ? 1 : 0;
-    const PrefixList& S = p.list[sl];
     int np = 0, nsu = 0;
     size_t p_at = 0, s_at = 0;  // partial rows of the first worker
     if (sees && pu > 0) {
       const int row = ((req - gi * p.group) * p.n + i) * G + g;
       const int tile = row / P.tile_rows, ul = kvh * P.prefix_tiles + tile;
       int w0, w1;
-      unit_workers(p, P, gi, ul, po, pu, per[li], &w0, &w1);
+      unit_workers(p, P, gi, ul, po, pu, pper, &w0, &w1);
       np = w1 - w0 + 1;
       p_at = static_cast<size_t>(units_before(p, P, gi) + ul + w0) * P.tile_rows + row - tile * P.tile_rows;
     }
-    if (sees && su[sl] > 0) {
+    if (sees && su > 0) {
       const int row = i * G + g;
       const int tile = row / S.tile_rows, ul = kvh * S.suffix_tiles + tile;
       int w0, w1;
-      unit_workers(p, S, se, ul, so_[sl], su[sl], per[sl], &w0, &w1);
+      unit_workers(p, S, se, ul, so_, su, sper, &w0, &w1);
       nsu = w1 - w0 + 1;
       s_at = static_cast<size_t>(units_before(p, S, se) + ul + w0) * S.tile_rows + row - tile * S.tile_rows;
     }
@@ -409,9 +400,9 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
   const float inv = any ? 1.f / l : 0.f;
   uint16_t* dst = p.out + static_cast<size_t>(vec) * D + lane * VEC;
   if constexpr (VEC == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+    __stcs(reinterpret_cast<uint2*>(dst), make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv)));
   else
-    *reinterpret_cast<uint32_t*>(dst) = bf16x2(acc[0] * inv, acc[1] * inv);
+    __stcs(reinterpret_cast<uint32_t*>(dst), bf16x2(acc[0] * inv, acc[1] * inv));
   if (p.lse != nullptr && lane == 0)
     p.lse[vec] = any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
@@ -462,7 +453,7 @@ void prefix_attention_shape(PrefixParams* p) {
   S.chunk_keys = 16;
   S.tile_rows = kSmallRows;
   S.prefix_tiles = tc_p || p->group == 1 ? 0 : (rows_p + kSmallRows - 1) / kSmallRows;
-  S.suffix_tiles = (rows_s + kSmallRows - 1) / kSmallRows;
+  S.suffix_tiles = tc_s ? 0 : (rows_s + kSmallRows - 1) / kSmallRows;
   S.workers = S.prefix_tiles + S.suffix_tiles > 0 ? kSmallCtas * kSmallWarps : 0;
   S.prefix_cost = S.suffix_cost = 1;
   PrefixList& T = p->list[1];
@@ -476,8 +467,11 @@ void prefix_attention_shape(PrefixParams* p) {
   T.suffix_split = rows_s <= 128;
   T.prefix_cost = T.prefix_split ? 1 : 2;
   T.suffix_cost = T.suffix_split ? 1 : 2;
-  T.unit_cost = 2;
-  p->large_keys = kTcMinKeys;
+  // a segment's fixed cost (Q, the pipeline's start, the partial) is about that of
+  // ten chunks of half a tile
+  T.unit_cost = 10;
+  p->inv_n = p->n > 1 ? static_cast<unsigned>((1ull << 32) / p->n + 1) : 0;
+  p->inv_G = G > 1 ? static_cast<unsigned>((1ull << 32) / G + 1) : 0;
 }
 
 cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,

@@ -53,8 +53,7 @@ struct PrefixParams {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int large_keys;              // a request with this many keys past the prefix is the large
-                               // tiles' where they take requests at all
+  unsigned inv_n, inv_G;       // for n and hq / hkv: 2^32 / d rounded up (0 for d = 1)
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
 };
 
@@ -69,11 +68,6 @@ __device__ __forceinline__ int entity_tiles(const PrefixParams& p, const PrefixL
   return e < p.ng ? L.prefix_tiles : L.suffix_tiles;
 }
 
-// Whether a list takes what follows the prefix of a request, of `keys` keys.
-__device__ __forceinline__ bool takes_suffix(const PrefixParams& p, int list, int keys) {
-  const bool large = p.list[1].suffix_tiles > 0 && (keys >= p.large_keys || p.list[0].suffix_tiles == 0);
-  return (list == 1) == large;
-}
 __device__ __forceinline__ int chunk_cost(const PrefixParams& p, const PrefixList& L, int e) {
   return e < p.ng ? L.prefix_cost : L.suffix_cost;
 }
@@ -130,7 +124,6 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, con
       keys = pl.cut[e];
     } else {
       keys = max(0, pl.ctx[e - p.ng] - pl.cut[(e - p.ng) / p.group]);
-      if (!takes_suffix(p, list, keys)) keys = 0;
     }
     const int n = (keys + L.chunk_keys - 1) / L.chunk_keys;
     return n > 0 ? L.unit_cost + n * chunk_cost(p, L, e) : 0;
@@ -226,19 +219,26 @@ __device__ __forceinline__ void unit_workers(const PrefixParams& p, const Prefix
   *w1 = small_div(off_e + (ul + 1) * unit - chunk_cost(p, L, e), per);
 }
 
-// Row `row` of an entity: its request, block row, and vector of q and out
+// x / d by its rounded-up inverse: exact while x * d < 2^32 (rows of an entity
+// stay below 2^19, d is at most 32).
+__device__ __forceinline__ int inv_div(int x, unsigned inv) {
+  return inv == 0 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), inv));
+}
+
+// Row `row` of an entity: its block row, and its vector of q and out
 // ([batch][n][hq]); false past the entity's rows.
 struct RowMap {
-  int e, ng, group, n, G, hq, kvh, rows;
-  __device__ RowMap(const PrefixParams& p, int entity, int kv_head)
-      : e(entity), ng(p.ng), group(p.group), n(p.n), G(p.hq / p.hkv), hq(p.hq), kvh(kv_head),
-        rows((entity < p.ng ? p.group : 1) * p.n * (p.hq / p.hkv)) {}
-  __device__ bool at(int row, int* req, int* i, size_t* vec) const {
+  int req0, n, G, hq, kvh, rows;
+  unsigned inv_n, inv_G;
+  __device__ RowMap(const PrefixParams& p, int e, int kv_head)
+      : req0(e < p.ng ? e * p.group : e - p.ng), n(p.n), G(p.hq / p.hkv), hq(p.hq), kvh(kv_head),
+        rows((e < p.ng ? p.group : 1) * p.n * (p.hq / p.hkv)), inv_n(p.inv_n), inv_G(p.inv_G) {}
+  __device__ __forceinline__ bool at(int row, int* i, size_t* vec) const {
     if (row >= rows) return false;
-    const int h = row % G, bi = row / G;
-    *i = bi % n;
-    *req = e < ng ? e * group + bi / n : e - ng;
-    *vec = (static_cast<size_t>(*req) * n + *i) * hq + kvh * G + h;
+    const int bi = inv_div(row, inv_G), h = row - bi * G;
+    const int r = inv_div(bi, inv_n);
+    *i = bi - r * n;
+    *vec = (static_cast<size_t>(req0) * n + bi) * hq + kvh * G + h;
     return true;
   }
 };

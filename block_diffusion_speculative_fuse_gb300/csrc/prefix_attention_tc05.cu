@@ -379,10 +379,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint4 x[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            int rq, ri;
+            int ri;
             size_t vec;
             x[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (rows.at(row0 + tile * 128 + b + j * RS + r0, &rq, &ri, &vec))
+            if (rows.at(row0 + tile * 128 + b + j * RS + r0, &ri, &vec))
               x[j] = __ldcg(reinterpret_cast<const uint4*>(p.q + vec * D + c * 8));
           }
 #pragma unroll
@@ -400,9 +400,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int my_row = row0 + (split ? r128 : tile * 128 + r128);
       int lim = 0, stale = 0x7FFFFFFF;  // stale: keys from here on hold no data of the request
       {
-        int rq, ri;
+        int ri = 0;
         size_t vec;
-        const bool real = rows.at(my_row, &rq, &ri, &vec);
+        const bool real = rows.at(my_row, &ri, &vec);
         const int base = (pre ? 0 : pl.cut[(e - p.ng) / p.group]) + seg.chunk0 * kChunk;
         const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];
         lim = (real && !pre && p.causal ? ctx - p.n + ri + 1 : ctx) - base;
