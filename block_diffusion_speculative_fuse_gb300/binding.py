@@ -360,8 +360,15 @@ def _space(fn, dev, ws):
     return ws.data_ptr(), ws.nbytes
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, dev):
+    """Handle of a stream, or of the current one (without making a Stream
+    object for it where torch offers that)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
 def _device(fn, t):
@@ -405,7 +412,7 @@ def dflash_kv_rope_append(heads: DflashHeads, rope: DflashRope, layer, q, k, v, 
         ctypes.byref(heads), ctypes.byref(rope), layer, qp, ldq, kp, ldk, vp, ldv,
         0 if dt is _BF16 else 1, qn, kn, eps, _dense(fn, dev, row_req, _I32, (T,)),
         _dense(fn, dev, row_pos, _I32, (T,)), T, op, ldo, ctypes.byref(kv), w, wn,
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def dflash_attention_prefix_bytes(heads: DflashHeads, batch, n, group) -> int:
@@ -430,7 +437,7 @@ def dflash_attention_prefix(heads: DflashHeads, layer, q, batch, n, group, causa
         1 if causal else 0, scale, ctypes.byref(kv), _dense(fn, dev, ctx_len, _I32, (batch,)),
         _dense(fn, dev, prefix_len, _I32, (batch // group,)), _dense(fn, dev, out, _BF16, shape),
         _dense(fn, dev, lse, _F32, (batch, n, hq)) if lse is not None else None, w, wn,
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def dflash_sample_filtered_bytes(rows, vocab) -> int:
@@ -462,4 +469,4 @@ def dflash_sample_filtered(logits, rows, vocab, temperature, top_k, top_p, min_p
         _dense(fn, dev, a, _F64, one), _dense(fn, dev, token, _I32, one),
         _dense(fn, dev, n_kept, _I32, one) if n_kept is not None else None,
         _dense(fn, dev, logprob, _F32, one) if logprob is not None else None, w, wn,
-        _stream(stream)))
+        _stream(stream, dev)))

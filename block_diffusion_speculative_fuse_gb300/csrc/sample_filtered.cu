@@ -72,6 +72,7 @@ struct Shared {
   float f0[kMaxWarps], f1[kMaxWarps];
   float tot0, tot1;
   float ch, cl, scale;               // log2(e)/T as a float pair; bins per unit of z
+  double inv_T, min_p_z, ln_S;       // 1/T; T ln min_p; ln of the kept mass
   unsigned key_m;                    // smallest key that min_p keeps
   int b_lo, b_hi;
   int found;
@@ -692,6 +693,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const float mp = p.min_p != nullptr ? p.min_p[row] : 0.f;
   const double a = p.a[row];
 
+  // (fp64 is slow here: one thread, before the logits have arrived)
+  if (tid == 32) {
+    const double Td = fmax(static_cast<double>(T), 1e-30);
+    if (mp > 0.f) sh->min_p_z = Td * log(fmin(static_cast<double>(mp), 1.0));
+    sh->inv_T = 1.0 / Td;
+  }
+
   // ---- the logits' maximum, and the slice to shared memory
   R.n_loc = max(0, min(slice, V - rank * slice));
   R.vals = p.logits + row * p.ld + static_cast<int64_t>(rank) * slice;
@@ -708,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     mx = max_nan(mx, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
   });
   if constexpr (HELD) R.vals = vals;
-  if (tid == 0) {
+  if (tid == kThreads - 1) {
     // log2(e)/T as a float pair: the quotient, then that of its remainder
     const float t = fmaxf(T, 1e-30f);
     constexpr double L2E = 1.44269504088896340736;
@@ -750,11 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
   if (mp > 0.f) {
     if (tid == 0) {
-      // smallest float z with (z - m) / T >= ln min_p
-      const double Td = fmax(static_cast<double>(T), 1e-30);
-      const double lim = log(fmin(static_cast<double>(mp), 1.0)), md = m;
-      auto ok = [&](float x) { return (static_cast<double>(x) - md) / Td >= lim; };
-      unsigned kz = key_of(static_cast<float>(fmax(md + Td * lim, -static_cast<double>(FLT_MAX))));
+      // smallest float z with z - m >= T ln min_p
+      const double lim = sh->min_p_z, md = m;
+      auto ok = [&](float x) { return static_cast<double>(x) - md >= lim; };
+      unsigned kz = key_of(static_cast<float>(fmax(md + lim, -static_cast<double>(FLT_MAX))));
       const unsigned kmax = top, kmin = key_of(-FLT_MAX);
       while (kz < kmax && !ok(of_key(kz))) ++kz;
       while (kz > kmin && ok(of_key(kz - 1))) --kz;
@@ -846,16 +853,19 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       __syncthreads();
       if (f >= 0) {
         k_bin = f;
-        // the keys of its tokens
-        unsigned lo = ~0u, hi = 0;
-        R.each([&](float z, int) {
-          if (bin_of(R.w, z) != f) return;
-          lo = min(lo, key_of(z));
-          hi = max(hi, key_of(z));
-        });
-        u64 z0 = 0, z1 = 0;
-        R.reduce(z0, z1, lo, hi);
-        bk = R.template border<false>(fn, lo, hi, ku, before, false, [](float, int) { return true; });
+        unsigned lo = 0, hi = ~0u;
+        if (fn > kList) {  // the keys of its tokens
+          lo = ~0u;
+          hi = 0;
+          R.each([&](float z, int) {
+            if (bin_of(R.w, z) != f) return;
+            lo = min(lo, key_of(z));
+            hi = max(hi, key_of(z));
+          });
+          u64 z0 = 0, z1 = 0;
+          R.reduce(z0, z1, lo, hi);
+        }
+        bk = R.template border<false>(fn, lo, hi, ku, before, false, [&](float z, int) { return bin_of(R.w, z) == f; });
       }
     }
     auto in_k = [&](float z, int i) {
@@ -1031,17 +1041,18 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   if (need > S) need = S;
   int idx;
   float z;
-  if (R.locate(buf, need, value, &idx, &z)) {
+  if (tid == kThreads - 32 && p.logprob != nullptr)
+    sh->ln_S = log(static_cast<double>(S)) - (45 - R.w.extra) * 0.693147180559945309417;
+  const bool here = R.locate(buf, need, value, &idx, &z);
+  __syncthreads();
+  if (here) {
     p.token[row] = idx;
     if (p.n_kept != nullptr) {
       if (k > 0 && kept > static_cast<u64>(k)) kept = k;  // K's border lies in the tail
       p.n_kept[row] = static_cast<int32_t>(kept);
     }
-    if (p.logprob != nullptr) {
-      const double Td = fmax(static_cast<double>(T), 1e-30);
-      p.logprob[row] = static_cast<float>((static_cast<double>(z) - static_cast<double>(m)) / Td -
-                                          log(ldexp(static_cast<double>(S), R.w.extra - 45)));
-    }
+    if (p.logprob != nullptr)
+      p.logprob[row] = static_cast<float>((static_cast<double>(z) - static_cast<double>(m)) * sh->inv_T - sh->ln_S);
   }
 }
 
