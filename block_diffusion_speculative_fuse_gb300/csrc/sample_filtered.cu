@@ -1042,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   int idx;
   float z;
   if (tid == kThreads - 32 && p.logprob != nullptr)
-    sh->ln_S = log(static_cast<double>(S)) - (45 - R.w.extra) * 0.693147180559945309417;
+    sh->ln_S = log(static_cast<double>(S) * (R.w.extra ? 0x1p-44 : 0x1p-45));  // one token: exactly 0
   const bool here = R.locate(buf, need, value, &idx, &z);
   __syncthreads();
   if (here) {

@@ -488,6 +488,15 @@ def test_sample_border_past_the_counted_range():
     check_rows(z, [1.0] * 4, [1000, 0, 3999, 2000], None, [0.0, 1e-30, 1e-25, 1e-35])
 
 
+def test_sample_single_token_has_probability_one():
+    """One kept token: its logprob is exactly 0."""
+    g = np.random.default_rng(11)
+    for vocab in (1, 700, 300001):
+        z = g.standard_normal((4, vocab)).astype(np.float32)
+        tok, kept, lp, _, _ = draw_rows(z, [0.8, 0.3, 1.0, 0.0], [1, 1, 1, 1])
+        assert np.array_equal(tok, z.argmax(1)) and np.all(kept == 1) and np.all(lp == 0.0)
+
+
 def test_sample_bad_rows():
     g = np.random.default_rng(8)
     z = g.standard_normal((9, 500)).astype(np.float32)
