@@ -76,10 +76,12 @@ __device__ __forceinline__ void store8_lo(uint16_t* p, const float (&x)[8]) {
 
 // NI: head vectors per thread and round.
 template <int D, typename In, int NI>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 8 : 4) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
   constexpr int TPH = D / 16;          // threads per head vector
   constexpr int HPR = kThreads / TPH;  // head vectors per round and NI
-  __shared__ float2 cs[64];
+  // (cos, sin) of pair 8 s + 2 i + b at [i][s][b]: thread s of a head reads its
+  // eight pairs as four vectors, neighbours next to each other
+  __shared__ float4 cs[4][8];
   griddep_launch_dependents();
   griddep_wait();
   const int t = blockIdx.x;
@@ -124,7 +126,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         const unsigned long long phase = static_cast<unsigned long long>(pos) * p.turns[threadIdx.x];
         float s, c;
         sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f, &s, &c);
-        cs[threadIdx.x] = make_float2(c * p.mscale, s * p.mscale);
+        const int pair = threadIdx.x;
+        reinterpret_cast<float2*>(&cs[pair / 2 % 4][pair / 8])[pair % 2] = make_float2(c * p.mscale, s * p.mscale);
       }
       __syncthreads();
     }
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
 #pragma unroll
         for (int o = TPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (gain != nullptr) {
-          const float r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
           float g0[8], g1[8];
           load8(gain + c0, g0);
           load8(gain + c1, g1);
@@ -162,30 +165,31 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
           }
         }
       }
-      if (!is_v) {
+      if (!is_v && sub < (half + 7) / 8) {
+        float2 w[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = cs[i][sub];
+          w[2 * i] = make_float2(v.x, v.y);
+          w[2 * i + 1] = make_float2(v.z, v.w);
+        }
         if (split) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 w = cs[c0 + j];
             const float a = x[j], b = y[j];
-            x[j] = a * w.x - b * w.y;
-            y[j] = fmaf(a, w.y, b * w.x);
+            x[j] = a * w[j].x - b * w[j].y;
+            y[j] = fmaf(a, w[j].y, b * w[j].x);
           }
         } else if (p.interleaved) {
+          // rot_dim is a multiple of 16: all of a thread's pairs turn, or none
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            if (c0 + j < rot) {
-              const float2 w = cs[(c0 + j) / 2];
-              const float a = x[j], b = x[j + 1];
-              x[j] = a * w.x - b * w.y;
-              x[j + 1] = fmaf(a, w.y, b * w.x);
-            }
-            if (c1 + j < rot) {
-              const float2 w = cs[(c1 + j) / 2];
-              const float a = y[j], b = y[j + 1];
-              y[j] = a * w.x - b * w.y;
-              y[j + 1] = fmaf(a, w.y, b * w.x);
-            }
+            const float a = x[j], b = x[j + 1], c = y[j], d = y[j + 1];
+            const float2 u0 = w[j / 2], u1 = w[4 + j / 2];
+            x[j] = a * u0.x - b * u0.y;
+            x[j + 1] = fmaf(a, u0.y, b * u0.x);
+            y[j] = c * u1.x - d * u1.y;
+            y[j + 1] = fmaf(c, u1.y, d * u1.x);
           }
         }
       }
