@@ -70,15 +70,15 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
   const uint64_t pol = l2_policy_evict_first();  // keys are read once, or by neighbouring workers at once
 
   Segments seg(L, pl.off, ne, worker);
-  while (seg.next(p, L, pl.off)) {
+  while (seg.next(p, L, pl)) {
     // ---- the segment: unit (e, kvh, tile), its pages [pg0, pg1)
     const int e = seg.e, pg0 = seg.chunk0, pg1 = seg.chunk1;
     const int tiles = entity_tiles(p, L, e);
-    const int kvh = seg.ul / tiles, tile = seg.ul % tiles;
+    const int kvh = small_div(seg.ul, tiles), tile = seg.ul - kvh * tiles;
     const int slot = units_before(p, L, e) + seg.ul + worker;
     const bool pre = e < p.ng;
     const int req_t = pre ? pl.live[e] : e - p.ng;               // whose table row
-    const int page0 = pre ? 0 : pl.cut[(e - p.ng) / p.group] / 16;
+    const int page0 = pre ? 0 : pl.cut[inv_div(e - p.ng, p.inv_group)] / 16;
     const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];  // keys at or past it take no part
     const int32_t* table = p.page_table + static_cast<size_t>(req_t) * p.max_pages + page0;
     const RowMap map(p, e, kvh);
@@ -288,10 +288,10 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
   if (on) {
-    const int req = row_q / p.n, i = row_q - req * p.n;
-    const int gi = req / p.group, se = p.ng + req;
+    const int req = inv_div(row_q, p.inv_n), i = row_q - req * p.n;
+    const int gi = inv_div(req, p.inv_group), se = p.ng + req;
     const int G = p.hq / p.hkv;
-    const int kvh = h / G, g = h - kvh * G;
+    const int kvh = inv_div(h, p.inv_G), g = h - kvh * G;
     const PrefixList& P = p.list[p.list[0].prefix_tiles > 0 ? 0 : 1];
     const PrefixList& S = p.list[p.list[0].suffix_tiles > 0 ? 0 : 1];
     const int so_ = __ldcg(S.off + se), su = __ldcg(S.unit + se), sper = __ldcg(S.unit + ne);
@@ -450,14 +450,14 @@ void prefix_attention_shape(PrefixParams* p) {
   p->ng = p->batch / p->group;
   const bool tc_p = p->group > 1 && rows_p > kTcMinRows, tc_s = rows_s > kTcMinRows;
   PrefixList& S = p->list[0];
-  S.chunk_keys = 16;
+  S.chunk_shift = 4;
   S.tile_rows = kSmallRows;
   S.prefix_tiles = tc_p || p->group == 1 ? 0 : (rows_p + kSmallRows - 1) / kSmallRows;
   S.suffix_tiles = tc_s ? 0 : (rows_s + kSmallRows - 1) / kSmallRows;
   S.workers = S.prefix_tiles + S.suffix_tiles > 0 ? kSmallCtas * kSmallWarps : 0;
-  S.prefix_cost = S.suffix_cost = 1;
+  S.prefix_cost = S.suffix_cost = 0;
   PrefixList& T = p->list[1];
-  T.chunk_keys = 128;
+  T.chunk_shift = 7;
   T.tile_rows = 256;
   T.prefix_tiles = tc_p ? (rows_p + 255) / 256 : 0;
   T.suffix_tiles = tc_s ? (rows_s + 255) / 256 : 0;
@@ -465,13 +465,15 @@ void prefix_attention_shape(PrefixParams* p) {
   // up to 128 rows leave half of a tile's tensor work to do
   T.prefix_split = rows_p <= 128;
   T.suffix_split = rows_s <= 128;
-  T.prefix_cost = T.prefix_split ? 1 : 2;
-  T.suffix_cost = T.suffix_split ? 1 : 2;
+  T.prefix_cost = T.prefix_split ? 0 : 1;
+  T.suffix_cost = T.suffix_split ? 0 : 1;
   // a segment's fixed cost (Q, the pipeline's start, the partial) is about that of
   // ten chunks of half a tile
   T.unit_cost = 10;
-  p->inv_n = p->n > 1 ? static_cast<unsigned>((1ull << 32) / p->n + 1) : 0;
-  p->inv_G = G > 1 ? static_cast<unsigned>((1ull << 32) / G + 1) : 0;
+  auto inverse = [](int d) { return d > 1 ? static_cast<unsigned>((1ull << 32) / d + 1) : 0u; };
+  p->inv_n = inverse(p->n);
+  p->inv_G = inverse(G);
+  p->inv_group = inverse(p->group);
 }
 
 cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,

@@ -28,13 +28,13 @@ namespace dflash {
 constexpr int kMaxPrefixBatch = 1024;
 
 struct PrefixList {            // one kernel's share of the work
-  int chunk_keys;              // keys per chunk
+  int chunk_shift;             // log2 of the keys per chunk
   int tile_rows;               // rows per unit
   int workers;
   int prefix_tiles;            // row tiles of a prefix (0: not this kernel's)
   int suffix_tiles;            // row tiles of a request (0: not this kernel's)
   int unit_cost;               // see above; a range is at least one chunk's cost
-  int prefix_cost, suffix_cost;  // of a chunk
+  int prefix_cost, suffix_cost;  // of a chunk: log2
   int prefix_split, suffix_split;  // large tiles: at most 128 rows (see there)
   int* off;                    // [entities + 1] cost before each entity (written for the join)
   int* unit;                   // [entities + 1] cost of one of its units; last: of a worker's range
@@ -53,7 +53,7 @@ struct PrefixParams {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  unsigned inv_n, inv_G;       // for n and hq / hkv: 2^32 / d rounded up (0 for d = 1)
+  unsigned inv_n, inv_G, inv_group;  // for n, hq / hkv and group: 2^32 / d rounded up (0 for d = 1)
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
 };
 
@@ -68,12 +68,28 @@ __device__ __forceinline__ int entity_tiles(const PrefixParams& p, const PrefixL
   return e < p.ng ? L.prefix_tiles : L.suffix_tiles;
 }
 
+// x / d by its rounded-up inverse: exact while x * d < 2^32 (rows of an entity
+// stay below 2^19 with d up to 32, requests and groups below 2^11).
+__device__ __forceinline__ int inv_div(int x, unsigned inv) {
+  return inv == 0 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), inv));
+}
+
+// a / b for 0 <= a, 0 < b and a quotient below 2^20, by way of a float quotient
+// that is off by one at most.
+__device__ __forceinline__ int small_div(int a, int b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  const int r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
+}
+
 __device__ __forceinline__ int chunk_cost(const PrefixParams& p, const PrefixList& L, int e) {
   return e < p.ng ? L.prefix_cost : L.suffix_cost;
 }
 
 __device__ __forceinline__ int cost_per_worker(const PrefixList& L, int total) {
-  return max(max(L.prefix_cost, L.suffix_cost), (total + L.workers - 1) / L.workers);
+  return max(1 << max(L.prefix_cost, L.suffix_cost), (total + L.workers - 1) / L.workers);
 }
 
 // What every CTA works out first, in shared memory.
@@ -82,10 +98,12 @@ struct PrefixPlan {
   int* cut;      // [ng] keys of each group's prefix
   int* live;     // [ng] a request of the group whose page-table row is read for it
   int* off;      // [entities + 1] cost before each entity
+  int* unit;     // [entities] cost of one of its units
   int* scratch;  // [32]
-  __host__ __device__ static int ints(int batch, int ng) { return 2 * batch + 3 * ng + 33; }
+  __host__ __device__ static int ints(int batch, int ng) { return 3 * batch + 4 * ng + 33; }
   __device__ PrefixPlan(int* mem, int batch, int ng)
-      : ctx(mem), cut(ctx + batch), live(cut + ng), off(live + ng), scratch(off + ng + batch + 1) {}
+      : ctx(mem), cut(ctx + batch), live(cut + ng), off(live + ng), unit(off + ng + batch + 1),
+        scratch(unit + ng + batch) {}
 };
 
 // The list, by all threads of a CTA.
@@ -105,7 +123,7 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, con
   __syncthreads();
   if (p.group > 1) {
     for (int r = tid; r < p.batch; r += nt) {
-      const int c = pl.ctx[r], g = r / p.group;
+      const int c = pl.ctx[r], g = inv_div(r, p.inv_group);
       if (c > 0) {
         atomicMin(&pl.cut[g], p.causal ? max(0, c - p.n + 1) : c);
         atomicMin(&pl.live[g], r);
@@ -118,17 +136,13 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, con
   // exclusive scan of the entities' costs, thread t taking a run of them
   const int ne = p.ng + p.batch;
   const int per = (ne + nt - 1) / nt;
-  auto unit_of = [&](int e) {
-    int keys;
-    if (e < p.ng) {
-      keys = pl.cut[e];
-    } else {
-      keys = max(0, pl.ctx[e - p.ng] - pl.cut[(e - p.ng) / p.group]);
-    }
-    const int n = (keys + L.chunk_keys - 1) / L.chunk_keys;
-    return n > 0 ? L.unit_cost + n * chunk_cost(p, L, e) : 0;
+  auto cost = [&](int e) {
+    const int keys = e < p.ng ? pl.cut[e] : max(0, pl.ctx[e - p.ng] - pl.cut[inv_div(e - p.ng, p.inv_group)]);
+    const int n = (keys + (1 << L.chunk_shift) - 1) >> L.chunk_shift;
+    const int unit = n > 0 ? L.unit_cost + (n << chunk_cost(p, L, e)) : 0;
+    pl.unit[e] = unit;
+    return unit * p.hkv * entity_tiles(p, L, e);
   };
-  auto cost = [&](int e) { return unit_of(e) * p.hkv * entity_tiles(p, L, e); };
   const int e0 = min(ne, tid * per), e1 = min(ne, e0 + per);
   int sum = 0;
   for (int e = e0; e < e1; ++e) sum += cost(e);
@@ -144,14 +158,14 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int list, con
   for (int w = 0; w < tid / 32; ++w) run += pl.scratch[w];
   for (int e = e0; e < e1; ++e) {
     pl.off[e] = run;
-    run += cost(e);
+    run += pl.unit[e] * p.hkv * entity_tiles(p, L, e);
   }
   if (tid == nt - 1) pl.off[ne] = run;  // the last thread's run ends at the total
   __syncthreads();
   if (blockIdx.x == 0) {
     for (int e = tid; e <= ne; e += nt) {
       L.off[e] = pl.off[e];
-      L.unit[e] = e < ne ? unit_of(e) : cost_per_worker(L, pl.off[ne]);
+      L.unit[e] = e < ne ? pl.unit[e] : cost_per_worker(L, pl.off[ne]);
     }
   }
 }
@@ -182,18 +196,17 @@ struct Segments {
     end = min(total - c, per) + c;
     e = c < end ? find_entity(off, ne, c) : 0;
   }
-  __device__ bool next(const PrefixParams& p, const PrefixList& L, const int* off) {
+  __device__ bool next(const PrefixParams& p, const PrefixList& L, const PrefixPlan& pl) {
     while (c < end) {
-      while (off[e + 1] <= c) ++e;
-      const int cw = chunk_cost(p, L, e);
-      const int units = p.hkv * entity_tiles(p, L, e);
-      const int unit = (off[e + 1] - off[e]) / units;  // cost of one
-      nch = (unit - L.unit_cost) / cw;
-      ul = (c - off[e]) / unit;
-      const int first = off[e] + ul * unit + L.unit_cost;  // where its chunks start
+      while (pl.off[e + 1] <= c) ++e;
+      const int cw = chunk_cost(p, L, e), half = (1 << cw) - 1;
+      const int unit = pl.unit[e];
+      nch = (unit - L.unit_cost) >> cw;
+      ul = small_div(c - pl.off[e], unit);
+      const int first = pl.off[e] + ul * unit + L.unit_cost;  // where its chunks start
       // chunks whose start lies in [c, end)
-      chunk0 = c > first ? (c - first + cw - 1) / cw : 0;
-      chunk1 = end > first ? min(nch, (end - first + cw - 1) / cw) : 0;
+      chunk0 = c > first ? (c - first + half) >> cw : 0;
+      chunk1 = end > first ? min(nch, (end - first + half) >> cw) : 0;
       c = first - L.unit_cost + unit;
       if (chunk0 < chunk1) return true;
     }
@@ -201,28 +214,12 @@ struct Segments {
   }
 };
 
-// a / b for 0 <= a, 0 < b and a quotient below 2^20, by way of a float quotient
-// that is off by one at most.
-__device__ __forceinline__ int small_div(int a, int b) {
-  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
-  const int r = a - q * b;
-  if (r < 0) --q;
-  if (r >= b) ++q;
-  return q;
-}
-
 // The workers [w0, w1] that have chunks of unit ul of entity e (off_e: the cost
 // before the entity, unit: of one unit, per: of a worker's range).
 __device__ __forceinline__ void unit_workers(const PrefixParams& p, const PrefixList& L, int e, int ul, int off_e,
                                              int unit, int per, int* w0, int* w1) {
   *w0 = small_div(off_e + ul * unit + L.unit_cost, per);
-  *w1 = small_div(off_e + (ul + 1) * unit - chunk_cost(p, L, e), per);
-}
-
-// x / d by its rounded-up inverse: exact while x * d < 2^32 (rows of an entity
-// stay below 2^19, d is at most 32).
-__device__ __forceinline__ int inv_div(int x, unsigned inv) {
-  return inv == 0 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), inv));
+  *w1 = small_div(off_e + (ul + 1) * unit - (1 << chunk_cost(p, L, e)), per);
 }
 
 // Row `row` of an entity: its block row, and its vector of q and out

@@ -182,11 +182,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int at = 0;                                   // planes requested so far
     Cursor cur;
     bool ok = true;
-    while (ok && seg.next(p, L, pl.off)) {
+    while (ok && seg.next(p, L, pl)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
       const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
-      const int kvh = seg.ul / entity_tiles(p, L, e);
-      const int page0 = (pre ? 0 : pl.cut[(e - p.ng) / p.group] / 16) + seg.chunk0 * 8;
+      const int kvh = small_div(seg.ul, entity_tiles(p, L, e));
+      const int page0 = (pre ? 0 : pl.cut[inv_div(e - p.ng, p.inv_group)] / 16) + seg.chunk0 * 8;
       const int pages_end = pre ? pl.cut[e] / 16 : (pl.ctx[e - p.ng] + 15) / 16;
       const int npg = min(n * 8, pages_end - page0);
       const int32_t* table = p.page_table + static_cast<size_t>(pre ? pl.live[e] : e - p.ng) * p.max_pages + page0;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         np[tile] ^= 1;
         return true;
       };
-      while (ok && seg.next(p, L, pl.off)) {
+      while (ok && seg.next(p, L, pl)) {
         const int n = seg.chunk1 - seg.chunk0;
         const bool split = seg.e < p.ng ? L.prefix_split : L.suffix_split;
         ok = mbar_wait(q_full, segs++ & 1, abort_flag);
@@ -363,11 +363,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // are void (the status word says so).
     int at = 0, segs = 0, ns = 0;
     bool ok = true;
-    while (seg.next(p, L, pl.off)) {
+    while (seg.next(p, L, pl)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
       const bool pre = e < p.ng, split = pre ? L.prefix_split : L.suffix_split;
       const int tiles = entity_tiles(p, L, e);
-      const int kvh = seg.ul / tiles, row0 = seg.ul % tiles * L.tile_rows;
+      const int kvh = small_div(seg.ul, tiles), row0 = (seg.ul - kvh * tiles) * L.tile_rows;
       const RowMap rows(p, e, kvh);
       // ---- Q of the segment (split: A's warps load it for both)
       if (tile == 0 || !split) {
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int ri = 0;
         size_t vec;
         const bool real = rows.at(my_row, &ri, &vec);
-        const int base = (pre ? 0 : pl.cut[(e - p.ng) / p.group]) + seg.chunk0 * kChunk;
+        const int base = (pre ? 0 : pl.cut[inv_div(e - p.ng, p.inv_group)]) + seg.chunk0 * kChunk;
         const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];
         lim = (real && !pre && p.causal ? ctx - p.n + ri + 1 : ctx) - base;
         if (ctx % 16) stale = ctx - base;

@@ -234,9 +234,11 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
   for (const PrefixList& L : p.list) {
     const double units = static_cast<double>(p.hkv) *
                          (static_cast<double>(p.ng) * L.prefix_tiles + static_cast<double>(batch) * L.suffix_tiles);
-    const double cost = std::max(L.prefix_cost, L.suffix_cost) *
-                        (static_cast<double>(kv->max_pages) * 16 / L.chunk_keys + 1) + L.unit_cost;
-    if (units * cost >= 2147483648.0) return DFLASH_ERR_UNSUPPORTED;
+    const double cost = (1 << std::max(L.prefix_cost, L.suffix_cost)) *
+                        (static_cast<double>(kv->max_pages) * 16 / (1 << L.chunk_shift) + 1) + L.unit_cost;
+    if (units * cost >= 2147483648.0 ||
+        static_cast<double>(p.hkv) * std::max(L.prefix_tiles, L.suffix_tiles) >= 1048576.0)
+      return DFLASH_ERR_UNSUPPORTED;
   }
   rc = check_ws(ws, ws_bytes, layout_prefix(&p, d, static_cast<uint8_t*>(ws)));
   if (rc) return rc;
