@@ -349,6 +349,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) {
         *abort_flag = 1;
         raise_status(p.status, DFLASH_ERR_TIMEOUT, 524);
+        // the products in flight end before their memory is given back
+        umma_commit(o_full);
+        mbar_wait(o_full, (segs - 1) & 1, nullptr);
       }
     }
   } else {

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 8 : 4) rope_append
   const bool split = !p.interleaved && sub < rot / 16;
   const int c0 = (split ? sub : 2 * sub) * 8;
   const int c1 = split ? c0 + half : c0 + 8;
-  const int pos = __ldg(p.row_pos + t), req = __ldg(p.row_req + t);
+  const int pos = __ldcg(p.row_pos + t), req = __ldcg(p.row_req + t);
 
   bool first = true;
   long long page = -1;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 8 : 4) rope_append
       if (pos < 0) return;  // the whole CTA
       // where the row's K and V go
       if (req >= 0 && req < p.n_req && pos / 16 < p.max_pages)
-        page = __ldg(p.page_table + static_cast<size_t>(req) * p.max_pages + pos / 16);
+        page = __ldcg(p.page_table + static_cast<size_t>(req) * p.max_pages + pos / 16);
       if (page >= p.n_pages) page = -1;
       if (page < 0 && threadIdx.x == 0) raise_status(p.status, DFLASH_ERR_CAPACITY, 501);
       if (threadIdx.x < half) {

@@ -61,8 +61,8 @@ struct Shared {
   float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(46-j/64) in two words
   u64 list[2 * kList];               // candidates: orders, weights
   unsigned hist[kBins];
-  unsigned dist[kBins];              // sums of (distance + 1/2) * 2^14
-  unsigned keys[4][kKeyBins];        // counts; masses in limbs of 16 bits (a slice has fewer than 2^16 logits)
+  unsigned dist[kBins];              // sums of (distance + 1/2) * 2^13: 32 bits hold a whole row's
+  unsigned keys[5][kKeyBins];        // counts; masses in limbs
   u64 xch[2][kMaxCluster][2];        // exchanged values, one row per rank of the cluster
   unsigned xch32[2][kMaxCluster][2];
   u64 wred[kMaxWarps][2];
@@ -295,6 +295,10 @@ struct Row {
   [[maybe_unused]] static constexpr int kWarps = kThreads / 32;
   [[maybe_unused]] static constexpr int BPT = kBins / kThreads;  // steps of t per thread
   [[maybe_unused]] static constexpr unsigned kCand = HELD ? 512 : 4096;  // candidates a CTA keeps aside
+  // A weight (46 bits) is summed per key in limbs of 16 bits when the CTA has a
+  // slice, of fewer than 2^16 logits, and of 12 bits when it has the row: 32
+  // bits hold a limb's sum.
+  [[maybe_unused]] static constexpr int kLimbs = HELD ? 3 : 4, kLimbBits = HELD ? 16 : 12;
   Shared* sh;
   u64 *cand_order, *cand_w;  // [kCand]
   const float* vals;   // this CTA's slice (HELD: padded with -inf to kWarps * cs)
@@ -316,12 +320,12 @@ struct Row {
     if constexpr (HELD) return *reinterpret_cast<const float4*>(vals + o);
     float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     if (vec && o + 3 < n_loc) {
-      v = __ldg(reinterpret_cast<const float4*>(vals + o));
+      v = __ldcg(reinterpret_cast<const float4*>(vals + o));
     } else {
-      if (o < n_loc) v.x = __ldg(vals + o);
-      if (o + 1 < n_loc) v.y = __ldg(vals + o + 1);
-      if (o + 2 < n_loc) v.z = __ldg(vals + o + 2);
-      if (o + 3 < n_loc) v.w = __ldg(vals + o + 3);
+      if (o < n_loc) v.x = __ldcg(vals + o);
+      if (o + 1 < n_loc) v.y = __ldcg(vals + o + 1);
+      if (o + 2 < n_loc) v.z = __ldcg(vals + o + 2);
+      if (o + 3 < n_loc) v.w = __ldcg(vals + o + 3);
     }
     return v;
   }
@@ -553,16 +557,17 @@ struct Row {
     };
     while (n > kList && lo < hi) {
       const int shift = max(0, 32 - __clz(hi - lo) - 8);
-      if (tid < kKeyBins) sh->keys[0][tid] = sh->keys[1][tid] = sh->keys[2][tid] = sh->keys[3][tid] = 0;
+      if (tid < kKeyBins)
+        for (int j = 0; j <= kLimbs; ++j) sh->keys[j][tid] = 0;
       if (tid == 0) sh->found = -1;
       __syncthreads();
       candidates([&](u64 o, u64 x) {
         const unsigned b = (hi - ~static_cast<unsigned>(o >> 32)) >> shift;
         atomicAdd(&sh->keys[0][b], 1u);
         if (MASS) {
-          atomicAdd(&sh->keys[1][b], static_cast<unsigned>(x) & 0xFFFFu);
-          atomicAdd(&sh->keys[2][b], static_cast<unsigned>(x) >> 16);
-          atomicAdd(&sh->keys[3][b], static_cast<unsigned>(x >> 32));
+#pragma unroll
+          for (int j = 0; j < kLimbs; ++j)
+            atomicAdd(&sh->keys[1 + j][b], static_cast<unsigned>(x >> (j * kLimbBits)) & ((1u << kLimbBits) - 1));
         }
       });
       barrier();
@@ -570,11 +575,11 @@ struct Row {
       unsigned cn = 0;
       if (tid < kKeyBins) {
 #pragma unroll
-        for (int j = 0; j < (MASS ? 4 : 1); ++j) {
+        for (int j = 0; j < (MASS ? 1 + kLimbs : 1); ++j) {
           u64 x = 0;
           for (int r = 0; r < nc; ++r) x += nc > 1 ? ld_cluster_u32(&sh->keys[j][tid], r) : sh->keys[j][tid];
           if (j == 0) cn = static_cast<unsigned>(x);
-          else v += x << (16 * (j - 1));
+          else v += x << (kLimbBits * (j - 1));
         }
         if (!MASS) v = cn;
       }
@@ -688,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 
   // ---- settings (used after the first reduction)
   const float T = p.temperature[row];
+  const float Tc = fminf(fmaxf(T, 1e-30f), 1e30f);  // (0 and bad values are dealt with below)
   const int k = p.top_k != nullptr ? p.top_k[row] : 0;
   const float tp = p.top_p != nullptr ? p.top_p[row] : 1.f;
   const float mp = p.min_p != nullptr ? p.min_p[row] : 0.f;
@@ -695,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 
   // (fp64 is slow here: one thread, before the logits have arrived)
   if (tid == 32) {
-    const double Td = fmax(static_cast<double>(T), 1e-30);
+    const double Td = Tc;
     if (mp > 0.f) sh->min_p_z = Td * log(fmin(static_cast<double>(mp), 1.0));
     sh->inv_T = 1.0 / Td;
   }
@@ -718,12 +724,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   if constexpr (HELD) R.vals = vals;
   if (tid == kThreads - 1) {
     // log2(e)/T as a float pair: the quotient, then that of its remainder
-    const float t = fmaxf(T, 1e-30f);
     constexpr double L2E = 1.44269504088896340736;
     constexpr float LH = static_cast<float>(L2E), LL = static_cast<float>(L2E - static_cast<double>(LH));
-    const float ch = LH / t;
+    const float ch = LH / Tc;
     sh->ch = ch;
-    sh->cl = (fmaf(-ch, t, LH) + LL) / t;
+    sh->cl = (fmaf(-ch, Tc, LH) + LL) / Tc;
     sh->scale = ch * ((kBins - 1) / kMaxLog2);
   }
   R.barrier();  // every CTA of the cluster runs before its shared memory is written
@@ -803,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       const int b = bin_of(R.w, z, &d);
       if (b < kBins - 1) {
         atomicAdd(&sh->hist[b], 1u);
-        if (use_p) atomicAdd(&sh->dist[b], static_cast<unsigned>(magic_int(fmaf(d, 16384.f, kMagic + 8192.f))));
+        if (use_p) atomicAdd(&sh->dist[b], static_cast<unsigned>(magic_int(fmaf(d, 8192.f, kMagic + 4096.f))));
       }
     });
     R.barrier();
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
         const int b = BPT * tid + j;
         const float mid = exp2f(-b * step);
         part[j] = b < k_bin ? cnt[j] : 0;
-        low[j] = fmaf(-c, dist[j] * (1.f / 16384.f) - 0.5f * cnt[j], static_cast<float>(cnt[j])) * mid * (1.f - 3e-5f);
+        low[j] = fmaf(-c, dist[j] * (1.f / 8192.f) - 0.5f * cnt[j], static_cast<float>(cnt[j])) * mid * (1.f - 3e-5f);
         high[j] = low[j] * (1.f + 2e-4f);
         if (b >= k_bin || part[j] == 0) low[j] = high[j] = 0.f;
         if (b == k_bin && b < kBins - 1) {

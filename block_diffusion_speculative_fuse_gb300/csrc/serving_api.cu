@@ -156,7 +156,7 @@ int dflash_kv_rope_append(const dflash_heads* heads, const dflash_rope* rope, in
   if ((q_norm != nullptr && !aligned(q_norm, 16)) || (k_norm != nullptr && !aligned(k_norm, 16)))
     return DFLASH_ERR_INVALID_ARG;
   if (rope->rot_dim < 0 || rope->rot_dim % 16 || rope->rot_dim > d) return DFLASH_ERR_UNSUPPORTED;
-  if ((rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->mscale))
+  if ((rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(static_cast<float>(rope->mscale)))
     return DFLASH_ERR_INVALID_ARG;
   rc = check_cache(heads, layer, kv);
   if (!rc) rc = check_ws(ws, ws_bytes, kHeaderBytes);
@@ -230,13 +230,13 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
   if (kv->dtype != 0 || terms_of(heads) != 1) return DFLASH_ERR_UNSUPPORTED;
   if (batch > kv->n_rows) return DFLASH_ERR_CAPACITY;
   const int d = heads->head_dim;
-  // costs are counted in 32 bits
+  // costs are counted in 32 bits, the units of an entity in 20
   for (const PrefixList& L : p.list) {
     const double units = static_cast<double>(p.hkv) *
                          (static_cast<double>(p.ng) * L.prefix_tiles + static_cast<double>(batch) * L.suffix_tiles);
     const double cost = (1 << std::max(L.prefix_cost, L.suffix_cost)) *
                         (static_cast<double>(kv->max_pages) * 16 / (1 << L.chunk_shift) + 1) + L.unit_cost;
-    if (units * cost >= 2147483648.0 ||
+    if (units * cost >= 1073741824.0 ||
         static_cast<double>(p.hkv) * std::max(L.prefix_tiles, L.suffix_tiles) >= 1048576.0)
       return DFLASH_ERR_UNSUPPORTED;
   }
@@ -246,6 +246,7 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
   p.causal = causal;
   p.scale_log2 = static_cast<float>((scale == 0.f ? 1.0 / std::sqrt(static_cast<double>(d)) : scale) *
                                     1.44269504088896340736);
+  if (!std::isfinite(p.scale_log2)) return DFLASH_ERR_INVALID_ARG;
   p.pool = static_cast<const uint16_t*>(kv->pool) + layer_elems(heads, kv) * layer;
   p.page_table = kv->page_table;
   p.max_pages = kv->max_pages;

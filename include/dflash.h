@@ -412,8 +412,12 @@ int dflash_kv_rope_append(const dflash_heads* heads, const dflash_rope* rope, in
  * page id out of range there reads as zeros and is recorded as
  * DFLASH_ERR_CAPACITY (site 521), and so is a ctx_len beyond the page table
  * (site 522; the table's capacity is used).  Positions at or past ctx_len
- * never take part, whatever their pages hold.  K and V of the visible
- * positions must be finite.  batch <= 1024 and <= kv->n_rows, 1 <= n <= 32.
+ * never take part, whatever their pages hold.  q, and K and V of the visible
+ * positions, must be finite (else the rows that see them are undefined, no
+ * others).  batch <= 1024 and <= kv->n_rows, 1 <= n <= 32.  A table of more
+ * than 2^26 pages per request, or a call whose units of work (about
+ * n_kv_heads * batch * max_pages pages in all) pass 2^30, is
+ * DFLASH_ERR_UNSUPPORTED.
  * Scores, softmax statistics and accumulators are fp32; probabilities are
  * rounded to bf16 for the product with V.  Deterministic.
  * ws: initialised, dflash_attention_prefix_bytes(heads, batch, n, group)
@@ -439,7 +443,8 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
  * The draw is that of dflash_sample_rows over the kept tokens: the smallest
  * index with a * S < C (C the running sum of the kept w in index order, S
  * their total, a fp64 [rows] in [0, 1)).  temperature 0 takes the largest
- * logit (lowest index) alone; one below 1e-30 counts as 1e-30.
+ * logit (lowest index) alone; one below 1e-30 counts as 1e-30, one above 1e30
+ * as 1e30.
  * Outputs: token int32; optional n_kept int32 and logprob fp32 (ln of the
  * drawn token's probability among the kept).  Tokens with z = -inf are never
  * kept.  A row without a finite maximum (all -inf, a NaN or +inf in it) or

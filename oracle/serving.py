@@ -76,7 +76,7 @@ def sample(z, temperature, top_k, top_p, min_p, a):
         return -1, 0, 0.0, 1.0
     if temperature == 0:
         return int(np.argmax(z)), 1, 0.0, 1.0
-    t = (z - z.max()) / max(float(temperature), 1e-30)
+    t = (z - z.max()) / min(max(float(temperature), 1e-30), float(np.float32(1e30)))
     order = [int(i) for i in np.lexsort((np.arange(len(z)), -z)) if z[i] > -np.inf]
     if top_k > 0:
         order = order[:top_k]

@@ -532,6 +532,95 @@ def test_sample_row_results_do_not_depend_on_the_batch(rows):
         assert (one[0][0], one[1][0], one[2][0]) == (tok[i], kept[i], lp[i])
 
 
+def long_rows(vocab, rows, special, T, k, p, m, a):
+    """Checks the special rows in a batch that is wide enough to take one CTA
+    per row (the others are filler)."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    z = 3 * torch.randn(rows, vocab, generator=g, device="cuda")
+    at = np.arange(len(special)) * (rows // len(special))
+    z[torch.from_numpy(at).cuda()] = torch.from_numpy(np.stack(special)).cuda()
+
+    def full(x, off):
+        out = np.full(rows, off, np.float64)
+        out[at] = x
+        return out
+    tok, kept, lp, st, _ = draw_rows(z, full(T, 1.0), full(k, 0), full(p, 0.95), full(m, 0.0), full(a, 0.5))
+    f32 = lambda x: float(np.float32(x))  # noqa: E731
+    for j, i in enumerate(at):
+        want = O.sample(special[j], f32(T[j]), int(k[j]), f32(p[j]), f32(m[j]), a[j])
+        assert (tok[i], kept[i]) == want[:2], (j, tok[i], kept[i], want)
+        assert abs(lp[i] - want[2]) <= 2.0 ** -23 * abs(want[2]) + 1e-8
+    return tok, kept, lp, st
+
+
+def test_sample_many_long_rows():
+    """Batches of rows too long to lie in shared memory all at once: borders
+    among a few, among thousands and among tied logits, odd vocabulary."""
+    g = np.random.default_rng(21)
+    vocab = 151937
+    flat = (g.standard_normal((3, vocab)) * 0.2).astype(np.float32)      # thousands of candidates per step
+    peaked = (g.standard_normal((3, vocab)) * 4).astype(np.float32)
+    steps = np.round(g.standard_normal((3, vocab)) * 2).astype(np.float32)
+    equal = np.full(vocab, -7.25, np.float32)
+    holes = peaked[0].copy()
+    holes[g.random(vocab) < 0.7] = -np.inf
+    special = [*flat, *peaked, *steps, equal, holes, peaked[1] * np.float32(0.01)]
+    n = len(special)
+    T = [1.0, 0.7, 2.0] * 4
+    _, _, _, st = long_rows(vocab, 48, special, T, [0, 5000, 0, 0, 40, 0, 0, 30000, 0, 99, 0, 7],
+                            [0.9, 0.5, 0.3, 0.95, 1.0, 0.8, 0.5, 0.7, 1.0, 0.4, 0.9, 0.6],
+                            [0.0, 0.0, 0.0, 0.0, 0.0, 0.01, 0.0, 0.0, 0.2, 0.0, 1e-4, 0.0], g.random(n))
+    assert st == (0, 0)
+    long_rows(vocab, 45, special, T, [0] * n, [1.0] * n, [0.0] * n, g.random(n))
+    special[4] = special[4].copy()
+    special[4][vocab - 1] = np.nan
+    tok, kept, lp, st = long_rows(vocab, 48, special, [0.0] + T[1:], [0] * n, [0.9] * n, [0.0] * n, g.random(n))
+    assert st == (-1, 541) and tok[16] == -1 and kept[16] == 0
+
+
+def test_sample_many_long_rows_with_plateaus():
+    """A top-p border among more than 2^16 logits of the same value, with
+    others a few units in the last place away."""
+    vocab, special, p = 300001, [], []
+    g = np.random.default_rng(22)
+    for x in (-0.3, -1.7, -3.1, -4.03, -5.9, -7.77):
+        z = np.full(vocab, x, np.float32)
+        z[g.random(vocab) < 0.4] = np.nextafter(np.float32(x), np.float32(0))
+        z[12345] = 0.0
+        special.append(z)
+        p.append(0.2 + 0.6 * g.random())
+    n = len(special)
+    long_rows(vocab, 42, special, [1.0] * n, [0] * n, p, [0.0] * n, g.random(n))
+
+
+def test_sample_many_long_rows_with_a_full_step():
+    """More than 2^18 logits within one of the steps that a row's mass is first
+    counted by, and a border close to the step's end."""
+    vocab, many, special, p = 393216, 300000, [], []
+    g = np.random.default_rng(23)
+    ln2 = math.log(2.0)
+    for over in (-0.003, 0.003, -0.001, 0.001):
+        z = np.empty(vocab, np.float32)
+        z[0] = 0.0
+        z[1:many + 1] = -(100 + 0.49) * 46 / 1023 * ln2
+        z[many + 1:] = -(101 + g.integers(1, 9, vocab - many - 1)) * 46 / 1023 * ln2
+        w = np.exp(z.astype(np.float64))
+        p.append((1 + over) * w[:many + 1].sum() / w.sum())
+        special.append(g.permutation(z))
+    n = len(special)
+    long_rows(vocab, 40, special, [1.0] * n, [0] * n, p, [0.0] * n, g.random(n))
+
+
+def test_sample_huge_and_tiny_temperatures():
+    """A temperature outside [1e-30, 1e30] counts as the bound."""
+    g = np.random.default_rng(24)
+    z = (g.standard_normal((6, 5000)) * 1e30).astype(np.float32)
+    z[3:] = np.float32(3e38) * np.sign(z[3:])
+    T = [1e30, 3e38, 1e-38, 1e38, 1e31, 1e-45]
+    check_rows(z, T, None, [0.9] * 6, None, g.random(6))
+    check_rows(z, T, [100] * 6, None, [0.0, 0.3, 0.0, 0.5, 0.0, 0.5], g.random(6))
+
+
 # ----------------------------------------------------------------- together
 def test_decode_steps_together_eager_and_captured():
     """append -> attend -> logits -> sample, three tokens for requests that
