@@ -415,6 +415,67 @@ def test_attention_far_pages():
     assert torch.equal(pool[0, n_pages - 1, :, :, 15], torch.stack((k[0], v[0])))
 
 
+ATTEND_LONG = [
+    (24, 1, 24, 16, 2, 128, True, [6000], [6001 + 40 * i if i % 5 else 0 for i in range(24)]),   # 192 rows, two tiles
+    (300, 1, 300, 4, 1, 64, True, [1504], [1505 + 11 * (i % 40) for i in range(300)]),           # five row tiles
+    (2, 32, 1, 16, 1, 128, True, [0, 0], [5000, 1]),               # 512 rows of one request; rows before the start
+    (2, 7, 2, 12, 1, 128, False, [4090], [4096, 4091]),            # 84 rows, odd and even chunks apart
+    (1024, 1, 1024, 2, 1, 64, True, [160], [1 + i for i in range(1024)]),
+    (1, 1, 1, 8, 8, 128, True, [0], [70001]),                      # more partials than a warp has lanes
+    (1, 32, 1, 16, 16, 64, True, [0], [129]),
+]
+
+
+@pytest.mark.parametrize("batch,n,group,hq,hkv,d,causal,prefix,ctx", ATTEND_LONG)
+def test_attention_long(batch, n, group, hq, hkv, d, causal, prefix, ctx):
+    s = attention_case(batch, n, group, hq, hkv, d, causal, prefix, ctx, layers=2, layer=1, seed=batch + n)
+    assert B_().dflash_get_status(s["ws"]) == (0, 0)
+    check_attention(s, batch, n, hq, d, causal, ctx, layer=1,
+                    requests=range(0, batch, max(1, batch // 40)))
+
+
+def test_attention_bad_page_in_a_shared_prefix():
+    """Its keys read as zeros for every request of the group."""
+    B = B_()
+    ctx = [700 + i for i in range(12)]
+    s = attention_case(12, 1, 12, 16, 2, 128, False, [640], ctx, spoil=False)
+    bad = 20                                 # positions 320 .. 335
+    s["c"].table_d[:, bad] = -7
+    B.dflash_attention_prefix(*s["args"])
+    assert B.dflash_get_status(s["ws"]) == (-3, 521)
+    s["c"].pool[0, s["ids"][0][bad]] = 0     # the oracle's copy of that page
+    check_attention(s, 12, 1, 16, 128, False, ctx)
+
+
+def test_attention_graphs_that_share_a_workspace():
+    """Two captured calls of different shapes, replayed in turn on one stream
+    with lengths that changed since the capture."""
+    B = B_()
+    shapes = [dict(batch=12, n=1, group=12, hq=16, hkv=2, d=128, causal=True, prefix=[640], ctx=[700 + i for i in range(12)]),
+              dict(batch=3, n=4, group=1, hq=8, hkv=2, d=64, causal=True, prefix=[0] * 3, ctx=[90, 40, 200])]
+    cases = [attention_case(**x) for x in shapes]
+    ws = workspace(max(s["args"][-1].nbytes for s in cases))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for s in cases:
+        s["args"] = (*s["args"][:-1], ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            B.dflash_attention_prefix(*s["args"])
+        graphs.append(graph)
+    for cut in (0, 30, 60, 7):
+        ctx = [[max(0, c - cut) for c in x["ctx"]] for x in shapes]
+        for s, graph, c in zip(cases, graphs, ctx):
+            s["out"].fill_(9.0)
+            s["args"][9].copy_(i32(c))
+            graph.replay()
+        torch.cuda.synchronize()
+        for s, x, c in zip(cases, shapes, ctx):
+            check_attention(s, x["batch"], x["n"], x["hq"], x["d"], True, c)
+    assert B.dflash_get_status(ws) == (0, 0)
+
+
 # ----------------------------------------------------------------- sampling
 def draw_rows(z, T, k=None, p=None, m=None, a=None, outputs=True):
     B = B_()
