@@ -12,11 +12,13 @@
 // row again in every pass (the rows in flight fit L2); that saves the cluster's
 // barriers, which cost a row as much as its arithmetic.
 //
-// Weights.  2^-t with t = (m - z) log2(e) / T is evaluated as a 46-bit integer
-// (45 fractional bits): t as an unevaluated float pair, t = j/64 + r with a
-// table of 2^(-j/64) (P. T. P. Tang's table-driven scheme) and the Taylor
-// series of exp(-r ln 2), the parts added in fixed point; relative error
-// 2^-34 per weight and without bias, so a row's sum is good to about 1e-12.
+// Weights.  2^-t with t = (m - z) log2(e) / T is evaluated as an integer with
+// 45 fractional bits: t as an unevaluated float pair, t = j/16 + r with a table
+// of 2^(-j/16) (P. T. P. Tang's table-driven scheme) and the Taylor series of
+// exp(-r ln 2), all as float pairs; relative error 2^-35 per weight and without
+// bias, so a row's sum is good to about 1e-12.  Sixteen entries, because a
+// warp's lanes then read them without bank conflicts; with 64, and a series
+// shorter by a term, the loads took as long as the arithmetic.
 // fp64 would do, but its rate here is a sixty-fourth of fp32's.  Integer sums
 // are exact: results do not depend on how the row is split or in which order
 // atomics arrive.
@@ -58,9 +60,9 @@ constexpr int kMaxCluster = 8;
 static_assert(kMaxSampleVocab / kMaxCluster * 4 + 28672 <= 227 * 1024, "a slice fits shared memory");
 
 struct Shared {
-  float4 tab[64];                    // 2^(-j/64): float pair, then the integer 2^(46-j/64) in two words
+  float tab[32];                     // 2^(-j/16) as float pairs: high parts, then low parts
   u64 list[2 * kList];               // candidates: orders, weights
-  unsigned hist[kBins];
+  unsigned hist[kBins];              // counts by step
   unsigned dist[kBins];              // sums of (distance + 1/2) * 2^13: 32 bits hold a whole row's
   unsigned keys[5][kKeyBins];        // counts; masses in limbs
   u64 xch[2][kMaxCluster][2];        // exchanged values, one row per rank of the cluster
@@ -85,15 +87,15 @@ struct Shared {
   int border_index;
 };
 
-// 2^(-j/64) for the kernel, made on the host
+// 2^(-j/16) for the kernel, made on the host
 struct WeightTable {
-  float4 e[64];
+  float e[32];
 };
 
 struct Weights {
-  const float4* tab;
+  const float* tab;
   float m, ch, cl, scale;
-  int extra;                         // 1: 44 fractional bits
+  unsigned unit;                     // bits of 2^23 (2^22: 44 fractional bits)
 };
 
 // increasing integer key of a float (no NaN); -0 and +0 share one
@@ -120,65 +122,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 constexpr float kLastStep = kMagic + (kBins - 2);
-// The step of t nearest to the logit's, non-decreasing as z falls; *dist = how
-// far past the step's middle, in steps.
-__device__ __forceinline__ int bin_of(const Weights& w, float z, float* dist) {
-  const float dh = w.m - z;
-  const float k = fmaf(dh, w.scale, kMagic);  // one rounding: every pass has the same steps
-  *dist = fmaf(dh, w.scale, kMagic - k);
-  return k <= kLastStep ? magic_int(k) : kBins - 1;
-}
+// The step of t nearest to the logit's, non-decreasing as z falls.
 __device__ __forceinline__ int bin_of(const Weights& w, float z) {
-  float dist;
-  return bin_of(w, z, &dist);
-}
-
-__device__ __forceinline__ long long mad_wide(int a, int b, long long c) {
-  long long r;
-  asm("mad.wide.s32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(b), "l"(c));
-  return r;
-}
-// The table's 46-bit integer plus the two corrections (as magic sums, of units
-// 2^-29 and 2^-37), times 2^-n, rounded to 45 fractional bits.
-__device__ __forceinline__ u64 join_weight(const float4& tj, float ax, float bx, int n) {
-  const u64 fix = (static_cast<u64>(__float_as_uint(tj.w)) << 32) | __float_as_uint(tj.z);
-  const long long R = mad_wide(magic_int(bx), 1 << 9, mad_wide(magic_int(ax), 1 << 17, static_cast<long long>(fix)));
-  return ((static_cast<u64>(R) >> n) + 1) >> 1;
-}
-
-// the weight of logit z <= m, not in the tail (no product is contracted with a
-// sum: weight_of2 gives the same bits)
-__device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
-  // m - z = dh + dl exactly
-  const float dh = w.m - z;
-  const float bb = dh - w.m;
-  const float dl = (w.m - (dh - bb)) + (-z - bb);
-  const float t = __fmul_rn(dh, w.ch);
-  float e = fmaf(dh, w.ch, -t);
-  e = fmaf(dh, w.cl, e);
-  e = fmaf(dl, w.ch, e);
-  const float kx = fmaf(t, 64.f, kMagic);
-  const int k = magic_int(kx);
-  const float r = fmaf(kx - kMagic, -1.f / 64.f, t);
-  // u = -(r + e) ln 2 = uh + ul
-  constexpr double LN2 = 0.693147180559945309;
-  constexpr float LH = static_cast<float>(-LN2);
-  constexpr float LL = static_cast<float>(-LN2 - static_cast<double>(LH));
-  const float uh = __fmul_rn(r, LH);
-  float ul = fmaf(r, LH, -uh);
-  ul = fmaf(r, LL, ul);
-  ul = fmaf(e, LH, ul);
-  const float tail = fmaf(__fmul_rn(uh, uh), fmaf(uh, fmaf(uh, 1.f / 24.f, 1.f / 6.f), 0.5f),
-                          fmaf(uh, ul, ul));  // exp(u) - 1 = uh + tail
-  const float4 tj = w.tab[k & 63];
-  const float ph = __fmul_rn(tj.x, uh);               // below 2^-7
-  float low = fmaf(tj.x, uh, -ph);
-  low = fmaf(tj.y, uh, low);
-  low = fmaf(tj.x, tail, low);              // below 2^-15
-  // to integers: ph in units of 2^-29 (what that leaves goes to low), low of 2^-37
-  const float ax = fmaf(ph, 0x1p29f, kMagic);
-  low += fmaf(ax - kMagic, -0x1p-29f, ph);
-  return join_weight(tj, ax, fmaf(low, 0x1p37f, kMagic), (k >> 6) + w.extra);
+  const float k = fmaf(w.m - z, w.scale, kMagic);  // one rounding: every pass has the same steps
+  return k <= kLastStep ? magic_int(k) : kBins - 1;
 }
 
 // Two fp32 operations in one instruction.
@@ -190,6 +137,7 @@ __device__ __forceinline__ F2 f2(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
 __device__ __forceinline__ void un2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
 __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 r;
@@ -207,48 +155,82 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// weight_of for two logits, to the same bits: a packed product that only a sum
-// uses is fused with it by the compiler, so where that would round differently
-// both write the fma.
-__device__ __forceinline__ void weight_of2(const Weights& w, float z0, float z1, u64* w0, u64* w1) {
-  const F2 neg = f2(-1.f, -1.f), m = f2(w.m, w.m), z = f2(z0, z1), ch = f2(w.ch, w.ch), cl = f2(w.cl, w.cl);
-  const F2 magic = f2(kMagic, kMagic), unmagic = f2(-kMagic, -kMagic);
-  const F2 dh = fma(z, neg, m);
-  const F2 bb = fma(m, neg, dh);
-  const F2 dl = add(fma(fma(bb, neg, dh), neg, m), mul(add(z, bb), neg));
-  const F2 t = mul(dh, ch);
-  F2 e = fma(dh, ch, mul(t, neg));
-  e = fma(dh, cl, e);
-  e = fma(dl, ch, e);
-  const F2 kx = fma(t, f2(64.f, 64.f), magic);
-  const F2 r = fma(add(kx, unmagic), f2(-1.f / 64.f, -1.f / 64.f), t);
+// A weight in two parts, hi 2^-23 + lo 2^-45, as the bits of floats whose last
+// place is one unit: sums of a few hundred may be taken of the bits, modulo 2^32
+// (hi <= 2^23, |lo| <= 2^21).
+constexpr unsigned kHiBits = 0x4B000000u, kLoBits = 0x4B400000u;  // of hi = 0, lo = 0
+struct Parts {
+  unsigned hi, lo;
+  // n: number of weights summed
+  __device__ __forceinline__ u64 sum(unsigned n) const {
+    return (static_cast<u64>(hi - n * kHiBits) << 22) + static_cast<u64>(static_cast<long long>(static_cast<int>(lo - n * kLoBits)));
+  }
+};
+
+// The weights of two logits z <= m that are not in the tail; without `take`, a
+// weight of 0.  All that is written as a product stays one (none is only added
+// to), so that every place this is compiled into gives the same bits.
+__device__ __forceinline__ void weight_parts(const Weights& w, float z0, float z1, bool take0, bool take1, Parts* p0, Parts* p1) {
+  const F2 neg = f2(-1.f), magic = f2(kMagic);
+  const F2 z = f2(take0 ? z0 : w.m, take1 ? z1 : w.m);
+  // z - m = d + dl exactly
+  const F2 d = add(z, f2(-w.m));
+  const F2 b = add(d, f2(w.m));
+  const F2 dl = add(fma(b, neg, z), fma(fma(b, neg, d), neg, f2(-w.m)));
+  // -t = t - e
+  const F2 t = mul(d, f2(w.ch));
+  F2 e = fma(d, f2(-w.ch), t);
+  e = fma(d, f2(-w.cl), e);
+  e = fma(dl, f2(-w.ch), e);
+  // k = 16 n + j nearest to 16 t; r = k / 16 - t
+  const F2 kx = fma(t, f2(-16.f), magic);
+  const F2 r = fma(add(kx, f2(-kMagic)), f2(1.f / 16.f), t);
+  float k[2];
+  un2(kx, k[0], k[1]);
+  float th_[2], tl_[2], sc_[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const unsigned kb = __float_as_uint(k[i]);
+    th_[i] = w.tab[kb & 15];
+    tl_[i] = w.tab[16 + (kb & 15)];
+    // 2^(23 - n), or 0 (of the bits that make kMagic, the shifts leave nothing)
+    sc_[i] = __uint_as_float((i == 0 ? take0 : take1) ? w.unit - ((kb >> 4) << 23) : 0u);
+  }
+  const F2 th = f2(th_[0], th_[1]), tl = f2(tl_[0], tl_[1]), sc = f2(sc_[0], sc_[1]);
+  // u = (r - e) ln 2 = uh - ul
   constexpr double LN2 = 0.693147180559945309;
-  constexpr float LH = static_cast<float>(-LN2);
-  constexpr float LL = static_cast<float>(-LN2 - static_cast<double>(LH));
-  const F2 lh = f2(LH, LH);
-  const F2 uh = mul(r, lh);
-  F2 ul = fma(r, lh, mul(uh, neg));
-  ul = fma(r, f2(LL, LL), ul);
-  ul = fma(e, lh, ul);
-  const F2 tail = fma(mul(uh, uh), fma(uh, fma(uh, f2(1.f / 24.f, 1.f / 24.f), f2(1.f / 6.f, 1.f / 6.f)), f2(0.5f, 0.5f)),
-                      fma(uh, ul, ul));
-  float k0, k1;
-  un2(kx, k0, k1);
-  const int ka = magic_int(k0), kb = magic_int(k1);
-  const float4 ta = w.tab[ka & 63], tb = w.tab[kb & 63];
-  const F2 th = f2(ta.x, tb.x);
-  const F2 ph = mul(th, uh);
-  F2 low = fma(th, uh, mul(ph, neg));
-  low = fma(f2(ta.y, tb.y), uh, low);
-  low = fma(th, tail, low);
-  const F2 ax = fma(ph, f2(0x1p29f, 0x1p29f), magic);
-  low = add(low, fma(add(ax, unmagic), f2(-0x1p-29f, -0x1p-29f), ph));
-  const F2 bx = fma(low, f2(0x1p37f, 0x1p37f), magic);
-  float a0, a1, b0, b1;
-  un2(ax, a0, a1);
-  un2(bx, b0, b1);
-  *w0 = join_weight(ta, a0, b0, (ka >> 6) + w.extra);
-  *w1 = join_weight(tb, a1, b1, (kb >> 6) + w.extra);
+  constexpr float LH = static_cast<float>(LN2), LL = static_cast<float>(LN2 - static_cast<double>(LH));
+  const F2 uh = mul(r, f2(LH));
+  F2 ul = fma(r, f2(-LH), uh);
+  ul = fma(r, f2(-LL), ul);
+  ul = fma(e, f2(LH), ul);
+  // exp(u) - 1 = uh - tail = v + vl
+  const F2 sq = mul(uh, uh);
+  const F2 q = fma(uh, fma(uh, fma(uh, f2(-1.f / 120.f), f2(-1.f / 24.f)), f2(-1.f / 6.f)), f2(-0.5f));
+  const F2 tail = fma(sq, q, fma(fma(sq, f2(0.5f), uh), ul, ul));
+  const F2 v = fma(tail, neg, uh);
+  const F2 vl = fma(tail, neg, fma(v, neg, uh));
+  // (th + tl) exp(u) = s + sl
+  const F2 s = fma(th, v, th);
+  F2 sl = fma(th, v, fma(s, neg, th));
+  sl = fma(tl, v, sl);
+  sl = add(fma(th, vl, sl), tl);
+  // in units of 2^-23, and what is left in units of 2^-45
+  const F2 top = f2(8388608.f);
+  const F2 hi = fma(s, sc, top);
+  const F2 lo = fma(fma(sl, sc, fma(s, sc, fma(hi, neg, top))), f2(0x1p22f), magic);
+  float x0, x1;
+  un2(hi, x0, x1);
+  p0->hi = __float_as_uint(x0);
+  p1->hi = __float_as_uint(x1);
+  un2(lo, x0, x1);
+  p0->lo = __float_as_uint(x0);
+  p1->lo = __float_as_uint(x1);
+}
+__device__ __forceinline__ u64 weight_of(const Weights& w, float z) {
+  Parts p, q;
+  weight_parts(w, z, z, true, true, &p, &q);
+  return p.sum(1);
 }
 
 __device__ __forceinline__ u64 shfl_xor64(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
@@ -686,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   R.nc = nc;
   R.rank = rank;
   R.par = 0;
-  if (tid < 64) sh->tab[tid] = table.e[tid];
+  if (tid < 32) sh->tab[tid] = table.e[tid];
   if (tid == 0) sh->list_n = 0;
   if (tid < kMaxWarps) sh->wadd[tid] = 0;
   griddep_wait();
@@ -779,7 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   R.w.ch = sh->ch;
   R.w.cl = sh->cl;
   R.w.scale = sh->scale;
-  R.w.extra = V > (1 << 18) ? 1 : 0;
+  // (sums of weights stay below 2^64: one bit less for the longest rows)
+  const bool longest = V > (1 << 18);
+  R.w.unit = __float_as_uint(longest ? 0x1p22f : 0x1p23f);
 
   // the kept set: keys above v, and key v up to index vi
   unsigned v = mp > 0.f ? sh->key_m : 0;
@@ -803,13 +787,25 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     // ---- counts by t
     for (int j = tid; j < kBins; j += kThreads) sh->hist[j] = sh->dist[j] = 0;
     __syncthreads();
-    R.each([&](float z, int) {
-      float d;
-      const int b = bin_of(R.w, z, &d);
-      if (b < kBins - 1) {
+    auto count2 = [&](float z0, float z1) {
+      // bin_of's steps, two at a time, and the distances
+      const F2 dh = fma(f2(z0, z1), f2(-1.f), f2(m)), sc = f2(R.w.scale);
+      const F2 k = fma(dh, sc, f2(kMagic));
+      const F2 d = fma(fma(dh, sc, fma(k, f2(-1.f), f2(kMagic))), f2(8192.f), f2(kMagic + 4096.f));
+      float k_[2], d_[2];
+      un2(k, k_[0], k_[1]);
+      un2(d, d_[0], d_[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (!(k_[j] <= kLastStep)) continue;
+        const int b = magic_int(k_[j]);
         atomicAdd(&sh->hist[b], 1u);
-        if (use_p) atomicAdd(&sh->dist[b], static_cast<unsigned>(magic_int(fmaf(d, 8192.f, kMagic + 4096.f))));
+        if (use_p) atomicAdd(&sh->dist[b], static_cast<unsigned>(magic_int(d_[j])));
       }
+    };
+    R.each4([&](const float4& v4, int) {
+      count2(v4.x, v4.y);
+      count2(v4.z, v4.w);
     });
     R.barrier();
     unsigned cnt[BPT], cum[BPT];
@@ -935,7 +931,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       const unsigned n_cand = sh->found_n;
       __syncthreads();
       // K's mass, and the mass above the steps in question; their tokens go aside
-      u64 M = 0, A = 0;
+      // (the sums' parts fit 32 bits: a thread has at most 384 logits, or 256 of 45 bits)
+      Parts sum = {0, 0}, above = {0, 0};
+      unsigned pairs = 0, n_above = 0;
       unsigned lo = ~0u, hi = 0;
       bool overflow = false;
       // steps as bin_of's magic sums, two at a time
@@ -962,23 +960,33 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           t1 = t1 && in_k(z1, i + 1);
         }
         if (!t0 && !t1) return;
-        u64 x0, x1;
-        weight_of2(R.w, t0 ? z0 : m, t1 ? z1 : m, &x0, &x1);
-        x0 = t0 ? x0 : 0;
-        x1 = t1 ? x1 : 0;
-        M += x0 + x1;
-        A += (f0 < f_lo ? x0 : 0) + (f1 < f_lo ? x1 : 0);
+        Parts x0, x1;
+        weight_parts(R.w, z0, z1, t0, t1, &x0, &x1);
+        sum.hi += x0.hi + x1.hi;
+        sum.lo += x0.lo + x1.lo;
+        ++pairs;
+        if (f0 < f_lo) {
+          above.hi += x0.hi;
+          above.lo += x0.lo;
+          ++n_above;
+        }
+        if (f1 < f_lo) {
+          above.hi += x1.hi;
+          above.lo += x1.lo;
+          ++n_above;
+        }
         // (rarely) a candidate
         const bool c0 = t0 && f0 >= f_lo && f0 <= f_hi, c1 = t1 && f1 >= f_lo && f1 <= f_hi;
         if (c0 || c1) {
-          if (c0) put_aside(z0, i, x0);
-          if (c1) put_aside(z1, i + 1, x1);
+          if (c0) put_aside(z0, i, x0.sum(1));
+          if (c1) put_aside(z1, i + 1, x1.sum(1));
         }
       };
       R.each4([&](const float4& v4, int i) {
         pair(v4.x, v4.y, i);
         pair(v4.z, v4.w, i + 2);
       });
+      u64 M = sum.sum(2 * pairs), A = above.sum(n_above);
       sure = A;
       R.reduce(M, A, lo, hi);
       if (n_cand > R.kCand) {  // some CTA may have had more than it can keep aside
@@ -1032,9 +1040,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
           take[t] = in && b < kBins - 1 && (!by_p || b >= p_lo);
         }
         if (!take[0] && !take[1]) continue;
-        u64 x0, x1;
-        weight_of2(R.w, take[0] ? zs[j] : m, take[1] ? zs[j + 1] : m, &x0, &x1);
-        mine += (take[0] ? x0 : 0) + (take[1] ? x1 : 0);
+        Parts x0, x1;
+        weight_parts(R.w, zs[j], zs[j + 1], take[0], take[1], &x0, &x1);
+        mine += x0.sum(1) + x1.sum(1);
       }
     });
   }
@@ -1047,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   int idx;
   float z;
   if (tid == kThreads - 32 && p.logprob != nullptr)
-    sh->ln_S = log(static_cast<double>(S) * (R.w.extra ? 0x1p-44 : 0x1p-45));  // one token: exactly 0
+    sh->ln_S = log(static_cast<double>(S) * (longest ? 0x1p-44 : 0x1p-45));  // one token: exactly 0
   const bool here = R.locate(buf, need, value, &idx, &z);
   __syncthreads();
   if (here) {
@@ -1064,14 +1072,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 const WeightTable& weight_table() {
   static const WeightTable t = [] {
     WeightTable x;
-    for (int j = 0; j < 64; ++j) {
-      const double e = std::exp2(-j / 64.0);
-      const float hi = static_cast<float>(e);
-      const u64 fix = static_cast<u64>(e * 0x1p46 + 0.5);
-      const uint32_t w[2] = {static_cast<uint32_t>(fix), static_cast<uint32_t>(fix >> 32)};
-      float f[2];
-      std::memcpy(f, w, sizeof(f));
-      x.e[j] = make_float4(hi, static_cast<float>(e - static_cast<double>(hi)), f[0], f[1]);
+    for (int j = 0; j < 16; ++j) {
+      const double e = std::exp2(-j / 16.0);
+      x.e[j] = static_cast<float>(e);
+      x.e[16 + j] = static_cast<float>(e - static_cast<double>(x.e[j]));
     }
     return x;
   }();
