@@ -48,8 +48,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
   const PrefixList& L = p.list[0];
   const int ne = p.ng + p.batch;
   const PrefixPlan pl(reinterpret_cast<int*>(smem + kSmallWarps * C::RING), p.batch, p.ng);
+  // After the large-tile kernel there is nothing to wait for: this one starts
+  // only when every CTA of that one has waited for what came before (it lets its
+  // dependents go after that), and the two share no memory.  So the first CTAs
+  // start here while the last still work there.
+  const bool behind_tc = p.list[1].workers > 0;
   griddep_launch_dependents();
-  griddep_wait();
+  if (!behind_tc) griddep_wait();
   prefix_plan(p, 0, pl);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -265,6 +270,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
       }
     }
   }
+  if (behind_tc) griddep_wait();  // the join waits for this kernel, and so for both
 }
 
 // Joins the partials of each vector (row, query head): WPV warps per vector,
