@@ -1115,14 +1115,20 @@ static cudaError_t launch_sample(const SampleFilteredParams& p, int nc, cudaStre
 
 cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s) {
   // CTAs per row: a slice of at most kSlice logits, so that two CTAs fit an SM;
-  // more (down to kMinSlice logits) while the rows leave SMs without work
-  constexpr int kSlice = 20480, kMinSlice = 4096, kResident = 2 * 152;
+  // more, down to kMinSlice logits, while the rows leave SMs without work (one row
+  // of 32000: slices of 4000 17.7 us, of 8000 21.6, of 2000 no faster)
+  constexpr int kSlice = 20480, kMinSlice = 4096, kSms = 152;
   int nc = 1;
   while (nc < kMaxCluster && ((p.vocab + nc - 1) / nc > kSlice ||
-                              (2 * nc * p.rows <= kResident && p.vocab / (2 * nc) >= kMinSlice)))
+                              (2 * nc * p.rows <= 2 * kSms && p.vocab / (2 * nc) >= kMinSlice)))
     nc *= 2;
-  // more clusters than fit at once: see above
-  if (nc > 1 && nc * p.rows > kResident) return launch_sample<1024, false>(p, 1, s);
+  // Clusters take time in proportion to the rows; whole-row CTAs, 152 at a time,
+  // that of 85 rows per round.  Clusters / whole rows, top-p alone: 151936 tokens,
+  // 48 rows 81 / 116 us, 80 rows 117 / 123, 96 rows 134 / 126, 170 rows 218 / 220,
+  // 200 rows 253 / 223, 512 rows 614 / 434; 50000 tokens, 76 rows 50 / 50, 120 rows
+  // 65 / 51.  Clusters of two stay ahead (32000 tokens, 600 rows: 130 / 140).
+  const int rounds = (p.rows + kSms - 1) / kSms;
+  if (nc > 2 && p.rows > 85 * rounds) return launch_sample<1024, false>(p, 1, s);
   return launch_sample<512, true>(p, nc, s);
 }
 

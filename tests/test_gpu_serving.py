@@ -614,7 +614,8 @@ def long_rows(vocab, rows, special, T, k, p, m, a):
     return tok, kept, lp, st
 
 
-def test_sample_many_long_rows():
+@pytest.mark.parametrize("rows", [48, 96])
+def test_sample_many_long_rows(rows):
     """Batches of rows too long to lie in shared memory all at once: borders
     among a few, among thousands and among tied logits, odd vocabulary."""
     g = np.random.default_rng(21)
@@ -628,18 +629,20 @@ def test_sample_many_long_rows():
     special = [*flat, *peaked, *steps, equal, holes, peaked[1] * np.float32(0.01)]
     n = len(special)
     T = [1.0, 0.7, 2.0] * 4
-    _, _, _, st = long_rows(vocab, 48, special, T, [0, 5000, 0, 0, 40, 0, 0, 30000, 0, 99, 0, 7],
+    _, _, _, st = long_rows(vocab, rows, special, T, [0, 5000, 0, 0, 40, 0, 0, 30000, 0, 99, 0, 7],
                             [0.9, 0.5, 0.3, 0.95, 1.0, 0.8, 0.5, 0.7, 1.0, 0.4, 0.9, 0.6],
                             [0.0, 0.0, 0.0, 0.0, 0.0, 0.01, 0.0, 0.0, 0.2, 0.0, 1e-4, 0.0], g.random(n))
     assert st == (0, 0)
-    long_rows(vocab, 45, special, T, [0] * n, [1.0] * n, [0.0] * n, g.random(n))
+    long_rows(vocab, rows - 3, special, T, [0] * n, [1.0] * n, [0.0] * n, g.random(n))
     special[4] = special[4].copy()
     special[4][vocab - 1] = np.nan
-    tok, kept, lp, st = long_rows(vocab, 48, special, [0.0] + T[1:], [0] * n, [0.9] * n, [0.0] * n, g.random(n))
-    assert st == (-1, 541) and tok[16] == -1 and kept[16] == 0
+    tok, kept, lp, st = long_rows(vocab, rows, special, [0.0] + T[1:], [0] * n, [0.9] * n, [0.0] * n, g.random(n))
+    at = 4 * (rows // n)
+    assert st == (-1, 541) and tok[at] == -1 and kept[at] == 0
 
 
-def test_sample_many_long_rows_with_plateaus():
+@pytest.mark.parametrize("rows", [42, 100])
+def test_sample_many_long_rows_with_plateaus(rows):
     """A top-p border among more than 2^16 logits of the same value, with
     others a few units in the last place away."""
     vocab, special, p = 300001, [], []
@@ -651,10 +654,11 @@ def test_sample_many_long_rows_with_plateaus():
         special.append(z)
         p.append(0.2 + 0.6 * g.random())
     n = len(special)
-    long_rows(vocab, 42, special, [1.0] * n, [0] * n, p, [0.0] * n, g.random(n))
+    long_rows(vocab, rows, special, [1.0] * n, [0] * n, p, [0.0] * n, g.random(n))
 
 
-def test_sample_many_long_rows_with_a_full_step():
+@pytest.mark.parametrize("rows", [40, 100])
+def test_sample_many_long_rows_with_a_full_step(rows):
     """More than 2^18 logits within one of the steps that a row's mass is first
     counted by, and a border close to the step's end."""
     vocab, many, special, p = 393216, 300000, [], []
@@ -669,7 +673,7 @@ def test_sample_many_long_rows_with_a_full_step():
         p.append((1 + over) * w[:many + 1].sum() / w.sum())
         special.append(g.permutation(z))
     n = len(special)
-    long_rows(vocab, 40, special, [1.0] * n, [0] * n, p, [0.0] * n, g.random(n))
+    long_rows(vocab, rows, special, [1.0] * n, [0] * n, p, [0.0] * n, g.random(n))
 
 
 def test_sample_huge_and_tiny_temperatures():
