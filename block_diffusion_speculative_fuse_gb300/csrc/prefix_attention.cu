@@ -280,39 +280,43 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
 
 // Joins the partials of each vector (row, query head): WPV warps per vector,
 // warp `sub` taking the partials sub, sub + WPV, ...; the order is fixed.  The
-// bound is the latency of a few dependent loads, so each level of them (the
-// list's offsets, all (m, l), then four O rows at a time) is issued at once.
+// bound is the latency of a few dependent loads, so there are two levels only:
+// the lists' offsets, once per CTA (loaded by every warp they were hot spots of
+// L2, up to 6 us of a call), then (m, l) and O, four rows at a time.
 template <int D, int WPV>
-__global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(256, 5) prefix_join_kernel(const PrefixParams p) {
   constexpr int VEC = D / 32;  // columns per lane
   __shared__ float so[8][D];
   __shared__ float sml[8][2];
-  griddep_launch_dependents();
-  griddep_wait();
+  __shared__ int head[8];  // of the CTA's request: see below
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row_q = blockIdx.y;  // request * n + block row
+  const int req = inv_div(row_q, p.inv_n), i = row_q - req * p.n;
+  const int gi = inv_div(req, p.inv_group), se = p.ng + req;
+  const PrefixList& P = p.list[p.list[0].prefix_tiles > 0 ? 0 : 1];
+  const PrefixList& S = p.list[p.list[0].suffix_tiles > 0 ? 0 : 1];
+  griddep_launch_dependents();
+  griddep_wait();
+  if (threadIdx.x < 7) {
+    const int* src[7] = {S.off + se, S.unit + se, S.unit + p.ng + p.batch, p.ctx_len + req,
+                         P.off + gi, P.unit + gi, P.unit + p.ng + p.batch};
+    const int* from = src[0];
+#pragma unroll
+    for (int j = 1; j < 7; ++j) from = threadIdx.x == j ? src[j] : from;
+    head[threadIdx.x] = threadIdx.x < 4 || P.prefix_tiles > 0 ? __ldcg(from) : 0;
+  }
+  __syncthreads();
   const int h = blockIdx.x * (8 / WPV) + warp / WPV, sub = warp % WPV;
   const bool on = h < p.hq;
   const int vec = row_q * p.hq + h;
-  const int ne = p.ng + p.batch;
   float m = -INFINITY, l = 0.f, acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
   if (on) {
-    const int req = inv_div(row_q, p.inv_n), i = row_q - req * p.n;
-    const int gi = inv_div(req, p.inv_group), se = p.ng + req;
     const int G = p.hq / p.hkv;
     const int kvh = inv_div(h, p.inv_G), g = h - kvh * G;
-    const PrefixList& P = p.list[p.list[0].prefix_tiles > 0 ? 0 : 1];
-    const PrefixList& S = p.list[p.list[0].suffix_tiles > 0 ? 0 : 1];
-    const int so_ = __ldcg(S.off + se), su = __ldcg(S.unit + se), sper = __ldcg(S.unit + ne);
-    int po = 0, pu = 0, pper = 1;
-    if (P.prefix_tiles > 0) {
-      po = __ldcg(P.off + gi);
-      pu = __ldcg(P.unit + gi);
-      pper = __ldcg(P.unit + ne);
-    }
-    const int ctx = clamped_ctx(p, req);
+    const int so_ = head[0], su = head[1], sper = head[2], po = head[4], pu = head[5], pper = head[6];
+    const int ctx = min(max(head[3], 0), p.max_pages * 16);
     const bool sees = (p.causal ? ctx - p.n + i + 1 : ctx) > 0;
     int np = 0, nsu = 0;
     size_t p_at = 0, s_at = 0;  // partial rows of the first worker
@@ -336,18 +340,40 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
     for (int b = sub; b < parts; b += 32 * WPV) {
       const int mine = b + lane * WPV;  // this lane's partial
       const int cnt = min(32, (parts - b + WPV - 1) / WPV);
-      const float* o = nullptr;
+      auto at = [&](int k, const PrefixList** L) {  // row of partial k in its list's buffers
+        const bool pre = k < np;
+        *L = pre ? &P : &S;
+        return pre ? p_at + static_cast<size_t>(k) * P.tile_rows : s_at + static_cast<size_t>(k - np) * S.tile_rows;
+      };
+      float v[4][VEC];
+      auto load4 = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int t = 0; t < VEC; ++t) v[j][t] = 0.f;
+          if (j0 + j < cnt) {
+            const PrefixList* L;
+            const size_t ps = at(b + (j0 + j) * WPV, &L);
+            const float* src = L->part_o + ps * D;
+            if constexpr (VEC == 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+              v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+            } else {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+              v[j][0] = x.x, v[j][1] = x.y;
+            }
+          }
+        }
+      };
       float ms = -INFINITY, ls = 0.f;
       if (mine < parts) {
-        const bool pre = mine < np;
-        const PrefixList& L = pre ? P : S;
-        const size_t ps = pre ? p_at + static_cast<size_t>(mine) * P.tile_rows
-                              : s_at + static_cast<size_t>(mine - np) * S.tile_rows;
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(L.part_ml + ps * 2));
-        o = L.part_o + ps * D;
-        ms = v.x;
-        ls = v.y;
+        const PrefixList* L;
+        const size_t ps = at(mine, &L);
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(L->part_ml + ps * 2));
+        ms = x.x;
+        ls = x.y;
       }
+      load4(0);
       // -inf: the row saw none of that segment's keys, and no O was written
       const float mn = fmaxf(m, warp_max(ms));
       const float ref = mn == -INFINITY ? 0.f : mn;
@@ -358,26 +384,15 @@ __global__ void __launch_bounds__(256, 6) prefix_join_kernel(const PrefixParams 
       for (int j = 0; j < VEC; ++j) acc[j] *= f0;
       m = mn;
       for (int j0 = 0; j0 < cnt; j0 += 4) {
-        float v[4][VEC], wj[4];
+        if (j0 > 0) load4(j0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float* src = reinterpret_cast<const float*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (j0 + j) & 31));
-          wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-          const bool use = j0 + j < cnt && wj[j] > 0.f;
-          if (!use) wj[j] = 0.f;
-          if constexpr (VEC == 4) {
-            const float4 x = use ? __ldcg(reinterpret_cast<const float4*>(src) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
-          } else {
-            const float2 x = use ? __ldcg(reinterpret_cast<const float2*>(src) + lane) : make_float2(0.f, 0.f);
-            v[j][0] = x.x, v[j][1] = x.y;
+          const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+          if (j0 + j < cnt && wj > 0.f) {
+#pragma unroll
+            for (int t = 0; t < VEC; ++t) acc[t] = fmaf(v[j][t], wj, acc[t]);
           }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int t = 0; t < VEC; ++t) acc[t] = fmaf(v[j][t], wj[j], acc[t]);
       }
     }
   }

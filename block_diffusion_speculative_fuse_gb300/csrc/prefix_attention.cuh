@@ -57,9 +57,6 @@ struct PrefixParams {
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
 };
 
-__device__ __forceinline__ int clamped_ctx(const PrefixParams& p, int r) {
-  return min(max(__ldcg(p.ctx_len + r), 0), p.max_pages * 16);
-}
 // Units before entity e of the list (for the slots).
 __device__ __forceinline__ int units_before(const PrefixParams& p, const PrefixList& L, int e) {
   return p.hkv * (min(e, p.ng) * L.prefix_tiles + max(e - p.ng, 0) * L.suffix_tiles);

@@ -10,7 +10,8 @@
 // its slice of the logits in shared memory, so the row is read from memory once
 // however many passes follow.  Many long rows: one CTA per row, which reads the
 // row again in every pass (the rows in flight fit L2); that saves the cluster's
-// barriers, which cost a row as much as its arithmetic.
+// barriers, which cost a row as much as its arithmetic (both sides' times are at
+// the rule, in sample_filtered_launch).
 //
 // Weights.  2^-t with t = (m - z) log2(e) / T is evaluated as an integer with
 // 45 fractional bits: t as an unevaluated float pair, t = j/16 + r with a table
@@ -34,9 +35,13 @@
 // exact masses.  A border that falls on many equal logits is settled by
 // counting them in index order.
 //
-// Bound: for a batch of rows instruction issue (about 45 instructions per
-// weight, evaluated once per token of K), for a few rows the latency of about
-// ten passes, each ending in a cluster barrier.
+// Bound: for many rows instruction issue.  512 rows of 151936 under top-p take
+// 434 us, 0.7 TB/s; a row's 95 us on its SM are 8 for the maximum, 19 for the
+// counts, 47 for the weights (about 75 instructions each, issued at nearly one a
+// cycle) and 20 for the border and the draw.  Cheaper weights (fp32's 2^-22) would
+// halve the 47 but move borders that 64-bit arithmetic puts elsewhere.  For a few
+// rows the latency of about ten passes, each ending in a cluster barrier: one row
+// of 151936 under top-k and top-p takes 26 us, 32 rows with mixed settings 47 us.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -1116,7 +1121,8 @@ static cudaError_t launch_sample(const SampleFilteredParams& p, int nc, cudaStre
 cudaError_t sample_filtered_launch(const SampleFilteredParams& p, cudaStream_t s) {
   // CTAs per row: a slice of at most kSlice logits, so that two CTAs fit an SM;
   // more, down to kMinSlice logits, while the rows leave SMs without work (one row
-  // of 32000: slices of 4000 17.7 us, of 8000 21.6, of 2000 no faster)
+  // of 32000: slices of 16000 21.6 us, of 8000 17.7, of 4000 no faster; nor are
+  // clusters of 16: one row of 151936 26.7 us to 27.3 with 8, nine rows 35.9 to 29.2)
   constexpr int kSlice = 20480, kMinSlice = 4096, kSms = 152;
   int nc = 1;
   while (nc < kMaxCluster && ((p.vocab + nc - 1) / nc > kSlice ||
