@@ -11,7 +11,9 @@
 // ranges favour independent workers over large tiles.  A worker is one warp:
 // a page (16 keys) is a step of two m16n8 score tiles and one k16 step of the
 // product with V, fed by the warp's own ring of pages through cp.async, with
-// no barrier between warps.
+// no barrier between warps.  32 requests of 1024 own keys, 8 KV heads of 128:
+// 68 MB in 16 us (22 alone from cold), 4.2 TB/s; a warp's range is 13 pages, so
+// the plan and the ring's start are a third of it.
 #include <climits>
 
 #include "attention.cuh"
@@ -282,7 +284,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
 // warp `sub` taking the partials sub, sub + WPV, ...; the order is fixed.  The
 // bound is the latency of a few dependent loads, so there are two levels only:
 // the lists' offsets, once per CTA (loaded by every warp they were hot spots of
-// L2, up to 6 us of a call), then (m, l) and O, four rows at a time.
+// L2, up to 6 us of a call), then (m, l) and O, four rows at a time.  1024
+// vectors of about 25 partials: 6 us; 16384 of about 4: 12 us.
 template <int D, int WPV>
 __global__ void __launch_bounds__(256, 5) prefix_join_kernel(const PrefixParams p) {
   constexpr int VEC = D / 32;  // columns per lane
