@@ -30,13 +30,13 @@
 // Bound: with 256 rows (a block verify: 16384 shared keys, 2048 rows on each of
 // 8 KV heads, and 512 own keys for 64 rows of 32 requests) the products: a chunk's
 // four take 1.05 us of the tensor pipe and, S reading Q and K, P V reading V, the
-// loads writing both, 256 KB or 1.05 us of shared memory; it comes every 1.75 us,
-// 128 us in all, 1.07 PFLOP/s.  The loads are never waited for (pairs of CTAs
-// sharing them by multicast changed nothing), and a tile's softmax, 0.7 us, runs
-// under the other's products.  With up to 128 rows (a decode of the same prefix:
-// 67 MB in 20 us, 3.4 TB/s) the pipeline's start in each CTA's one or two segments
-// of about seven chunks.  One tile over alternating chunks there takes 53 us a
-// call where two tiles, half of them empty, take 59.
+// loads writing both, 256 KB or 1.05 us of shared memory; it comes every 1.4-1.5
+// us, 112 us in all, 1.25 PFLOP/s.  The loads are never waited for, and a tile's
+// softmax, 0.7 us, runs under the other's products; the hand-overs between them
+// are the rest.  With up to 128 rows (a decode of the same prefix: 67 MB in 20 us,
+// 3.4 TB/s) the pipeline's start in each CTA's one or two segments of about seven
+// chunks.  One tile over alternating chunks there takes 53 us a call where two
+// tiles, half of them empty, take 59.
 #include "common.cuh"
 #include "kernels.h"
 #include "prefix_attention.cuh"

@@ -423,6 +423,8 @@ ATTEND_LONG = [
     (1024, 1, 1024, 2, 1, 64, True, [160], [1 + i for i in range(1024)]),
     (1, 1, 1, 8, 8, 128, True, [0], [70001]),                      # more partials than a warp has lanes
     (1, 32, 1, 16, 16, 64, True, [0], [129]),
+    (20, 16, 20, 8, 2, 128, True, [640], [656 + 7 * i for i in range(20)]),   # 1280 rows of 128, requests of 64
+    (8, 16, 8, 8, 1, 128, False, [2048], [2048] * 8),              # nothing but the prefix
 ]
 
 
