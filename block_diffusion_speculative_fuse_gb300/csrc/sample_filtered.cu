@@ -492,6 +492,45 @@ struct Row {
     return false;
   }
 
+  // Adds a token to the list in rank 0's shared memory.
+  __device__ __forceinline__ void push(u64 order, u64 weight) {
+    u64 *orders = sh->list, *weights = sh->list + kList;
+    if (nc > 1) {
+      const unsigned at = add_cluster_u32(&sh->list_n, 0, 1);
+      if (at < kList) {
+        st_cluster_u64(&orders[at], 0, order);
+        st_cluster_u64(&weights[at], 0, weight);
+      }
+    } else {
+      const unsigned at = atomicAdd(&sh->list_n, 1u);
+      if (at < kList) {
+        orders[at] = order;
+        weights[at] = weight;
+      }
+    }
+  }
+
+  // Sums of two values over the threads of this CTA.
+  __device__ void sum_cta(u64& s0, u64& s1) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s0 += shfl_xor64(s0, o);
+      s1 += shfl_xor64(s1, o);
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sh->wred[warp][0] = s0;
+      sh->wred[warp][1] = s1;
+    }
+    __syncthreads();
+    s0 = s1 = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      s0 += sh->wred[i][0];
+      s1 += sh->wred[i][1];
+    }
+  }
+
   // Of the admitted logits with this key, the index of the c-th in index
   // order (INT_MAX if there are no more than c).
   template <typename In>
@@ -595,21 +634,7 @@ struct Row {
     // ---- the list, in rank 0's shared memory
     u64* orders = sh->list;
     u64* weights = sh->list + kList;
-    candidates([&](u64 o, u64 x) {
-      if (nc > 1) {
-        const unsigned at = add_cluster_u32(&sh->list_n, 0, 1);
-        if (at < kList) {
-          st_cluster_u64(&orders[at], 0, o);
-          st_cluster_u64(&weights[at], 0, x);
-        }
-      } else {
-        const unsigned at = atomicAdd(&sh->list_n, 1u);
-        if (at < kList) {
-          orders[at] = o;
-          weights[at] = x;
-        }
-      }
-    });
+    candidates([&](u64 o, u64 x) { push(o, x); });
     barrier();
     if (rank == 0) {
       // TPC threads per candidate, each summing a part of what precedes it
@@ -859,6 +884,60 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
       __syncthreads();
       if (f >= 0) {
         k_bin = f;
+        if (before + fn <= kList) {
+          // K is among a few tokens: rank 0 settles the row from a list of them
+          R.each([&](float z, int i) {
+            if (bin_of(R.w, z) <= f) R.push(order_of(key_of(z), i), weight_of(R.w, z));
+          });
+          R.barrier();
+          if (rank != 0) return;
+          const u64* orders = sh->list;
+          u64* weights = sh->list + kList;
+          constexpr int TPC = kThreads / kList;  // threads per token, each summing a part
+          const int c = tid / TPC, cnt = static_cast<int>(sh->list_n);
+          const bool on = c < cnt, one = tid % TPC == 0;
+          const u64 mine = on ? orders[c] : 0, wm = on ? weights[c] : 0;
+          u64 mass = 0;  // of what precedes it
+          unsigned pos = 0;
+          for (int j = tid % TPC; j < cnt; j += TPC) {
+            const bool less = orders[j] < mine;
+            mass += less ? weights[j] : 0;
+            pos += less;
+          }
+#pragma unroll
+          for (int o = TPC / 2; o > 0; o >>= 1) {
+            mass += shfl_xor64(mass, o);
+            pos += __shfl_xor_sync(0xffffffffu, pos, o);
+          }
+          bool keep = on && pos < ku;
+          u64 M = keep && one ? wm : 0, none = 0;
+          R.sum_cta(M, none);
+          if (use_p) {
+            u64 need = static_cast<u64>(ceil(static_cast<double>(fmaxf(tp, 0.f)) * static_cast<double>(M)));
+            keep = keep && mass < max(min(need, M), 1ull);
+          }
+          const unsigned key = ~static_cast<unsigned>(mine >> 32), idx = static_cast<unsigned>(mine);
+          keep = keep && key >= v;
+          u64 S = keep && one ? wm : 0, kept = keep && one ? 1 : 0;
+          R.sum_cta(S, kept);  // (its barriers: all weights have been read)
+          if (on && one && !keep) weights[c] = 0;
+          if (tid == kThreads - 32 && p.logprob != nullptr)
+            sh->ln_S = log(static_cast<double>(S) * (longest ? 0x1p-44 : 0x1p-45));
+          __syncthreads();
+          u64 sum = 0;  // of the kept up to it, in index order
+          for (int j = tid % TPC; j < cnt; j += TPC) sum += static_cast<unsigned>(orders[j]) <= idx ? weights[j] : 0;
+#pragma unroll
+          for (int o = TPC / 2; o > 0; o >>= 1) sum += shfl_xor64(sum, o);
+          const u64 need = min(static_cast<u64>(a * static_cast<double>(S)) + 1, S);
+          if (keep && one && need <= sum && sum - wm < need) {
+            p.token[row] = static_cast<int32_t>(idx);
+            if (p.n_kept != nullptr) p.n_kept[row] = static_cast<int32_t>(kept);
+            if (p.logprob != nullptr)
+              p.logprob[row] =
+                  static_cast<float>((static_cast<double>(of_key(key)) - static_cast<double>(m)) * sh->inv_T - sh->ln_S);
+          }
+          return;
+        }
         unsigned lo = 0, hi = ~0u;
         if (fn > kList) {  // the keys of its tokens
           lo = ~0u;
