@@ -34,18 +34,21 @@
 // they are first split by their exact 32-bit key, eight bits a pass, with the
 // exact masses.  A border that falls on many equal logits is settled by
 // counting them in index order.
+// And where the steps up to top-k's border hold no more tokens than the list,
+// one CTA settles the whole row from a list of those.
 //
 // Bound: for many rows instruction issue.  512 rows of 151936 under top-p take
 // 434 us, 0.7 TB/s; a row's 95 us on its SM are 8 for the maximum, 19 for the
 // counts, 47 for the weights (about 75 instructions each, issued at nearly one a
 // cycle) and 20 for the border and the draw.  Cheaper weights (fp32's 2^-22) would
 // halve the 47 but move borders that 64-bit arithmetic puts elsewhere.  For a few
-// rows the latency of about ten passes, each ending in a cluster barrier: one row
-// of 151936 under top-k and top-p takes 26 us, 32 rows with mixed settings 47 us.
+// rows the latency of the passes, each ending in a cluster barrier: one row of
+// 151936 takes 31 us under top-p alone, about ten passes, and 17 under top-k 50
+// and top-p, five passes and a list (26 without the list); 32 rows with mixed
+// settings 48 us.
 #include <cfloat>
 #include <climits>
 #include <cmath>
-#include <cstring>
 
 #include "common.cuh"
 #include "kernels.h"
