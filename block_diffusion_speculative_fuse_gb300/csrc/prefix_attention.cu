@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
     const int req_t = pre ? pl.live[e] : e - p.ng;               // whose table row
     const int page0 = pre ? 0 : pl.cut[inv_div(e - p.ng, p.inv_group)] / 16;
     const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];  // keys at or past it take no part
+    const int common = pre || !p.causal ? ctx : ctx - p.n + 1;  // keys before it are seen by all rows
     const int32_t* table = p.page_table + static_cast<size_t>(req_t) * p.max_pages + page0;
     const RowMap map(p, e, kvh);
 
@@ -179,10 +180,25 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
       const uint32_t vb = kb + C::PAGE;
       st_use = st_use == C::STAGES - 1 ? 0 : st_use + 1;
       const int key0 = (page0 + pg) * 16;
-      if (key0 + 16 > ctx) {
-        // rows at or past the context hold whatever was there: 0 * V must be 0
-        for (int i = lane; i < 16 * (D / 8); i += 32)
-          if (key0 + i / (D / 8) >= ctx) st_shared_u4(vb + swz<D>(i / (D / 8), i % (D / 8)), make_uint4(0u, 0u, 0u, 0u));
+      if (key0 + 16 > common) {
+        // 0 * V must be 0.  Positions at or past the context hold whatever was
+        // there; of those that only some rows see, what is not finite goes, and
+        // the rows that see it get a NaN by way of l
+        int bad = INT_MAX;
+        for (int i = lane; i < 16 * (D / 8); i += 32) {
+          const int key = key0 + i / (D / 8);
+          if (key < common) continue;
+          const uint32_t at = vb + swz<D>(i / (D / 8), i % (D / 8));
+          if (key < ctx) {
+            if (!bf16_not_finite(ld_shared_u4(at))) continue;
+            bad = min(bad, key);
+          }
+          st_shared_u4(at, make_uint4(0u, 0u, 0u, 0u));
+        }
+        bad = __reduce_min_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (lim[h] > bad) l_r[h] = __int_as_float(0x7FFFFFFF);
         __syncwarp();
       }
       // S = Q K^T: keys 0-7 and 8-15, each in two independent sums

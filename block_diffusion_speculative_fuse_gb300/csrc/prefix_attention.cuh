@@ -243,6 +243,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Whether one of eight bf16 is infinite or NaN: the carry out of a full exponent.
+__device__ __forceinline__ bool bf16_not_finite(uint4 v) {
+  auto full = [](uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; };
+  return ((full(v.x) | full(v.y) | full(v.z) | full(v.w)) & 0x80008000u) != 0u;
+}
+
 // Large tiles (prefix_attention_tc05.cu).  map: the pool as [rows / 8][d / 64][8
 // rows][64 columns], box one 16-row page.
 constexpr int kTcCtas = 152;

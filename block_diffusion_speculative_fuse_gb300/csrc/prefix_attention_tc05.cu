@@ -27,6 +27,12 @@
 // through one ring in the order in which the MMAs use them, each released by
 // the MMA that read it last.
 //
+// 0 * V must be 0, so before its product the issuing warp goes over the part of V
+// that a row may not see (clean_v): past the context it puts zeros; among the keys
+// of the block's own rows it puts them for what is not finite, and the rows that do
+// see such a key get a NaN in the end.  A block verify takes 130.3 us without and
+// 131.1 with it; done by the softmax warps, which have no registers to spare, 134.
+//
 // Bound: with 256 rows (a block verify: 16384 shared keys, 2048 rows on each of
 // 8 KV heads, and 512 own keys for 64 rows of 32 requests) the products: a chunk's
 // four take 1.05 us of the tensor pipe and, S reading Q and K, P V reading V, the
@@ -37,6 +43,8 @@
 // 3.4 TB/s) the pipeline's start in each CTA's one or two segments of about seven
 // chunks.  One tile over alternating chunks there takes 53 us a call where two
 // tiles, half of them empty, take 59.
+#include <climits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "prefix_attention.cuh"
@@ -141,8 +149,38 @@ struct Cursor {
 // Place of a segment's planes in the ring's order (n chunks): two tiles per
 // chunk K0 V0 K1 V1 ...; split K0 K1 V0 K2 V1 K3 ...
 __device__ __forceinline__ int place_k(bool split, int c) { return split ? c + max(0, c - 1) : 2 * c; }
-__device__ __forceinline__ int place_v(bool split, int c, int n) {
-  return split ? c + min(n, c + 2) : 2 * c + 1;
+// Of a V plane (one warp): makes the keys [first, live) finite and those from live
+// to the end of its page zero.  The lane's first key that was not finite, else
+// kChunk.  Not inlined: its code in the issuing warp's loop made a block verify 3
+// to 15 us longer even where it was not run.
+template <int D>
+__device__ __noinline__ int clean_v(uint8_t* plane, int first, int live) {
+  constexpr int HALVES = TcCfg<D>::HALVES, PIECES = HALVES * 8;  // 16-byte pieces of a key
+  auto piece = [&](int i) {
+    const int key = i / PIECES, half = i / 8 % HALVES;
+    return reinterpret_cast<uint4*>(plane + (key / 8) * (HALVES * 1024) + half * 1024 + (key % 8) * 128 +
+                                    (((i ^ key) & 7) << 4));
+  };
+  const int lane = threadIdx.x % 32;
+  const int i0 = max(first, 0) * PIECES + lane, i1 = min(live, kChunk) * PIECES;
+  bool found = false;
+#pragma unroll 8
+  for (int i = i0; i < i1; i += 32) found |= bf16_not_finite(*piece(i));
+  int bad = kChunk;
+  if (__any_sync(0xffffffffu, found)) {
+#pragma unroll 1
+    for (int i = i0; i < i1; i += 32) {
+      if (!bf16_not_finite(*piece(i))) continue;
+      bad = min(bad, i / PIECES);
+      *piece(i) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+#pragma unroll 1
+  for (int i = max(live, 0) * PIECES + lane; i < min((live + 15) & ~15, kChunk) * PIECES; i += 32)
+    *piece(i) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+  return bad;
 }
 
 template <int D>
@@ -159,12 +197,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* s_full = empty + C::MAX_SLOTS;  // [2] S of a tile is complete (and the PV before it)
   uint64_t* p_full = s_full + 2;            // [2][2] P of a tile is in TMEM: upper, lower 64 keys
   uint64_t* q_full = p_full + 4;            // Q of the segment is in shared memory
-  uint64_t* o_full = q_full + 1;            // all of the segment's products are complete
+  uint64_t* o_full = q_full + 1;            // all of the segment's products are complete; bad_key
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* bad_key = abort_flag + 1;   // the segment's first key with a V that is not finite
   const PrefixList& L = p.list[1];
   const int ne = p.ng + p.batch;
-  const PrefixPlan pl(reinterpret_cast<int*>(tmem_slot + 2), p.batch, p.ng);
+  const PrefixPlan pl(reinterpret_cast<int*>(tmem_slot + 4), p.batch, p.ng);
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
@@ -178,8 +217,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&p_full[2 * t + 1], 4);
     }
     mbar_init(q_full, 8);
-    mbar_init(o_full, 1);
+    mbar_init(o_full, 2);
     *abort_flag = 0;
+    *bad_key = INT_MAX;
     fence_barrier_init();
     tma_prefetch_desc(&map);
   }
@@ -273,11 +313,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t q_addr = smem_u32(sm), ring_addr = smem_u32(ring);
       int segs = 0;
       int np[2] = {0, 0};  // parity of the next P of each tile
+      int bad = INT_MAX;   // see above
       bool ok = true;
       Cursor cur;          // the next plane: they are used in the order they arrive
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) umma_commit(bar);
         __syncwarp();
+      };
+      // the end of a segment
+      auto finish = [&]() {
+        bad = __reduce_min_sync(0xffffffffu, bad);
+        if (lane == 0) {
+          *bad_key = bad;
+          mbar_arrive(o_full);
+        }
+        commit(o_full);
       };
       // waits for the next plane and takes it: its slot, or -1
       auto take = [&]() {
@@ -319,9 +369,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         np[tile] ^= 1;
         return true;
       };
+      int tail = INT_MAX;  // from this key of the segment on V is gone over
+      const int hidden = p.causal ? p.n - 1 : 0;
+      auto clean = [&](int c, int st) {
+        if ((c + 1) * kChunk > tail) {
+          const int first = tail - c * kChunk;
+          const int b = clean_v<D>(ring + st * C::PLANE, first, first + hidden);
+          if (b < kChunk) bad = min(bad, c * kChunk + b);
+        }
+      };
       while (ok && seg.next(p, L, pl)) {
         const int n = seg.chunk1 - seg.chunk0;
         const bool split = seg.e < p.ng ? L.prefix_split : L.suffix_split;
+        tail = bad = INT_MAX;
+        if (seg.e >= p.ng) {  // (a prefix is whole pages that all rows see)
+          const int r = seg.e - p.ng, ctx = pl.ctx[r];
+          if (hidden > 0 || ctx % 16) tail = ctx - hidden - pl.cut[inv_div(r, p.inv_group)] - seg.chunk0 * kChunk;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(q_full, segs++ & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
@@ -335,6 +399,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           for (int c = 0; ok && c < n; ++c) {
             const int t = c & 1, iv = take();
+            if (iv >= 0) clean(c, iv);
             ok = iv >= 0 && issue_pv(t, iv, c >= 2);
             if (!ok) break;
             commit(&empty[iv]);
@@ -357,6 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; ok && c < n; ++c) {
             const bool more = c + 1 < n;
             const int iv = take();
+            if (iv >= 0) clean(c, iv);
             ok = iv >= 0 && issue_pv(0, iv, c > 0);
             if (!ok) break;
             if (more) {
@@ -374,13 +440,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        if (ok) commit(o_full);
+        if (ok) finish();
       }
       if (!ok) {
         *abort_flag = 1;
         if (lane == 0) raise_status(p.status, DFLASH_ERR_TIMEOUT, 524);
         // the products in flight end before their memory is given back
-        commit(o_full);
+        finish();
         mbar_wait(o_full, (segs - 1) & 1, nullptr);
       }
     }
@@ -394,7 +460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // After a wait that gave up, a warp goes on through the segments without
     // waiting, so that all warps meet at the same named barriers; the results
     // are void (the status word says so).
-    int at = 0, segs = 0, ns = 0;
+    int segs = 0, ns = 0;
     bool ok = true;
     while (seg.next(p, L, pl)) {
       const int e = seg.e, n = seg.chunk1 - seg.chunk0;
@@ -431,7 +497,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(q_full);
       // keys this row sees, from the segment's first
       const int my_row = row0 + (split ? r128 : tile * 128 + r128);
-      int lim = 0, stale = 0x7FFFFFFF;  // stale: keys from here on hold no data of the request
+      int lim = 0;
       {
         int ri = 0;
         size_t vec;
@@ -439,7 +505,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int base = (pre ? 0 : pl.cut[inv_div(e - p.ng, p.inv_group)]) + seg.chunk0 * kChunk;
         const int ctx = pre ? pl.cut[e] : pl.ctx[e - p.ng];
         lim = (real && !pre && p.causal ? ctx - p.n + ri + 1 : ctx) - base;
-        if (ctx % 16) stale = ctx - base;
       }
       float m = -INFINITY, l = 0.f;
       for (int c = split ? tile : 0; ok && c < n; c += split ? 2 : 1) {
@@ -494,23 +559,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l *= alpha;
         }
         if (raise) m = mc;
-        if ((c + 1) * kChunk > stale) {
-          // the page the context ends in holds whatever was there past it: 0 * V must be 0
-          const int iv = at + place_v(split, c, n);
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[iv % slots], (iv / slots) & 1, abort_flag))) {
-            ok = false;
-            break;
-          }
-          uint8_t* vp = ring + (iv % slots) * C::PLANE;
-          for (int i = tid % 128; i < 16 * C::HALVES * 8; i += 128) {
-            const int key = (stale - c * kChunk) / 16 * 16 + i / (C::HALVES * 8);
-            const int hf = i / 8 % C::HALVES, c16 = i % 8;
-            if (key >= stale - c * kChunk && key < kChunk)
-              *reinterpret_cast<uint4*>(vp + (key / 8) * (C::HALVES * 1024) + hf * 1024 + (key % 8) * 128 +
-                                        ((c16 ^ (key & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
         // P = exp2(scale S - m) in bf16.  The upper 64 keys first, still in
         // registers: the product with V starts on them while the lower 64,
         // read again from TMEM, are formed.
@@ -553,6 +601,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) ok = false;
       ++segs;
       tc_fence_after();
+      if (lim > *bad_key) l = __int_as_float(0x7FFFFFFF);
       // ---- partial of the segment.  O goes through shared memory (the Q
       // tiles are free now: a quarter of one for each warp's 32 rows, half a row
       // at a time) so that rows are written to global memory whole.  Split: B
@@ -635,7 +684,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // the next Q overwrites the stages: all of the tiles' warps are done
       asm volatile("bar.sync 5, 256;" ::: "memory");
       tc_fence_before();
-      at += 2 * n;
     }
     if (!ok) {
       *abort_flag = 1;
@@ -652,7 +700,7 @@ cudaError_t launch(const CUtensorMap& map, int group0, int oob_group, const Pref
   using C = TcCfg<D>;
   constexpr int kMax = 227 * 1024;
   // barriers and flags, the plan, slack for the alignment
-  const int fixed = (2 * C::MAX_SLOTS + 8) * 8 + 8 + PrefixPlan::ints(p.batch, p.ng) * 4 + 1024;
+  const int fixed = (2 * C::MAX_SLOTS + 8) * 8 + 16 + PrefixPlan::ints(p.batch, p.ng) * 4 + 1024;
   int slots = (kMax - fixed - 2 * C::Q_TILE) / C::PLANE;
   if (slots > C::MAX_SLOTS) slots = C::MAX_SLOTS;
   const int smem = fixed + 2 * C::Q_TILE + slots * C::PLANE;
