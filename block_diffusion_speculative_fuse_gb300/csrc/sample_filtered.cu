@@ -778,14 +778,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
   if (mp > 0.f) {
     if (tid == 0) {
-      // smallest float z with z - m >= T ln min_p
+      // the smallest float z with z - m >= T ln min_p, by its key: from the nearest
+      // float in steps that double until it is between two of them, then by halves
+      // (where m and T ln min_p cancel, the differences of up to 10^9 floats round to
+      // the same double)
       const double lim = sh->min_p_z, md = m;
-      auto ok = [&](float x) { return static_cast<double>(x) - md >= lim; };
-      unsigned kz = key_of(static_cast<float>(fmax(md + lim, -static_cast<double>(FLT_MAX))));
-      const unsigned kmax = top, kmin = key_of(-FLT_MAX);
-      while (kz < kmax && !ok(of_key(kz))) ++kz;
-      while (kz > kmin && ok(of_key(kz - 1))) --kz;
-      sh->key_m = kz;
+      auto ok = [&](unsigned key) { return static_cast<double>(of_key(key)) - md >= lim; };
+      unsigned lo = key_of(-FLT_MAX), hi = top;  // (m itself passes)
+      unsigned at = min(max(key_of(static_cast<float>(fmax(md + lim, -static_cast<double>(FLT_MAX)))), lo), hi);
+      const bool down = ok(at);
+      if (down) hi = at;
+      else lo = at + 1;
+      for (unsigned step = 1; lo < hi; step *= 2) {
+        at = down ? hi - min(step, hi - lo) : lo + min(step - 1, hi - 1 - lo);
+        const bool in = ok(at);
+        if (in) hi = at;
+        else lo = at + 1;
+        if (in != down) break;
+      }
+      while (lo < hi) {
+        at = lo + (hi - lo) / 2;
+        if (ok(at)) hi = at;
+        else lo = at + 1;
+      }
+      sh->key_m = lo;
     }
     __syncthreads();
   }

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_serving import PAGE, B_, attention_case, built, check_attention  # noqa: F401
+from test_gpu_serving import (PAGE, B_, attention_case, built, check_attention, check_rows,  # noqa: F401
+                              workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,40 @@ def test_attention_keys_that_only_later_rows_see_may_hold_anything(batch, n, gro
                 if plane == 1:
                     assert not torch.isfinite(s["out"][sees]).all(-1).any(), (r, back)
     assert tries > 0 and B.dflash_get_status(s["ws"]) == (0, 0)
+
+
+# ----------------------------------------------------------------- sampling
+CANCEL = [  # largest logit, temperature, min_p (found by search): m + T ln min_p is 0 in double precision
+    ("0x1.3c68dep+1", "0x1.19999ap-1", "0x1.6e0b3p-7"), ("0x1.1df886p+3", "0x1.8p-1", "0x1.c0b5c6p-18"),
+    ("0x1.94c292p+0", "0x1.733334p+0", "0x1.58250cp-2"), ("0x1.c47a38p+2", "0x1.e66666p-1", "0x1.3345a6p-11"),
+    ("0x1.014df8p+4", "0x1.19999ap+0", "0x1.e08158p-22"),
+]
+
+
+@pytest.mark.parametrize("vocab", [300, 40000])
+def test_sample_min_p_border_at_a_logit_of_zero(vocab):
+    """The differences from the largest logit of hundreds of millions of floats
+    around 0 round to the border; it is found in a bounded number of steps."""
+    m, T, mp = (np.array([float.fromhex(c[i]) for c in CANCEL]) for i in range(3))
+    assert np.array_equal(m, m.astype(np.float32)) and np.all(np.abs(m + T * np.log(mp)) <= 2.0 ** -52 * m)
+    g = np.random.default_rng(31)
+    rows = len(CANCEL)
+    z = (g.standard_normal((rows, vocab)) * 0.5).astype(np.float32)
+    z = np.minimum(z, (m[:, None] * 0.9).astype(np.float32))
+    # close to the border, but farther than the double's rounding
+    z[:, 10:30] = np.geomspace(1e-9, 1e-5, 20) * np.where(np.arange(20) % 2, 1, -1)
+    z[:, 7] = m
+    check_rows(z, T, None, None, mp)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    B = B_()
+    zt, out = torch.from_numpy(z).cuda(), torch.empty(rows, dtype=torch.int32, device="cuda")
+    to = lambda x, t: torch.from_numpy(x.astype(t)).cuda()  # noqa: E731
+    args = (to(T, np.float32), None, None, to(mp, np.float32), to(np.full(rows, 0.3), np.float64))
+    ws = workspace(B.dflash_sample_filtered_bytes(rows, vocab))
+    torch.cuda.synchronize()
+    start.record()
+    B.dflash_sample_filtered(zt, rows, vocab, *args, out, None, None, ws)
+    end.record()
+    end.synchronize()
+    # 6 10^8 steps of an fp64 subtraction would take seconds, a bounded search microseconds
+    assert start.elapsed_time(end) < 50.0
