@@ -89,8 +89,12 @@ def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u:
     """Autoregressive decoding with filtered sampling (dflash_sample_filtered),
     one target forward per token.  u [batch][n_tokens]: the draws' uniforms in
     [0, 1).  The settings are numbers or one value per request.  keep_logits:
-    a list that receives each step's logits (host)."""
+    a list that receives each step's logits (host).  Prompt and tokens must fit
+    runner.max_len (but for the last token, which is not fed back); an error
+    that the device recorded is raised at the end."""
     b, P = prompts.shape
+    if P - 1 + n_tokens > runner.max_len:
+        raise B.DflashError(f"sample_generate ({P} + {n_tokens} tokens, room for {runner.max_len})", -3)
     dev, vocab = runner.device, runner.shape.vocab
 
     def per_request(x, dtype):
@@ -113,9 +117,13 @@ def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u:
             keep_logits.append(logits.cpu().numpy())
         tok = res[i].view(b, 1)
         pos += 1
-    status, site = B.dflash_get_status(ws)
-    if status != 0:
-        raise B.DflashError(f"dflash_sample_filtered (site {site})", status)
+    used = [("dflash_target_forward", runner.workspace(n))
+            for n in sorted({P - 1, 1 if n_tokens > 0 else 0} - {0})]
+    for fn, w in used + [("dflash_sample_filtered", ws)]:
+        status, site = B.dflash_get_status(w)
+        if status != 0:
+            B.dflash_workspace_init(w)   # the runner stays usable
+            raise B.DflashError(f"{fn} (site {site})", status)
     return res.T.contiguous().cpu().numpy()
 
 

@@ -90,3 +90,40 @@ def test_sample_min_p_border_at_a_logit_of_zero(vocab):
     end.synchronize()
     # 6 10^8 steps of an fp64 subtraction would take seconds, a bounded search microseconds
     assert start.elapsed_time(end) < 50.0
+
+
+# --------------------------------------------------------------- generation
+def tiny_model():
+    import workload as W
+    from block_diffusion_speculative_fuse_gb300.device import DeviceModel
+    t = W.get_workload("tiny_e2e").target
+    return t, DeviceModel(t, W.target_weights(t, 71, std=0.05), W.shared_weights(t, 71, std=0.05), draft=False)
+
+
+@pytest.mark.parametrize("where", [0, -1])     # in the prompt's own pass, in the first step
+def test_sampled_generation_reports_the_target_forwards_errors(where):
+    from block_diffusion_speculative_fuse_gb300.generate import TargetRunner, sample_generate
+    t, model = tiny_model()
+    good = np.random.default_rng(2).integers(0, t.vocab, (2, 5)).astype(np.int32)
+    u = np.random.default_rng(3).random((2, 3))
+    runner = TargetRunner(model, 2, 32, 5)
+    want = sample_generate(runner, good, 3, u)
+    bad = good.copy()
+    bad[1, where] = t.vocab                    # no such token: recorded, token 0 in its place
+    with pytest.raises(B_().DflashError) as e:
+        sample_generate(runner, bad, 3, u)
+    assert e.value.code == -1 and "302" in str(e.value)
+    assert np.array_equal(sample_generate(runner, good, 3, u), want)
+
+
+def test_sampled_generation_fills_the_runner_and_no_more():
+    from block_diffusion_speculative_fuse_gb300.generate import TargetRunner, sample_generate
+    t, model = tiny_model()
+    prompts = np.random.default_rng(2).integers(0, t.vocab, (2, 5)).astype(np.int32)
+    u = np.random.default_rng(3).random((2, 29))
+    want = sample_generate(TargetRunner(model, 2, 64, 5), prompts, 28, u)
+    runner = TargetRunner(model, 2, 32, 5)     # positions 0 .. 31: the last token's is not needed
+    assert np.array_equal(sample_generate(runner, prompts, 28, u), want)
+    with pytest.raises(B_().DflashError) as e:
+        sample_generate(runner, prompts, 29, u)
+    assert e.value.code == -3
