@@ -93,6 +93,10 @@ def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u:
     runner.max_len (but for the last token, which is not fed back); an error
     that the device recorded is raised at the end."""
     b, P = prompts.shape
+    u = np.asarray(u, np.float64)
+    if b != runner.batch or P < 1 or u.ndim != 2 or u.shape[0] != b or u.shape[1] < n_tokens:
+        raise ValueError(f"prompts {prompts.shape} and u {u.shape}: {runner.batch} requests of one token "
+                         f"or more, {n_tokens} uniforms each")
     if P - 1 + n_tokens > runner.max_len:
         raise B.DflashError(f"sample_generate ({P} + {n_tokens} tokens, room for {runner.max_len})", -3)
     dev, vocab = runner.device, runner.shape.vocab
@@ -101,7 +105,7 @@ def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u:
         return torch.as_tensor(np.broadcast_to(np.asarray(x), (b,)).copy()).to(dev, dtype)
     settings = (per_request(temperature, torch.float32), per_request(top_k, torch.int32),
                 per_request(top_p, torch.float32), per_request(min_p, torch.float32))
-    uniforms = torch.as_tensor(np.ascontiguousarray(np.asarray(u, np.float64).T)).to(dev)
+    uniforms = torch.as_tensor(np.ascontiguousarray(u.T)).to(dev)
     logits = torch.empty((b, vocab), dtype=torch.float32, device=dev)
     ws = torch.empty(B.dflash_sample_filtered_bytes(b, vocab), dtype=torch.uint8, device=dev)
     B.dflash_workspace_init(ws)

@@ -21,3 +21,11 @@ def test_sampled_generation_refuses_more_positions_than_the_runner_has():
     with pytest.raises(B.DflashError) as e:
         sample_generate(Runner(), np.zeros((2, 10), np.int32), 8, np.zeros((2, 8)))
     assert e.value.code == -3
+
+
+@pytest.mark.parametrize("prompts,u", [((1, 4), (1, 3)), ((3, 4), (3, 3)), ((2, 0), (2, 3)), ((2, 4), (1, 3)),
+                                       ((2, 4), (3, 3)), ((2, 4), (2, 2)), ((2, 4), (6,))])
+def test_sampled_generation_refuses_shapes_the_target_would_misread(prompts, u):
+    """The target's forward reads and writes rows for all of the runner's requests."""
+    with pytest.raises(ValueError):
+        sample_generate(Runner(), np.zeros(prompts, np.int32), 3, np.zeros(u))
