@@ -52,6 +52,17 @@ size_t layer_elems(const dflash_heads* h, const dflash_kv* kv) {
   return static_cast<size_t>(kv->n_pages) * 2 * terms_of(h) * h->n_kv_heads * 16 * h->head_dim;
 }
 
+// The fraction of a turn that the angle f is, in units of 2^-64, off by one at most
+// for f up to 1e9: the quotient by 2 pi as two doubles (the first alone is off by
+// 286 units at f = 1, and loses what its whole turns take).
+unsigned long long turn_fraction(double f) {
+  constexpr double kTwoPiLow = 2.449293598294706414e-16;  // 2 pi - kTwoPi
+  const double q = f / kTwoPi;
+  const double low = (std::fma(-q, kTwoPi, f) - q * kTwoPiLow) / kTwoPi;
+  auto units = [](double t) { return static_cast<unsigned long long>(std::ldexp(t - std::floor(t), 64)); };
+  return low < 0.0 ? units(q) - units(-low) : units(q) + units(low);
+}
+
 // Workspace of the prefix attention: header, the lists' chunk offsets, then
 // the partial results.  Returns the bytes; fills the pointers when base is set.
 size_t layout_prefix(PrefixParams* p, int d, uint8_t* base) {
@@ -166,8 +177,7 @@ int dflash_kv_rope_append(const dflash_heads* heads, const dflash_rope* rope, in
   for (int j = 0; j < rope->rot_dim / 2; ++j) {
     const double f = rope->inv_freq[j];
     if (!(f >= 0.0) || !std::isfinite(f)) return DFLASH_ERR_INVALID_ARG;
-    const double turns = f / kTwoPi;
-    p.turns[j] = static_cast<unsigned long long>(std::ldexp(turns - std::floor(turns), 64));
+    p.turns[j] = turn_fraction(f);
   }
   p.q = q;
   p.k = k;

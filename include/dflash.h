@@ -384,7 +384,7 @@ int dflash_rope_init(dflash_rope* rope, int32_t rot_dim, int32_t interleaved, do
  * written.  The (request, position) pairs of one call must be distinct.
  * ws: an initialised workspace of at least 64 KiB; only its status word is
  * used.  The angle is formed modulo one turn in 64-bit fixed point, so far
- * positions lose nothing; norms and rotations are fp32. */
+ * positions lose nothing (frequencies up to 1e9); norms and rotations are fp32. */
 int dflash_kv_rope_append(const dflash_heads* heads, const dflash_rope* rope, int32_t layer,
                           const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                           int64_t ld_v, int32_t in_dtype, const void* q_norm, const void* k_norm,

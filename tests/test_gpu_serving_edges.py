@@ -1,11 +1,14 @@
 """Serving operators on the GPU: calls that their documentation allows and
 that once gave wrong results."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
 
 from test_gpu_serving import (PAGE, B_, attention_case, built, check_attention, check_rows,  # noqa: F401
-                              workspace)
+                              heads, i32, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +130,39 @@ def test_sampled_generation_fills_the_runner_and_no_more():
     with pytest.raises(B_().DflashError) as e:
         sample_generate(runner, prompts, 29, u)
     assert e.value.code == -3
+
+
+# ------------------------------------------------------------------- append
+def test_append_angles_of_far_positions_and_high_frequencies():
+    """The angle pos * inv_freq modulo a turn, where pos * inv_freq passes what a
+    double holds: frequencies of up to 1e9, positions of up to 2^24."""
+    B = B_()
+    T, d, cols = 48, 128, 1 << 20
+    g = np.random.default_rng(41)
+    rope = B.dflash_rope_init(d)
+    f = np.concatenate((10.0 ** g.uniform(3, 9, 40), 10.0 ** g.uniform(-6, 3, 20), [0.0, 1e9, 2 * math.pi, 1.0]))
+    for p, x in enumerate(f):
+        rope.inv_freq[p] = float(x)
+    pos = np.concatenate(([0, 1, cols * PAGE - 1], g.integers(1 << 20, cols * PAGE, T - 3)))
+    # a pool page for every table column that is used
+    table = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
+    used = sorted({int(p) // PAGE for p in pos})
+    table[0, torch.tensor(used).cuda()] = torch.arange(len(used), dtype=torch.int32, device="cuda")
+    pool = torch.zeros(1, len(used), 4, 1, PAGE, d, dtype=torch.bfloat16, device="cuda")
+    kv = B.DflashKV(pool=pool.data_ptr(), page_table=table.data_ptr(), n_pages=len(used), max_pages=cols, n_rows=1,
+                    dtype=0, scales=None)
+    k = torch.zeros(T, 1, d, device="cuda")
+    k[..., :d // 2] = 1.0                      # (1, 0) turns to (cos, sin)
+    ws = workspace()
+    B.dflash_kv_rope_append(heads(1, 1, 1, d, 2), rope, 0, None, k, k, i32(np.zeros(T)), i32(pos), T, None, kv, ws)
+    assert B.dflash_get_status(ws) == (0, 0)
+    got = pool.double().cpu().numpy()
+    turn = 2 * Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+    for t, at in enumerate(pos):
+        page, slot = used.index(int(at) // PAGE), at % PAGE
+        x = got[0, page, 0, 0, slot] + got[0, page, 2, 0, slot]
+        part = [Fraction(float(v)) * int(at) / turn for v in f]
+        a = np.array([float((q - math.floor(q)) * turn) for q in part])
+        # two bf16 terms: 2^-16 of the value; the angle: 2^-22 rad
+        assert np.all(np.abs(x[:d // 2] - np.cos(a)) <= 2.0 ** -16 * np.abs(np.cos(a)) + 2.0 ** -21), at
+        assert np.all(np.abs(x[d // 2:] - np.sin(a)) <= 2.0 ** -16 * np.abs(np.sin(a)) + 2.0 ** -21), at
