@@ -451,12 +451,14 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
  * with a setting that is NaN, a temperature that is negative or infinite, or
  * a outside [0, 1) gives token -1, n_kept 0, logprob 0 and records
  * DFLASH_ERR_INVALID_ARG (site 541); the other rows are drawn as usual.
- * Weights and sums are fixed point with 45 fractional bits (44 above 2^18
- * tokens), summed exactly, so the result does not depend on any order; a
- * weight below 2^-46 of the largest counts as zero mass.  A decision can
- * differ from exact arithmetic only when its border is met within about 1e-11
- * (relative, 1e-9 where nearly all tokens are about that far below the
- * largest).  1 <= vocab <= 393216 (else DFLASH_ERR_UNSUPPORTED), ld >= vocab.
+ * Weights (good to 2^-35 of themselves) and sums are fixed point with 45
+ * fractional bits (44 above 2^18 tokens), summed exactly, so the result does
+ * not depend on any order; a weight below about 2^-46 of the largest (2^-45
+ * above 2^18 tokens) counts as zero mass.  So every sum is within 2^-35 of
+ * itself, and within vocab * 1.5e-14 of the largest weight (vocab * 2.9e-14
+ * above 2^18 tokens: 1.1e-8 at most), of the exact one, and a decision can
+ * differ from exact arithmetic only where the sums that it compares are that
+ * close.  1 <= vocab <= 393216 (else DFLASH_ERR_UNSUPPORTED), ld >= vocab.
  * ws: initialised, dflash_sample_filtered_bytes(rows, vocab) bytes. */
 size_t dflash_sample_filtered_bytes(int32_t rows, int32_t vocab);
 int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_t vocab,
