@@ -166,3 +166,37 @@ def test_append_angles_of_far_positions_and_high_frequencies():
         # two bf16 terms: 2^-16 of the value; the angle: 2^-22 rad
         assert np.all(np.abs(x[:d // 2] - np.cos(a)) <= 2.0 ** -16 * np.abs(np.cos(a)) + 2.0 ** -21), at
         assert np.all(np.abs(x[d // 2:] - np.sin(a)) <= 2.0 ** -16 * np.abs(np.sin(a)) + 2.0 ** -21), at
+
+
+@pytest.mark.parametrize("vocab,rows", [(50001, 96), (151936, 200), (300001, 90)])
+def test_sample_rows_of_a_wide_batch_are_those_of_single_calls(vocab, rows):
+    """Bit for bit, for batches so wide that a row is one CTA's and is read again
+    in every pass (more than 85 rows a round of SMs, of more than 40960 tokens),
+    against calls in which a cluster holds it: all settings, flat, peaked and tied
+    logits, holes."""
+    B = B_()
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    rnd = np.random.default_rng(vocab)
+    z = torch.randn(rows, vocab, generator=g, device="cuda") * torch.linspace(0.2, 5.0, rows, device="cuda")[:, None]
+    z[::7] = torch.round(z[::7])
+    z[3::9, ::3] = float("-inf")
+    z[5] = 0.25
+    to = lambda x, t: torch.from_numpy(np.asarray(x).astype(t)).cuda()  # noqa: E731
+    pick = lambda xs: np.array(xs)[rnd.integers(0, len(xs), rows)]      # noqa: E731
+    T = to(pick([0.0, 0.5, 0.8, 1.0, 1.3]), np.float32)
+    k = to(pick([0, 0, 1, 50, 200, 300, 20000, vocab]), np.int32)
+    p = to(pick([1.0, 1.0, 0.3, 0.9, 0.95, 0.999]), np.float32)
+    m = to(pick([0.0, 0.0, 0.02, 1e-6]), np.float32)
+    a = to(rnd.random(rows), np.float64)
+    ws = workspace(B.dflash_sample_filtered_bytes(rows, vocab))
+
+    def call(i, n):
+        out = [torch.empty(n, dtype=t, device="cuda") for t in (torch.int32, torch.int32, torch.float32)]
+        s = slice(i, i + n)
+        B.dflash_sample_filtered(z[s], n, vocab, T[s], k[s], p[s], m[s], a[s], *out, ws)
+        return out
+    wide = call(0, rows)
+    single = [torch.cat(x) for x in zip(*(call(i, 1) for i in range(rows)))]
+    for x, y in zip(wide, single):
+        assert torch.equal(x, y)
+    assert B.dflash_get_status(ws) == (0, 0)
