@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import serving as O
 from test_gpu_serving import (PAGE, B_, attention_case, built, check_attention, check_rows,  # noqa: F401
                               heads, i32, workspace)
 
@@ -200,3 +201,40 @@ def test_sample_rows_of_a_wide_batch_are_those_of_single_calls(vocab, rows):
     for x, y in zip(wide, single):
         assert torch.equal(x, y)
     assert B.dflash_get_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("d,rot,inter,norm", [(128, 128, False, True), (64, 48, True, True), (128, 64, False, False)])
+def test_append_error_of_the_norm_and_the_rotation(d, rot, inter, norm):
+    """Two-term store of fp32 rows.  In units of 2^-24 of the pair's magnitude:
+    the angle 3.4 (2^-22.2 rad), sine and cosine 2, mscale 1, the rotation 3;
+    with a norm the mean square's 8 (up to 20 roundings, halved by the root),
+    its inverse root 4 and two products 2: 24 in all, below 2^-19; the store
+    2^-16 of the value."""
+    B = B_()
+    T, hkv = 300, 4
+    g = torch.Generator(device="cuda").manual_seed(d + rot)
+    k, v = (5 * torch.randn(T, hkv, d, generator=g, device="cuda") for _ in range(2))
+    gain = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16)
+    pages = (T + PAGE - 1) // PAGE
+    pool = torch.zeros(1, pages, 4, hkv, PAGE, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    kv = B.DflashKV(pool=pool.data_ptr(), page_table=table.data_ptr(), n_pages=pages, max_pages=pages, n_rows=1,
+                    dtype=0, scales=None)
+    rope = B.dflash_rope_init(rot, inter, scaling="yarn", factor=4.0, orig_ctx=256)
+    ws = workspace()
+    B.dflash_kv_rope_append(heads(1, 4, hkv, d, 2), rope, 0, None, k, v, i32(np.zeros(T)), i32(np.arange(T)), T, None,
+                            kv, ws, k_norm=gain if norm else None)
+    assert B.dflash_get_status(ws) == (0, 0)
+    got = pool.double().cpu().numpy()[0].transpose(1, 0, 3, 2, 4).reshape(4, -1, hkv, d)[:, :T]
+    x = k.double().cpu().numpy()
+    if norm:
+        x = O.rms_norm(x, gain.double().cpu().numpy(), float(np.float32(1e-6)))
+    f, mag = O.rope_freqs(rot, 1e6, "yarn", 4.0, 256)
+    e = O.rotate(x, np.arange(T), f, mag, inter)
+    size = np.abs(x)
+    i = np.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    size[..., a] = size[..., b] = mag * np.hypot(x[..., a], x[..., b])
+    assert np.all(np.abs(got[0] + got[2] - e) <= 2.0 ** -16 * np.abs(e) + 2.0 ** -19 * size)
+    vd = v.double().cpu().numpy()
+    assert np.all(np.abs(got[1] + got[3] - vd) <= 2.0 ** -16 * np.abs(vd))
