@@ -32,7 +32,10 @@ constexpr int kSmallRows = 16;
 // not known here).  Small / large, us a call, 8 KV heads of 128: a prefix of 8192
 // keys, 32 rows 24.3 / 27.2, 48 rows 27.7 / 28.5, 128 rows 41.4 / 30.3; 16 or 32
 // requests' own keys, 32 rows of 64 keys 13.2 / 23.8, of 600 keys 37.1 / 36.0, of
-// 2048 keys 49.5 / 35.4, 64 rows of 2048 keys 88.3 / 38.0.
+// 2048 keys 49.5 / 35.4, 64 rows of 2048 keys 88.3 / 38.0.  At 17 to 32 rows the
+// small tiles lose with the length, because the second tile of 16 rows fetches the
+// keys again: 32 requests, 32 rows, 608 keys 29.7 / 33.3, 2048 keys 90.2 / 60.5,
+// 16384 keys 616 / 325.
 constexpr int kTcMinRows = 32;
 
 template <int D>
@@ -236,7 +239,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
       }
       // the reference maximum moves, and O and l with it, only when exceeded by
-      // 2^8 (P stays below 2^8; its rounding to bf16 is relative)
+      // 2^8 (P stays below 2^8; its rounding to bf16, the type of V, is relative:
+      // the output is off by 2.2e-3 rms of its values where the rounding of the
+      // output alone makes 1.7e-3)
       const bool up0 = mx[0] > m_r[0] + 8.f, up1 = mx[1] > m_r[1] + 8.f;
       if (__any_sync(0xffffffffu, up0 || up1)) {
         const float f0 = up0 ? ex2(m_r[0] - mx[0]) : 1.f, f1 = up1 ? ex2(m_r[1] - mx[1]) : 1.f;

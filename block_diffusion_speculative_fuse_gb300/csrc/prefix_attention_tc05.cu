@@ -16,8 +16,10 @@
 // Softmax: a thread per row (warps 0-3 tile A, 4-7 tile B), no exchange
 // between threads.  The row's reference maximum is raised, and O rescaled,
 // only when a chunk exceeds it by more than 2^8, which after the first chunks
-// is rare; P then stays below 2^8, exact enough in bf16 (relative rounding),
-// and l is summed in fp32.
+// is rare; P then stays below 2^8, exact enough in bf16 (relative rounding; the
+// products want P in V's type, and a second term of P would be half as many products
+// again: the output is off by 2.3e-3 rms of its values, of which 1.7e-3 are its own
+// rounding), and l is summed in fp32.
 //
 // Keys arrive by TMA, one 4 KB box per page and plane, as [8-row group][column
 // half][8 rows][128 B]: the 8-row groups of a 128-key plane then lie at one

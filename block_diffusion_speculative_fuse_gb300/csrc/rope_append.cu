@@ -21,7 +21,8 @@
 // the row's sines and cosines are made while its first loads are on their way,
 // once for all heads, and passed through shared memory.  8192 rows of 32 + 8 + 8
 // heads of 128: bf16 37 us, 5.4 TB/s; fp32 47 us, 6.4 TB/s (four CTAs to an SM 56
-// us; loads of up to four head vectors ahead of the work on them no faster).  A
+// us; loads of up to four head vectors ahead of the work on them no faster).  Whole
+// calls: bf16 40 us, into an E4M3 cache 46, of fp32 52, into two terms 54.  A
 // row alone: 3 us, the latency of its two dependent loads and a launch.
 #include "common.cuh"
 #include "kernels.h"

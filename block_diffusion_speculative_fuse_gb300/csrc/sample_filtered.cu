@@ -37,11 +37,15 @@
 // And where the steps up to top-k's border hold no more tokens than the list,
 // one CTA settles the whole row from a list of those.
 //
-// Bound: for many rows instruction issue.  512 rows of 151936 under top-p take
-// 434 us, 0.7 TB/s; a row's 95 us on its SM are 8 for the maximum, 19 for the
-// counts, 47 for the weights (about 75 instructions each, issued at nearly one a
-// cycle) and 20 for the border and the draw.  Cheaper weights (fp32's 2^-22) would
-// halve the 47 but move borders that 64-bit arithmetic puts elsewhere.  For a few
+// Bound: 512 rows of 151936 under top-p take 428 us, 0.7 TB/s.  A row's 95 us on
+// its SM are 8 for the maximum, 19 for the counts, 47 for the weights and 20 for
+// the border and the draw.  The weights are bound by instruction issue (about 75
+// each, at nearly one a cycle); the rest is not: the one CTA of 1024 threads on an
+// SM has nothing to run under its barriers and loads, so that over the kernel 52 %
+// of the issue slots are used, and 512 rows on 152 SMs are 3.4 rounds run as four.
+// Cheaper weights (fp32's 2^-22) would halve the 47 but move borders that 64-bit
+// arithmetic puts elsewhere.  Under top-k 50, settled from the list, they take 197
+// us (214 with top-p), under top-k 1000 364 (403).  For a few
 // rows the latency of the passes, each ending in a cluster barrier: one row of
 // 151936 takes 31 us under top-p alone, about ten passes, and 17 under top-k 50
 // and top-p, five passes and a list (26 without the list); 32 rows with mixed
