@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
     const int e = seg.e, pg0 = seg.chunk0, pg1 = seg.chunk1;
     const int tiles = entity_tiles(p, L, e);
     const int kvh = small_div(seg.ul, tiles), tile = seg.ul - kvh * tiles;
-    const int slot = units_before(p, L, e) + seg.ul + worker;
+    const size_t slot_row = part_row(p, L, e, seg.ul, worker);
     const bool pre = e < p.ng;
     const int req_t = pre ? pl.live[e] : e - p.ng;               // whose table row
     const int page0 = pre ? 0 : pl.cut[inv_div(e - p.ng, p.inv_group)] / 16;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1) prefix_small_kernel(const
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       const int row = tile * kSmallRows + tg + 8 * h;
       if (row < map.rows) {
-        const size_t ps = static_cast<size_t>(slot) * kSmallRows + tg + 8 * h;
+        const size_t ps = slot_row + tg + 8 * h;
         float* dst = L.part_o + ps * D;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256, 5) prefix_join_kernel(const PrefixParams 
       int w0, w1;
       unit_workers(p, P, gi, ul, po, pu, pper, &w0, &w1);
       np = w1 - w0 + 1;
-      p_at = static_cast<size_t>(units_before(p, P, gi) + ul + w0) * P.tile_rows + row - tile * P.tile_rows;
+      p_at = part_row(p, P, gi, ul, w0) + row - tile * P.tile_rows;
     }
     if (sees && su > 0) {
       const int row = i * G + g;
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(256, 5) prefix_join_kernel(const PrefixParams 
       int w0, w1;
       unit_workers(p, S, se, ul, so_, su, sper, &w0, &w1);
       nsu = w1 - w0 + 1;
-      s_at = static_cast<size_t>(units_before(p, S, se) + ul + w0) * S.tile_rows + row - tile * S.tile_rows;
+      s_at = part_row(p, S, se, ul, w0) + row - tile * S.tile_rows;
     }
     const int parts = np + nsu;
     for (int b = sub; b < parts; b += 32 * WPV) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(256, 5) prefix_join_kernel(const PrefixParams 
       auto at = [&](int k, const PrefixList** L) {  // row of partial k in its list's buffers
         const bool pre = k < np;
         *L = pre ? &P : &S;
-        return pre ? p_at + static_cast<size_t>(k) * P.tile_rows : s_at + static_cast<size_t>(k - np) * S.tile_rows;
+        return pre ? p_at + static_cast<size_t>(k) * P.worker_rows : s_at + static_cast<size_t>(k - np) * S.worker_rows;
       };
       float v[4][VEC];
       auto load4 = [&](int j0) {
@@ -522,6 +522,11 @@ void prefix_attention_shape(PrefixParams* p) {
   // a segment's fixed cost (Q, the pipeline's start, the partial) is about that of
   // ten chunks of half a tile (a block verify with 0, 10, 20: 318, 152, 168 us)
   T.unit_cost = 10;
+  for (PrefixList& L : p->list) {
+    L.prefix_rows = L.prefix_tiles == 0 ? 0 : L.prefix_tiles > 1 ? L.tile_rows : rows_p;
+    L.suffix_rows = L.suffix_tiles == 0 ? 0 : L.suffix_tiles > 1 ? L.tile_rows : rows_s;
+    L.worker_rows = L.prefix_rows > L.suffix_rows ? L.prefix_rows : L.suffix_rows;
+  }
   auto inverse = [](int d) { return d > 1 ? static_cast<unsigned>((1ull << 32) / d + 1) : 0u; };
   p->inv_n = inverse(p->n);
   p->inv_G = inverse(G);

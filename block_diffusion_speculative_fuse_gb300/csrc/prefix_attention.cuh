@@ -13,9 +13,10 @@
 // with a cost of unit_cost plus chunk_cost for every chunk, cut into ranges of
 // equal cost, one per worker; a chunk belongs to the worker in whose range its
 // cost starts.  A unit's part in one range is a segment; each leaves a partial
-// (O, m, l) for the unit's rows.  Unit + worker is unique per segment and below
-// units + workers, which fixes its slot.  A last kernel joins the partials of
-// each row in order.
+// (O, m, l) for the unit's rows.  From one segment to the next the unit goes up, or
+// the worker, so the rows of the units before plus the worker times the rows of the
+// largest unit fix a place for it that no other segment's overlaps.  A last kernel
+// joins the partials of each row in order.
 //
 // A prefix is cut short to whole pages that every row of the group sees
 // (causal rows near its end, short requests), so prefix chunks need no mask.
@@ -30,6 +31,8 @@ constexpr int kMaxPrefixBatch = 1024;
 struct PrefixList {            // one kernel's share of the work
   int chunk_shift;             // log2 of the keys per chunk
   int tile_rows;               // rows per unit
+  int prefix_rows, suffix_rows;  // of a unit's partial: tile_rows, or less in a single tile
+  int worker_rows;             // the larger of them, of those that there are
   int workers;
   int prefix_tiles;            // row tiles of a prefix (0: not this kernel's)
   int suffix_tiles;            // row tiles of a request (0: not this kernel's)
@@ -38,8 +41,8 @@ struct PrefixList {            // one kernel's share of the work
   int prefix_split, suffix_split;  // large tiles: at most 128 rows (see there)
   int* off;                    // [entities + 1] cost before each entity (written for the join)
   int* unit;                   // [entities + 1] cost of one of its units; last: of a worker's range
-  float* part_o;               // [units + workers][tile_rows][d]
-  float* part_ml;              // [units + workers][tile_rows][2]
+  float* part_o;               // [rows of all units + workers * worker_rows][d]
+  float* part_ml;              // [the same][2]
 };
 
 struct PrefixParams {
@@ -57,9 +60,11 @@ struct PrefixParams {
   PrefixList list[2];          // small tiles (mma.sync), large tiles (tcgen05)
 };
 
-// Units before entity e of the list (for the slots).
-__device__ __forceinline__ int units_before(const PrefixParams& p, const PrefixList& L, int e) {
-  return p.hkv * (min(e, p.ng) * L.prefix_tiles + max(e - p.ng, 0) * L.suffix_tiles);
+// First row of the partial that `worker` leaves for unit ul of entity e.
+__device__ __forceinline__ size_t part_row(const PrefixParams& p, const PrefixList& L, int e, int ul, int worker) {
+  const size_t before = static_cast<size_t>(p.hkv * min(e, p.ng) * L.prefix_tiles + (e < p.ng ? ul : 0)) * L.prefix_rows;
+  const size_t own = e < p.ng ? 0 : static_cast<size_t>(p.hkv * (e - p.ng) * L.suffix_tiles + ul) * L.suffix_rows;
+  return before + own + static_cast<size_t>(worker) * L.worker_rows;
 }
 __device__ __forceinline__ int entity_tiles(const PrefixParams& p, const PrefixList& L, int e) {
   return e < p.ng ? L.prefix_tiles : L.suffix_tiles;

@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         pair_sync();
       }
-      const size_t slot_row = static_cast<size_t>(units_before(p, L, e) + seg.ul + worker) * L.tile_rows;
+      const size_t slot_row = part_row(p, L, e, seg.ul, worker);
       const int first = (split ? 0 : tile * 128) + (warp % 4) * 32;  // the warp's first row in the unit
       const int rows_here = min(32, rows.rows - row0 - first);
 #pragma unroll 1

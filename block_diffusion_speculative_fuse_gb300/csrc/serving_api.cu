@@ -73,13 +73,13 @@ size_t layout_prefix(PrefixParams* p, int d, uint8_t* base) {
     return q;
   };
   for (PrefixList& L : p->list) {
-    const size_t units = static_cast<size_t>(p->hkv) *
-                         (static_cast<size_t>(p->ng) * L.prefix_tiles + static_cast<size_t>(p->batch) * L.suffix_tiles);
-    const size_t slots = L.workers > 0 ? units + L.workers : 0;
+    const size_t rows = static_cast<size_t>(p->hkv) * (static_cast<size_t>(p->ng) * L.prefix_tiles * L.prefix_rows +
+                                                       static_cast<size_t>(p->batch) * L.suffix_tiles * L.suffix_rows) +
+                        static_cast<size_t>(L.workers) * L.worker_rows;
     L.off = reinterpret_cast<int*>(take((p->ng + p->batch + 1) * sizeof(int)));
     L.unit = reinterpret_cast<int*>(take((p->ng + p->batch + 1) * sizeof(int)));
-    L.part_o = reinterpret_cast<float*>(take(slots * L.tile_rows * d * sizeof(float)));
-    L.part_ml = reinterpret_cast<float*>(take(slots * L.tile_rows * 2 * sizeof(float)));
+    L.part_o = reinterpret_cast<float*>(take(rows * d * sizeof(float)));
+    L.part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
   }
   return off;
 }
