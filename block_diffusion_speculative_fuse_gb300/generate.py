@@ -123,10 +123,12 @@ def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u:
         pos += 1
     used = [("dflash_target_forward", runner.workspace(n))
             for n in sorted({P - 1, 1 if n_tokens > 0 else 0} - {0})]
-    for fn, w in used + [("dflash_sample_filtered", ws)]:
-        status, site = B.dflash_get_status(w)
+    found = [(fn, w, *B.dflash_get_status(w)) for fn, w in used + [("dflash_sample_filtered", ws)]]
+    for _, w, status, _ in found:
         if status != 0:
             B.dflash_workspace_init(w)   # the runner stays usable
+    for fn, _, status, site in found:
+        if status != 0:
             raise B.DflashError(f"{fn} (site {site})", status)
     return res.T.contiguous().cpu().numpy()
 

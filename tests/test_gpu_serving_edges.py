@@ -104,7 +104,7 @@ def tiny_model():
     return t, DeviceModel(t, W.target_weights(t, 71, std=0.05), W.shared_weights(t, 71, std=0.05), draft=False)
 
 
-@pytest.mark.parametrize("where", [0, -1])     # in the prompt's own pass, in the first step
+@pytest.mark.parametrize("where", [[0], [-1], [0, -1]])     # in the prompt's own pass, in the first step, in both
 def test_sampled_generation_reports_the_target_forwards_errors(where):
     from block_diffusion_speculative_fuse_gb300.generate import TargetRunner, sample_generate
     t, model = tiny_model()
