@@ -11,9 +11,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdflash_gb300.so")
 SOURCES = ["dflash_api.cu", "gemm_tc05.cu", "attention.cu", "attention_tc05.cu", "small_kernels.cu",
            "noalloc.cu", "sampling.cu", "rope_append.cu", "prefix_attention.cu",
-           "prefix_attention_tc05.cu",
+           "prefix_attention_tc05.cu", "attention_chunk.cu",
            "sample_filtered.cu", "serving_api.cu"]
-HEADERS = ["common.cuh", "kernels.h", "epilogue.cuh", "attention.cuh", "prefix_attention.cuh"]
+HEADERS = ["common.cuh", "kernels.h", "epilogue.cuh", "attention.cuh", "prefix_attention.cuh",
+           "tc05.cuh", "attention_chunk.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

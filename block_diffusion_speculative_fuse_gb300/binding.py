@@ -141,6 +141,14 @@ EXPORTS = {
                                                ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
                                                ctypes.POINTER(DflashKV)] + [ctypes.c_void_p] * 5 +
                                 [ctypes.c_size_t, ctypes.c_void_p]),
+    "dflash_attention_chunk_bytes": (ctypes.c_size_t, [ctypes.POINTER(DflashHeads),
+                                                       ctypes.c_int32, ctypes.c_int32]),
+    "dflash_attention_chunk": (ctypes.c_int, [ctypes.POINTER(DflashHeads), ctypes.c_int32,
+                                              ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_float, ctypes.POINTER(DflashKV),
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64] +
+                               [ctypes.c_void_p] * 2 + [ctypes.c_size_t, ctypes.c_void_p]),
     "dflash_sample_filtered_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "dflash_sample_filtered": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                               ctypes.c_int32] + [ctypes.c_void_p] * 9 +
@@ -437,6 +445,30 @@ def dflash_attention_prefix(heads: DflashHeads, layer, q, batch, n, group, causa
         1 if causal else 0, scale, ctypes.byref(kv), _dense(fn, dev, ctx_len, _I32, (batch,)),
         _dense(fn, dev, prefix_len, _I32, (batch // group,)), _dense(fn, dev, out, _BF16, shape),
         _dense(fn, dev, lse, _F32, (batch, n, hq)) if lse is not None else None, w, wn,
+        _stream(stream, dev)))
+
+
+def dflash_attention_chunk_bytes(heads: DflashHeads, batch, T) -> int:
+    size = load().dflash_attention_chunk_bytes(ctypes.byref(heads), batch, T)
+    if size == 0:
+        raise DflashError("dflash_attention_chunk_bytes", -1)
+    return int(size)
+
+
+def dflash_attention_chunk(heads: DflashHeads, layer, q, row_start, batch, T, causal, scale,
+                           kv: DflashKV, ctx_len, out, lse, ws, stream=None):
+    """q, out bf16 [T][hq][d] (rows may be strided); row_start int32 [batch + 1]; lse fp32
+    [T][hq] or None."""
+    fn = "dflash_attention_chunk"
+    dev = _device(fn, q)
+    hq, d = heads.n_q_heads, heads.head_dim
+    qp, ldq = _rows(fn, dev, q, _BF16, T, hq, d)
+    op, ldo = _rows(fn, dev, out, _BF16, T, hq, d)
+    w, wn = _space(fn, dev, ws)
+    return _check(fn, load().dflash_attention_chunk(
+        ctypes.byref(heads), layer, qp, ldq, _dense(fn, dev, row_start, _I32, (batch + 1,)), batch,
+        T, 1 if causal else 0, scale, ctypes.byref(kv), _dense(fn, dev, ctx_len, _I32, (batch,)),
+        op, ldo, _dense(fn, dev, lse, _F32, (T, hq)) if lse is not None else None, w, wn,
         _stream(stream, dev)))
 
 

@@ -678,6 +678,19 @@ int encode_kv_pages(CUtensorMap* map, const void* base, uint64_t groups, uint32_
   return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_ERR_INVALID_ARG;
 }
 
+int encode_q_rows(CUtensorMap* map, const void* q, int64_t ld, int T, int hq, int G, int tokens, int d) {
+  const int rc = load_encode();
+  if (rc) return rc;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hq), static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[2] = {d * 2ull, static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_ERR_INVALID_ARG;
+}
+
 // Argument and capacity checks of dflash_ctx_fuse (nothing is launched).
 int ctx_fuse_check(const dflash_model_s* m, const void* taps, int32_t T, const void* ctx,
                    const void* ws, size_t ws_bytes) {

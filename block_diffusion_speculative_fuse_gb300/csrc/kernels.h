@@ -281,6 +281,28 @@ void prefix_attention_shape(PrefixParams* p);
 // group0: 8-row group of the layer's first page, oob_group: one past the end.
 cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,
                                     int oob_group, cudaStream_t s);
+// Chunk attention (attention_chunk.cu).
+constexpr int kChunkWorkers = 152;  // one CTA per SM
+struct ChunkParams {
+  const int32_t *row_start, *ctx_len, *page_table;
+  int batch, T, hq, hkv, G;
+  int tokens;                  // rows of the call in a tile: 128 / G
+  int causal, max_pages, n_pages;
+  float scale_log2;            // scale / ln 2
+  uint16_t* out;
+  int64_t ld_out;
+  float* lse;                  // [T][hq] or null
+  int slot_rows;               // of a partial
+  float *part_o, *part_ml;     // [2 * workers][slot_rows][d], [..][2]
+  void* records;               // [workers], 32 bytes each
+  int* status;
+};
+cudaError_t attention_chunk_launch(const ChunkParams& p, int d, const CUtensorMap& kv_map,
+                                   const CUtensorMap& q_map, int group0, int oob_group, cudaStream_t s);
+// 3-D map over rows [T][hq][d] bf16, rows ld elements apart: box (64 columns, G
+// heads, `tokens` rows), 128-byte swizzled, zero fill past T.
+int encode_q_rows(CUtensorMap* map, const void* q, int64_t ld, int T, int hq, int G, int tokens, int d);
+
 // 4-D map over `groups` groups of 8 rows of d bf16: box (64 columns, 8 rows,
 // d/64 column halves, 2 groups), one 16-row page as [group][half][8][128 B],
 // 128-byte swizzled, zero fill out of bounds.  A DFLASH_* code.

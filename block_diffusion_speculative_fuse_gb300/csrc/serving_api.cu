@@ -96,6 +96,43 @@ bool prefix_sizes(const dflash_heads* h, int32_t batch, int32_t n, int32_t group
   return true;
 }
 
+// Workspace of the chunk attention: header, the workers' records, the pieces'
+// partial results.  Returns the bytes; fills the pointers when base is set.
+size_t layout_chunk(ChunkParams* p, int d, uint8_t* base) {
+  size_t off = kHeaderBytes;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = base == nullptr ? nullptr : base + off;
+    off = al256(off + bytes);
+    return q;
+  };
+  const size_t rows = 2 * static_cast<size_t>(kChunkWorkers) * p->slot_rows;
+  p->records = take(kChunkWorkers * 32);
+  p->part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
+  p->part_o = reinterpret_cast<float*>(take(rows * d * sizeof(float)));
+  return off;
+}
+
+bool chunk_sizes(const dflash_heads* h, int32_t batch, int32_t T, ChunkParams* p) {
+  if (batch < 1 || T < 1) return false;
+  std::memset(p, 0, sizeof(*p));
+  p->batch = batch;
+  p->T = T;
+  p->hq = h->n_q_heads;
+  p->hkv = h->n_kv_heads;
+  p->G = p->hq / p->hkv;
+  p->tokens = 128 / p->G;
+  p->slot_rows = T <= p->tokens ? T * p->G : 256;
+  return true;
+}
+
+// The softmax's scale in base 2: 0 stands for 1 / sqrt(d).
+bool scale_of(float scale, int d, float* scale_log2) {
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return false;
+  *scale_log2 = static_cast<float>((scale == 0.f ? 1.0 / std::sqrt(static_cast<double>(d)) : scale) *
+                                   1.44269504088896340736);
+  return std::isfinite(*scale_log2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -277,6 +314,56 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
   }
   const cudaError_t e = prefix_attention_launch(p, d, &map, static_cast<int>(layer_groups * layer),
                                                 static_cast<int>(groups), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
+}
+
+size_t dflash_attention_chunk_bytes(const dflash_heads* heads, int32_t batch, int32_t T) {
+  ChunkParams p;
+  if (check_heads(heads) || !chunk_sizes(heads, batch, T, &p)) return 0;
+  return layout_chunk(&p, heads->head_dim, nullptr);
+}
+
+int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,
+                           const int32_t* row_start, int32_t batch, int32_t T, int32_t causal,
+                           float scale, const dflash_kv* kv, const int32_t* ctx_len, void* out,
+                           int64_t ld_out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_heads(heads);
+  if (rc) return rc;
+  ChunkParams p;
+  if (q == nullptr || out == nullptr || row_start == nullptr || ctx_len == nullptr || !aligned(q, 16) ||
+      !aligned(out, 16) || !aligned(row_start, 4) || !aligned(ctx_len, 4) || !aligned(lse, 4) ||
+      (causal != 0 && causal != 1) || !chunk_sizes(heads, batch, T, &p))
+    return DFLASH_ERR_INVALID_ARG;
+  const int d = heads->head_dim;
+  const int64_t row = static_cast<int64_t>(p.hq) * d;
+  if (ld_q < row || ld_out < row || ld_q % 8 || ld_out % 8 || !scale_of(scale, d, &p.scale_log2))
+    return DFLASH_ERR_INVALID_ARG;
+  rc = check_cache(heads, layer, kv);
+  if (rc) return rc;
+  if (kv->dtype != 0 || terms_of(heads) != 1) return DFLASH_ERR_UNSUPPORTED;
+  if (batch > kv->n_rows) return DFLASH_ERR_CAPACITY;
+  // TMA coordinates are 32 bits, a map's strides 40
+  const uint64_t layer_groups = static_cast<uint64_t>(kv->n_pages) * 2 * heads->n_kv_heads * 2;
+  const uint64_t groups = layer_groups * heads->n_layers;
+  if (groups >= (1ull << 31) - 2 || T > (1 << 30) || ld_q >= (1ll << 38)) return DFLASH_ERR_UNSUPPORTED;
+  rc = check_ws(ws, ws_bytes, layout_chunk(&p, d, static_cast<uint8_t*>(ws)));
+  if (rc) return rc;
+  p.row_start = row_start;
+  p.ctx_len = ctx_len;
+  p.page_table = kv->page_table;
+  p.causal = causal;
+  p.max_pages = kv->max_pages;
+  p.n_pages = kv->n_pages;
+  p.out = static_cast<uint16_t*>(out);
+  p.ld_out = ld_out;
+  p.lse = lse;
+  p.status = static_cast<int32_t*>(ws);
+  CUtensorMap kv_map, q_map;
+  rc = encode_kv_pages(&kv_map, kv->pool, groups, d);
+  if (!rc) rc = encode_q_rows(&q_map, q, ld_q, T, p.hq, p.G, p.tokens, d);
+  if (rc) return rc;
+  const cudaError_t e = attention_chunk_launch(p, d, kv_map, q_map, static_cast<int>(layer_groups * layer),
+                                               static_cast<int>(groups), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
 }
 

@@ -430,6 +430,39 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
                             const int32_t* prefix_len, void* out, float* lse, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* Attention of a ragged batch of new rows to one layer of a bf16 one-term
+ * cache: single tokens of a decode, chunks of prompts and whole prompts in one
+ * call.  Rows [row_start[r], row_start[r+1]) of q belong to request r, whose
+ * K and V are in the cache already (dflash_kv_rope_append).
+ *   q    bf16 [T][n_q_heads][head_dim], rows ld_q elements apart
+ *   out  bf16, same shape, rows ld_out elements apart; lse fp32 [T][n_q_heads]
+ *        or NULL
+ *   row_start int32 [batch + 1], ctx_len int32 [batch]: cached positions of
+ *   each request, its rows' own included; both on the device.
+ * Row i of the n rows of request r sees positions [0, ctx_len[r]) or, causal,
+ * [0, ctx_len[r] - n + i].  A row that sees none gives out = 0, lse = -inf.
+ * out, lse and scale as in dflash_attention_prefix.  Rows of no request (those
+ * before row_start[0] and from row_start[batch] on) are left as they are.
+ * A request may have no rows.  One whose rows lie outside [0, T) or in falling
+ * order is skipped and recorded as DFLASH_ERR_CAPACITY (site 551), a ctx_len
+ * beyond the page table is recorded (site 552) and counts as the table's
+ * capacity, a page id out of range reads as zeros and is recorded (site 553).
+ * Row ranges of one call must not overlap; out must not overlap q.
+ * Pages and values that a row does not see never reach it, whatever they hold;
+ * q, and K and V of what a row sees, must be finite (else that row, no other,
+ * is undefined: a V that is not finite makes the rows that see it NaN).
+ * Row strides are multiples of 8 elements, base pointers 16-byte aligned.
+ * batch <= kv->n_rows, T <= 2^30.
+ * Scores, softmax statistics and accumulators are fp32; probabilities are
+ * rounded to bf16 for the product with V.  Deterministic.
+ * ws: initialised, dflash_attention_chunk_bytes(heads, batch, T) bytes (0:
+ * unsupported sizes); a workspace for larger T serves smaller calls. */
+size_t dflash_attention_chunk_bytes(const dflash_heads* heads, int32_t batch, int32_t T);
+int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,
+                           const int32_t* row_start, int32_t batch, int32_t T, int32_t causal,
+                           float scale, const dflash_kv* kv, const int32_t* ctx_len, void* out,
+                           int64_t ld_out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* One draw per row of logits (fp32 [rows][vocab], rows ld elements apart)
  * under per-row settings, device arrays [rows]:
  *   w_i = exp((z_i - max z) / temperature), tokens ordered by (z descending,
