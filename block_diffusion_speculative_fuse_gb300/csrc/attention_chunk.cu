@@ -8,13 +8,15 @@ namespace dflash {
 
 namespace {
 
-constexpr int kThreads = 384;     // warps 0-7 softmax, 8 TMA, 9 products, 10 V's values, 11 idle
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // of a thread
+constexpr int kThreads = 640;     // warps 0-15 softmax, 16 TMA, 17 products, 18 V's values, 19 plan
+constexpr int kWarps = kThreads / 32;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // of a thread
 constexpr int kChunk = 128;       // keys
 constexpr float kRaise = 8.f;     // log2
-// Cost of a unit, in keys that one tile goes over (two tiles: twice the keys):
-constexpr int kUnitCost = 300;    // its start and end
-constexpr int kWorkerCost = 512;  // the least share of a worker
+constexpr int kPieces = 4;        // planned ahead
+// Costs are counted in 64 keys that one tile of 128 rows goes over (32 bits).
+constexpr int kUnitCost = 5;      // a unit's start and end
+constexpr int kWorkerCost = 8;    // the least share of a worker
 constexpr int kLeast = 2;         // chunks of a piece of a unit
 
 template <int D>
@@ -23,16 +25,24 @@ struct Cfg {
   static constexpr int PAGE = 16 * D * 2;
   static constexpr int PLANE = kChunk * D * 2;           // K or V of a chunk
   static constexpr int Q_TILE = 128 * D * 2;             // [HALVES][128 rows][128 B]
-  static constexpr int SLOTS = D == 128 ? 4 : 8;
-  static constexpr int STAGE = 32 * 128;                 // of a softmax warp: 32 rows of 128 B
-  static constexpr uint32_t S_COL = 0, P_COL = 64, O_COL = 256;
-  static constexpr int FIXED = 2 * Q_TILE + SLOTS * PLANE + 8 * STAGE;
+  static constexpr int SLOTS = D == 128 ? 5 : 10;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;      // + 128 * tile
+  static constexpr int FIXED = 2 * Q_TILE + SLOTS * PLANE;
   static constexpr int SMEM = FIXED + 3072;
 };
 
 // A place in the work: requests, their KV heads, their row units, chunks of keys.
 struct Place {
   int r, h, i, c;
+};
+
+// Chunks [c0, c0 + n) of a unit, for all warps of the CTA.
+struct Piece {
+  int n, c0;               // n -1: the end
+  int keys;                // that the unit's last row sees
+  int see, step;           // keys that its row k sees: max(0, see + k * step)
+  int r, h, token0, tokens;  // request, KV head, first row of the call, rows
+  int split, begins, ends;   // one tile; the piece is the unit's first, its last
 };
 
 // What a worker leaves for the join.
@@ -46,29 +56,28 @@ struct WorkerRecord {
 // Units of a request: `per` rows (tokens) each; a last one of at most half as many has
 // one tile.
 struct Units {
-  int n, ctx, per, half, tiles;
-  bool causal;
+  int n, ctx, per, tiles, causal;
   __device__ Units(const ChunkRequest& q, int tokens, int causal_)
-      : n(q.n), ctx(q.ctx), per(2 * tokens), half(tokens), tiles((q.n + 2 * tokens - 1) / (2 * tokens)),
-        causal(causal_) {}
-  __device__ int rows(int i) const { return min(per, n - i * per); }
-  __device__ bool split(int i) const { return n - i * per <= half; }
+      : n(q.n), ctx(q.ctx), per(2 * tokens), tiles((q.n + 2 * tokens - 1) / (2 * tokens)), causal(causal_) {}
+  __device__ bool split(int i) const { return 2 * (n - i * per) <= per; }
   // keys that the unit's last row sees
   __device__ int keys(int i) const { return causal ? max(0, ctx - n + min(n, (i + 1) * per)) : ctx; }
   __device__ int chunks(int i) const { return (keys(i) + kChunk - 1) / kChunk; }
-  // cost of units [0, k), k < tiles: keys in closed form
-  __device__ long long cost(int k) const {
-    long long s = static_cast<long long>(kUnitCost) * k;
-    if (!causal) return s + 2ll * k * ctx;
-    const long long base = ctx - n;
-    const long long skip = base < 0 ? min(static_cast<long long>(k), -base / per) : 0;  // units that see nothing
-    return s + 2 * ((k - skip) * base + per * (static_cast<long long>(k) * (k + 1) - skip * (skip + 1)) / 2);
+  // cost of units [0, k), k < tiles, from the sum of their keys in closed form
+  __device__ int cost(int k) const {
+    long long s = static_cast<long long>(k) * ctx;
+    if (causal) {
+      const int base = ctx - n, skip = base < 0 ? min(k, -base / per) : 0;  // units that see nothing
+      s = static_cast<long long>(k - skip) * base +
+          per * (static_cast<long long>(k) * (k + 1) - static_cast<long long>(skip) * (skip + 1)) / 2;
+    }
+    return kUnitCost * k + static_cast<int>(s >> 5);
   }
-  __device__ long long total() const {
-    return tiles == 0 ? 0 : cost(tiles - 1) + kUnitCost + static_cast<long long>(split(tiles - 1) ? 1 : 2) * keys(tiles - 1);
+  __device__ int total() const {
+    return tiles == 0 ? 0 : cost(tiles - 1) + kUnitCost + (keys(tiles - 1) >> (split(tiles - 1) ? 6 : 5));
   }
   // the unit and chunk at which a boundary at cost x of [0, total()) cuts
-  __device__ void find(long long x, int* i, int* c) const {
+  __device__ void find(int x, int* i, int* c) const {
     int lo = 0, hi = tiles - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -76,9 +85,8 @@ struct Units {
       else hi = mid - 1;
     }
     *i = lo;
-    const int all = chunks(lo);
-    const long long at = (x - cost(lo) - kUnitCost) / (split(lo) ? 1 : 2);
-    int cut = static_cast<int>(max(0ll, at + kChunk / 2) / kChunk);
+    const int all = chunks(lo), at = max(0, x - cost(lo) - kUnitCost);
+    int cut = split(lo) ? (at + 1) / 2 : at / 4 + (at % 4 > 1);
     // no pieces below kLeast chunks
     if (all < 2 * kLeast) cut = 2 * cut <= all ? 0 : all;
     else if (cut < kLeast) cut = 0;
@@ -92,98 +100,74 @@ __device__ __forceinline__ ChunkRequest request(const ChunkParams& p, int r) {
 }
 
 // Start and end of a worker's range, by all threads of the CTA; ends with a barrier.
-// scratch: kThreads / 32 + 1 words of 64 bits.
-__device__ void find_range(const ChunkParams& p, int worker, int workers, Place* out, long long* scratch) {
+// scratch: kWarps words.
+__device__ void find_range(const ChunkParams& p, int worker, int workers, Place* out, int* scratch) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  auto cost_of = [&](int r) {
-    return r < p.batch ? Units(request(p, r), p.tokens, p.causal).total() * p.hkv : 0ll;
-  };
-  auto inclusive = [&](long long v) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    return v;
-  };
-  long long mine = 0;
-  for (int r = tid; r < p.batch; r += kThreads) mine += cost_of(r);
-  mine = inclusive(mine);
-  if (lane == 31) scratch[warp] = mine;
   if (tid < 2) out[tid] = Place{p.batch, 0, 0, 0};
-  __syncthreads();
-  long long all = 0;
-  for (int w = 0; w < kThreads / 32; ++w) all += scratch[w];
-  const long long used = min(static_cast<long long>(workers), (all + kWorkerCost - 1) / kWorkerCost);
-  __syncthreads();
-  if (worker < used) {
-    const long long x[2] = {all * worker / used, all * (worker + 1) / used};
-    long long before = 0;
+  int all = 0, used = 0, x0 = 0, x1 = 0;
+  // a first round adds up the costs, a second finds the boundaries
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    int before = 0;
+#pragma unroll 1
     for (int base = 0; base < p.batch; base += kThreads) {
-      const long long v = cost_of(base + tid), upto = inclusive(v);
+      const int r = base + tid;
+      const Units u(r < p.batch ? request(p, r) : ChunkRequest(), p.tokens, p.causal);
+      const int one = u.total(), v = one * p.hkv;
+      int upto = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      __syncthreads();
       if (lane == 31) scratch[warp] = upto;
       __syncthreads();
-      long long at = before + upto - v;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) at += scratch[w];
-        before += scratch[w];
+      int at = before + upto - v;
+      const int part = lane < kWarps ? scratch[lane] : 0;
+      at += __reduce_add_sync(0xffffffffu, lane < warp ? part : 0);
+      before += __reduce_add_sync(0xffffffffu, part);
+      if (round == 0 && p.batch <= kThreads) {  // the sum is known at once
+        round = 1;
+        all = before;
       }
-      for (int j = 0; j < 2; ++j)
-        if (v > 0 && x[j] >= at && x[j] < at + v) {
-          const Units u(request(p, base + tid), p.tokens, p.causal);
-          const long long one = v / p.hkv;
-          const int h = static_cast<int>((x[j] - at) / one);
-          Place pl{base + tid, h, 0, 0};
-          u.find(x[j] - at - h * one, &pl.i, &pl.c);
+      if (round == 1) {
+        if (base == 0) {
+          used = min(workers, (all + kWorkerCost - 1) / kWorkerCost);
+          if (worker >= used) break;
+          const int share = all / used, rest = all - share * used;
+          x0 = share * worker + rest * worker / used;
+          x1 = share * (worker + 1) + rest * (worker + 1) / used;
+        }
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          const int x = (j == 0 ? x0 : x1) - at;
+          if (x < 0 || x >= v) continue;
+          Place pl{r, x / one, 0, 0};
+          u.find(x - pl.h * one, &pl.i, &pl.c);
           out[j] = pl;
         }
-      __syncthreads();
+      }
     }
+    if (round == 0) all = before;
   }
   __syncthreads();
 }
 
-// Walks a worker's range piece by piece: of unit (r, h, i) the chunks [c0, c1).
-struct Pieces {
-  Place at, end;
-  int c0, c1, all;   // of the piece; chunks of its unit
-  ChunkRequest q;
-  int loaded;
-  __device__ Pieces(const Place* range) : at(range[0]), end(range[1]), c0(0), c1(0), all(0), loaded(-1) {}
-  __device__ bool past() const {
-    if (at.r != end.r) return at.r > end.r;
-    if (at.h != end.h) return at.h > end.h;
-    if (at.i != end.i) return at.i > end.i;
-    return at.c >= end.c;
-  }
-  int r, h, i;
-  __device__ bool next(const ChunkParams& p) {
-    while (at.r < p.batch && !past()) {
-      if (loaded != at.r) {
-        q = request(p, at.r);
-        loaded = at.r;
-      }
-      const Units u(q, p.tokens, p.causal);
-      if (at.i >= u.tiles) {  // the request's next head, or the next request
-        at.i = at.c = 0;
-        if (u.tiles == 0 || ++at.h >= p.hkv) {
-          at.h = 0;
-          ++at.r;
-        }
-        continue;
-      }
-      r = at.r, h = at.h, i = at.i, c0 = at.c;
-      all = u.chunks(i);
-      const bool here = r == end.r && h == end.h && i == end.i;
-      c1 = here ? end.c : all;
-      ++at.i;
-      at.c = 0;
-      if (c0 >= c1 && !(all == 0 && !here)) continue;
-      return true;
-    }
-    return false;
-  }
-};
+// A barrier of `threads` threads; and one that tells whether any of them says so.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_any(int id, int threads, bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return r != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -193,34 +177,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int SLOTS = C::SLOTS;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint8_t* ring = sm + 2 * C::Q_TILE;
-  uint8_t* stages = ring + SLOTS * C::PLANE;
-  float2* exch = reinterpret_cast<float2*>(stages + 8 * C::STAGE);  // [256] (m, l) of a row
-  uint64_t* full = reinterpret_cast<uint64_t*>(exch + 256);
+  float* exch = reinterpret_cast<float*>(ring + SLOTS * C::PLANE);  // [2 tiles][2 halves][128 rows]
+  uint64_t* full = reinterpret_cast<uint64_t*>(exch + 512);
   uint64_t* empty = full + SLOTS;
   uint64_t* clean = empty + SLOTS;          // the plane's V has been gone over
   uint64_t* s_full = clean + SLOTS;         // [2] S of a tile is complete (and the PV before it)
-  uint64_t* p_full = s_full + 2;            // [2][2] P of a tile is in TMEM: upper, lower 64 keys
+  uint64_t* p_full = s_full + 2;            // [2][2] P of a tile is in TMEM: of each 64 keys the first 32, the others
   uint64_t* q_full = p_full + 4;            // Q of the piece is in shared memory
   uint64_t* q_free = q_full + 1;            // its last S is complete
   uint64_t* o_full = q_free + 1;            // all of the piece's products are complete; bad
-  long long* scratch = reinterpret_cast<long long*>(o_full + 1);  // [kThreads / 32]
-  Place* range = reinterpret_cast<Place*>(scratch + kThreads / 32);  // [2]
-  volatile int* bad = reinterpret_cast<volatile int*>(range + 2);    // [16] first key with a V that is not finite
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(bad) + 16);
+  uint64_t* piece_full = o_full + 1;        // [kPieces]
+  uint64_t* piece_free = piece_full + kPieces;
+  Piece* pieces = reinterpret_cast<Piece*>(piece_free + kPieces);  // [kPieces]
+  Place* range = reinterpret_cast<Place*>(pieces + kPieces);       // [2]
+  int* scratch = reinterpret_cast<int*>(range + 2);                // [kWarps]
+  volatile int* bad = reinterpret_cast<volatile int*>(scratch + kWarps);  // [kPieces] first key with a V that is not finite
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(bad) + kPieces);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(256 * 8 + (3 * SLOTS + 9) * 8 + kThreads / 32 * 8 + 2 * 16 + 18 * 4 <= 3072, "fits");
+  static_assert(512 * 4 + (3 * SLOTS + 9 + 2 * kPieces) * 8 + kPieces * sizeof(Piece) + 2 * sizeof(Place) +
+                        (kWarps + kPieces + 2) * 4 <= 3072, "fits");
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
+#pragma unroll 1
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 2);
       mbar_init(&clean[s], 1);
     }
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[2 * t], 4);
-      mbar_init(&p_full[2 * t + 1], 4);
+      mbar_init(&p_full[2 * t], 8);
+      mbar_init(&p_full[2 * t + 1], 8);
+    }
+#pragma unroll 1
+    for (int t = 0; t < kPieces; ++t) {
+      mbar_init(&piece_full[t], 1);
+      mbar_init(&piece_free[t], 19);
     }
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -230,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&kv_map);
     tma_prefetch_desc(&q_map);
   }
-  if (warp == 9) tmem_alloc(tmem_slot, 512);
+  if (warp == 17) tmem_alloc(tmem_slot, 512);
   griddep_wait();
   griddep_launch_dependents();
   const int worker = blockIdx.x;
@@ -239,24 +233,106 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Pieces seg(range);
 
-  if (warp >= 8) {
+  // The next piece, for a whole warp; false at the end.  A role that gives up on a
+  // wait says so (give_up) and goes on through the pieces without working on them,
+  // so that all warps meet at the same barriers and every piece is handed back.
+  int taken = 0;
+  bool ok = true;
+  auto next_piece = [&](Piece* pc) {
+    const int at = taken % kPieces;
+    if (!__all_sync(0xffffffffu, mbar_wait_for(&piece_full[at], (taken / kPieces) & 1, nullptr, 4 * kWaitLimitNs)))
+      return false;
+    *pc = pieces[at];
+    return pc->n >= 0;
+  };
+  auto give_up = [&](int site) {
+    ok = false;
+    *abort_flag = 1;
+    if (lane == 0) raise_status(p.status, DFLASH_ERR_TIMEOUT, site);
+  };
+  auto piece_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_free[taken % kPieces]);
+    ++taken;
+  };
+  // A plane's chunk in the order of their use: K0 V0 K1 V1 ..., one tile K0 K1 V0 K2 V1 ...
+  auto is_key = [](bool split, int n, int k, int j) { return k < n && (split ? k + max(0, k - 1) : 2 * k) == j; };
+
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
+    if (warp == 19) {
+      // ------------------------------------------------ plan: the worker's range, piece by piece
+      Place at = range[0];
+      const Place end = range[1];
+      ChunkRequest q;
+      int loaded = -1, count = 0;
+      bool last = false;
+      while (!last) {
+        Piece pc;
+        pc.n = -1;
+        while (true) {
+          const bool same = at.r == end.r, there = same && at.h == end.h && at.i == end.i;
+          if (at.r >= p.batch || at.r > end.r ||
+              (same && (at.h > end.h || (at.h == end.h && (at.i > end.i || (there && at.c >= end.c)))))) {
+            last = true;
+            break;
+          }
+          if (loaded != at.r) {
+            q = request(p, at.r);
+            loaded = at.r;
+          }
+          const Units u(q, p.tokens, p.causal);
+          if (at.i >= u.tiles) {  // the request's next head, or the next request
+            at.i = at.c = 0;
+            if (u.tiles == 0 || ++at.h >= p.hkv) {
+              at.h = 0;
+              ++at.r;
+            }
+            continue;
+          }
+          const int all = u.chunks(at.i), c0 = at.c, c1 = there ? end.c : all;
+          const int i = at.i++;
+          at.c = 0;
+          if (c0 >= c1 && all > 0) continue;
+          const int first = u.ctx - u.n + i * u.per + 1;
+          pc.n = c1 - c0;
+          pc.c0 = c0;
+          pc.keys = u.keys(i);
+          pc.see = u.causal ? first : u.ctx;
+          pc.step = u.causal;
+          pc.r = at.r;
+          pc.h = at.h;
+          pc.token0 = q.start + i * u.per;
+          pc.tokens = min(u.per, u.n - i * u.per);
+          pc.split = u.split(i);
+          pc.begins = c0 == 0;
+          pc.ends = c1 == all;
+          break;
+        }
+        const int slot = count % kPieces;
+        if (count >= kPieces && !__all_sync(0xffffffffu, mbar_wait_for(&piece_free[slot], (count / kPieces + 1) & 1,
+                                                                       nullptr, 4 * kWaitLimitNs))) {
+          give_up(558);
+          break;
+        }
+        if (lane == 0) {
+          pieces[slot] = pc;
+          mbar_arrive(&piece_full[slot]);
+        }
+        __syncwarp();
+        ++count;
+      }
+    } else if (warp == 16) {
       // ------------------------------------------------ TMA producer
       const uint64_t pol = l2_policy_evict_normal();
       int at = 0, segs = 0;                        // planes, pieces requested so far
       Cursor cur;
-      bool ok = true;
-      while (ok && seg.next(p)) {
-        const int n = seg.c1 - seg.c0;
-        if (n == 0) continue;
-        const Units u(seg.q, p.tokens, p.causal);
-        const bool split = u.split(seg.i);
-        const int page0 = seg.c0 * 8;
-        const int npg = min(n * 8, (u.keys(seg.i) + 15) / 16 - page0);
-        const int32_t* table = p.page_table + static_cast<size_t>(seg.r) * p.max_pages + page0;
+      Piece pc;
+      while (next_piece(&pc)) {
+        const int n = ok ? pc.n : 0, page0 = pc.c0 * 8;
+        const int npg = min(n * 8, (pc.keys + 15) / 16 - page0);
+        const int32_t* table = p.page_table + static_cast<size_t>(pc.r) * p.max_pages + page0;
         // lane -> 8-row group of its page's K plane in the map, 32 pages a time,
         // the next 32 requested ahead
         auto ids_of = [&](int b) {
@@ -264,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return j < npg ? max(__ldcg(table + j), -1) : -2;  // -2: past the piece
         };
         auto check = [&](int id) {
-          if (id >= 0 && id < p.n_pages) return group0 + (id * 2 * p.hkv + seg.h) * 2;
+          if (id >= 0 && id < p.n_pages) return group0 + (id * 2 * p.hkv + pc.h) * 2;
           if (id != -2) raise_status(p.status, DFLASH_ERR_CAPACITY, 553);
           return oob_group;
         };
@@ -272,9 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int next_id = ids_of(1);
         int kg = check(ids_of(0)), vg = kg;
         int k = 0, v = 0;
+#pragma unroll 1
         for (int j = 0; j < 2 * n; ++j, ++at, cur.advance(SLOTS)) {
-          // planes in the order of their use: K0 V0 K1 V1 ..., one tile K0 K1 V0 K2 V1 ...
-          const bool is_k = k < n && (split ? k + max(0, k - 1) : 2 * k) == j;
+          const bool is_k = is_key(pc.split, n, k, j);
           const int c = is_k ? k++ : v++;
           if (is_k) {
             if (c / 4 != kb) {  // K runs ahead: V's batch is the previous one until it follows
@@ -292,15 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             if (at >= SLOTS && !mbar_wait(&empty[st], cur.parity ^ 1, abort_flag)) go = 0;
             if (go && j == 0 && segs > 0 && !mbar_wait(q_free, (segs - 1) & 1, abort_flag)) go = 0;
-            if (go) {
-              mbar_arrive_expect_tx(&full[st], C::PLANE);
-            } else {
-              *abort_flag = 1;
-              raise_status(p.status, DFLASH_ERR_TIMEOUT, 554);
-            }
+            if (go) mbar_arrive_expect_tx(&full[st], C::PLANE);
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) {
-            ok = false;
+            give_up(554);
             break;
           }
           if (lane < 8) {
@@ -309,32 +380,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j == 0) {  // Q of the piece: [tile][column half], `tokens` rows of G heads each
             if (lane == 0) {
-              const int boxes = (split ? 1 : 2) * C::HALVES;
+              const int boxes = (pc.split ? 1 : 2) * C::HALVES;
               mbar_arrive_expect_tx(q_full, boxes * p.tokens * p.G * 128);
+#pragma unroll 1
               for (int b = 0; b < boxes; ++b)
-                tma_load_3d(sm + b * (128 * 128), &q_map, b % C::HALVES * 64, seg.h * p.G,
-                            seg.q.start + seg.i * u.per + b / C::HALVES * p.tokens, q_full, pol);
+                tma_load_3d(sm + b * (128 * 128), &q_map, b % C::HALVES * 64, pc.h * p.G,
+                            pc.token0 + b / C::HALVES * p.tokens, q_full, pol);
             }
             __syncwarp();
             ++segs;
           }
         }
+        piece_done();
       }
       // copies still in flight after an abort land before the CTA exits
       if (lane == 0) {
+#pragma unroll 1
         for (int j = max(0, at - SLOTS); j < at; ++j) mbar_wait(&full[j % SLOTS], (j / SLOTS) & 1, nullptr);
         if (segs > 0) mbar_wait(q_full, (segs - 1) & 1, nullptr);
       }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       // ------------------------------------------------ products
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
       constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D) | (1u << 16);  // V MN-major
       constexpr uint32_t GS = C::HALVES * 1024;  // between 8-row groups of a plane
       const uint32_t q_addr = smem_u32(sm), ring_addr = smem_u32(ring);
       int segs = 0;
-      int np[2] = {0, 0};  // parity of the next P of each tile
-      bool ok = true;
+      int np = 0;          // parity of the next P of each tile (bits)
       Cursor cur;          // the next plane: they are used in the order they arrive
+      Piece pc;
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) umma_commit(bar);
         __syncwarp();
@@ -363,119 +437,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      // waits for the tile's P, half by half, and issues O += P V
+      // waits for the tile's P, part by part, and issues O += P V
       auto issue_pv = [&](int tile, int st, bool accumulate) {
         const uint32_t v = desc_lo(ring_addr + st * C::PLANE, 1024);
-        const uint32_t o = tmem + C::O_COL + tile * 128, pa = tmem + C::P_COL + tile * 128;
+        const uint32_t o = tmem + C::O_COL + tile * 128, pa = tmem + C::S_COL + tile * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&p_full[2 * tile + h], np[tile], abort_flag))) return false;
+        for (int g = 0; g < 2; ++g) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&p_full[2 * tile + g], (np >> tile) & 1, abort_flag))) return false;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int j = (1 - h) * 4 + i;  // the upper keys first
-              umma_ts(o, pa + j * 8, desc_of(v + j * (C::PAGE / 16), desc_hi(GS)), idesc_pv,
-                      h + i > 0 ? 1u : accumulate ? 1u : 0u);
+              const int j = (i / 2) * 4 + 2 * g + i % 2;  // 16 keys
+              umma_ts(o, pa + (j / 4) * 64 + (j % 4) * 8, desc_of(v + j * (C::PAGE / 16), desc_hi(GS)), idesc_pv,
+                      g + i > 0 ? 1u : accumulate ? 1u : 0u);
             }
           }
           __syncwarp();
         }
-        np[tile] ^= 1;
+        np ^= 1 << tile;
         return true;
       };
-      while (ok && seg.next(p)) {
-        const int n = seg.c1 - seg.c0;
-        if (n == 0) continue;
-        const bool split = Units(seg.q, p.tokens, p.causal).split(seg.i);
+      while (next_piece(&pc)) {
+        const int n = pc.n;
+        if (n == 0 || !ok) {
+          piece_done();
+          continue;
+        }
+        // two tiles: S_A S_B | PV_A S_A' PV_B S_B' | ...; one tile takes turns over
+        // the chunks: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ...
         ok = __all_sync(0xffffffffu, mbar_wait(q_full, segs++ & 1, abort_flag));
-        if (!ok) break;
-        if (split) {
-          for (int c = 0; ok && c < min(2, n); ++c) {
-            const int ik = take(false);
+        const int lead = pc.split ? min(2, n) : 1;
+        int ik = -1;
+#pragma unroll 1
+        for (int c = 0; ok && c < lead; ++c) {
+          ik = take(false);
+          ok = ik >= 0;
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(c, 0, ik);
+          if (!pc.split) issue_s(1, 1, ik);
+          commit(&empty[ik]);
+          if (c + 1 == n) commit(q_free);
+        }
+#pragma unroll 1
+        for (int c = 0; ok && c < n; ++c) {
+          const int t = pc.split ? c & 1 : 0;
+          const bool more = c + lead < n && (!pc.split || n > 1);
+          const int iv = take(true);
+          ok = iv >= 0 && issue_pv(t, iv, pc.split ? c >= 2 : c > 0);
+          if (!ok) break;
+          if (pc.split) commit(&empty[iv]);
+          if (more) {
+            ik = take(false);
             ok = ik >= 0;
             if (!ok) break;
-            tc_fence_after();
-            issue_s(c, 0, ik);
-            commit(&empty[ik]);
-            if (c + 1 == n) commit(q_free);
+            issue_s(t, 0, ik);
           }
-          for (int c = 0; ok && c < n; ++c) {
-            const int t = c & 1, iv = take(true);
-            ok = iv >= 0 && issue_pv(t, iv, c >= 2);
-            if (!ok) break;
-            commit(&empty[iv]);
-            if (c + 2 < n) {
-              const int ik = take(false);
-              ok = ik >= 0;
-              if (!ok) break;
-              issue_s(t, 0, ik);
-              commit(&empty[ik]);
-            }
-            if (c + 3 == n) commit(q_free);
-          }
-        } else {
-          int ik = take(false);
-          ok = ik >= 0;
-          if (ok) {
-            tc_fence_after();
-            issue_s(0, 0, ik);
-            issue_s(1, 1, ik);
-            commit(&empty[ik]);
-            if (n == 1) commit(q_free);
-          }
-          for (int c = 0; ok && c < n; ++c) {
-            const bool more = c + 1 < n;
-            const int iv = take(true);
-            ok = iv >= 0 && issue_pv(0, iv, c > 0);
-            if (!ok) break;
-            if (more) {
-              ik = take(false);
-              ok = ik >= 0;
-              if (!ok) break;
-              issue_s(0, 0, ik);
-            }
+          if (!pc.split) {
             ok = issue_pv(1, iv, c > 0);
             if (!ok) break;
             commit(&empty[iv]);
-            if (more) {
-              issue_s(1, 1, ik);
-              commit(&empty[ik]);
-              if (c + 2 == n) commit(q_free);
-            }
+            if (more) issue_s(1, 1, ik);
+          }
+          if (more) {
+            commit(&empty[ik]);
+            if (c + lead + 1 == n) commit(q_free);
           }
         }
         if (ok) finish();
+        else give_up(555);
+        piece_done();
       }
       if (!ok) {
-        *abort_flag = 1;
-        if (lane == 0) raise_status(p.status, DFLASH_ERR_TIMEOUT, 555);
         // the products in flight end before their memory is given back
         finish();
         mbar_wait(o_full, (segs - 1) & 1, nullptr);
       }
-    } else if (warp == 10) {
+    } else {
       // ------------------------------------------------ V's values
-      int segs = 0;
-      bool ok = true;
       Cursor cur;
-      while (ok && seg.next(p)) {
-        const int n = seg.c1 - seg.c0;
-        if (n == 0) continue;
-        const Units u(seg.q, p.tokens, p.causal);
-        const bool split = u.split(seg.i);
+      Piece pc;
+      while (next_piece(&pc)) {
+        const int n = ok ? pc.n : 0;
         // keys from the piece's first one: all rows see those before `first`, none those from `live` on
-        const int live = u.keys(seg.i) - seg.c0 * kChunk;
-        const int first = u.causal ? max(0, u.ctx - u.n + seg.i * u.per + 1) - seg.c0 * kChunk : live;
-        int found = INT_MAX;
-        if (lane == 0) bad[segs % 16] = INT_MAX;
-        int k = 0, v = 0;
+        const int live = pc.keys - pc.c0 * kChunk;
+        const int first = max(0, pc.see) - pc.c0 * kChunk;
+        int found = INT_MAX, k = 0, v = 0;
+#pragma unroll 1
         for (int j = 0; j < 2 * n; ++j) {
-          const bool is_k = k < n && (split ? k + max(0, k - 1) : 2 * k) == j;
+          const bool is_k = is_key(pc.split, n, k, j);
           const int c = is_k ? k++ : v++;
           const int st = cur.slot;
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[st], cur.parity, abort_flag));
-          if (!ok) break;
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[st], cur.parity, abort_flag))) {
+            give_up(556);
+            break;
+          }
           cur.advance(SLOTS);
           if (!is_k && (c + 1) * kChunk > first) {
             const int b = clean_v<D>(ring + st * C::PLANE, first - c * kChunk, live - c * kChunk);
@@ -483,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j == 2 * n - 1) {
             found = __reduce_min_sync(0xffffffffu, found);
-            if (lane == 0) bad[segs % 16] = found;
+            if (lane == 0) bad[taken % kPieces] = found;
           }
           __syncwarp();
           if (lane == 0) {
@@ -491,189 +548,167 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&empty[st]);
           }
         }
-        ++segs;
-      }
-      if (!ok) {
-        *abort_flag = 1;
-        if (lane == 0) raise_status(p.status, DFLASH_ERR_TIMEOUT, 556);
+        piece_done();
       }
     }
   } else {
-    // ------------------------------------------------ softmax: a thread per row
+    // ------------------------------------------------ softmax: two threads per row, each
+    // for 64 of a chunk's keys and half of O's columns
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int tile = warp / 4;
-    const int r128 = (warp % 4) * 32 + lane;  // row of the tile, TMEM lane
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t s_addr = lane_base + C::S_COL + tile * 128;
+    const int tile = warp / 8, half = warp / 4 % 2, quad = warp % 4;
+    const int r128 = quad * 32 + lane;        // row of the tile, TMEM lane
+    const int pair = 1 + tile * 4 + quad;     // barrier of the two halves' warps
+    const int four = 9 + quad;                // and of both tiles'
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t s_addr = lane_base + C::S_COL + tile * 128 + half * 64;
     const uint32_t o_addr = lane_base + C::O_COL + tile * 128;
-    uint8_t* stage = stages + warp * C::STAGE;
-    // row / G for rows below 128
-    const int inv_G = 65536 / p.G + 1;
-    WorkerRecord rec = {};
-    // After a wait that gave up, a warp goes on through the pieces without
-    // waiting, so that all warps meet at the same named barriers; the results
-    // are void (the status word says so).
+    float* mine = exch + (tile * 2 + half) * 128 + r128;
+    const float* theirs = exch + (tile * 2 + 1 - half) * 128 + r128;
+    const int inv_G = 65536 / p.G + 1;        // row / G for rows below 128
+    const int tok = r128 * inv_G >> 16;       // of the tile
     int segs = 0, ns = 0;
-    bool ok = true, first_piece = true;
-    while (seg.next(p)) {
-      const int n = seg.c1 - seg.c0;
-      const Units u(seg.q, p.tokens, p.causal);
-      const bool split = u.split(seg.i);
-      const int tokens = u.rows(seg.i);                    // of the unit
-      const int token0 = seg.q.start + seg.i * u.per;      // its first row of the call
-      if (first_piece && seg.c0 > 0) {
-        rec.cont = 1;
-        rec.ends = seg.c1 == seg.all;
-      }
-      if (seg.c0 == 0 && seg.c1 < seg.all) {
-        rec.head = 1;
-        rec.token0 = token0;
-        rec.tokens = tokens;
-        rec.kvh = seg.h;
-      }
-      first_piece = false;
-      // keys this row sees, from the piece's first
-      const int tok = r128 * inv_G >> 16;                  // of the tile
-      const int my_token = (split ? 0 : tile * u.half) + tok;
-      const bool real = tok < u.half && my_token < tokens;
-      int lim = INT_MAX;   // rows that do not exist see whatever lies there
-      if (real) lim = (u.causal ? max(0, u.ctx - u.n + seg.i * u.per + my_token + 1) : u.ctx) - seg.c0 * kChunk;
-      float m = -INFINITY, l = 0.f;
-      for (int c = split ? tile : 0; ok && c < n; c += split ? 2 : 1) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[tile], ns++ & 1, abort_flag))) {
-          ok = false;
-          break;
+    Piece pc;
+    WorkerRecord* rec = reinterpret_cast<WorkerRecord*>(p.records) + worker;
+    if (tid == 0) *rec = WorkerRecord{};
+    while (next_piece(&pc)) {
+      const int n = pc.n;
+      if (tid == 0) {
+        if (taken == 0) {
+          rec->cont = !pc.begins;
+          rec->ends = !pc.begins && pc.ends;
         }
+        if (pc.begins && !pc.ends) {
+          rec->head = 1;
+          rec->token0 = pc.token0;
+          rec->tokens = pc.tokens;
+          rec->kvh = pc.h;
+        }
+      }
+      // keys this row sees, from the half's first of the piece
+      const int my_token = (pc.split ? 0 : tile * p.tokens) + tok;
+      const bool real = tok < p.tokens && my_token < pc.tokens;
+      int lim = 1 << 30;   // rows that do not exist see whatever lies there
+      if (real) lim = max(0, pc.see + my_token * pc.step) - pc.c0 * kChunk - half * 64;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int c = pc.split ? tile : 0; c < n; c += pc.split ? 2 : 1) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(&s_full[tile], ns++ & 1, abort_flag))) give_up(557);
         tc_fence_after();
-        // the row's maximum; in a chunk that ends past this row's keys the
-        // scores beyond them become -inf, here and in TMEM
-        const bool masked = __any_sync(0xffffffffu, (c + 1) * kChunk > lim);
-        uint32_t x[4][32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32_nowait(s_addr + j * 32, x[j]);
+        uint32_t x[2][32];
+        tmem_ld32_nowait(s_addr, x[0]);
+        tmem_ld32_nowait(s_addr + 32, x[1]);
+        const int left = lim - c * kChunk;
         tmem_wait_ld(x[0]);
+        tmem_regs_ready(x[1]);
+        // keys past this row's count -inf
+        if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
-        for (int j = 1; j < 4; ++j) tmem_regs_ready(x[j]);
-        if (masked) {
-          const int left = lim - c * kChunk;
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
+          for (int j = 0; j < 64; ++j)
             if (j >= left) x[j / 32][j % 32] = 0xFF800000u;
-          tmem_st32(s_addr, x[0]);
-          tmem_st32(s_addr + 32, x[1]);
-          tmem_wait_st();
         }
         float mx4[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          mx4[j] = fmaxf(__uint_as_float(x[j][0]), __uint_as_float(x[j][1]));
+          mx4[j] = fmaxf(__uint_as_float(x[j / 2][j % 2 * 16]), __uint_as_float(x[j / 2][j % 2 * 16 + 1]));
 #pragma unroll
-          for (int i = 2; i < 32; i += 2)
-            mx4[j] = fmaxf(mx4[j], fmaxf(__uint_as_float(x[j][i]), __uint_as_float(x[j][i + 1])));
+          for (int i = 2; i < 16; i += 2)
+            mx4[j] = fmaxf(mx4[j], fmaxf(__uint_as_float(x[j / 2][j % 2 * 16 + i]),
+                                         __uint_as_float(x[j / 2][j % 2 * 16 + i + 1])));
         }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        const float mc = mx * p.scale_log2;
-        const bool raise = mc > m + kRaise;
-        const bool rescale = raise && m != -INFINITY;
-        if (__any_sync(0xffffffffu, rescale)) {
-          // S is complete, so the PV before it is too: O may be read
-          const float alpha = rescale ? ex2(m - mc) : 1.f;
+        float mc = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+        // the reference is raised, for both halves, where one exceeds it by more than kRaise
+        if (named_any(pair, 64, mc > m + kRaise)) {
+          *mine = mc;
+          named_sync(pair, 64);
+          mc = fmaxf(mc, *theirs);
+          const bool raise = mc > m + kRaise, rescale = raise && m != -INFINITY;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // S is complete, so the PV before it is too: O may be read
+            const float alpha = rescale ? ex2(m - mc) : 1.f;
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32_nowait(o_addr + q * 32, o);
-            tmem_wait_ld(o);
+            for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
+              uint32_t o[16];
+              tmem_ld16_raw(o_addr + q * 16, o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tmem_st32(o_addr + q * 32, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st16(o_addr + q * 16, o);
+            }
             tmem_wait_st();
+            l *= alpha;
           }
-          l *= alpha;
+          if (raise) m = mc;
         }
-        if (raise) m = mc;
-        // P = exp2(scale S - m) in bf16.  The upper 64 keys first, still in
-        // registers: the product with V starts on them while the lower 64,
-        // read again from TMEM, are formed.
+        // P = exp2(scale S - m) in bf16 takes the place of S
         const float neg = m == -INFINITY ? 0.f : -m;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(neg, neg);
         float2 la = make_float2(0.f, 0.f), lb = la;
-        auto form = [&](const uint32_t (&y)[32], uint32_t* pk) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float2 t = fma2(make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), sc2, neg2);
+            float2 t = fma2(make_float2(__uint_as_float(x[g][2 * j]), __uint_as_float(x[g][2 * j + 1])), sc2, neg2);
             t.x = ex2(t.x);
             t.y = ex2(t.y);
             if (j & 1) lb = add2(lb, t);
             else la = add2(la, t);
             pk[j] = bf16x2(t.x, t.y);
           }
-        };
-        const uint32_t p_addr = lane_base + C::P_COL + tile * 128;
-#pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          uint32_t pk[32];
-          if (h == 0) {
-            tmem_wait_ld(x[0]);
-            tmem_regs_ready(x[1]);
-          }
-          form(x[2 * h], pk);
-          form(x[2 * h + 1], pk + 16);
-          tmem_st32(p_addr + h * 32, pk);
-          if (h == 1) {
-            tmem_ld32_nowait(s_addr, x[0]);
-            tmem_ld32_nowait(s_addr + 32, x[1]);
-          }
+          tmem_st16(s_addr + g * 16, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * tile + 1 - h]);
+          if (lane == 0) mbar_arrive(&p_full[2 * tile + g]);
         }
         l += (la.x + la.y) + (lb.x + lb.y);
       }
       if (n > 0) {
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) ok = false;
-        if (lim > bad[segs % 16]) l = __int_as_float(0x7FFFFFFF);
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) give_up(557);
+        if (lim + half * 64 > bad[taken % kPieces]) l = __int_as_float(0x7FFFFFFF);
         ++segs;
         tc_fence_after();
       }
-      // ---- result of the piece.  One tile: the two states are joined, A's warps
-      // taking the lower half of the columns, B's the upper.
-      const bool have = n > (split ? tile : 0);
+      // ---- result of the piece: the halves' l; one tile: the tiles' states too
+      named_sync(pair, 64);
+      *mine = l;
+      named_sync(pair, 64);
+      l = half == 0 ? l + *theirs : *theirs + l;
+      const bool have = n > (pc.split ? tile : 0), have_b = pc.split && n > 1 - tile;
       float wa = have ? 1.f : 0.f, wb = 0.f;   // weights of this tile's O and the other's
-      auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + warp % 4) : "memory"); };
-      if (split) {
-        exch[tile * 128 + r128] = make_float2(m, l);
-        pair_sync();
-        const float2 y = exch[(1 - tile) * 128 + r128];
-        const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn;
+      if (pc.split) {
+        named_sync(four, 128);
+        *mine = half == 0 ? m : l;
+        named_sync(four, 128);
+        const float om = exch[(1 - tile) * 256 + r128], ol = exch[(1 - tile) * 256 + 128 + r128];
+        const float mn = fmaxf(m, om), ref = mn == -INFINITY ? 0.f : mn;
         wa = have ? ex2(m - ref) : 0.f;
-        wb = n > 1 - tile ? ex2(y.x - ref) : 0.f;
-        // (the same order of summation in both tiles' warps)
-        const float mine = l * wa, other = y.y * wb;
-        l = tile == 0 ? mine + other : other + mine;
+        wb = have_b ? ex2(om - ref) : 0.f;
+        const float a = l * wa, b = ol * wb;
+        l = tile == 0 ? a + b : b + a;   // (the same order in both tiles' warps)
         m = mn;
       }
-      const bool whole = seg.c0 == 0 && seg.c1 == seg.all;
-      const int row0 = (split ? 0 : tile * 128) + (warp % 4) * 32;   // the warp's first row in the unit
-      constexpr int HALF = D / 2;
-      const int col0 = split ? tile * HALF : 0, cols = split ? HALF : D;
+      const bool whole = pc.begins && pc.ends;
       const float inv = whole ? (m == -INFINITY ? 0.f : 1.f / l) : 1.f;
       const float fa = wa * inv, fb = wb * inv;
-      const size_t slot = 2 * static_cast<size_t>(worker) + (seg.c0 > 0 ? 0 : 1);
+      const size_t slot_row = (2 * static_cast<size_t>(worker) + (pc.begins ? 1 : 0)) * p.slot_rows +
+                              (pc.split ? 0 : tile * 128) + r128;
+      const int hq0 = pc.h * p.G + r128 - tok * p.G;   // this row's query head
+      // one tile: A's warps take the lower half of the columns, B's the upper
+      const int col0 = pc.split ? tile * (D / 2) + half * 32 : half * (D / 2);
+      const int col1 = pc.split ? (half * 32 < D / 2 ? col0 + 32 : col0) : col0 + D / 2;
 #pragma unroll 1
-      for (int cc = col0; cc < col0 + cols; cc += 32) {
+      for (int cc = col0; cc < col1; cc += 32) {
         uint32_t o[32];
-        const bool use_a = n > 0 && (!split || have), use_b = split && n > 1 - tile;
-        if (use_a) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
+        if (have) {
           tmem_ld32_nowait(o_addr + cc, o);
           tmem_wait_ld(o);
+          // a state without keys left nothing in O (0 * what lies there)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fa == 0.f ? 0.f : __uint_as_float(o[j]) * fa);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
+          for (int j = 0; j < 32; ++j) o[j] = fa == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * fa);
         }
-        if (use_b) {
+        if (have_b) {
           uint32_t y[32];
           tmem_ld32_nowait(lane_base + C::O_COL + (1 - tile) * 128 + cc, y);
           tmem_wait_ld(y);
@@ -681,60 +716,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j)
             o[j] = __float_as_uint(__uint_as_float(o[j]) + (fb == 0.f ? 0.f : __uint_as_float(y[j]) * fb));
         }
-        // through shared memory, so that whole lines are written
-        auto at16 = [&](int r, int piece) { return reinterpret_cast<uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4)); };
-        if (whole) {  // bf16: 32 columns are four pieces
+        if (real && whole) {
+          uint16_t* dst = p.out + static_cast<size_t>(pc.token0 + my_token) * p.ld_out + hq0 * D + cc;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t w[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) w[t] = bf16x2(__uint_as_float(o[8 * j + 2 * t]), __uint_as_float(o[8 * j + 2 * t + 1]));
-            *at16(lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          __syncwarp();
+        } else if (real) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot_row * D + cc);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int r = b * 8 + lane / 4, rt = (warp % 4) * 32 + r, t = rt * inv_G >> 16;
-            const int token = (split ? 0 : tile * u.half) + t;
-            if (t < u.half && token < tokens)
-              *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(token0 + token) * p.ld_out +
-                                        (seg.h * p.G + rt - t * p.G) * D + cc + lane % 4 * 8) = *at16(r, lane % 4);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) *at16(lane, j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const int r = b * 4 + lane / 8, rt = (warp % 4) * 32 + r, t = rt * inv_G >> 16;
-            if (t < u.half && (split ? 0 : tile * u.half) + t < tokens)
-              *reinterpret_cast<uint4*>(p.part_o + (slot * p.slot_rows + row0 + r) * D + cc + lane % 8 * 4) =
-                  *at16(r, lane % 8);
-          }
+          for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
         __syncwarp();
       }
-      if (real && (!split || tile == 0)) {
-        if (!whole) {
-          *reinterpret_cast<float2*>(p.part_ml + (slot * p.slot_rows + row0 + lane) * 2) = make_float2(m, l);
-        } else if (p.lse != nullptr) {
-          p.lse[static_cast<size_t>(token0 + my_token) * p.hq + seg.h * p.G + r128 - tok * p.G] =
+      if (real && half == 0 && (!pc.split || tile == 0)) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + slot_row * 2) = make_float2(m, l);
+        else if (p.lse != nullptr)
+          p.lse[static_cast<size_t>(pc.token0 + my_token) * p.hq + hq0] =
               m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
-        }
       }
       // both tiles' O have been read before either's next product
-      if (split) pair_sync();
+      if (pc.split) named_sync(four, 128);
       tc_fence_before();
+      piece_done();
     }
-    if (!ok) {
-      *abort_flag = 1;
-      if (lane == 0) raise_status(p.status, DFLASH_ERR_TIMEOUT, 557);
-    }
-    if (tid == 0) reinterpret_cast<WorkerRecord*>(p.records)[worker] = rec;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // Joins the pieces of the units that were cut: a CTA takes 32 rows of the unit that
@@ -835,7 +848,7 @@ cudaError_t launch(const ChunkParams& p, const CUtensorMap& kv_map, const CUtens
     // the warpgroups' shares come out of what the block is launched with
     cudaFuncAttributes a;
     e = cudaFuncGetAttributes(&a, chunk_kernel<D>);
-    if (e == cudaSuccess && a.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs)
+    if (e == cudaSuccess && a.numRegs * kThreads < 512 * kSoftmaxRegs + 128 * kOtherRegs)
       e = cudaErrorInvalidConfiguration;
     if (e != cudaSuccess) allowed = -1;
   }
@@ -861,6 +874,11 @@ cudaError_t launch(const ChunkParams& p, const CUtensorMap& kv_map, const CUtens
 }
 
 }  // namespace
+
+bool attention_chunk_fits(const ChunkParams& p) {
+  const double units = p.T / (2 * p.tokens) + static_cast<double>(p.batch);
+  return units * p.hkv * (kUnitCost + p.max_pages * 0.5 + 1) < 1073741824.0;
+}
 
 cudaError_t attention_chunk_launch(const ChunkParams& p, int d, const CUtensorMap& kv_map,
                                    const CUtensorMap& q_map, int group0, int oob_group, cudaStream_t s) {

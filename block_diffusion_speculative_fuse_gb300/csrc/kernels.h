@@ -297,6 +297,8 @@ struct ChunkParams {
   void* records;               // [workers], 32 bytes each
   int* status;
 };
+// Whether the costs of a call's work stay within 32 bits.
+bool attention_chunk_fits(const ChunkParams& p);
 cudaError_t attention_chunk_launch(const ChunkParams& p, int d, const CUtensorMap& kv_map,
                                    const CUtensorMap& q_map, int group0, int oob_group, cudaStream_t s);
 // 3-D map over rows [T][hq][d] bf16, rows ld elements apart: box (64 columns, G

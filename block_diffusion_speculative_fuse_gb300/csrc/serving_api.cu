@@ -354,6 +354,7 @@ int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void*
   p.causal = causal;
   p.max_pages = kv->max_pages;
   p.n_pages = kv->n_pages;
+  if (!attention_chunk_fits(p)) return DFLASH_ERR_UNSUPPORTED;
   p.out = static_cast<uint16_t*>(out);
   p.ld_out = ld_out;
   p.lse = lse;

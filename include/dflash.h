@@ -452,7 +452,9 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
  * q, and K and V of what a row sees, must be finite (else that row, no other,
  * is undefined: a V that is not finite makes the rows that see it NaN).
  * Row strides are multiples of 8 elements, base pointers 16-byte aligned.
- * batch <= kv->n_rows, T <= 2^30.
+ * batch <= kv->n_rows, T <= 2^30; a call whose work may pass n_kv_heads *
+ * (T / 16 + batch) * max_pages = 2^30 is DFLASH_ERR_UNSUPPORTED (some larger
+ * ones with fewer than 16 query heads to a KV head are not).
  * Scores, softmax statistics and accumulators are fp32; probabilities are
  * rounded to bf16 for the product with V.  Deterministic.
  * ws: initialised, dflash_attention_chunk_bytes(heads, batch, T) bytes (0:
