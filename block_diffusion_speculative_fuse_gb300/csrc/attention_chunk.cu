@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(512 * 4 + (3 * SLOTS + 9 + 2 * kPieces) * 8 + kPieces * sizeof(Piece) + 2 * sizeof(Place) +
                         (kWarps + kPieces + 2) * 4 <= 3072, "fits");
 
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // (one lane's word for it, so that the compiler knows roles and pieces to be the
+  // warp's and keeps what depends on them in uniform registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
   if (tid == 0) {
 #pragma unroll 1
     for (int s = 0; s < SLOTS; ++s) {
@@ -243,7 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int at = taken % kPieces;
     if (!__all_sync(0xffffffffu, mbar_wait_for(&piece_full[at], (taken / kPieces) & 1, nullptr, 4 * kWaitLimitNs)))
       return false;
-    *pc = pieces[at];
+    int w = lane < sizeof(Piece) / 4 ? reinterpret_cast<const int*>(pieces + at)[lane] : 0;
+#pragma unroll
+    for (int j = 0; j < sizeof(Piece) / 4; ++j) reinterpret_cast<int*>(pc)[j] = __shfl_sync(0xffffffffu, w, j);
     return pc->n >= 0;
   };
   auto give_up = [&](int site) {
@@ -418,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(o_full);
       };
       // waits for the next plane and takes it: its slot, or -1
-      auto take = [&](bool is_v) {
+      auto take = [&](bool cleaned) {
         const int st = cur.slot;
         bool r = mbar_wait(&full[st], cur.parity, abort_flag);
-        if (r && is_v) r = mbar_wait(&clean[st], cur.parity, abort_flag);
+        if (cleaned) r = r && mbar_wait(&clean[st], cur.parity, abort_flag);
         cur.advance(SLOTS);
         return __all_sync(0xffffffffu, r) ? st : -1;
       };
@@ -468,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the chunks: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ...
         ok = __all_sync(0xffffffffu, mbar_wait(q_full, segs++ & 1, abort_flag));
         const int lead = pc.split ? min(2, n) : 1;
+        // chunks from here on have keys that not all rows see
+        const int clean0 = max(0, pc.see) / kChunk - pc.c0;
         int ik = -1;
 #pragma unroll 1
         for (int c = 0; ok && c < lead; ++c) {
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; ok && c < n; ++c) {
           const int t = pc.split ? c & 1 : 0;
           const bool more = c + lead < n && (!pc.split || n > 1);
-          const int iv = take(true);
+          const int iv = take(c >= clean0);
           ok = iv >= 0 && issue_pv(t, iv, pc.split ? c >= 2 : c > 0);
           if (!ok) break;
           if (pc.split) commit(&empty[iv]);
