@@ -15,7 +15,9 @@ constexpr int kChunk = 128;       // keys
 constexpr float kRaise = 8.f;     // log2
 constexpr int kPieces = 4;        // planned ahead
 // Costs are counted in 64 keys that one tile of 128 rows goes over (32 bits).
-constexpr int kUnitCost = 5;      // a unit's start and end
+constexpr int kUnitCost = 10;     // a unit's start and end
+constexpr int kSplitCost = 4;     // of a chunk with one tile: as much as with two, since the
+                                  // loads bound it (2, 3, 4: a mixed batch 384, 304, 288 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
 constexpr int kLeast = 2;         // chunks of a piece of a unit
 
@@ -34,6 +36,7 @@ struct Cfg {
 // A place in the work: requests, their KV heads, their row units, chunks of keys.
 struct Place {
   int r, h, i, c;
+  ChunkRequest q;
 };
 
 // Chunks [c0, c0 + n) of a unit, for all warps of the CTA.
@@ -74,7 +77,7 @@ struct Units {
     return kUnitCost * k + static_cast<int>(s >> 5);
   }
   __device__ int total() const {
-    return tiles == 0 ? 0 : cost(tiles - 1) + kUnitCost + (keys(tiles - 1) >> (split(tiles - 1) ? 6 : 5));
+    return tiles == 0 ? 0 : cost(tiles - 1) + kUnitCost + (split(tiles - 1) ? keys(tiles - 1) / kChunk * kSplitCost : keys(tiles - 1) >> 5);
   }
   // the unit and chunk at which a boundary at cost x of [0, total()) cuts
   __device__ void find(int x, int* i, int* c) const {
@@ -86,7 +89,7 @@ struct Units {
     }
     *i = lo;
     const int all = chunks(lo), at = max(0, x - cost(lo) - kUnitCost);
-    int cut = split(lo) ? (at + 1) / 2 : at / 4 + (at % 4 > 1);
+    int cut = split(lo) ? (at + kSplitCost / 2) / kSplitCost : at / 4 + (at % 4 > 1);
     // no pieces below kLeast chunks
     if (all < 2 * kLeast) cut = 2 * cut <= all ? 0 : all;
     else if (cut < kLeast) cut = 0;
@@ -103,7 +106,7 @@ __device__ __forceinline__ ChunkRequest request(const ChunkParams& p, int r) {
 // scratch: kWarps words.
 __device__ void find_range(const ChunkParams& p, int worker, int workers, Place* out, int* scratch) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  if (tid < 2) out[tid] = Place{p.batch, 0, 0, 0};
+  if (tid < 2) out[tid] = Place{p.batch, 0, 0, 0, ChunkRequest()};
   int all = 0, used = 0, x0 = 0, x1 = 0;
   // a first round adds up the costs, a second finds the boundaries
 #pragma unroll 1
@@ -112,7 +115,8 @@ __device__ void find_range(const ChunkParams& p, int worker, int workers, Place*
 #pragma unroll 1
     for (int base = 0; base < p.batch; base += kThreads) {
       const int r = base + tid;
-      const Units u(r < p.batch ? request(p, r) : ChunkRequest(), p.tokens, p.causal);
+      const ChunkRequest q = r < p.batch ? request(p, r) : ChunkRequest();
+      const Units u(q, p.tokens, p.causal);
       const int one = u.total(), v = one * p.hkv;
       int upto = v;
 #pragma unroll
@@ -143,7 +147,7 @@ __device__ void find_range(const ChunkParams& p, int worker, int workers, Place*
         for (int j = 0; j < 2; ++j) {
           const int x = (j == 0 ? x0 : x1) - at;
           if (x < 0 || x >= v) continue;
-          Place pl{r, x / one, 0, 0};
+          Place pl{r, x / one, 0, 0, q};
           u.find(x - pl.h * one, &pl.i, &pl.c);
           out[j] = pl;
         }
@@ -167,6 +171,25 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool mine) {
       : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
       : "memory");
   return r != 0;
+}
+
+// 32 bytes, in one instruction where they are aligned to their size.
+__device__ __forceinline__ void store_32(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+__device__ __forceinline__ void scale2(uint32_t* x, float f) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+r"(x[0]), "+r"(x[1])
+      : "r"(__float_as_uint(f)));
 }
 
 template <int D>
@@ -269,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ plan: the worker's range, piece by piece
       Place at = range[0];
       const Place end = range[1];
-      ChunkRequest q;
-      int loaded = -1, count = 0;
+      ChunkRequest q = at.q;
+      int loaded = at.r, count = 0;
       bool last = false;
       while (!last) {
         Piece pc;
@@ -696,23 +719,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = pc.begins && pc.ends;
       const float inv = whole ? (m == -INFINITY ? 0.f : 1.f / l) : 1.f;
       const float fa = wa * inv, fb = wb * inv;
-      const size_t slot_row = (2 * static_cast<size_t>(worker) + (pc.begins ? 1 : 0)) * p.slot_rows +
-                              (pc.split ? 0 : tile * 128) + r128;
-      const int hq0 = pc.h * p.G + r128 - tok * p.G;   // this row's query head
+      const int row0 = pc.split ? 0 : tile * 128;      // the tile's first in the unit
+      const size_t slot_row = (2 * static_cast<size_t>(worker) + (pc.begins ? 1 : 0)) * p.slot_rows + row0 + r128;
+      const int64_t out_row = (pc.token0 + my_token) * p.ld_out + (pc.h * p.G + r128 - tok * p.G) * D;
       // one tile: A's warps take the lower half of the columns, B's the upper
       const int col0 = pc.split ? tile * (D / 2) + half * 32 : half * (D / 2);
       const int col1 = pc.split ? (half * 32 < D / 2 ? col0 + 32 : col0) : col0 + D / 2;
 #pragma unroll 1
       for (int cc = col0; cc < col1; cc += 32) {
         uint32_t o[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0u;
         if (have) {
           tmem_ld32_nowait(o_addr + cc, o);
           tmem_wait_ld(o);
-          // a state without keys left nothing in O (0 * what lies there)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = fa == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * fa);
+          for (int j = 0; j < 32; j += 2) scale2(o + j, fa);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
         if (have_b) {
           uint32_t y[32];
@@ -720,21 +743,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld(y);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            o[j] = __float_as_uint(__uint_as_float(o[j]) + (fb == 0.f ? 0.f : __uint_as_float(y[j]) * fb));
+            o[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), fb, __uint_as_float(o[j])));
         }
+        // a thread writes its own row, 32 bytes an instruction (16 bytes, half a sector,
+        // were the limit of short units; so were the instructions of a transpose to whole
+        // lines, with 16 warps at it together)
         if (real && whole) {
-          uint16_t* dst = p.out + static_cast<size_t>(pc.token0 + my_token) * p.ld_out + hq0 * D + cc;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+          for (int j = 0; j < 2; ++j) {
+            uint32_t w[8];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) w[t] = bf16x2(__uint_as_float(o[8 * j + 2 * t]), __uint_as_float(o[8 * j + 2 * t + 1]));
-            *reinterpret_cast<uint4*>(dst + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int t = 0; t < 8; ++t)
+              w[t] = bf16x2(__uint_as_float(o[16 * j + 2 * t]), __uint_as_float(o[16 * j + 2 * t + 1]));
+            store_32(p.out + out_row + cc + j * 16, w, p.wide);
           }
         } else if (real) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + slot_row * D + cc);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 4; ++j) store_32(p.part_o + slot_row * D + cc + j * 8, o + 8 * j, true);
         }
         __syncwarp();
       }
@@ -742,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole)
           *reinterpret_cast<float2*>(p.part_ml + slot_row * 2) = make_float2(m, l);
         else if (p.lse != nullptr)
-          p.lse[static_cast<size_t>(pc.token0 + my_token) * p.hq + hq0] =
+          p.lse[static_cast<size_t>(pc.token0 + my_token) * p.hq + pc.h * p.G + r128 - tok * p.G] =
               m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
       }
       // both tiles' O have been read before either's next product

@@ -291,6 +291,7 @@ struct ChunkParams {
   float scale_log2;            // scale / ln 2
   uint16_t* out;
   int64_t ld_out;
+  int wide;                    // out's rows start at multiples of 32 bytes
   float* lse;                  // [T][hq] or null
   int slot_rows;               // of a partial
   float *part_o, *part_ml;     // [2 * workers][slot_rows][d], [..][2]

@@ -357,6 +357,7 @@ int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void*
   if (!attention_chunk_fits(p)) return DFLASH_ERR_UNSUPPORTED;
   p.out = static_cast<uint16_t*>(out);
   p.ld_out = ld_out;
+  p.wide = aligned(out, 32) && ld_out % 16 == 0;
   p.lse = lse;
   p.status = static_cast<int32_t*>(ws);
   CUtensorMap kv_map, q_map;
