@@ -153,6 +153,11 @@ EXPORTS = {
     "dflash_sample_filtered": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                               ctypes.c_int32] + [ctypes.c_void_p] * 9 +
                                [ctypes.c_size_t, ctypes.c_void_p]),
+    "dflash_score_tokens_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
+    "dflash_score_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                           ctypes.c_int32, ctypes.c_int32] + [ctypes.c_void_p] * 5 +
+                            [ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                            [ctypes.c_size_t, ctypes.c_void_p]),
     "dflash_synth_target": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64,
                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
@@ -502,3 +507,36 @@ def dflash_sample_filtered(logits, rows, vocab, temperature, top_k, top_p, min_p
         _dense(fn, dev, n_kept, _I32, one) if n_kept is not None else None,
         _dense(fn, dev, logprob, _F32, one) if logprob is not None else None, w, wn,
         _stream(stream, dev)))
+
+
+def dflash_score_tokens_bytes(rows, vocab, n_top) -> int:
+    size = load().dflash_score_tokens_bytes(rows, vocab, n_top)
+    if size == 0:
+        raise DflashError("dflash_score_tokens_bytes", -1)
+    return int(size)
+
+
+def dflash_score_tokens(logits, rows, vocab, temperature, ids, logprob, rank, entropy, n_top, top_id,
+                        top_logprob, ws, stream=None):
+    """logits fp32 or bf16 [rows][vocab] (rows may be strided); temperature, ids, logprob, rank
+    and entropy may be None, top_id and top_logprob where n_top is 0."""
+    fn = "dflash_score_tokens"
+    dev = _device(fn, logits)
+    dt = logits.dtype
+    if (dt is not _F32 and dt is not _BF16) or logits.get_device() != dev or \
+            logits.shape != (rows, vocab):
+        raise DflashError(fn, -1)
+    ld, s1 = logits.stride()
+    if s1 != 1 and vocab > 1:
+        raise DflashError(fn, -1)
+    one, top = (rows,), (rows, n_top)
+    w, wn = _space(fn, dev, ws)
+    return _check(fn, load().dflash_score_tokens(
+        logits.data_ptr(), ld if rows > 1 else vocab, rows, vocab, 1 if dt is _F32 else 0,
+        _dense(fn, dev, temperature, _F32, one) if temperature is not None else None,
+        _dense(fn, dev, ids, _I32, one) if ids is not None else None,
+        _dense(fn, dev, logprob, _F32, one) if logprob is not None else None,
+        _dense(fn, dev, rank, _I32, one) if rank is not None else None,
+        _dense(fn, dev, entropy, _F32, one) if entropy is not None else None, n_top,
+        _dense(fn, dev, top_id, _I32, top) if n_top else None,
+        _dense(fn, dev, top_logprob, _F32, top) if n_top else None, w, wn, _stream(stream, dev)))

@@ -281,6 +281,22 @@ void prefix_attention_shape(PrefixParams* p);
 // group0: 8-row group of the layer's first page, oob_group: one past the end.
 cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,
                                     int oob_group, cudaStream_t s);
+// Scores of given tokens (score_tokens.cu).
+struct ScoreParams {
+  const void* logits;          // bf16 or fp32 rows
+  int64_t ld;
+  int rows, vocab, n_top;
+  const float* temperature;    // [rows] or null: 1
+  const int32_t* ids;          // [rows] or null
+  float *logprob, *entropy;    // [rows] or null
+  int32_t* rank;
+  int32_t* top_id;             // [rows][n_top]
+  float* top_logprob;
+  int32_t* status;
+};
+constexpr int kMaxScoreTop = 64;
+cudaError_t score_tokens_launch(const ScoreParams& p, bool half, cudaStream_t s);
+
 // Chunk attention (attention_chunk.cu).
 constexpr int kChunkWorkers = 152;  // one CTA per SM
 struct ChunkParams {

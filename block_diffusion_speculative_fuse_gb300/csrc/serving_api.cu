@@ -404,4 +404,41 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
   return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
 }
 
+size_t dflash_score_tokens_bytes(int32_t rows, int32_t vocab, int32_t n_top) {
+  if (rows < 1 || vocab < 1 || vocab > kMaxSampleVocab || n_top < 0 || n_top > kMaxScoreTop) return 0;
+  return kHeaderBytes;  // the status word; a row's work stays on chip
+}
+
+int dflash_score_tokens(const void* logits, int64_t ld, int32_t rows, int32_t vocab, int32_t in_dtype,
+                        const float* temperature, const int32_t* ids, float* logprob, int32_t* rank,
+                        float* entropy, int32_t n_top, int32_t* top_id, float* top_logprob, void* ws,
+                        size_t ws_bytes, void* stream) {
+  if (logits == nullptr || rows < 1 || vocab < 1 || ld < vocab || (in_dtype != 0 && in_dtype != 1) ||
+      n_top < 0 || (n_top > 0 && (top_id == nullptr || top_logprob == nullptr)) ||
+      (ids == nullptr && (logprob != nullptr || rank != nullptr)) ||
+      !aligned(logits, in_dtype == 1 ? 4 : 2) || !aligned(temperature, 4) || !aligned(ids, 4) ||
+      !aligned(logprob, 4) || !aligned(rank, 4) || !aligned(entropy, 4) || !aligned(top_id, 4) ||
+      !aligned(top_logprob, 4))
+    return DFLASH_ERR_INVALID_ARG;
+  if (vocab > kMaxSampleVocab || rows > (1 << 24) || n_top > kMaxScoreTop) return DFLASH_ERR_UNSUPPORTED;
+  const int rc = check_ws(ws, ws_bytes, kHeaderBytes);
+  if (rc) return rc;
+  ScoreParams p;
+  p.logits = logits;
+  p.ld = ld;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.n_top = n_top;
+  p.temperature = temperature;
+  p.ids = ids;
+  p.logprob = logprob;
+  p.rank = rank;
+  p.entropy = entropy;
+  p.top_id = top_id;
+  p.top_logprob = top_logprob;
+  p.status = static_cast<int32_t*>(ws);
+  const cudaError_t e = score_tokens_launch(p, in_dtype == 0, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
+}
+
 }  // extern "C"

@@ -501,6 +501,35 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
                            const float* min_p, const double* a, int32_t* token, int32_t* n_kept,
                            float* logprob, void* ws, size_t ws_bytes, void* stream);
 
+/* What rows of logits (in_dtype 0 = bf16, 1 = fp32; [rows][vocab], rows ld
+ * elements apart) say of given tokens, at temperature T (device fp32 [rows];
+ * NULL: 1; values below 1e-30 or above 1e30 count as those):
+ *   lse = ln sum_i exp(z_i / T)
+ *   logprob fp32 [rows]   z_id / T - lse of the token ids[r] (int32)
+ *   rank int32 [rows]     tokens with a larger logit, or an equal one and a
+ *                         lower index
+ *   entropy fp32 [rows]   -sum_i p_i ln p_i, p = softmax(z / T)
+ *   top_id int32, top_logprob fp32 [rows][n_top]: the n_top best tokens
+ *                         (largest logit first, equals by lower index)
+ * Each output may be NULL (top_id and top_logprob where n_top is 0); without
+ * ids logprob and rank must be.  n_top <= 64.  A negative id stands for no
+ * token: logprob 0, rank -1.  Tokens with z = -inf have logprob -inf and are
+ * no alternatives; where there are fewer than n_top, the places left hold -1
+ * and -inf.  An id >= vocab gives logprob NaN, rank -1 and is recorded as
+ * DFLASH_ERR_INVALID_ARG (site 572).  A row without a finite maximum (all
+ * -inf, a NaN or +inf in it), or with a temperature that is not finite and
+ * positive, gives NaN, rank -1 and top_id -1 and is recorded (site 571); the
+ * other rows are scored as usual.
+ * Sums are fp32 in a fixed order over groups of logits (relative error of
+ * lse's sum about 2^-20); ranks and alternatives are exact.  Deterministic.
+ * 1 <= vocab <= 393216, rows <= 2^24.
+ * ws: initialised, dflash_score_tokens_bytes(rows, vocab, n_top) bytes. */
+size_t dflash_score_tokens_bytes(int32_t rows, int32_t vocab, int32_t n_top);
+int dflash_score_tokens(const void* logits, int64_t ld, int32_t rows, int32_t vocab, int32_t in_dtype,
+                        const float* temperature, const int32_t* ids, float* logprob, int32_t* rank,
+                        float* entropy, int32_t n_top, int32_t* top_id, float* top_logprob, void* ws,
+                        size_t ws_bytes, void* stream);
+
 /* ----------------------------------------------- end-to-end loop helpers */
 
 /* Causal target forward over `batch` requests x `n` consecutive rows

@@ -95,3 +95,21 @@ def sample(z, temperature, top_k, top_p, min_p, a):
     j = min(int(np.count_nonzero(c <= a * c[-1])), len(kept) - 1)
     margin = min(margin, float(np.abs(c[:-1] - a * c[-1]).min() / c[-1]) if len(kept) > 1 else 1.0)
     return kept[j], len(kept), float(t[kept[j]] - math.log(c[-1])), margin
+
+
+def score(z, temperature, token, n):
+    """(logprob, rank, entropy, ids, logprobs) of a token and the n best ones
+    of a row of logits; None for a row without a finite maximum."""
+    z = np.asarray(z, dtype=np.float64)
+    if np.isnan(z).any() or not np.isfinite(z.max()):
+        return None
+    t = z / min(max(float(temperature), 1e-30), float(np.float32(1e30)))
+    t = t - t.max()
+    lp = t - math.log(np.exp(t).sum())
+    p = np.exp(lp)
+    entropy = -float((p[p > 0] * lp[p > 0]).sum())
+    order = [int(i) for i in np.lexsort((np.arange(len(z)), -z)) if z[i] > -np.inf][:n]
+    if token < 0:
+        return 0.0, -1, entropy, order, [float(lp[i]) for i in order]
+    rank = int(np.count_nonzero(z > z[token]) + np.count_nonzero(z[:token] == z[token]))
+    return float(lp[token]), rank, entropy, order, [float(lp[i]) for i in order]

@@ -182,3 +182,126 @@ def test_chunk_many_requests(d):
 def test_chunk_second_layer_scale_and_no_lse():
     s = chunk_case([30, 1], [90, 300], 8, 2, 64, layers=3, layer=1, scale=0.3, lse=False, width=40)
     check_chunk(s, 8, 64, layer=1, scale=0.3)
+
+
+# ------------------------------------------------------------- token scores
+def check_scores(z, T, ids, n, bad=(), wrong_id=(), stride=None):
+    """Runs a call on logits z (a tensor) and compares every row."""
+    B = B_()
+    rows, vocab = z.shape
+    ws = workspace(B.dflash_score_tokens_bytes(rows, vocab, n))
+    lp, ent = (torch.full((rows,), 7.0, device="cuda") for _ in range(2))
+    rank = torch.full((rows,), 7, dtype=torch.int32, device="cuda")
+    ti = torch.full((rows, n), 7, dtype=torch.int32, device="cuda") if n else None
+    tl = torch.full((rows, n), 7.0, device="cuda") if n else None
+    Td = torch.as_tensor(T, dtype=torch.float32).cuda() if T is not None else None
+    B.dflash_score_tokens(z, rows, vocab, Td, i32(ids), lp, rank, ent, n, ti, tl, ws)
+    torch.cuda.synchronize()
+    status = B.dflash_get_status(ws)
+    assert status == ((0, 0) if not bad and not wrong_id else (-1, 571 if bad and not wrong_id else status[1]))
+    zh = z.double().cpu().numpy()
+    lp, rank, ent = lp.double().cpu().numpy(), rank.cpu().numpy(), ent.double().cpu().numpy()
+    for r in range(rows):
+        if r in bad:
+            assert np.isnan(lp[r]) and np.isnan(ent[r]) and rank[r] == -1
+            if n:
+                assert (ti[r] == -1).all() and torch.isnan(tl[r]).all()
+            continue
+        tok = -1 if r in wrong_id else ids[r]
+        e = O.score(zh[r], 1.0 if T is None else T[r], tok, n)
+        mean = math.log(vocab) + 15
+        tol = 2.0 ** -22 * (1 + mean)
+        assert abs(ent[r] - e[2]) <= 2 * tol + 2.0 ** -22 * (abs(e[2]) + mean), (r, ent[r], e[2])
+        if r in wrong_id:
+            assert np.isnan(lp[r]) and rank[r] == -1
+        else:
+            assert rank[r] == e[1]
+            if np.isfinite(e[0]):
+                assert abs(lp[r] - e[0]) <= tol + 2.0 ** -22 * (abs(e[0]) + mean), (r, lp[r], e[0])
+            else:
+                assert lp[r] == e[0]
+        if n:
+            got, gl = ti[r].cpu().numpy(), tl[r].double().cpu().numpy()
+            k = len(e[3])
+            assert list(got[:k]) == e[3] and (got[k:] == -1).all() and (gl[k:] == -np.inf).all()
+            assert np.all(np.abs(gl[:k] - e[4]) <= tol + 2.0 ** -22 * (np.abs(e[4]) + mean))
+
+
+def logits(rows, vocab, spread=2.0, dtype=torch.float32, seed=0, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = (spread * torch.randn(rows, vocab + pad, generator=g, device="cuda")).to(dtype)
+    return z[:, :vocab]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab,n,pad", [
+    (1, 1, 1, 0), (3, 2, 5, 1), (5, 7, 0, 0), (2, 64, 64, 3), (7, 1009, 8, 0), (4, 1009, 64, 2), (1, 4097, 20, 0),
+    (1, 40000, 20, 0), (3, 40001, 64, 5), (40, 12345, 5, 1), (200, 9000, 3, 0), (330, 501, 1, 0), (2, 151936, 20, 0),
+    (1, 393216, 10, 0)])
+def test_score(dtype, rows, vocab, n, pad):
+    rnd = np.random.default_rng(vocab + n)
+    z = logits(rows, vocab, dtype=dtype, seed=vocab, pad=pad)
+    if vocab > 20:
+        z[:, 3:9] = -math.inf
+    ids = rnd.integers(0, vocab, rows)
+    ids[rnd.random(rows) < 0.2] = -rnd.integers(1, 200)
+    if rows > 2 and vocab > 20:
+        ids[1] = 5      # a token whose logit is -inf
+    check_scores(z, rnd.choice([0.3, 0.7, 1.0, 3.0], rows).astype(np.float32) if n % 2 else None, ids, n)
+
+
+@pytest.mark.parametrize("vocab", [33, 3000, 70001])
+def test_score_ties(vocab):
+    """Plateaus: constant rows, two levels, steps; -0 and +0 are equal."""
+    z = torch.zeros(5, vocab, device="cuda")
+    z[0, 1::2] = -0.0
+    z[1, 7::3] = 1.0
+    z[2] = (torch.arange(vocab, device="cuda") // 5 % 40).float()
+    z[3] = -math.inf
+    z[3, vocab // 2:vocab // 2 + 9] = 2.5
+    z[4] = torch.linspace(-3, 3, vocab, device="cuda")     # ascending
+    ids = [vocab - 1, 7, vocab // 3, vocab // 2 + 4, 0]
+    for n in (1, 20, 64):
+        check_scores(z, None, ids, n)
+        check_scores(z.to(torch.bfloat16), [0.5] * 5, ids, n)
+
+
+def test_score_bad_rows_and_ids():
+    z = logits(9, 5000)
+    z[1, 77] = math.nan
+    z[2, 4999] = math.inf
+    z[3] = -math.inf
+    z[4, :2500] = math.nan
+    z[4, 2500:] = -math.inf
+    T = [1.0, 1.0, 1.0, 1.0, 1.0, 0.0, math.nan, math.inf, 1.0]
+    check_scores(z, T, [4] * 9, 4, bad=(1, 2, 3, 4, 5, 6, 7))
+    check_scores(logits(3, 300), None, [1, 300, 2 ** 31 - 1], 4, wrong_id=(1, 2))
+
+
+def test_score_extreme_temperatures_and_logits():
+    z = logits(6, 20000, spread=1.0)
+    z[4] *= 1e4
+    z[5] = z[5] * 1e30
+    check_scores(z, [1e-35, 1e-3, 1e6, 1e38, 1.0, 1e30], [int(z[0].argmax()), 3, 4, 5, int(z[4].argmax()), 9], 5)
+
+
+def test_score_optional_outputs_and_single_rows():
+    """Outputs may be left out, and a row's results do not depend on the others."""
+    B = B_()
+    z = logits(170, 151936, seed=5)
+    ids = i32(np.arange(170) * 7)
+    ws = workspace()
+    res = []
+    for lo, hi in ((0, 170), (0, 1), (3, 40), (169, 170)):
+        k = hi - lo
+        ent, ti, tl = (torch.zeros(k, device="cuda"), torch.zeros(k, 6, dtype=torch.int32, device="cuda"),
+                       torch.zeros(k, 6, device="cuda"))
+        B.dflash_score_tokens(z[lo:hi], k, 151936, None, None, None, None, ent, 6, ti, tl, ws)
+        lp = torch.zeros(k, device="cuda")
+        B.dflash_score_tokens(z[lo:hi], k, 151936, None, ids[lo:hi].contiguous(), lp, None, None, 0, None, None, ws)
+        res.append((lo, hi, ent, ti, tl, lp))
+    assert B.dflash_get_status(ws) == (0, 0)
+    for lo, hi, ent, ti, tl, lp in res[1:]:
+        assert torch.equal(ti, res[0][3][lo:hi])
+        for a, b in ((ent, res[0][2]), (tl, res[0][4]), (lp, res[0][5])):
+            assert torch.allclose(a, b[lo:hi], rtol=0, atol=2.0 ** -22 * (1 + math.log(151936) + 30))
