@@ -12,7 +12,7 @@
 // whose second product's rounding all weights would share.
 //
 // The alternatives need no sort and no second pass: a thread also keeps the maximum of
-// each of its groups (16 fp32 or 32 bf16 logits).  The n-th largest of the threads'
+// each of its groups of 16 logits.  The n-th largest of the threads'
 // maxima bounds the n-th largest logit from below, so only groups that reach it are read
 // again, about n of them, and what reaches it there is ranked by counting.  Where
 // too many do (plateaus of equal logits), the n-th largest is found by digits of its key,
@@ -24,14 +24,15 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc05.cuh"
 
 namespace dflash {
 
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kUnroll = 4;         // vectors of a group
-constexpr int kCandidates = 2048;
+constexpr int kGroup = 16;         // logits that a thread reads together
+constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309f;
 
@@ -39,12 +40,6 @@ struct Stats {
   float m, s, e;   // maximum, sum of 2^t, sum of 2^t t (t in base 2, relative to m)
   int better;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Ordered as floats are; -0 and +0 alike.
 __device__ __forceinline__ uint32_t key_of(float z) {
@@ -85,6 +80,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
 template <bool HALF>
 struct Row {
   static constexpr int PER = HALF ? 8 : 4;   // logits of a 16-byte vector
+  static constexpr int UNROLL = kGroup / PER;
   const uint8_t* base;   // of vector 0 (the row may start inside it)
   int shift, vocab;      // logits of vector 0 before the row
   __device__ Row(const ScoreParams& p, int row) : vocab(p.vocab) {
@@ -217,7 +213,7 @@ __device__ __noinline__ int many_equal(const Row<HALF>& row, int v0, int v1, int
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constant__ ScoreParams p, int cluster) {
   using R = Row<HALF>;
-  constexpr int PER = R::PER;
+  constexpr int PER = R::PER, kUnroll = R::UNROLL;
   extern __shared__ float group_max[];   // [groups][kThreads] (only for alternatives)
   __shared__ float2 list[kCandidates];
   __shared__ float2 best[kMaxCluster * kMaxScoreTop];   // of all slices (rank 0's)
@@ -235,6 +231,16 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   const R row(p, r);
   const int vectors = row.vectors(), slice = (vectors + cluster - 1) / cluster;
   const int v0 = min(rank * slice, vectors), v1 = min(v0 + slice, vectors);
+  const int groups = (v1 - v0 + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+  uint4 raw[kUnroll];
+  auto fetch = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int v = v0 + (g * kUnroll + u) * kThreads + tid;
+      raw[u] = v < v1 ? row.load(v) : R::none();
+    }
+  };
+  fetch(0);
   int id = p.ids != nullptr ? __ldg(p.ids + r) : -1;
   const bool bad_id = id >= p.vocab;
   if (bad_id || id < 0) id = -1;
@@ -248,25 +254,15 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 
   // ---- the pass
   Stats st = {-INFINITY, 0.f, 0.f, 0};
-  const int groups = (v1 - v0 + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  uint4 raw[kUnroll];
-  auto fetch = [&](int g) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int v = v0 + (g * kUnroll + u) * kThreads + tid;
-      raw[u] = v < v1 ? row.load(v) : R::none();
-    }
-  };
-  fetch(0);
 #pragma unroll 1
   for (int g = 0; g < groups; ++g) {
-    float z[kUnroll * PER];
+    float z[kGroup];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) R::unpack(raw[u], z + u * PER);
     if (g + 1 < groups) fetch(g + 1);
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kUnroll * PER; ++j) top = fmaxf(top, z[j]);
+    for (int j = 0; j < kGroup; ++j) top = fmaxf(top, z[j]);
     if (p.n_top > 0) group_max[g * kThreads + tid] = top;
     if (top > st.m) {
       if (st.m > -INFINITY) {
@@ -278,18 +274,20 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     }
     if (st.m == -INFINITY) {   // nothing yet (NaN is no maximum)
 #pragma unroll
-      for (int j = 0; j < kUnroll * PER; ++j)
+      for (int j = 0; j < kGroup; ++j)
         if (z[j] != z[j]) st.s = z[j];
     } else {
-      float s[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};
+      float2 s = make_float2(0.f, 0.f), e = s;
+      const float2 m2 = make_float2(-st.m, -st.m), c2 = make_float2(c, c);
 #pragma unroll
-      for (int j = 0; j < kUnroll * PER; ++j) {
-        const float t = (z[j] - st.m) * c, w = ex2(t);
-        s[j % 2] += w;
-        e[j % 2] = fmaf(w, fmaxf(t, -200.f), e[j % 2]);
+      for (int j = 0; j < kGroup; j += 2) {
+        const float2 t = mul2(add2(make_float2(z[j], z[j + 1]), m2), c2);
+        const float2 w = make_float2(ex2(t.x), ex2(t.y));
+        s = add2(s, w);
+        e = fma2(w, make_float2(fmaxf(t.x, -200.f), fmaxf(t.y, -200.f)), e);
       }
-      st.s += s[0] + s[1];
-      st.e += e[0] + e[1];
+      st.s += s.x + s.y;
+      st.e += e.x + e.y;
     }
     if (id >= 0) {
 #pragma unroll
@@ -444,22 +442,20 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     if (cluster == 1) place = x;
     else
       for (int k = 0; k < cluster; ++k)
-        for (int y = 0; y < n; ++y) {   // a slice's are in order
-          const float2 w = best[k * kMaxScoreTop + y];
+      {   // a slice's are in order: how many precede this one
+        int lo = 0, hi = n;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          const float2 w = best[k * kMaxScoreTop + mid];
           const int j = __float_as_int(w.y);
-          if (j < 0 || (i >= 0 && !before(w.x, j, v.x, i))) break;
-          ++place;
+          if (j >= 0 && (i < 0 || before(w.x, j, v.x, i))) lo = mid + 1;
+          else hi = mid;
         }
+        place += lo;
+      }
     // empty places come after all others, in any order
     if (i < 0 && cluster > 1) {
-      int total = 0, empties = 0;
-      for (int k = 0; k < cluster; ++k)
-        for (int y = 0; y < n; ++y) {
-          const bool none = __float_as_int(best[k * kMaxScoreTop + y].y) < 0;
-          total += !none;
-          empties += none && k * n + y < x;
-        }
-      place = total + empties;
+      for (int y = 0; y < x; ++y) place += __float_as_int(best[y / n * kMaxScoreTop + y % n].y) < 0;
     }
     if (place < n) {
       p.top_id[static_cast<size_t>(r) * n + place] = bad ? -1 : i;
@@ -471,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 
 template <bool HALF>
 cudaError_t launch(const ScoreParams& p, cudaStream_t s) {
-  constexpr int PER = Row<HALF>::PER;
+  constexpr int PER = Row<HALF>::PER, kUnroll = Row<HALF>::UNROLL;
   const int vectors = p.vocab / PER + 2;
   // Rows are cut until the CTAs fill the machine twice, down to one group a thread.
   int cluster = 1;
