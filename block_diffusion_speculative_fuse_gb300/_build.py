@@ -12,6 +12,7 @@ LIB = os.path.join(HERE, "libdflash_gb300.so")
 SOURCES = ["dflash_api.cu", "gemm_tc05.cu", "attention.cu", "attention_tc05.cu", "small_kernels.cu",
            "noalloc.cu", "sampling.cu", "rope_append.cu", "prefix_attention.cu",
            "prefix_attention_tc05.cu", "attention_chunk.cu", "score_tokens.cu",
+           "attention_mass.cu", "kv_evict.cu",
            "sample_filtered.cu", "serving_api.cu"]
 HEADERS = ["common.cuh", "kernels.h", "epilogue.cuh", "attention.cuh", "prefix_attention.cuh",
            "tc05.cuh", "attention_chunk.cuh"]

@@ -153,6 +153,22 @@ EXPORTS = {
     "dflash_sample_filtered": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                               ctypes.c_int32] + [ctypes.c_void_p] * 9 +
                                [ctypes.c_size_t, ctypes.c_void_p]),
+    "dflash_attention_mass_bytes": (ctypes.c_size_t, [ctypes.POINTER(DflashHeads),
+                                                      ctypes.c_int32, ctypes.c_int32]),
+    "dflash_attention_mass": (ctypes.c_int, [ctypes.POINTER(DflashHeads), ctypes.c_int32,
+                                             ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
+                              [ctypes.c_int32] * 4 +
+                              [ctypes.c_float, ctypes.POINTER(DflashKV)] + [ctypes.c_void_p] * 3 +
+                              [ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                               ctypes.c_void_p]),
+    "dflash_kv_evict_bytes": (ctypes.c_size_t, [ctypes.POINTER(DflashHeads), ctypes.c_int32,
+                                                ctypes.c_int32]),
+    "dflash_kv_evict": (ctypes.c_int, [ctypes.POINTER(DflashHeads), ctypes.c_int32,
+                                       ctypes.POINTER(DflashKV), ctypes.POINTER(DflashKV),
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_int32, ctypes.c_int32] +
+                        [ctypes.c_void_p, ctypes.c_int64] * 2 +
+                        [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
     "dflash_score_tokens_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
     "dflash_score_tokens": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                            ctypes.c_int32, ctypes.c_int32] + [ctypes.c_void_p] * 5 +
@@ -506,6 +522,62 @@ def dflash_sample_filtered(logits, rows, vocab, temperature, top_k, top_p, min_p
         _dense(fn, dev, a, _F64, one), _dense(fn, dev, token, _I32, one),
         _dense(fn, dev, n_kept, _I32, one) if n_kept is not None else None,
         _dense(fn, dev, logprob, _F32, one) if logprob is not None else None, w, wn,
+        _stream(stream, dev)))
+
+
+def dflash_attention_mass_bytes(heads: DflashHeads, batch, T) -> int:
+    size = load().dflash_attention_mass_bytes(ctypes.byref(heads), batch, T)
+    if size == 0:
+        raise DflashError("dflash_attention_mass_bytes", -1)
+    return int(size)
+
+
+def _head_rows(fn, dev, t, dtype, batch, h):
+    """Address and row length of a dense [batch][h][length] tensor."""
+    if t is None or t.dim() != 3 or t.shape[2] < 1:
+        raise DflashError(fn, -1)
+    return _dense(fn, dev, t, dtype, (batch, h, t.shape[2])), t.shape[2]
+
+
+def dflash_attention_mass(heads: DflashHeads, layer, q, row_start, batch, T, last, causal, scale,
+                          kv: DflashKV, ctx_len, lse, mass, accumulate, ws, stream=None):
+    """q bf16 [T][hq][d] (rows may be strided); row_start int32 [batch + 1]; lse fp32 [T][hq];
+    mass fp32 [batch][hkv][positions]."""
+    fn = "dflash_attention_mass"
+    dev = _device(fn, q)
+    hq = heads.n_q_heads
+    qp, ldq = _rows(fn, dev, q, _BF16, T, hq, heads.head_dim)
+    mp, ldm = _head_rows(fn, dev, mass, _F32, batch, heads.n_kv_heads)
+    w, wn = _space(fn, dev, ws)
+    return _check(fn, load().dflash_attention_mass(
+        ctypes.byref(heads), layer, qp, ldq, _dense(fn, dev, row_start, _I32, (batch + 1,)), batch,
+        T, last, 1 if causal else 0, scale, ctypes.byref(kv),
+        _dense(fn, dev, ctx_len, _I32, (batch,)), _dense(fn, dev, lse, _F32, (T, hq)), mp, ldm,
+        1 if accumulate else 0, w, wn, _stream(stream, dev)))
+
+
+def dflash_kv_evict_bytes(heads: DflashHeads, batch, dst_pages) -> int:
+    size = load().dflash_kv_evict_bytes(ctypes.byref(heads), batch, dst_pages)
+    if size == 0:
+        raise DflashError("dflash_kv_evict_bytes", -1)
+    return int(size)
+
+
+def dflash_kv_evict(heads: DflashHeads, layer, src: DflashKV, dst: DflashKV, batch, ctx_len, keep,
+                    sink, recent, mass, kept, new_len, mass_out, ws, stream=None):
+    """ctx_len, keep int32 [batch]; mass fp32 [batch][hkv][positions]; kept int32
+    [batch][hkv][places]; new_len int32 [batch] and mass_out (as mass) may be None."""
+    fn = "dflash_kv_evict"
+    dev = _device(fn, mass)
+    h = heads.n_kv_heads
+    mp, ldm = _head_rows(fn, dev, mass, _F32, batch, h)
+    kp, ldk = _head_rows(fn, dev, kept, _I32, batch, h)
+    w, wn = _space(fn, dev, ws)
+    return _check(fn, load().dflash_kv_evict(
+        ctypes.byref(heads), layer, ctypes.byref(src), ctypes.byref(dst), batch,
+        _dense(fn, dev, ctx_len, _I32, (batch,)), _dense(fn, dev, keep, _I32, (batch,)), sink, recent,
+        mp, ldm, kp, ldk, _dense(fn, dev, new_len, _I32, (batch,)) if new_len is not None else None,
+        _dense(fn, dev, mass_out, _F32, mass.shape) if mass_out is not None else None, w, wn,
         _stream(stream, dev)))
 
 

@@ -281,6 +281,46 @@ void prefix_attention_shape(PrefixParams* p);
 // group0: 8-row group of the layer's first page, oob_group: one past the end.
 cudaError_t prefix_attention_launch(const PrefixParams& p, int d, const CUtensorMap* map, int group0,
                                     int oob_group, cudaStream_t s);
+// Attention weight of each key (attention_mass.cu).
+constexpr int kMaxMassBatch = 1024;
+struct MassParams {
+  const int32_t *row_start, *ctx_len, *page_table;
+  int batch, T, hq, hkv, G;
+  int tokens;                  // rows of the call in a tile: 128 / G
+  int last;                    // rows of a request that weigh (0: all)
+  int causal, max_pages, n_pages, accumulate;
+  float scale_log2;            // scale / ln 2
+  const float* lse;            // [T][hq]
+  float* mass;                 // [batch][hkv][ld_mass]
+  int64_t ld_mass;
+  int* status;
+};
+cudaError_t attention_mass_launch(const MassParams& p, int d, const CUtensorMap& kv_map, const CUtensorMap& q_map,
+                                  int group0, int oob_group, cudaStream_t s);
+
+// Eviction (kv_evict.cu).
+struct EvictParams {
+  const void* src_pool;        // layer bases
+  void* dst_pool;
+  const float* src_scales;     // E4M3 caches, else null
+  float* dst_scales;
+  const int32_t *src_table, *dst_table;
+  int src_pages, src_max_pages, dst_pages, dst_max_pages;
+  int same_pool;               // pages of both tables are the same memory's
+  int batch, hkv, planes;
+  const int32_t *ctx_len, *keep;
+  int sink, recent;
+  const float* mass;           // [batch][hkv][ld_mass]
+  float* mass_out;             // same, or null
+  int64_t ld_mass, ld_kept;
+  int32_t* kept;               // [batch][hkv][ld_kept]
+  int32_t* new_len;            // [batch] or null
+  int* conflict;               // set where a page is written twice, or read and written;
+  unsigned* owner;             // [dst_pages], 256 bytes behind it
+  int* status;
+};
+cudaError_t kv_evict_launch(const EvictParams& p, int vector_bytes, cudaStream_t s);
+
 // Scores of given tokens (score_tokens.cu).
 struct ScoreParams {
   const void* logits;          // bf16 or fp32 rows

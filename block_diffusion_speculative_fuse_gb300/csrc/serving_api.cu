@@ -404,6 +404,132 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
   return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
 }
 
+size_t dflash_attention_mass_bytes(const dflash_heads* heads, int32_t batch, int32_t T) {
+  if (check_heads(heads) || batch < 1 || batch > kMaxMassBatch || T < 1) return 0;
+  return kHeaderBytes;  // the status word
+}
+
+int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,
+                          const int32_t* row_start, int32_t batch, int32_t T, int32_t last, int32_t causal,
+                          float scale, const dflash_kv* kv, const int32_t* ctx_len, const float* lse,
+                          float* mass, int64_t ld_mass, int32_t accumulate, void* ws, size_t ws_bytes,
+                          void* stream) {
+  int rc = check_heads(heads);
+  if (rc) return rc;
+  MassParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int d = heads->head_dim;
+  if (q == nullptr || row_start == nullptr || ctx_len == nullptr || lse == nullptr || mass == nullptr ||
+      !aligned(q, 16) || !aligned(row_start, 4) || !aligned(ctx_len, 4) || !aligned(lse, 4) || !aligned(mass, 4) ||
+      batch < 1 || T < 1 || last < 0 || (causal != 0 && causal != 1) || (accumulate != 0 && accumulate != 1) ||
+      ld_mass < 1 || ld_q < static_cast<int64_t>(heads->n_q_heads) * d || ld_q % 8 || !scale_of(scale, d, &p.scale_log2))
+    return DFLASH_ERR_INVALID_ARG;
+  rc = check_cache(heads, layer, kv);
+  if (rc) return rc;
+  if (kv->dtype != 0 || terms_of(heads) != 1 || batch > kMaxMassBatch) return DFLASH_ERR_UNSUPPORTED;
+  if (batch > kv->n_rows) return DFLASH_ERR_CAPACITY;
+  const uint64_t layer_groups = static_cast<uint64_t>(kv->n_pages) * 2 * heads->n_kv_heads * 2;
+  const uint64_t groups = layer_groups * heads->n_layers;
+  // TMA coordinates are 32 bits, a map's strides 40; units are counted in 31 bits
+  if (groups >= (1ull << 31) - 2 || T > (1 << 30) || ld_q >= (1ll << 38) ||
+      static_cast<double>(batch) * heads->n_kv_heads * (kv->max_pages / 16 + 1) >= 1073741824.0)
+    return DFLASH_ERR_UNSUPPORTED;
+  rc = check_ws(ws, ws_bytes, kHeaderBytes);
+  if (rc) return rc;
+  p.row_start = row_start;
+  p.ctx_len = ctx_len;
+  p.page_table = kv->page_table;
+  p.batch = batch;
+  p.T = T;
+  p.hq = heads->n_q_heads;
+  p.hkv = heads->n_kv_heads;
+  p.G = p.hq / p.hkv;
+  p.tokens = 128 / p.G;
+  p.last = last;
+  p.causal = causal;
+  p.max_pages = kv->max_pages;
+  p.n_pages = kv->n_pages;
+  p.accumulate = accumulate;
+  p.lse = lse;
+  p.mass = mass;
+  p.ld_mass = ld_mass;
+  p.status = static_cast<int32_t*>(ws);
+  CUtensorMap kv_map, q_map;
+  rc = encode_kv_pages(&kv_map, kv->pool, groups, d);
+  if (!rc) rc = encode_q_rows(&q_map, q, ld_q, T, p.hq, p.G, p.tokens, d);
+  if (rc) return rc;
+  const cudaError_t e = attention_mass_launch(p, d, kv_map, q_map, static_cast<int>(layer_groups * layer),
+                                              static_cast<int>(groups), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
+}
+
+size_t dflash_kv_evict_bytes(const dflash_heads* heads, int32_t batch, int32_t dst_pages) {
+  if (check_heads(heads) || batch < 1 || batch > 65535 || dst_pages < 1) return 0;
+  return kHeaderBytes + 256 + al256(static_cast<size_t>(dst_pages) * 4);
+}
+
+int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* src, const dflash_kv* dst,
+                    int32_t batch, const int32_t* ctx_len, const int32_t* keep, int32_t sink, int32_t recent,
+                    const float* mass, int64_t ld_mass, int32_t* kept, int64_t ld_kept, int32_t* new_len,
+                    float* mass_out, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_heads(heads);
+  if (!rc) rc = check_cache(heads, layer, src);
+  if (!rc) rc = check_cache(heads, layer, dst);
+  if (rc) return rc;
+  if (ctx_len == nullptr || keep == nullptr || mass == nullptr || kept == nullptr || batch < 1 || sink < 0 ||
+      recent < 0 || ld_mass < 1 || ld_kept < 1 || mass_out == mass || !aligned(ctx_len, 4) || !aligned(keep, 4) ||
+      !aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_len, 4) || !aligned(mass_out, 4) ||
+      src->dtype != dst->dtype)
+    return DFLASH_ERR_INVALID_ARG;
+  if (batch > 65535 || heads->n_kv_heads > 65535 || ld_mass > (1 << 30) || ld_kept > (1 << 30))
+    return DFLASH_ERR_UNSUPPORTED;
+  if (batch > src->n_rows || batch > dst->n_rows) return DFLASH_ERR_CAPACITY;
+  const int elem = src->dtype == 1 ? 1 : 2, d = heads->head_dim;
+  const size_t src_layer = layer_elems(heads, src) * elem, dst_layer = layer_elems(heads, dst) * elem;
+  // two caches are the same pool or apart
+  const auto a = reinterpret_cast<uintptr_t>(src->pool), b = reinterpret_cast<uintptr_t>(dst->pool);
+  const bool same = a == b;
+  if (same ? src->n_pages != dst->n_pages || src->scales != dst->scales
+           : a < b + dst_layer * heads->n_layers && b < a + src_layer * heads->n_layers)
+    return DFLASH_ERR_INVALID_ARG;
+  rc = check_ws(ws, ws_bytes, dflash_kv_evict_bytes(heads, batch, dst->n_pages));
+  if (rc) return rc;
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.src_pool = static_cast<const uint8_t*>(src->pool) + src_layer * layer;
+  p.dst_pool = static_cast<uint8_t*>(dst->pool) + dst_layer * layer;
+  if (src->dtype == 1) {
+    p.src_scales = src->scales + layer_elems(heads, src) / d * layer;
+    p.dst_scales = dst->scales + layer_elems(heads, dst) / d * layer;
+  }
+  p.src_table = src->page_table;
+  p.dst_table = dst->page_table;
+  p.src_pages = src->n_pages;
+  p.src_max_pages = src->max_pages;
+  p.dst_pages = dst->n_pages;
+  p.dst_max_pages = dst->max_pages;
+  p.same_pool = same;
+  p.batch = batch;
+  p.hkv = heads->n_kv_heads;
+  p.planes = 2 * terms_of(heads);
+  p.ctx_len = ctx_len;
+  p.keep = keep;
+  p.sink = sink;
+  p.recent = recent;
+  p.mass = mass;
+  p.mass_out = mass_out;
+  p.ld_mass = ld_mass;
+  p.ld_kept = ld_kept;
+  p.kept = kept;
+  p.new_len = new_len;
+  uint8_t* w = static_cast<uint8_t*>(ws) + kHeaderBytes;
+  p.conflict = reinterpret_cast<int*>(w);
+  p.owner = reinterpret_cast<unsigned*>(w + 256);
+  p.status = static_cast<int32_t*>(ws);
+  const cudaError_t e = kv_evict_launch(p, d * elem, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DFLASH_OK : record_cuda_error(e);
+}
+
 size_t dflash_score_tokens_bytes(int32_t rows, int32_t vocab, int32_t n_top) {
   if (rows < 1 || vocab < 1 || vocab > kMaxSampleVocab || n_top < 0 || n_top > kMaxScoreTop) return 0;
   return kHeaderBytes;  // the status word; a row's work stays on chip

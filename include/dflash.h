@@ -501,6 +501,58 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
                            const float* min_p, const double* a, int32_t* token, int32_t* n_kept,
                            float* logprob, void* ws, size_t ws_bytes, void* stream);
 
+/* The attention weight that each cached key receives:
+ *   mass[r][h][j] = (accumulate: mass[r][h][j] +) the sum of exp(scale * q . k_j
+ *   - lse) over the last `last` rows of request r (0: all its rows) that see
+ *   position j, and over the query heads of KV head h,
+ * for j < ctx_len[r]; positions from there on are left as they are.  q,
+ * row_start, ctx_len, causal and scale as in dflash_attention_chunk, lse fp32
+ * [T][n_q_heads] as that call leaves it.  mass fp32 [batch][n_kv_heads]
+ * [ld_mass].  A request without rows gets sums of 0 (unchanged when
+ * accumulating).  Bad row ranges, lengths and pages are treated and recorded
+ * as there (sites 561, 562, 563); a ctx_len above ld_mass is recorded (site
+ * 564) and the positions beyond are dropped.  A K that is not finite makes
+ * its own position's sum undefined, no other's.
+ * A bf16 one-term cache; batch <= 1024 and <= kv->n_rows; batch * n_kv_heads *
+ * max_pages below 2^34.  Products, exponents and sums are fp32, the sums in a
+ * fixed order.  Deterministic.
+ * ws: initialised, dflash_attention_mass_bytes(heads, batch, T) bytes. */
+size_t dflash_attention_mass_bytes(const dflash_heads* heads, int32_t batch, int32_t T);
+int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,
+                          const int32_t* row_start, int32_t batch, int32_t T, int32_t last,
+                          int32_t causal, float scale, const dflash_kv* kv, const int32_t* ctx_len,
+                          const float* lse, float* mass, int64_t ld_mass, int32_t accumulate,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction: of each request and KV head the min(keep[r], ctx_len[r]) positions
+ * with the largest mass are kept and moved together, in their order, to
+ * positions 0, 1, ... of row r of dst; the first `sink` and the last `recent`
+ * positions count as heavier than all others, equals go to the lower
+ * position, NaN comes last.  (Keys keep the rotation of the position at which
+ * they were appended; new rows go on from the old positions' angles.)
+ *   kept int32 [batch][n_kv_heads][ld_kept]: the positions, ascending
+ *   new_len int32 [batch] or NULL: how many
+ *   mass_out fp32, as mass, or NULL: their masses, in the same order
+ * What lies behind new_len in each is left as it is, and so are slots of dst
+ * behind it.  ctx_len, keep on the device; mass fp32 [batch][n_kv_heads]
+ * [ld_mass].  One layer of caches of one dtype (bf16 with one or two terms, or
+ * E4M3 with its scales), vectors copied bit for bit.  dst may be other pages
+ * of src's pool (same pool, n_pages and scales), or a pool apart from it.
+ * A page that rows of dst name twice within new_len, or that a kept request of
+ * the call reads, is recorded as DFLASH_ERR_INVALID_ARG (site 584) and nothing
+ * is copied.  Recorded as DFLASH_ERR_CAPACITY: a ctx_len beyond src's table or
+ * ld_mass (site 581) and a keep beyond dst's table or ld_kept (site 582), which
+ * count as those; a page id out of range, of dst (site 583: its positions are
+ * dropped) or of src (site 585: they read as zeros).
+ * batch <= 65535 and <= n_rows of both.  mass_out must not overlap mass.
+ * ws: initialised, dflash_kv_evict_bytes(heads, batch, dst->n_pages) bytes. */
+size_t dflash_kv_evict_bytes(const dflash_heads* heads, int32_t batch, int32_t dst_pages);
+int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* src,
+                    const dflash_kv* dst, int32_t batch, const int32_t* ctx_len, const int32_t* keep,
+                    int32_t sink, int32_t recent, const float* mass, int64_t ld_mass, int32_t* kept,
+                    int64_t ld_kept, int32_t* new_len, float* mass_out, void* ws, size_t ws_bytes,
+                    void* stream);
+
 /* What rows of logits (in_dtype 0 = bf16, 1 = fp32; [rows][vocab], rows ld
  * elements apart) say of given tokens, at temperature T (device fp32 [rows];
  * NULL: 1; values below 1e-30 or above 1e30 count as those):

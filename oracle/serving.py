@@ -113,3 +113,26 @@ def score(z, temperature, token, n):
         return 0.0, -1, entropy, order, [float(lp[i]) for i in order]
     rank = int(np.count_nonzero(z > z[token]) + np.count_nonzero(z[:token] == z[token]))
     return float(lp[token]), rank, entropy, order, [float(lp[i]) for i in order]
+
+
+def attention_mass(q, k, lse, scale, limits):
+    """q [w][hq][d] with lse [w][hq], k [keys][hkv][d]; row i sees the first
+    limits[i] keys.  Weight that each key receives, [hkv][keys]."""
+    hkv = k.shape[1]
+    G = q.shape[1] // hkv
+    mass = np.zeros((hkv, k.shape[0]))
+    for i in range(q.shape[0]):
+        m = max(0, min(int(limits[i]), k.shape[0]))
+        for h in range(q.shape[1]):
+            if m:
+                mass[h // G, :m] += np.exp(scale * (k[:m, h // G] @ q[i, h]) - lse[i, h])
+    return mass
+
+
+def evict(mass, ctx, keep, sink, recent):
+    """Kept positions, ascending, of one request and KV head."""
+    def weight(j):
+        if j < sink or j >= ctx - recent:
+            return (0, 0.0)
+        return (2, 0.0) if math.isnan(mass[j]) else (1, -float(mass[j]))
+    return sorted(sorted(range(ctx), key=lambda j: (weight(j), j))[:max(0, min(keep, ctx))])

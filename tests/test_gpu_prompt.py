@@ -305,3 +305,239 @@ def test_score_optional_outputs_and_single_rows():
         assert torch.equal(ti, res[0][3][lo:hi])
         for a, b in ((ent, res[0][2]), (tl, res[0][4]), (lp, res[0][5])):
             assert torch.allclose(a, b[lo:hi], rtol=0, atol=2.0 ** -22 * (1 + math.log(151936) + 30))
+
+
+# ----------------------------------------------------------- attention mass
+def mass_case(ns, ctx, hq, hkv, d, last=0, causal=True, add=False, seed=0, lead=1, tail=2, wide=8, room=5, layers=1,
+              layer=0, scale=0.0):
+    """A chunk attention call for the lse, then the mass call over the same rows."""
+    B = B_()
+    s = chunk_case(ns, ctx, hq, hkv, d, causal, seed=seed, lead=lead, tail=tail, wide=wide, layers=layers, layer=layer,
+                   scale=scale)
+    hd, kv, start, T = s["args"][0], s["c"].kv, s["args"][3], s["T"]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    mass0 = torch.rand(len(ns), hkv, max(1, max(ctx)) + room, generator=g, device="cuda")
+    s["mass0"], s["mass"] = mass0.clone(), mass0
+    ws = workspace(B.dflash_attention_mass_bytes(hd, len(ns), T))
+    s["mass_args"] = (hd, layer, s["q"], start, len(ns), T, last, causal, scale, kv, i32(ctx), s["lse"], mass0, add, ws)
+    B.dflash_attention_mass(*s["mass_args"])
+    torch.cuda.synchronize()
+    assert B.dflash_get_status(ws) == (0, 0)
+    return s
+
+
+def check_mass(s, hq, d, last=0, causal=True, add=False, layer=0, scale=0.0):
+    scale = scale or 1.0 / math.sqrt(d)
+    got, before = s["mass"].double().cpu().numpy(), s["mass0"].double().cpu().numpy()
+    lse = s["lse"].double().cpu().numpy()
+    for r, (n, m) in enumerate(zip(s["ns"], s["ctx"])):
+        w = min(n, last) if last else n
+        a = int(s["start"][r]) + n - w
+        k, _ = s["c"].keys(r, layer, m)
+        q = s["q"][a:a + w].double().cpu().numpy()
+        assert np.array_equal(got[r, :, m:], before[r, :, m:])
+        if m == 0:
+            continue
+        want = O.attention_mass(q, k, lse[a:a + w], scale, [m - w + i + 1 if causal else m for i in range(w)])
+        G = hq // k.shape[1]
+        worst = scale * max([float((np.abs(q[:, h]) @ np.abs(k[:, h // G]).T).max()) for h in range(hq)] + [0.0]) \
+            if w else 0.0
+        f = lse[a:a + w][np.isfinite(lse[a:a + w])]
+        size = worst + (float(np.abs(f).max()) if f.size else 0.0)
+        rel = (d + 16) * 2.0 ** -24 * worst + 2.0 ** -23 * size + 2.0 ** -21 + w * G * 2.0 ** -24
+        old = before[r, :, :m] if add else 0.0
+        err = np.abs(got[r, :, :m] - want - old)
+        tol = rel * want + 2.0 ** -23 * (want + old) + 1e-30
+        assert np.all(err <= tol), (r, float((err / tol).max()))
+
+
+MASS = [  # rows per request, cached positions, hq, hkv, d, last, causal, add
+    ([1], [1], 1, 1, 64, 0, True, False),
+    ([1], [0], 4, 2, 128, 0, True, False),
+    ([1], [4096], 32, 8, 128, 32, True, True),
+    ([0, 5, 0, 7, 0], [0, 5, 40, 29, 300], 8, 4, 64, 0, True, False),
+    ([0, 5, 2], [300, 5, 40], 8, 4, 64, 3, True, True),
+    ([40], [17], 8, 2, 128, 0, True, False),           # rows before the start
+    ([100, 3], [700, 129], 6, 2, 64, 33, True, False), # three heads to one
+    ([61], [500], 15, 3, 128, 0, False, True),
+    ([33], [300], 11, 1, 128, 0, True, False),
+    ([200, 64], [777, 64], 32, 8, 128, 0, True, False),    # many tiles
+    ([300], [300], 2, 2, 64, 0, True, True),           # a whole prompt, a head to one
+    ([70, 33], [1000, 2], 8, 2, 128, 16, False, False),
+    ([32, 32, 9], [9000, 6001, 8191], 8, 2, 128, 32, True, False),
+]
+
+
+@pytest.mark.parametrize("ns,ctx,hq,hkv,d,last,causal,add", MASS)
+def test_mass(ns, ctx, hq, hkv, d, last, causal, add):
+    s = mass_case(ns, ctx, hq, hkv, d, last, causal, add, seed=sum(ctx) + d)
+    check_mass(s, hq, d, last, causal, add)
+
+
+def test_mass_many_requests_layers_and_scale():
+    rnd = np.random.default_rng(4)
+    ns = [int(x) for x in rnd.choice([0, 1, 1, 2, 9], 700)]
+    ctx = [int(x) + n for x, n in zip(rnd.integers(0, 600, 700), ns)]
+    s = mass_case(ns, ctx, 4, 2, 64, 1, seed=3, layers=2, layer=1, scale=0.2)
+    check_mass(s, 4, 64, 1, layer=1, scale=0.2)
+
+
+def test_mass_of_all_rows_adds_up_to_the_rows():
+    s = mass_case([150, 20], [600, 20], 8, 2, 128, seed=9)
+    got = s["mass"].double().cpu().numpy()
+    for r, m in enumerate(s["ctx"]):
+        assert np.allclose(got[r, :, :m].sum(1), s["ns"][r] * 4, rtol=1e-4)
+
+
+# ------------------------------------------------------------------ eviction
+def evict_case(ctx, keep, hkv, d, sink=0, recent=0, kind="bf16", same_pool=False, seed=0, mass=None, layers=2, layer=1,
+               room=3, spread=3.0):
+    B = B_()
+    rnd = np.random.default_rng(seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    planes = 4 if kind == "two" else 2
+    new = [min(max(k, 0), c) for k, c in zip(keep, ctx)]
+    need = [(c + 15) // 16 for c in ctx], [(n + 15) // 16 for n in new]
+    total = [sum(x) + 2 for x in need]
+    if same_pool:
+        total = [sum(total)] * 2
+    perm = [rnd.permutation(total[0]), None]
+    perm[1] = perm[0][::-1] if same_pool else rnd.permutation(total[1])
+    tables = []
+    for side in (0, 1):
+        t = np.full((len(ctx), max(1, max(need[side])) + 1), -3, np.int32)
+        at = 0
+        for r, k in enumerate(need[side]):
+            t[r, :k] = perm[side][at:at + k]
+            at += k
+        tables.append(t)
+
+    def pool(pages):
+        if kind == "e4m3":
+            return (torch.randint(0, 256, (layers, pages, planes, hkv, PAGE, d), generator=g, device="cuda",
+                                  dtype=torch.uint8), torch.rand(layers, pages, planes, hkv, PAGE, generator=g,
+                                                                 device="cuda"))
+        return torch.randint(-2 ** 15, 2 ** 15, (layers, pages, planes, hkv, PAGE, d), generator=g, device="cuda",
+                             dtype=torch.int16), None
+    src = pool(total[0])
+    dst = src if same_pool else pool(total[1])
+    td = [i32(t) for t in tables]
+    kvs = [B.DflashKV(pool=x[0].data_ptr(), page_table=t.data_ptr(), n_pages=n, max_pages=t.shape[1], n_rows=len(ctx),
+                      dtype=1 if kind == "e4m3" else 0, scales=None if x[1] is None else x[1].data_ptr())
+           for x, t, n in zip((src, dst), td, total)]
+    if mass is None:
+        mass = torch.exp(spread * torch.randn(len(ctx), hkv, max(1, max(ctx)) + room, generator=g, device="cuda"))
+        mass = torch.where(mass < 0.3, 0.0, mass)
+    kept = torch.full((len(ctx), hkv, max(1, max(new)) + 1), -9, dtype=torch.int32, device="cuda")
+    new_len = torch.full((len(ctx),), -9, dtype=torch.int32, device="cuda")
+    mass_out = torch.full_like(mass, -9.0)
+    hd = heads(layers, hkv, hkv, d, planes // 2)
+    before = [None if x is None else x.clone() for x in src + dst]
+    ws = workspace(B.dflash_kv_evict_bytes(hd, len(ctx), total[1]))
+    args = (hd, layer, kvs[0], kvs[1], len(ctx), i32(ctx), i32(keep), sink, recent, mass, kept, new_len, mass_out, ws)
+    B.dflash_kv_evict(*args)
+    torch.cuda.synchronize()
+    return dict(src=src, dst=dst, before=before, tables=tables, td=td, mass=mass, kept=kept, new_len=new_len,
+                mass_out=mass_out, ws=ws, new=new, args=args, kvs=kvs)
+
+
+def check_evict(s, ctx, keep, hkv, sink, recent, layer=1):
+    assert B_().dflash_get_status(s["ws"]) == (0, 0)
+    assert list(s["new_len"].cpu().numpy()) == s["new"]
+    mass, kept, mass_out = (s[k].cpu().numpy() for k in ("mass", "kept", "mass_out"))
+    want = s["before"][2].clone()
+    scales = None if s["before"][3] is None else s["before"][3].clone()
+    for r, c in enumerate(ctx):
+        n = s["new"][r]
+        assert (kept[r, :, n:] == -9).all() and (mass_out[r, :, n:] == -9.0).all()
+        for h in range(hkv):
+            k = np.array(O.evict(mass[r, h], c, keep[r], sink, recent), np.int64)
+            assert np.array_equal(kept[r, h, :n], k), (r, h)
+            assert np.array_equal(mass_out[r, h, :n], mass[r, h, k], equal_nan=True)
+            if n == 0:
+                continue
+            at = np.arange(n)
+            to, ts = torch.from_numpy(s["tables"][1][r, at // 16].astype(np.int64)), torch.from_numpy(at % 16)
+            fr, fs = torch.from_numpy(s["tables"][0][r, k // 16].astype(np.int64)), torch.from_numpy(k % 16)
+            want[layer, to, :, h, ts] = s["before"][0][layer, fr, :, h, fs]
+            if scales is not None:
+                scales[layer, to, :, h, ts] = s["before"][1][layer, fr, :, h, fs]
+    assert torch.equal(s["dst"][0], want)
+    if scales is not None:
+        assert torch.equal(s["dst"][1], scales)
+
+
+EVICT = [  # ctx, keep, hkv, d, sink, recent, kind, same pool
+    ([1], [1], 1, 64, 0, 0, "bf16", False),
+    ([40], [17], 2, 128, 0, 0, "bf16", False),
+    ([0, 33, 5, 100], [4, 0, 9, 31], 4, 64, 4, 8, "bf16", True),
+    ([700, 1025, 16], [100, 1024, 3], 3, 128, 2, 5, "two", False),
+    ([3000], [1], 8, 64, 0, 0, "e4m3", False),
+    ([300, 299], [64, 250], 2, 128, 300, 10, "e4m3", True),   # more protected than kept
+    ([20001], [5000], 2, 128, 4, 64, "bf16", False),          # over a cluster
+    ([70000, 9], [12345, 9], 1, 64, 1, 1, "bf16", False),
+    ([64, 2500], [-3, 10 ** 6], 2, 64, 0, 0, "bf16", False),
+]
+
+
+@pytest.mark.parametrize("ctx,keep,hkv,d,sink,recent,kind,same", EVICT)
+def test_evict(ctx, keep, hkv, d, sink, recent, kind, same):
+    s = evict_case(ctx, keep, hkv, d, sink, recent, kind, same, seed=sum(ctx) + d)
+    check_evict(s, ctx, keep, hkv, sink, recent)
+
+
+@pytest.mark.parametrize("ctx", [900, 30000])
+def test_evict_ties_and_special_masses(ctx):
+    """Equal masses go to the lower position; NaN last, -0 and 0 alike."""
+    m = torch.zeros(5, 1, ctx, device="cuda")
+    m[0, 0, ::2] = -0.0
+    m[1, 0, ctx // 2:] = 1.0
+    m[2] = torch.arange(ctx, device="cuda") % 7
+    m[3, 0, ::3] = math.nan
+    m[3, 0, 1::3] = -math.inf
+    m[4, 0, 10:50] = math.inf
+    m[4, 0, 60:] = -1.0
+    keep = [ctx // 3, ctx // 2 + 5, ctx // 4, ctx // 3 * 2 + 9, 45]
+    for sink, recent in ((0, 0), (3, 20)):
+        s = evict_case([ctx] * 5, keep, 1, 64, sink, recent, mass=m, seed=ctx)
+        check_evict(s, [ctx] * 5, keep, 1, sink, recent)
+
+
+def test_evict_refuses_pages_in_use():
+    """A target page that the call reads, or writes twice: nothing is copied."""
+    B = B_()
+    for clash in ("read", "twice"):
+        s = evict_case([100, 90], [40, 40], 2, 64, same_pool=True, seed=1)
+        pool = s["dst"][0].clone()
+        s["td"][1][1, 2] = s["td"][0][0, 1] if clash == "read" else s["td"][1][0, 0]
+        s["dst"][0].random_(-100, 100)
+        before = s["dst"][0].clone()
+        B.dflash_kv_evict(*s["args"])
+        torch.cuda.synchronize()
+        assert B.dflash_get_status(s["ws"]) == (-1, 584)
+        assert torch.equal(s["dst"][0], before) and not torch.equal(pool, before)
+
+
+def test_evict_reports_bad_pages_and_lengths():
+    B = B_()
+    base = dict(ctx=[60, 50], keep=[30, 30], hkv=1, d=64)
+    s = evict_case(**base)
+    s["td"][1][0, 1] = 999                     # a target page: its positions are dropped
+    s["dst"][0].zero_()
+    B.dflash_kv_evict(*s["args"])
+    assert B.dflash_get_status(s["ws"]) == (-3, 583)
+    assert torch.count_nonzero(s["dst"][0][1, int(s["tables"][1][0, 1])]) == 0
+    assert torch.count_nonzero(s["dst"][0][1, int(s["tables"][1][1, 1])]) > 0
+    s = evict_case(**base)
+    s["td"][0][1, :] = -1                      # source pages: zeros
+    B.dflash_workspace_init(s["ws"])
+    B.dflash_kv_evict(*s["args"])
+    assert B.dflash_get_status(s["ws"]) == (-3, 585)
+    assert torch.count_nonzero(s["dst"][0][1, int(s["tables"][1][1, 0])]) == 0
+    for at, value, site in ((5, [10 ** 6, 50], 581), (6, [32, 10 ** 6], 582), (6, [30, 49], 582)):
+        s = evict_case(**base)
+        args = list(s["args"])
+        args[at] = i32(value)
+        B.dflash_kv_evict(*args)
+        torch.cuda.synchronize()
+        assert B.dflash_get_status(s["ws"]) == (-3, site)
