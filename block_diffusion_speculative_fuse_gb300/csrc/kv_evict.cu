@@ -8,8 +8,7 @@
 // masses, whose exponents lie together, do not all meet in one counter), then one pass that
 // numbers what is above it and the first equals in order of position.  One CTA per request
 // and head, or a cluster, each CTA a slice of the positions, where there are few.  The third
-// copies, a target page of a head at a time; source vectors are whole lines, and
-// a thread has eight of their pieces in flight.
+// copies whole vectors.
 //
 // Bound: the copy's bytes.
 #include <climits>
@@ -21,11 +20,12 @@ namespace dflash {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCached = 24;      // positions of a thread whose keys stay in registers
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kCopyThreads = 256;
-constexpr int kCopies = 8;       // pieces of a thread, all in flight
+constexpr int kCopies = 8;       // loads of a thread in flight
 
 // Kept positions of request r, and its length; errors are recorded by `tell`.
 struct Request {
@@ -77,29 +77,63 @@ __device__ __forceinline__ uint32_t key_of(float m) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p, int cluster) {
-  __shared__ uint32_t bins[2][kBins];
-  __shared__ int warps[2][kThreads / 32], found[2];
+// Keys of a block of positions, kCached to a thread.  A slice of one block keeps them in
+// registers through all passes; a longer one reads its masses again.
+struct Keys {
+  const float* mass;
+  int safe0, safe1, j1;
+  uint32_t k[kCached];
+  __device__ void load(int base) {   // positions base + i * kThreads + tid
+    float m[kCached];
+#pragma unroll
+    for (int i = 0; i < kCached; ++i) {
+      const int j = base + i * kThreads + threadIdx.x;
+      m[i] = j < j1 ? __ldg(mass + j) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kCached; ++i) {
+      const int j = base + i * kThreads + threadIdx.x;
+      k[i] = j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(m[i]);
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p, int cluster) {
+  __shared__ __align__(16) uint32_t bins[2][kBins];
+  __shared__ int warps[2][kWarps], found[2];
   __shared__ int2 slice_counts;   // of this CTA's slice: above the border, equal
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = blockIdx.x / cluster, r = unit / p.hkv, h = unit % p.hkv;
   const Request q(p, r, false);
   if (q.keep == 0) return;   // (the whole cluster)
-  const float* mass = p.mass + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
   const int slice = (q.ctx + cluster - 1) / cluster;
   const int j0 = min(rank * slice, q.ctx), j1 = min(j0 + slice, q.ctx);
-  const int safe0 = p.sink, safe1 = q.ctx - min(p.recent, q.ctx);
-  auto key_at = [&](int j, float* m) {
-    *m = __ldg(mass + j);
-    return j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(*m);
+  Keys keys;
+  keys.mass = p.mass + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
+  keys.safe0 = p.sink;
+  keys.safe1 = q.ctx - min(p.recent, q.ctx);
+  keys.j1 = j1;
+  constexpr int BLOCK = kCached * kThreads;
+  const bool one = j1 - j0 <= BLOCK;
+  if (one) keys.load(j0);
+  // f(key, position) for the slice's positions of this thread
+  auto each = [&](auto f) {
+#pragma unroll 1
+    for (int base = j0; base < j1; base += BLOCK) {
+      if (!one) keys.load(base);
+#pragma unroll
+      for (int i = 0; i < kCached; ++i) {
+        const int j = base + i * kThreads + tid;
+        if (j < j1) f(keys.k[i], j);
+      }
+    }
   };
-  auto sync_all = [&]() {
-    if (cluster > 1) cluster_sync();
-    else __syncthreads();
+  auto sum_of_lower = [&](int v) {   // of the warps before; v: lane w has warp w's
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? v : 0));
   };
   uint32_t border = 0;
-  int equals = 0;                 // kept of those at it
+  int equals = 0;                 // kept of those at the border
   if (q.keep < q.ctx) {
     uint32_t prefix = 0, mask = 0;
     int need = q.keep;            // of the positions with this prefix
@@ -109,31 +143,38 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
       uint32_t* mine = bins[pass & 1];
       for (int b = tid; b < kBins; b += kThreads) mine[b] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int j = j0 + tid; j < j1; j += kThreads) {
-        float m;
-        const uint32_t k = key_at(j, &m);
+      each([&](uint32_t k, int) {
         if ((k & mask) == prefix) atomicAdd(&mine[k >> shift & bits], 1u);
+      });
+      if (cluster > 1) cluster_sync();
+      else __syncthreads();
+      // counts from the largest bin down: thread t has the four from 2047 - 4 t on
+      static_assert(kBins == 4 * kThreads, "four bins a thread");
+      const int low = kBins - 4 - 4 * tid;
+      int c[4] = {0, 0, 0, 0};
+      if (cluster == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = mine[low + 3 - i];
+      } else {
+        const uint32_t at = smem_u32(&mine[low]);
+        uint4 v[kMaxCluster];
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x)
+          if (x < cluster)
+            asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w)
+                         : "r"(dsmem_map(at, x)));
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x)
+          if (x < cluster) {
+            c[0] += v[x].w;
+            c[1] += v[x].z;
+            c[2] += v[x].y;
+            c[3] += v[x].x;
+          }
       }
-      sync_all();
-      // counts of the two largest bins first: thread t has bins 2047 - 2 t and the one below
-      const int hi = kBins - 1 - 2 * tid;
-      int a = 0, b = 0;
-      for (int c = 0; c < cluster; ++c) {
-        if (cluster == 1) {
-          a = mine[hi];
-          b = mine[hi - 1];
-        } else {
-          uint2 v;
-          asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
-                       : "=r"(v.x), "=r"(v.y)
-                       : "r"(dsmem_map(smem_u32(&mine[hi - 1]), c))
-                       : "memory");
-          b += v.x;
-          a += v.y;
-        }
-      }
-      int upto = a + b;
+      const int sum = c[0] + c[1] + c[2] + c[3];
+      int upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -141,14 +182,14 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
       }
       if (lane == 31) warps[0][warp] = upto;
       __syncthreads();
-      const int part = warps[0][lane];
-      const int before = __reduce_add_sync(0xffffffffu, lane < warp ? part : 0) + upto - a - b;
-      if (before < need && before + a >= need) {
-        found[0] = hi;
-        found[1] = before;
-      } else if (before + a < need && before + a + b >= need) {
-        found[0] = hi - 1;
-        found[1] = before + a;
+      int before = sum_of_lower(lane < kWarps ? warps[0][lane] : 0) + upto - sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (before < need && before + c[i] >= need) {
+          found[0] = low + 3 - i;
+          found[1] = before;
+        }
+        before += c[i];
       }
       __syncthreads();
       prefix |= static_cast<uint32_t>(found[0]) << shift;
@@ -159,15 +200,14 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     equals = need;
   }
   // where this slice's kept positions go: count, then number them in order
-  int above0 = 0, equal0 = 0;
-  if (q.keep < q.ctx && cluster > 1) {
+  const bool all = q.keep >= q.ctx;
+  int above0 = all ? j0 : 0, equal0 = 0;
+  if (!all && cluster > 1) {
     int above = 0, equal = 0;
-    for (int j = j0 + tid; j < j1; j += kThreads) {
-      float m;
-      const uint32_t k = key_at(j, &m);
+    each([&](uint32_t k, int) {
       above += k > border;
       equal += k == border;
-    }
+    });
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
     __syncthreads();
@@ -177,107 +217,114 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     }
     __syncthreads();
     if (warp == 0) {
-      above = __reduce_add_sync(0xffffffffu, warps[0][lane]);
-      equal = __reduce_add_sync(0xffffffffu, warps[1][lane]);
+      above = __reduce_add_sync(0xffffffffu, lane < kWarps ? warps[0][lane] : 0);
+      equal = __reduce_add_sync(0xffffffffu, lane < kWarps ? warps[1][lane] : 0);
       if (lane == 0) slice_counts = make_int2(above, equal);
     }
     cluster_sync();
-    for (int c = 0; c < rank; ++c) {
-      int2 v;
-      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
-                   : "=r"(v.x), "=r"(v.y)
-                   : "r"(dsmem_map(smem_u32(&slice_counts), c))
-                   : "memory");
-      above0 += v.x;
-      equal0 += v.y;
+    int2 v[kMaxCluster];
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      v[x] = make_int2(0, 0);
+      if (x < rank)
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(v[x].x), "=r"(v[x].y)
+                     : "r"(dsmem_map(smem_u32(&slice_counts), x)));
+    }
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      above0 += v[x].x;
+      equal0 += v[x].y;
     }
   }
   int32_t* kept = p.kept + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_kept;
   float* mass_out = p.mass_out == nullptr ? nullptr : p.mass_out + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
-  const bool all = q.keep >= q.ctx;
-  if (all) above0 = j0;
 #pragma unroll 1
-  for (int base = j0; base < j1; base += kThreads) {
-    const int j = base + tid;
-    float m = 0.f;
-    uint32_t k = 0;
-    if (j < j1) k = key_at(j, &m);
-    const bool above = j < j1 && (all || k > border), equal = j < j1 && !all && k == border;
-    const unsigned va = __ballot_sync(0xffffffffu, above), ve = __ballot_sync(0xffffffffu, equal);
-    __syncthreads();
-    if (lane == 0) {
-      warps[0][warp] = __popc(va);
-      warps[1][warp] = __popc(ve);
-    }
-    __syncthreads();
-    const unsigned lower = (1u << lane) - 1;
-    const int pa = warps[0][lane], pe = warps[1][lane];
-    const int a = above0 + __reduce_add_sync(0xffffffffu, lane < warp ? pa : 0) + __popc(va & lower);
-    const int e = equal0 + __reduce_add_sync(0xffffffffu, lane < warp ? pe : 0) + __popc(ve & lower);
-    above0 += __reduce_add_sync(0xffffffffu, pa);
-    equal0 += __reduce_add_sync(0xffffffffu, pe);
-    if (above || (equal && e < equals)) {
-      const int at = a + min(e, equals);
-      if (at < q.keep) {
-        kept[at] = j;
-        if (mass_out != nullptr) mass_out[at] = m;
+  for (int base = j0; base < j1; base += BLOCK) {
+    if (!one) keys.load(base);
+#pragma unroll
+    for (int i = 0; i < kCached; ++i) {
+      const int j = base + i * kThreads + tid;
+      if (base + i * kThreads >= j1) break;   // (all threads)
+      const bool above = j < j1 && (all || keys.k[i] > border), equal = j < j1 && !all && keys.k[i] == border;
+      const unsigned va = __ballot_sync(0xffffffffu, above), ve = __ballot_sync(0xffffffffu, equal);
+      int (&counts)[2][kWarps] = reinterpret_cast<int(&)[2][kWarps]>(bins[0][(i & 1) * 2 * kWarps]);
+      if (lane == 0) {
+        counts[0][warp] = __popc(va);
+        counts[1][warp] = __popc(ve);
+      }
+      __syncthreads();
+      const unsigned lower = (1u << lane) - 1;
+      const int pa = lane < kWarps ? counts[0][lane] : 0, pe = lane < kWarps ? counts[1][lane] : 0;
+      const int a = above0 + sum_of_lower(pa) + __popc(va & lower);
+      const int e = equal0 + sum_of_lower(pe) + __popc(ve & lower);
+      above0 += __reduce_add_sync(0xffffffffu, pa);
+      equal0 += __reduce_add_sync(0xffffffffu, pe);
+      if (above || (equal && e < equals)) {
+        const int at = a + min(e, equals);
+        if (at < q.keep) {
+          kept[at] = j;
+          if (mass_out != nullptr) mass_out[at] = __ldg(keys.mass + j);
+        }
       }
     }
+    __syncthreads();
   }
   // (others may still read this CTA's counts)
   if (cluster > 1) cluster_sync();
 }
 
-// VEC: 16-byte pieces of a cached vector of one plane.
+// VEC: 16-byte pieces of a cached vector of one plane.  A warp moves 32 positions: its
+// lanes look up a source and a target each, then copy them together, 32 / VEC
+// vectors an instruction.
 template <int VEC>
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
-  constexpr int ROWS = kCopyThreads / VEC;   // vectors at once
-  const int r = blockIdx.z, h = blockIdx.y;
-  if (*p.conflict) return;
+__global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int AT_ONCE = 32 / VEC;
+  const int r = blockIdx.z, h = blockIdx.y, lane = threadIdx.x % 32;
+  const int i0 = (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32) * 32;
   const Request q(p, r, false);
-  const int32_t* kept = p.kept + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_kept;
-  const int planes = p.planes, per = kCopies / planes;   // positions of a thread
-  const int piece = threadIdx.x % VEC, first = blockIdx.x * ROWS * per + threadIdx.x / VEC;
-  if (blockIdx.x * ROWS * per >= q.keep) return;
+  if (i0 >= q.keep || *p.conflict) return;
+  const int i = i0 + lane;
   const size_t plane = static_cast<size_t>(p.hkv) * 16;      // vectors between planes
-  uint4 x[kCopies];
-  float sc[kCopies];
-  size_t to[kCopies];
-  bool on[kCopies];
-#pragma unroll
-  for (int k = 0; k < kCopies; ++k) {
-    const int i = first + k / planes * ROWS;
-    on[k] = i < q.keep && k / planes < per;
-    if (!on[k]) continue;
-    const int j = __ldg(kept + i);
-    const int from = __ldg(p.src_table + static_cast<size_t>(r) * p.src_max_pages + j / 16);
-    const int dest = __ldg(p.dst_table + static_cast<size_t>(r) * p.dst_max_pages + i / 16);
-    const size_t in = k % planes * plane + h * 16;
-    x[k] = make_uint4(0u, 0u, 0u, 0u);
-    sc[k] = 1.f;
-    if (from >= 0 && from < p.src_pages) {
-      const size_t v = static_cast<size_t>(from) * planes * plane + in + j % 16;
-      x[k] = __ldg(reinterpret_cast<const uint4*>(p.src_pool) + v * VEC + piece);
-      if (p.src_scales != nullptr && piece == 0) sc[k] = __ldg(p.src_scales + v);
-    } else if (piece == 0) {
-      raise_status(p.status, DFLASH_ERR_CAPACITY, 585);
-    }
-    on[k] = dest >= 0 && dest < p.dst_pages;
-    to[k] = static_cast<size_t>(dest) * planes * plane + in + i % 16;
+  long long from = -1, to = -1;                              // plane 0's vectors
+  if (i < q.keep) {
+    const int j = __ldg(p.kept + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_kept + i);
+    const int src = __ldg(p.src_table + static_cast<size_t>(r) * p.src_max_pages + j / 16);
+    const int dst = __ldg(p.dst_table + static_cast<size_t>(r) * p.dst_max_pages + i / 16);
+    if (src >= 0 && src < p.src_pages) from = static_cast<long long>(src * plane * p.planes + h * 16 + j % 16);
+    else raise_status(p.status, DFLASH_ERR_CAPACITY, 585);
+    if (dst >= 0 && dst < p.dst_pages) to = static_cast<long long>(dst * plane * p.planes + h * 16 + i % 16);
   }
+  const int piece = lane % VEC, sub = lane / VEC;
+#pragma unroll 1
+  for (int pl = 0; pl < p.planes; ++pl) {
+    const size_t off = pl * plane;
 #pragma unroll
-  for (int k = 0; k < kCopies; ++k) {
-    if (!on[k]) continue;
-    reinterpret_cast<uint4*>(p.dst_pool)[to[k] * VEC + piece] = x[k];
-    if (p.dst_scales != nullptr && piece == 0) p.dst_scales[to[k]] = sc[k];
+    for (int b = 0; b < 32 / AT_ONCE; b += kCopies) {
+      constexpr int N = kCopies < 32 / AT_ONCE ? kCopies : 32 / AT_ONCE;
+      uint4 x[N];
+      long long t[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int l = (b + k) * AT_ONCE + sub;
+        const long long f = __shfl_sync(0xffffffffu, from, l);
+        t[k] = __shfl_sync(0xffffffffu, to, l);
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (f >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(p.src_pool) + (f + off) * VEC + piece);
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (t[k] >= 0) reinterpret_cast<uint4*>(p.dst_pool)[(t[k] + off) * VEC + piece] = x[k];
+    }
+    if (p.dst_scales != nullptr && to >= 0) p.dst_scales[to + off] = from >= 0 ? __ldg(p.src_scales + from + off) : 1.f;
   }
 }
 
 template <int VEC>
 void launch_copy(const EvictParams& p, cudaStream_t s) {
-  const int64_t rows = kCopyThreads / VEC * (kCopies / p.planes);
   count_launch();
-  evict_copy_kernel<VEC><<<dim3(static_cast<unsigned>((p.ld_kept + rows - 1) / rows), p.hkv, p.batch), kCopyThreads, 0, s>>>(p);
+  evict_copy_kernel<VEC><<<dim3(static_cast<unsigned>((p.ld_kept + kCopyThreads - 1) / kCopyThreads), p.hkv, p.batch),
+                           kCopyThreads, 0, s>>>(p);
 }
 
 }  // namespace
@@ -287,10 +334,10 @@ cudaError_t kv_evict_launch(const EvictParams& p, int vector_bytes, cudaStream_t
   if (e != cudaSuccess) return e;
   count_launch();
   evict_check_kernel<<<p.batch, 256, 0, s>>>(p);
-  // slices of at least 4096 positions, until the CTAs fill the machine
+  // slices of at least 2048 positions, until the CTAs fill the machine
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(p.batch) * p.hkv * cluster * 2 <= 152 &&
-         p.ld_mass / (2 * cluster) >= 4096)
+  while (cluster < kMaxCluster && static_cast<int64_t>(p.batch) * p.hkv * cluster * 2 <= 304 &&
+         p.ld_mass / (2 * cluster) >= 2048)
     cluster *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
