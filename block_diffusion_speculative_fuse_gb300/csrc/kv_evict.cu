@@ -1,13 +1,13 @@
 // Eviction from a paged cache: of each request and KV head the positions with the largest
 // accumulated attention weight are kept and moved together, in order, into other pages.
 //
-// Three kernels.  The first marks the pages that are read and written, so that a target page
-// named twice, or read by the same call, is found before anything is moved.  The second
+// Two kernels.  The first marks the pages that are read and written, so that a target page
+// named twice, or read by the same call, is found before anything is moved, and
 // finds the kept positions: the border's 32-bit key by three digits of 11, 11 and 10 bits (a
 // histogram in shared memory each; the first holds sign, exponent and two bits, so that
 // masses, whose exponents lie together, do not all meet in one counter), then one pass that
 // numbers what is above it and the first equals in order of position.  One CTA per request
-// and head, or a cluster, each CTA a slice of the positions, where there are few.  The third
+// and head, or a cluster, each CTA a slice of the positions, where there are few.  The second
 // copies whole vectors.
 //
 // Bound: the copy's bytes.
@@ -21,7 +21,7 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kCached = 24;      // positions of a thread whose keys stay in registers
+constexpr int kCached = 24576;   // positions of a CTA whose keys stay in shared memory
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kCopyThreads = 256;
@@ -46,11 +46,8 @@ struct Request {
   }
 };
 
-// bit 0: written by the call, bit 1: read by it
-__global__ void evict_check_kernel(const __grid_constant__ EvictParams p) {
-  const int r = blockIdx.x;
-  const Request q(p, r, threadIdx.x == 0);
-  if (threadIdx.x == 0 && p.new_len != nullptr) p.new_len[r] = q.keep;
+// Marks the pages of a request (bit 0: written by the call, bit 1: read by it).
+__device__ void mark_pages(const EvictParams& p, int r, const Request& q) {
   auto mark = [&](int id, unsigned bit) {
     const unsigned old = atomicOr(p.owner + id, bit);
     if (old & (bit == 1 ? 3u : 1u)) {
@@ -77,57 +74,38 @@ __device__ __forceinline__ uint32_t key_of(float m) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Keys of a block of positions, kCached to a thread.  A slice of one block keeps them in
-// registers through all passes; a longer one reads its masses again.
-struct Keys {
-  const float* mass;
-  int safe0, safe1, j1;
-  uint32_t k[kCached];
-  __device__ void load(int base) {   // positions base + i * kThreads + tid
-    float m[kCached];
-#pragma unroll
-    for (int i = 0; i < kCached; ++i) {
-      const int j = base + i * kThreads + threadIdx.x;
-      m[i] = j < j1 ? __ldg(mass + j) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kCached; ++i) {
-      const int j = base + i * kThreads + threadIdx.x;
-      k[i] = j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(m[i]);
-    }
-  }
-};
-
-__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p, int cluster,
+                                                                         int cached) {
+  extern __shared__ uint32_t cache[];   // keys of the slice's first `cached` positions
   __shared__ __align__(16) uint32_t bins[2][kBins];
   __shared__ int warps[2][kWarps], found[2];
   __shared__ int2 slice_counts;   // of this CTA's slice: above the border, equal
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = blockIdx.x / cluster, r = unit / p.hkv, h = unit % p.hkv;
-  const Request q(p, r, false);
+  const bool first = h == 0 && rank == 0;
+  const Request q(p, r, first && tid == 0);
+  griddep_launch_dependents();
+  if (first) {
+    if (tid == 0 && p.new_len != nullptr) p.new_len[r] = q.keep;
+    mark_pages(p, r, q);
+  }
   if (q.keep == 0) return;   // (the whole cluster)
   const int slice = (q.ctx + cluster - 1) / cluster;
   const int j0 = min(rank * slice, q.ctx), j1 = min(j0 + slice, q.ctx);
-  Keys keys;
-  keys.mass = p.mass + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
-  keys.safe0 = p.sink;
-  keys.safe1 = q.ctx - min(p.recent, q.ctx);
-  keys.j1 = j1;
-  constexpr int BLOCK = kCached * kThreads;
-  const bool one = j1 - j0 <= BLOCK;
-  if (one) keys.load(j0);
-  // f(key, position) for the slice's positions of this thread
+  const float* mass = p.mass + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
+  const int safe0 = p.sink, safe1 = q.ctx - min(p.recent, q.ctx);
+  auto read_key = [&](int j) {
+    const float m = __ldg(mass + j);
+    return j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(m);
+  };
+  auto key_at = [&](int j) { return j - j0 < cached ? cache[j - j0] : read_key(j); };
+#pragma unroll 8
+  for (int j = j0 + tid; j < min(j1, j0 + cached); j += kThreads) cache[j - j0] = read_key(j);
+  // f(key) for the slice's positions of this thread
   auto each = [&](auto f) {
-#pragma unroll 1
-    for (int base = j0; base < j1; base += BLOCK) {
-      if (!one) keys.load(base);
-#pragma unroll
-      for (int i = 0; i < kCached; ++i) {
-        const int j = base + i * kThreads + tid;
-        if (j < j1) f(keys.k[i], j);
-      }
-    }
+#pragma unroll 4
+    for (int j = j0 + tid; j < j1; j += kThreads) f(key_at(j));
   };
   auto sum_of_lower = [&](int v) {   // of the warps before; v: lane w has warp w's
     return static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? v : 0));
@@ -143,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
       uint32_t* mine = bins[pass & 1];
       for (int b = tid; b < kBins; b += kThreads) mine[b] = 0;
       __syncthreads();
-      each([&](uint32_t k, int) {
+      each([&](uint32_t k) {
         if ((k & mask) == prefix) atomicAdd(&mine[k >> shift & bits], 1u);
       });
       if (cluster > 1) cluster_sync();
@@ -204,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   int above0 = all ? j0 : 0, equal0 = 0;
   if (!all && cluster > 1) {
     int above = 0, equal = 0;
-    each([&](uint32_t k, int) {
+    each([&](uint32_t k) {
       above += k > border;
       equal += k == border;
     });
@@ -239,36 +217,51 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   }
   int32_t* kept = p.kept + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_kept;
   float* mass_out = p.mass_out == nullptr ? nullptr : p.mass_out + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
+  __syncthreads();
 #pragma unroll 1
-  for (int base = j0; base < j1; base += BLOCK) {
-    if (!one) keys.load(base);
+  for (int base = j0; base < j1; base += 4 * kThreads) {
+    // four positions in a row to a thread; counts above and at the border in one word
+    const int first_j = base + 4 * tid;
+    uint32_t k[4];
+    int mine = 0;
 #pragma unroll
-    for (int i = 0; i < kCached; ++i) {
-      const int j = base + i * kThreads + tid;
-      if (base + i * kThreads >= j1) break;   // (all threads)
-      const bool above = j < j1 && (all || keys.k[i] > border), equal = j < j1 && !all && keys.k[i] == border;
-      const unsigned va = __ballot_sync(0xffffffffu, above), ve = __ballot_sync(0xffffffffu, equal);
-      int (&counts)[2][kWarps] = reinterpret_cast<int(&)[2][kWarps]>(bins[0][(i & 1) * 2 * kWarps]);
-      if (lane == 0) {
-        counts[0][warp] = __popc(va);
-        counts[1][warp] = __popc(ve);
-      }
-      __syncthreads();
-      const unsigned lower = (1u << lane) - 1;
-      const int pa = lane < kWarps ? counts[0][lane] : 0, pe = lane < kWarps ? counts[1][lane] : 0;
-      const int a = above0 + sum_of_lower(pa) + __popc(va & lower);
-      const int e = equal0 + sum_of_lower(pe) + __popc(ve & lower);
-      above0 += __reduce_add_sync(0xffffffffu, pa);
-      equal0 += __reduce_add_sync(0xffffffffu, pe);
+    for (int i = 0; i < 4; ++i) {
+      const int j = first_j + i;
+      k[i] = 0;
+      if (j >= j1) continue;
+      k[i] = all ? 1u : key_at(j);
+      if (all || k[i] > border) mine += 1;
+      else if (k[i] == border) mine += 1 << 16;
+    }
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    int* counts = warps[(base - j0) / (4 * kThreads) & 1];
+    if (lane == 31) counts[warp] = upto;
+    __syncthreads();
+    const int part = lane < kWarps ? counts[lane] : 0;
+    const int before = sum_of_lower(part) + upto - mine, whole = __reduce_add_sync(0xffffffffu, part);
+    int a = above0 + (before & 0xFFFF), e = equal0 + (before >> 16);
+    above0 += whole & 0xFFFF;
+    equal0 += whole >> 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = first_j + i;
+      if (j >= j1) break;
+      const bool above = all || k[i] > border, equal = !above && k[i] == border;
       if (above || (equal && e < equals)) {
         const int at = a + min(e, equals);
         if (at < q.keep) {
           kept[at] = j;
-          if (mass_out != nullptr) mass_out[at] = __ldg(keys.mass + j);
+          if (mass_out != nullptr) mass_out[at] = __ldg(mass + j);
         }
       }
+      a += above;
+      e += equal;
     }
-    __syncthreads();
   }
   // (others may still read this CTA's counts)
   if (cluster > 1) cluster_sync();
@@ -283,12 +276,14 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const __gri
   const int r = blockIdx.z, h = blockIdx.y, lane = threadIdx.x % 32;
   const int i0 = (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32) * 32;
   const Request q(p, r, false);
-  if (i0 >= q.keep || *p.conflict) return;
+  if (i0 >= q.keep) return;
+  griddep_wait();
+  if (*reinterpret_cast<volatile int*>(p.conflict)) return;
   const int i = i0 + lane;
   const size_t plane = static_cast<size_t>(p.hkv) * 16;      // vectors between planes
   long long from = -1, to = -1;                              // plane 0's vectors
   if (i < q.keep) {
-    const int j = __ldg(p.kept + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_kept + i);
+    const int j = __ldcg(p.kept + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_kept + i);
     const int src = __ldg(p.src_table + static_cast<size_t>(r) * p.src_max_pages + j / 16);
     const int dst = __ldg(p.dst_table + static_cast<size_t>(r) * p.dst_max_pages + i / 16);
     if (src >= 0 && src < p.src_pages) from = static_cast<long long>(src * plane * p.planes + h * 16 + j % 16);
@@ -321,10 +316,18 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const __gri
 }
 
 template <int VEC>
-void launch_copy(const EvictParams& p, cudaStream_t s) {
+cudaError_t launch_copy(const EvictParams& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.ld_kept + kCopyThreads - 1) / kCopyThreads), p.hkv, p.batch);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   count_launch();
-  evict_copy_kernel<VEC><<<dim3(static_cast<unsigned>((p.ld_kept + kCopyThreads - 1) / kCopyThreads), p.hkv, p.batch),
-                           kCopyThreads, 0, s>>>(p);
+  return cudaLaunchKernelEx(&cfg, evict_copy_kernel<VEC>, p);
 }
 
 }  // namespace
@@ -332,8 +335,6 @@ void launch_copy(const EvictParams& p, cudaStream_t s) {
 cudaError_t kv_evict_launch(const EvictParams& p, int vector_bytes, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(p.conflict, 0, 256 + static_cast<size_t>(p.dst_pages) * 4, s);
   if (e != cudaSuccess) return e;
-  count_launch();
-  evict_check_kernel<<<p.batch, 256, 0, s>>>(p);
   // slices of at least 2048 positions, until the CTAs fill the machine
   int cluster = 1;
   while (cluster < kMaxCluster && static_cast<int64_t>(p.batch) * p.hkv * cluster * 2 <= 304 &&
@@ -346,16 +347,19 @@ cudaError_t kv_evict_launch(const EvictParams& p, int vector_bytes, cudaStream_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.hkv * cluster);
   cfg.blockDim = dim3(kThreads);
+  const int64_t slice = (p.ld_mass + cluster - 1) / cluster;
+  const int cached = slice < kCached ? static_cast<int>(slice) : kCached;
+  cfg.dynamicSmemBytes = cached * 4;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  count_launch();
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cluster);
+  static thread_local int allowed = -1;
+  e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel), kCached * 4, &allowed);
   if (e != cudaSuccess) return e;
-  if (vector_bytes == 256) launch_copy<16>(p, s);
-  else if (vector_bytes == 128) launch_copy<8>(p, s);
-  else launch_copy<4>(p, s);
-  return cudaGetLastError();
+  count_launch();
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cluster, cached);
+  if (e != cudaSuccess) return e;
+  return vector_bytes == 256 ? launch_copy<16>(p, s) : vector_bytes == 128 ? launch_copy<8>(p, s) : launch_copy<4>(p, s);
 }
 
 }  // namespace dflash
