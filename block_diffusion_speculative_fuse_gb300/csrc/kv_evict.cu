@@ -22,8 +22,8 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCached = 24576;   // positions of a CTA whose keys stay in shared memory
-constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048, kCoarse = 64;
+constexpr int kMaxCluster = 16;
 constexpr int kCopyThreads = 256;
 constexpr int kCopies = 8;       // loads of a thread in flight
 
@@ -76,9 +76,9 @@ __device__ __forceinline__ uint32_t key_of(float m) {
 
 __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p, int cluster,
                                                                          int cached) {
-  extern __shared__ uint32_t cache[];   // keys of the slice's first `cached` positions
-  __shared__ __align__(16) uint32_t bins[2][kBins];
-  __shared__ int warps[2][kWarps], found[2];
+  extern __shared__ uint32_t cache[];   // keys of the slice, where they fit (cached)
+  __shared__ uint32_t bins[2][kBins], coarse[2][kCoarse];
+  __shared__ int gathered[kMaxCluster * kCoarse], warps[2][kWarps], found[2];
   __shared__ int2 slice_counts;   // of this CTA's slice: above the border, equal
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -95,24 +95,88 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   const int j0 = min(rank * slice, q.ctx), j1 = min(j0 + slice, q.ctx);
   const float* mass = p.mass + (static_cast<int64_t>(r) * p.hkv + h) * p.ld_mass;
   const int safe0 = p.sink, safe1 = q.ctx - min(p.recent, q.ctx);
-  auto read_key = [&](int j) {
-    const float m = __ldg(mass + j);
-    return j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(m);
-  };
-  auto key_at = [&](int j) { return j - j0 < cached ? cache[j - j0] : read_key(j); };
-#pragma unroll 8
-  for (int j = j0 + tid; j < min(j1, j0 + cached); j += kThreads) cache[j - j0] = read_key(j);
-  // f(key) for the slice's positions of this thread
+  auto key = [&](float m, int j) { return j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(m); };
+  const bool fits = j1 - j0 <= cached;
+  // f(key) for the slice's positions of this thread, eight reads at once
   auto each = [&](auto f) {
-#pragma unroll 4
-    for (int j = j0 + tid; j < j1; j += kThreads) f(key_at(j));
+#pragma unroll 1
+    for (int at = tid; at < j1 - j0; at += 8 * kThreads) {
+      uint32_t k[8];
+      if (fits) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = cache[min(at + i * kThreads, j1 - j0 - 1)];
+      } else {
+        float m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = __ldg(mass + min(j0 + at + i * kThreads, j1 - 1));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = key(m[i], j0 + at + i * kThreads);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (at + i * kThreads < j1 - j0) f(k[i]);
+    }
   };
   auto sum_of_lower = [&](int v) {   // of the warps before; v: lane w has warp w's
     return static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? v : 0));
   };
+  // Of n <= 64 counts in every CTA of the cluster, at `mine`: their sums, to gathered[0, n).
+  auto gather = [&](const uint32_t* mine, int n) {
+    __syncthreads();
+    for (int x = tid; x < cluster * n; x += kThreads) {
+      const int c = x / n;
+      int v;
+      if (cluster == 1) v = mine[x];
+      else
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_map(smem_u32(mine + x - c * n), c)));
+      gathered[x] = v;
+    }
+    __syncthreads();
+    int v = 0;
+    if (tid < n)
+      for (int c = 0; c < cluster; ++c) v += gathered[c * n + tid];
+    __syncthreads();
+    if (tid < n) gathered[tid] = v;
+    __syncthreads();
+  };
+  // Of gathered[0, n), from the last down: the one in which the need-th of them lies and
+  // how many lie above it (found), by the first warp.
+  auto search = [&](int n, int need) {
+    if (warp == 0) {
+      const int hi = n - 1 - 2 * lane;   // two to a lane (n = 64), or one
+      const int a = n == 64 ? gathered[hi] : gathered[n - 1 - lane], b = n == 64 ? gathered[hi - 1] : 0;
+      int upto = a + b;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int before = upto - a - b;
+      if (before < need && before + a >= need) {
+        found[0] = n == 64 ? hi : n - 1 - lane;
+        found[1] = before;
+      } else if (before + a < need && upto >= need) {
+        found[0] = hi - 1;
+        found[1] = before + a;
+      }
+    }
+    __syncthreads();
+  };
   uint32_t border = 0;
   int equals = 0;                 // kept of those at the border
-  if (q.keep < q.ctx) {
+  const bool all = q.keep >= q.ctx;
+  if (!all) {
+    if (fits) {
+#pragma unroll 1
+      for (int at = tid; at < j1 - j0; at += 8 * kThreads) {
+        float m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = __ldg(mass + min(j0 + at + i * kThreads, j1 - 1));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at + i * kThreads < j1 - j0) cache[at + i * kThreads] = key(m[i], j0 + at + i * kThreads);
+      }
+    }
     uint32_t prefix = 0, mask = 0;
     int need = q.keep;            // of the positions with this prefix
 #pragma unroll 1
@@ -124,61 +188,31 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
       each([&](uint32_t k) {
         if ((k & mask) == prefix) atomicAdd(&mine[k >> shift & bits], 1u);
       });
+      __syncthreads();
+      // sums of 32 bins, so that other CTAs' need not all be read: a warp adds up four
+#pragma unroll
+      for (int i = 0; i < kCoarse / kWarps; ++i) {
+        const int c = warp * (kCoarse / kWarps) + i;
+        const int sum = __reduce_add_sync(0xffffffffu, mine[c * 32 + lane]);
+        if (lane == 0) coarse[pass & 1][c] = sum;
+      }
       if (cluster > 1) cluster_sync();
       else __syncthreads();
-      // counts from the largest bin down: thread t has the four from 2047 - 4 t on
-      static_assert(kBins == 4 * kThreads, "four bins a thread");
-      const int low = kBins - 4 - 4 * tid;
-      int c[4] = {0, 0, 0, 0};
-      if (cluster == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = mine[low + 3 - i];
-      } else {
-        const uint32_t at = smem_u32(&mine[low]);
-        uint4 v[kMaxCluster];
-#pragma unroll
-        for (int x = 0; x < kMaxCluster; ++x)
-          if (x < cluster)
-            asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w)
-                         : "r"(dsmem_map(at, x)));
-#pragma unroll
-        for (int x = 0; x < kMaxCluster; ++x)
-          if (x < cluster) {
-            c[0] += v[x].w;
-            c[1] += v[x].z;
-            c[2] += v[x].y;
-            c[3] += v[x].x;
-          }
-      }
-      const int sum = c[0] + c[1] + c[2] + c[3];
-      int upto = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      if (lane == 31) warps[0][warp] = upto;
-      __syncthreads();
-      int before = sum_of_lower(lane < kWarps ? warps[0][lane] : 0) + upto - sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (before < need && before + c[i] >= need) {
-          found[0] = low + 3 - i;
-          found[1] = before;
-        }
-        before += c[i];
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(found[0]) << shift;
+      gather(coarse[pass & 1], kCoarse);
+      search(kCoarse, need);
+      const int c = found[0];
+      need -= found[1];
+      gather(mine + c * 32, 32);
+      search(32, need);
+      prefix |= static_cast<uint32_t>(c * 32 + found[0]) << shift;
       mask |= static_cast<uint32_t>(bits) << shift;
       need -= found[1];
+      __syncthreads();
     }
     border = prefix;
     equals = need;
   }
   // where this slice's kept positions go: count, then number them in order
-  const bool all = q.keep >= q.ctx;
   int above0 = all ? j0 : 0, equal0 = 0;
   if (!all && cluster > 1) {
     int above = 0, equal = 0;
@@ -223,13 +257,18 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
     // four positions in a row to a thread; counts above and at the border in one word
     const int first_j = base + 4 * tid;
     uint32_t k[4];
+    float m[4];
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = first_j + i;
-      k[i] = 0;
+      m[i] = __ldg(mass + min(j, j1 - 1));
+      k[i] = fits && !all ? cache[min(j, j1 - 1) - j0] : key(m[i], j);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = first_j + i;
       if (j >= j1) continue;
-      k[i] = all ? 1u : key_at(j);
       if (all || k[i] > border) mine += 1;
       else if (k[i] == border) mine += 1 << 16;
     }
@@ -256,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
         const int at = a + min(e, equals);
         if (at < q.keep) {
           kept[at] = j;
-          if (mass_out != nullptr) mass_out[at] = __ldg(mass + j);
+          if (mass_out != nullptr) mass_out[at] = m[i];
         }
       }
       a += above;
@@ -348,13 +387,18 @@ cudaError_t kv_evict_launch(const EvictParams& p, int vector_bytes, cudaStream_t
   cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.hkv * cluster);
   cfg.blockDim = dim3(kThreads);
   const int64_t slice = (p.ld_mass + cluster - 1) / cluster;
-  const int cached = slice < kCached ? static_cast<int>(slice) : kCached;
+  const int cached = slice <= kCached ? static_cast<int>(slice) : 0;
   cfg.dynamicSmemBytes = cached * 4;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static thread_local int allowed = -1;
+  const int was = allowed;
   e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel), kCached * 4, &allowed);
+  if (e == cudaSuccess && allowed != was) {   // clusters of 16 are more than every device has to offer
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) allowed = -1;
+  }
   if (e != cudaSuccess) return e;
   count_launch();
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cluster, cached);
