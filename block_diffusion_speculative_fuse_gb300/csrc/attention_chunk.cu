@@ -8,6 +8,9 @@ namespace dflash {
 
 namespace {
 
+#ifndef LEAST
+#define LEAST 4
+#endif
 constexpr int kThreads = 640;     // warps 0-15 softmax, 16 TMA, 17 products, 18 V's values, 19 plan
 constexpr int kWarps = kThreads / 32;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // of a thread
@@ -19,7 +22,7 @@ constexpr int kUnitCost = 10;     // a unit's start and end
 constexpr int kSplitCost = 4;     // of a chunk with one tile: as much as with two, since the
                                   // loads bound it (2, 3, 4: a mixed batch 384, 304, 288 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
-constexpr int kLeast = 2;         // chunks of a piece of a unit
+constexpr int kLeast = LEAST;         // chunks of a piece of a unit
 
 template <int D>
 struct Cfg {
@@ -782,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the units that were cut: a CTA takes 32 rows of the unit that
-// worker blockIdx.x began; a warp per row.
+// worker blockIdx.x began, a warp four of them, whose pieces are read together.
 constexpr int kJoinRows = 32;
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p, int workers) {
@@ -793,17 +796,18 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   const WorkerRecord* recs = reinterpret_cast<const WorkerRecord*>(p.records);
   const int w = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const WorkerRecord head = recs[w];
+  int cont = 0, ends = 0;
+  if (tid > w && tid < workers) {
+    cont = recs[tid].cont;
+    ends = recs[tid].ends;
+  }
   if (!head.head) return;
   if (tid == 0) {
     last = workers - 1;
     list[0] = 2 * w + 1;
   }
   __syncthreads();
-  int cont = 0;
-  if (tid > w && tid < workers) {
-    cont = recs[tid].cont;
-    if (cont && recs[tid].ends) atomicMin(&last, tid);
-  }
+  if (cont && ends) atomicMin(&last, tid);
   __syncthreads();
   cont = cont && tid <= last;
   const unsigned votes = __ballot_sync(0xffffffffu, cont);
@@ -815,57 +819,62 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     parts += count[j];
   }
   __syncthreads();
-  constexpr int MOST = (kChunkWorkers + 1 + 31) / 32;
-#pragma unroll 1
-  for (int row = blockIdx.y * kJoinRows + warp; row < min((blockIdx.y + 1) * kJoinRows, p.slot_rows); row += 8) {
-    const int rt = row % 128, t = rt / p.G, token = row / 128 * p.tokens + t;
-    if (t >= p.tokens || token >= head.tokens) continue;
-    float ms[MOST], ls[MOST], m = -INFINITY, l = 0.f;
+  const int row0 = blockIdx.y * kJoinRows + warp * 4;
+  float m[4], l[4], acc[4][VEC];
+  bool on[4];
+  int64_t vec[4];   // where the row goes, in query heads
 #pragma unroll
-    for (int j = 0; j < MOST; ++j) {
-      ms[j] = -INFINITY, ls[j] = 0.f;
-      if (j * 32 + lane < parts) {
-        const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (static_cast<size_t>(list[j * 32 + lane]) * p.slot_rows + row) * 2));
-        ms[j] = y.x, ls[j] = y.y;
-      }
-      m = fmaxf(m, ms[j]);
-    }
-    m = warp_max(m);
-    float acc[VEC] = {};
+  for (int k = 0; k < 4; ++k) {
+    const int row = row0 + k, rt = row % 128, t = rt / p.G, token = row / 128 * p.tokens + t;
+    on[k] = row < p.slot_rows && t < p.tokens && token < head.tokens;
+    vec[k] = head.token0 + token;
+    if (!on[k]) vec[k] = 0;
+    m[k] = -INFINITY;
+    l[k] = 0.f;
 #pragma unroll
-    for (int j = 0; j < MOST; ++j) {
-      const float weight = ms[j] == -INFINITY ? 0.f : exp2f(ms[j] - m);
-      l += warp_sum(weight == 0.f ? 0.f : ls[j] * weight);
-      const int here = min(32, parts - j * 32);
-#pragma unroll 4
-      for (int i = 0; i < here; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, weight, i);
-        const float* src = p.part_o + (static_cast<size_t>(list[j * 32 + i]) * p.slot_rows + row) * D + lane * VEC;
-        float v[VEC];
-        if constexpr (VEC == 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-          v[0] = y.x, v[1] = y.y;
-        }
-        if (wi > 0.f) {
+    for (int i = 0; i < VEC; ++i) acc[k][i] = 0.f;
+  }
+#pragma unroll 2
+  for (int part = 0; part < parts; ++part) {
+    const size_t at = static_cast<size_t>(list[part]) * p.slot_rows + row0;
+    float2 y[4];
+    float v[4][VEC];
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) acc[k] = fmaf(v[k], wi, acc[k]);
-        }
+    for (int k = 0; k < 4; ++k) {
+      if (!on[k]) continue;
+      y[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + k);
+      const float* src = p.part_o + (at + k) * D + lane * VEC;
+      if constexpr (VEC == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        v[k][0] = x.x, v[k][1] = x.y;
       }
     }
-    const bool any = m > -INFINITY;
-    const float inv = any ? 1.f / l : 0.f;
-    const int head_of_row = head.kvh * p.G + rt - t * p.G;
-    uint16_t* dst = p.out + static_cast<size_t>(head.token0 + token) * p.ld_out + head_of_row * D + lane * VEC;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!on[k] || y[k].x == -INFINITY) continue;   // (that piece's keys are none of the row's)
+      const float mn = fmaxf(m[k], y[k].x), a = exp2f(m[k] - mn), b = exp2f(y[k].x - mn);
+      l[k] = l[k] * a + y[k].y * b;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[k][i] = acc[k][i] * a + v[k][i] * b;
+      m[k] = mn;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (!on[k]) continue;
+    const int rt = (row0 + k) % 128, qh = head.kvh * p.G + rt % p.G;
+    const bool any = m[k] > -INFINITY;
+    const float inv = any ? 1.f / l[k] : 0.f;
+    uint16_t* dst = p.out + vec[k] * p.ld_out + qh * D + lane * VEC;
     if constexpr (VEC == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+      *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(acc[k][0] * inv, acc[k][1] * inv), bf16x2(acc[k][2] * inv, acc[k][3] * inv));
     else
-      *reinterpret_cast<uint32_t*>(dst) = bf16x2(acc[0] * inv, acc[1] * inv);
+      *reinterpret_cast<uint32_t*>(dst) = bf16x2(acc[k][0] * inv, acc[k][1] * inv);
     if (p.lse != nullptr && lane == 0)
-      p.lse[static_cast<size_t>(head.token0 + token) * p.hq + head_of_row] =
-          any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+      p.lse[vec[k] * p.hq + qh] = any ? (m[k] + log2f(l[k])) * 0.693147180559945309f : -INFINITY;
   }
 }
 
