@@ -8,9 +8,6 @@ namespace dflash {
 
 namespace {
 
-#ifndef LEAST
-#define LEAST 4
-#endif
 constexpr int kThreads = 640;     // warps 0-15 softmax, 16 TMA, 17 products, 18 V's values, 19 plan
 constexpr int kWarps = kThreads / 32;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // of a thread
@@ -22,7 +19,7 @@ constexpr int kUnitCost = 10;     // a unit's start and end
 constexpr int kSplitCost = 4;     // of a chunk with one tile: as much as with two, since the
                                   // loads bound it (2, 3, 4: a mixed batch 384, 304, 288 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
-constexpr int kLeast = LEAST;         // chunks of a piece of a unit
+constexpr int kLeast = 4;         // chunks of a piece of a unit
 
 template <int D>
 struct Cfg {
@@ -39,7 +36,14 @@ struct Cfg {
 // A place in the work: requests, their KV heads, their row units, chunks of keys.
 struct Place {
   int r, h, i, c;
+  int x;            // cost of everything before the request's units of this head
   ChunkRequest q;
+};
+
+// The deal: worker w's range starts at share * w + rest * w / used.
+struct Deal {
+  int share, rest, used;
+  __device__ int start(int w) const { return share * w + rest * w / used; }
 };
 
 // Chunks [c0, c0 + n) of a unit, for all warps of the CTA.
@@ -49,6 +53,7 @@ struct Piece {
   int see, step;           // keys that its row k sees: max(0, see + k * step)
   int r, h, token0, tokens;  // request, KV head, first row of the call, rows
   int split, begins, ends;   // one tile; the piece is the unit's first, its last
+  int x, all;              // of a unit with one tile: cost of everything before it; its chunks
 };
 
 // What a worker leaves for the join.
@@ -79,8 +84,11 @@ struct Units {
     }
     return kUnitCost * k + static_cast<int>(s >> 5);
   }
+  static __device__ int unit_cost(int keys, bool split) {
+    return kUnitCost + (split ? keys / kChunk * kSplitCost : keys >> 5);
+  }
   __device__ int total() const {
-    return tiles == 0 ? 0 : cost(tiles - 1) + kUnitCost + (split(tiles - 1) ? keys(tiles - 1) / kChunk * kSplitCost : keys(tiles - 1) >> 5);
+    return tiles == 0 ? 0 : cost(tiles - 1) + unit_cost(keys(tiles - 1), split(tiles - 1));
   }
   // the unit and chunk at which a boundary at cost x of [0, total()) cuts
   __device__ void find(int x, int* i, int* c) const {
@@ -91,13 +99,17 @@ struct Units {
       else hi = mid - 1;
     }
     *i = lo;
-    const int all = chunks(lo), at = max(0, x - cost(lo) - kUnitCost);
-    int cut = split(lo) ? (at + kSplitCost / 2) / kSplitCost : at / 4 + (at % 4 > 1);
+    *c = cut(x - cost(lo), chunks(lo), split(lo));
+  }
+  // the chunk at which a boundary at cost x of the unit cuts
+  static __device__ int cut(int x, int all, bool split) {
+    const int at = max(0, x - kUnitCost);
+    int cut = split ? (at + kSplitCost / 2) / kSplitCost : at / 4 + (at % 4 > 1);
     // no pieces below kLeast chunks
     if (all < 2 * kLeast) cut = 2 * cut <= all ? 0 : all;
     else if (cut < kLeast) cut = 0;
     else if (cut > all - kLeast) cut = all;
-    *c = cut;
+    return cut;
   }
 };
 
@@ -107,9 +119,9 @@ __device__ __forceinline__ ChunkRequest request(const ChunkParams& p, int r) {
 
 // Start and end of a worker's range, by all threads of the CTA; ends with a barrier.
 // scratch: kWarps words.
-__device__ void find_range(const ChunkParams& p, int worker, int workers, Place* out, int* scratch) {
+__device__ void find_range(const ChunkParams& p, int worker, int workers, Place* out, int* scratch, Deal* deal) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  if (tid < 2) out[tid] = Place{p.batch, 0, 0, 0, ChunkRequest()};
+  if (tid < 2) out[tid] = Place{p.batch, 0, 0, 0, 0, ChunkRequest()};
   int all = 0, used = 0, x0 = 0, x1 = 0;
   // a first round adds up the costs, a second finds the boundaries
 #pragma unroll 1
@@ -142,15 +154,17 @@ __device__ void find_range(const ChunkParams& p, int worker, int workers, Place*
         if (base == 0) {
           used = min(workers, (all + kWorkerCost - 1) / kWorkerCost);
           if (worker >= used) break;
-          const int share = all / used, rest = all - share * used;
-          x0 = share * worker + rest * worker / used;
-          x1 = share * (worker + 1) + rest * (worker + 1) / used;
+          const Deal d{all / used, all % used, used};
+          if (tid == 0) *deal = d;
+          x0 = d.start(worker);
+          x1 = d.start(worker + 1);
         }
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
           const int x = (j == 0 ? x0 : x1) - at;
           if (x < 0 || x >= v) continue;
-          Place pl{r, x / one, 0, 0, q};
+          Place pl{r, x / one, 0, 0, 0, q};
+          pl.x = at + pl.h * one;
           u.find(x - pl.h * one, &pl.i, &pl.c);
           out[j] = pl;
         }
@@ -188,6 +202,55 @@ __device__ __forceinline__ void store_32(void* dst, const uint32_t* w, bool wide
   }
 }
 
+// Row `row` of a unit with one tile, whose list[0] pieces lie in the slots list[1 ..]; a warp.
+template <int D>
+__device__ __forceinline__ void join_row(const ChunkParams& p, const int* list, int row, int token0, int kvh) {
+  constexpr int VEC = D / 32, MOST = (kChunkWorkers + 31) / 32;
+  const int lane = threadIdx.x % 32, parts = list[0];
+  float2 ml[MOST];
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int j = 0; j < MOST; ++j) {
+    ml[j] = make_float2(-INFINITY, 0.f);
+    if (j * 32 + lane < parts)
+      ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(list[1 + j * 32 + lane]) * p.slot_rows + row);
+    m = fmaxf(m, ml[j].x);
+  }
+  m = warp_max(m);
+  float acc[VEC] = {};
+#pragma unroll
+  for (int j = 0; j < MOST; ++j) {
+    const float weight = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - m);
+    l += warp_sum(weight == 0.f ? 0.f : ml[j].y * weight);
+    const int here = min(32, parts - j * 32);
+#pragma unroll 8
+    for (int i = 0; i < here; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, weight, i);
+      const float* src = p.part_o + (static_cast<size_t>(list[1 + j * 32 + i]) * p.slot_rows + row) * D + lane * VEC;
+      float v[VEC];
+      if constexpr (VEC == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+        v[0] = y.x, v[1] = y.y;
+      }
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[k] += wi > 0.f ? v[k] * wi : 0.f;
+    }
+  }
+  const bool any = m > -INFINITY;
+  const float inv = any ? 1.f / l : 0.f;
+  const int token = row / p.G, qh = kvh * p.G + row - token * p.G;
+  uint16_t* dst = p.out + (token0 + token) * p.ld_out + qh * D + lane * VEC;
+  if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = bf16x2(acc[0] * inv, acc[1] * inv);
+  if (p.lse != nullptr && lane == 0)
+    p.lse[static_cast<int64_t>(token0 + token) * p.hq + qh] = any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+}
+
 __device__ __forceinline__ void scale2(uint32_t* x, float f) {
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
       "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
@@ -216,11 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* piece_free = piece_full + kPieces;
   Piece* pieces = reinterpret_cast<Piece*>(piece_free + kPieces);  // [kPieces]
   Place* range = reinterpret_cast<Place*>(pieces + kPieces);       // [2]
-  int* scratch = reinterpret_cast<int*>(range + 2);                // [kWarps]
+  Deal* deal = reinterpret_cast<Deal*>(range + 2);
+  int* scratch = reinterpret_cast<int*>(deal + 1);                 // [kWarps]
   volatile int* bad = reinterpret_cast<volatile int*>(scratch + kWarps);  // [kPieces] first key with a V that is not finite
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(bad) + kPieces);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(512 * 4 + (3 * SLOTS + 9 + 2 * kPieces) * 8 + kPieces * sizeof(Piece) + 2 * sizeof(Place) +
+  static_assert(512 * 4 + (3 * SLOTS + 9 + 2 * kPieces) * 8 + kPieces * sizeof(Piece) + 2 * sizeof(Place) + sizeof(Deal) +
                         (kWarps + kPieces + 2) * 4 <= 3072, "fits");
 
   // (one lane's word for it, so that the compiler knows roles and pieces to be the
@@ -256,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
   const int worker = blockIdx.x;
-  find_range(p, worker, gridDim.x, range, scratch);  // ends with a barrier
+  find_range(p, worker, gridDim.x, range, scratch, deal);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -315,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Units u(q, p.tokens, p.causal);
           if (at.i >= u.tiles) {  // the request's next head, or the next request
             at.i = at.c = 0;
+            at.x += u.total();
             if (u.tiles == 0 || ++at.h >= p.hkv) {
               at.h = 0;
               ++at.r;
@@ -338,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           pc.split = u.split(i);
           pc.begins = c0 == 0;
           pc.ends = c1 == all;
+          pc.x = at.x;
+          pc.all = all;
           break;
         }
         const int slot = count % kPieces;
@@ -776,6 +843,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both tiles' O have been read before either's next product
       if (pc.split) named_sync(four, 128);
       tc_fence_before();
+      if (p.fused && !whole) {
+        // ---- the last of the unit's pieces joins them, a row to a warp
+        __threadfence();
+        named_sync(13, 512);
+        if (tid == 0) {
+          int* done = p.status + 64 + pc.r * p.hkv + pc.h;   // chunks that are done (left at 0)
+          scratch[0] = atomicAdd(done, n) + n == pc.all;
+          if (scratch[0]) *done = 0;
+        }
+        named_sync(13, 512);
+        if (scratch[0]) {
+          __threadfence();
+          int* list = reinterpret_cast<int*>(exch);
+          if (warp == 0) {
+            // the workers in whose ranges it lies
+            const Deal d = *deal;
+            const int end_x = pc.x + Units::unit_cost(pc.keys, true);
+            int parts = 0;
+            for (int w0 = 0; w0 < d.used; w0 += 32) {
+              const int w = w0 + lane, x0 = d.start(w), x1 = d.start(w + 1);
+              const int lo = x0 <= pc.x ? 0 : Units::cut(x0 - pc.x, pc.all, true);
+              const int hi = w + 1 >= d.used || x1 >= end_x ? pc.all : Units::cut(x1 - pc.x, pc.all, true);
+              const bool has = w < d.used && x0 < end_x && x1 > pc.x && lo < hi;
+              const unsigned votes = __ballot_sync(0xffffffffu, has);
+              if (has) list[1 + parts + __popc(votes & ((1u << lane) - 1))] = lo > 0 ? 2 * w : 2 * w + 1;
+              parts += __popc(votes);
+            }
+            if (lane == 0) list[0] = parts;
+          }
+          named_sync(13, 512);
+          for (int row = warp; row < pc.tokens * p.G; row += 16) join_row<D>(p, list, row, pc.token0, pc.h);
+        }
+        named_sync(13, 512);
+      }
       piece_done();
     }
   }
@@ -789,7 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinRows = 32;
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p, int workers) {
-  constexpr int VEC = D / 32;
   __shared__ int list[kChunkWorkers + 1], count[8], last;
   griddep_wait();
   griddep_launch_dependents();
@@ -819,63 +919,41 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     parts += count[j];
   }
   __syncthreads();
-  const int row0 = blockIdx.y * kJoinRows + warp * 4;
-  float m[4], l[4], acc[4][VEC];
-  bool on[4];
-  int64_t vec[4];   // where the row goes, in query heads
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = row0 + k, rt = row % 128, t = rt / p.G, token = row / 128 * p.tokens + t;
-    on[k] = row < p.slot_rows && t < p.tokens && token < head.tokens;
-    vec[k] = head.token0 + token;
-    if (!on[k]) vec[k] = 0;
-    m[k] = -INFINITY;
-    l[k] = 0.f;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[k][i] = 0.f;
-  }
+  // a warp's four rows, eight lanes to each; a lane has 4 columns of every 32
+  constexpr int COLS = D / 32;
+  const int row = blockIdx.y * kJoinRows + warp * 4 + lane / 8, rt = row % 128, t = rt / p.G;
+  const int token = row / 128 * p.tokens + t;
+  if (row >= p.slot_rows || t >= p.tokens || token >= head.tokens) return;
+  float m = -INFINITY, l = 0.f, acc[COLS][4] = {};
 #pragma unroll 2
   for (int part = 0; part < parts; ++part) {
-    const size_t at = static_cast<size_t>(list[part]) * p.slot_rows + row0;
-    float2 y[4];
-    float v[4][VEC];
+    const size_t at = static_cast<size_t>(list[part]) * p.slot_rows + row;
+    const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+    float4 v[COLS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!on[k]) continue;
-      y[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + k);
-      const float* src = p.part_o + (at + k) * D + lane * VEC;
-      if constexpr (VEC == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        v[k][0] = x.x, v[k][1] = x.y;
-      }
+    for (int i = 0; i < COLS; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + i * 8 + lane % 8);
+    const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), b = ex2(y.x - ref);
+    l = l * a + y.y * b;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+      acc[i][0] = fmaf(v[i].x, b, acc[i][0] * a);
+      acc[i][1] = fmaf(v[i].y, b, acc[i][1] * a);
+      acc[i][2] = fmaf(v[i].z, b, acc[i][2] * a);
+      acc[i][3] = fmaf(v[i].w, b, acc[i][3] * a);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!on[k] || y[k].x == -INFINITY) continue;   // (that piece's keys are none of the row's)
-      const float mn = fmaxf(m[k], y[k].x), a = exp2f(m[k] - mn), b = exp2f(y[k].x - mn);
-      l[k] = l[k] * a + y[k].y * b;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[k][i] = acc[k][i] * a + v[k][i] * b;
-      m[k] = mn;
-    }
+    m = mn;
   }
+  const bool any = m > -INFINITY;
+  const float inv = any ? 1.f / l : 0.f;
+  const int qh = head.kvh * p.G + rt - t * p.G;
+  uint16_t* dst = p.out + static_cast<int64_t>(head.token0 + token) * p.ld_out + qh * D + lane % 8 * 4;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!on[k]) continue;
-    const int rt = (row0 + k) % 128, qh = head.kvh * p.G + rt % p.G;
-    const bool any = m[k] > -INFINITY;
-    const float inv = any ? 1.f / l[k] : 0.f;
-    uint16_t* dst = p.out + vec[k] * p.ld_out + qh * D + lane * VEC;
-    if constexpr (VEC == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2(acc[k][0] * inv, acc[k][1] * inv), bf16x2(acc[k][2] * inv, acc[k][3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = bf16x2(acc[k][0] * inv, acc[k][1] * inv);
-    if (p.lse != nullptr && lane == 0)
-      p.lse[vec[k] * p.hq + qh] = any ? (m[k] + log2f(l[k])) * 0.693147180559945309f : -INFINITY;
-  }
+  for (int i = 0; i < COLS; ++i)
+    *reinterpret_cast<uint2*>(dst + i * 32) =
+        make_uint2(bf16x2(acc[i][0] * inv, acc[i][1] * inv), bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+  if (p.lse != nullptr && lane % 8 == 0)
+    p.lse[static_cast<int64_t>(head.token0 + token) * p.hq + qh] =
+        any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
 template <int D>
@@ -905,7 +983,7 @@ cudaError_t launch(const ChunkParams& p, const CUtensorMap& kv_map, const CUtens
   cfg.numAttrs = 1;
   count_launch();
   e = cudaLaunchKernelEx(&cfg, chunk_kernel<D>, kv_map, q_map, p, group0, oob_group);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.fused) return e;
   cfg.gridDim = dim3(kChunkWorkers, (p.slot_rows + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

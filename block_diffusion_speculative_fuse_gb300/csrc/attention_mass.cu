@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* u_full = drain + 1;          // [kUnits]
   uint64_t* u_free = u_full + kUnits;
   Unit* units = reinterpret_cast<Unit*>(u_free + kUnits);
-  int* scratch = reinterpret_cast<int*>(units + kUnits);  // [kWarps]
+  int* groups = reinterpret_cast<int*>(units + kUnits);   // [kUnits][16] K's 8-row groups in the map, by page
+  int* scratch = groups + kUnits * 16;                    // [kWarps]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + kWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* before = const_cast<int*>(abort_flag) + 1;         // [batch + 1] units of the requests before
@@ -217,16 +218,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         more = x.k0 >= 0;
         const int slot = count % kUnits;
+        int grp = oob_group;
+        if (more && x.tiles > x.t0 && lane < 16 && x.k0 / 16 + lane < (x.ctx + 15) / 16) {
+          const int id = __ldcg(p.page_table + static_cast<size_t>(x.r) * p.max_pages + x.k0 / 16 + lane);
+          if (id >= 0 && id < p.n_pages) grp = group0 + (id * 2 * p.hkv + x.h) * 2;
+          else raise_status(p.status, DFLASH_ERR_CAPACITY, 563);
+        }
         if (count >= kUnits && !__all_sync(0xffffffffu, mbar_wait_for(&u_free[slot], (count / kUnits + 1) & 1, nullptr,
                                                                       4 * kWaitLimitNs))) {
           give_up(568);
           more = false;
           break;
         }
-        if (lane == 0) {
-          units[slot] = x;
-          mbar_arrive(&u_full[slot]);
-        }
+        if (lane < 16) groups[slot * 16 + lane] = grp;
+        if (lane == 0) units[slot] = x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_full[slot]);
         __syncwarp();
         ++count;
       }
@@ -238,13 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor cur, qc;
     while (next_unit(&u)) {
       if (ok && tiles_of(u) > 0) {
-        const int planes = planes_of(u), npg = (u.ctx + 15) / 16;
-        int page = u.k0 / 16 + lane, grp = oob_group;
-        if (lane < 16 && page < npg) {
-          const int id = __ldcg(p.page_table + static_cast<size_t>(u.r) * p.max_pages + page);
-          if (id >= 0 && id < p.n_pages) grp = group0 + (id * 2 * p.hkv + u.h) * 2;
-          else raise_status(p.status, DFLASH_ERR_CAPACITY, 563);
-        }
+        const int planes = planes_of(u), *grp = groups + taken % kUnits * 16;
         // the first tile's Q goes before the keys, the others after
         auto load_q = [&](int t) {
           if (qn >= kQ && !wait(&q_free[qc.slot], qc.parity ^ 1, 565)) return;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u.load) load_q(u.t0);
 #pragma unroll 1
         for (int k = 0; ok && k < planes; ++k) {
-          const int st = cur.slot, y = __shfl_sync(0xffffffffu, grp, k * 8 + lane % 8);
+          const int st = cur.slot, y = grp[k * 8 + lane % 8];
           if (at >= SLOTS && !wait(&k_free[st], cur.parity ^ 1, 565)) break;
           if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::PLANE);
           __syncwarp();
@@ -443,7 +444,7 @@ cudaError_t launch(const MassParams& p, const CUtensorMap& kv_map, const CUtenso
                    int oob_group, cudaStream_t s) {
   using C = Cfg<D>;
   constexpr int fixed = kQ * C::Q_TILE + C::SLOTS * C::PLANE + kQ * 128 * 4 +
-                        (2 * C::SLOTS + 4 * kQ + 9 + 2 * kUnits) * 8 + kUnits * sizeof(Unit) + (kWarps + 2) * 4;
+                        (2 * C::SLOTS + 4 * kQ + 9 + 2 * kUnits) * 8 + kUnits * (sizeof(Unit) + 64) + (kWarps + 2) * 4;
   constexpr int most = fixed + (kMaxMassBatch + 1) * 4;
   static_assert(most <= 227 * 1024, "fits");
   static thread_local int allowed = -1;

@@ -352,6 +352,8 @@ struct ChunkParams {
   int slot_rows;               // of a partial
   float *part_o, *part_ml;     // [2 * workers][slot_rows][d], [..][2]
   void* records;               // [workers], 32 bytes each
+  int fused;                   // units have one tile; the last of a unit's pieces joins them (counters
+                               // of batch * hkv units 256 bytes behind the status word, left at 0)
   int* status;
 };
 // Whether the costs of a call's work stay within 32 bits.
