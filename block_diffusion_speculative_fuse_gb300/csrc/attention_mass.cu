@@ -10,10 +10,11 @@
 // exchange or atomics, and a key whose K is not finite spoils its own sum alone.
 //
 // A unit is 256 keys of one request and KV head, two planes of 128, and all rows in tiles
-// of 128 / G rows of the call (G query heads each).  Persistent CTAs take groups of units
-// in turn (w, w + 152, ...), so that causal units, the later the fewer rows, even out; a
-// group's units share Q where there is one tile.  Per tile and plane one D, in two stages
-// each, which the plane's four warps sum up.
+// of 128 / G rows of the call (G query heads each).  Persistent CTAs take a range of
+// units each where there are few rows, and otherwise groups of units in turn (w, w + 152,
+// ...), so that causal units, the later the fewer rows, even out (8 x 16384 keys, 32
+// rows: ranges 50 us, in turn 53); units in a row share Q where there is one tile.  Per tile
+// and plane one D, in two stages each, which the plane's four warps sum up.
 //
 // Bound: with the usual window of rows (32 rows of 4 heads, one tile) K's bytes.
 #include <climits>
@@ -179,15 +180,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 11) {
     // ------------------------------------------------ plan
     const int all = before[p.batch];
-    const int group = min(8, max(1, all / (kWorkers * 4)));
+    // with one or two tiles units cost the same: a range each; otherwise groups in turn
+    const int w = blockIdx.x;
+    const int start = p.few ? static_cast<int>(static_cast<int64_t>(all) * w / kWorkers) : 0;
+    const int group = p.few ? static_cast<int>(static_cast<int64_t>(all) * (w + 1) / kWorkers) - start
+                            : min(8, max(1, all / (kWorkers * 8)));
     int count = 0, r = 0, loaded = -1;
     ChunkRequest q;
     bool more = true;
 #pragma unroll 1
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * group; more; base += kWorkers * group) {
+    for (int64_t base = p.few ? start : w * group; more; base = p.few ? all : base + kWorkers * group) {
 #pragma unroll 1
-      for (int j = 0; j < group && more; ++j) {
-        const int64_t at = base + j;
+      for (int j = 0; j < max(group, 1) && more; ++j) {
+        const int64_t at = group > 0 ? base + j : all;
         Unit x;
         x.k0 = -1;
         if (at < all) {

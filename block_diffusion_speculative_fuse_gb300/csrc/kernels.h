@@ -288,6 +288,7 @@ struct MassParams {
   int batch, T, hq, hkv, G;
   int tokens;                  // rows of the call in a tile: 128 / G
   int last;                    // rows of a request that weigh (0: all)
+  int few;                     // at most two tiles for any request
   int causal, max_pages, n_pages, accumulate;
   float scale_log2;            // scale / ln 2
   const float* lse;            // [T][hq]

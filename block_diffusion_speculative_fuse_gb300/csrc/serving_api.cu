@@ -452,6 +452,7 @@ int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* 
   p.G = p.hq / p.hkv;
   p.tokens = 128 / p.G;
   p.last = last;
+  p.few = (last > 0 && last <= 2 * p.tokens) || T <= 2 * p.tokens;
   p.causal = causal;
   p.max_pages = kv->max_pages;
   p.n_pages = kv->n_pages;
