@@ -214,7 +214,9 @@ template <bool HALF>
 __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constant__ ScoreParams p, int cluster) {
   using R = Row<HALF>;
   constexpr int PER = R::PER, kUnroll = R::UNROLL;
-  extern __shared__ float group_max[];   // [groups][kThreads] (only for alternatives)
+  // upper halves of the keys of the groups' maxima, [groups][kThreads] (only for
+  // alternatives): what shared memory takes is missing to L1, which holds the loads in flight
+  extern __shared__ uint16_t group_max[];
   __shared__ float2 list[kCandidates];
   __shared__ float2 best[kMaxCluster * kMaxScoreTop];   // of all slices (rank 0's)
   __shared__ float4 slices[kMaxCluster];                // their statistics (rank 0's)
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) top = fmaxf(top, z[j]);
-    if (p.n_top > 0) group_max[g * kThreads + tid] = top;
+    if (p.n_top > 0) group_max[g * kThreads + tid] = static_cast<uint16_t>(key_of(top) >> 16);
     if (top > st.m) {
       if (st.m > -INFINITY) {
         const float d = (st.m - top) * c, w = ex2(d);
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     auto reaches = [&](float z) { return z > -INFINITY && key_of(z) >> 16 >= least; };
 #pragma unroll 1
     for (int g = 0; g < groups; ++g) {
-      if (!reaches(group_max[g * kThreads + tid])) continue;
+      if (group_max[g * kThreads + tid] < least) continue;
       fetch(g);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -476,10 +478,10 @@ cudaError_t launch(const ScoreParams& p, cudaStream_t s) {
     cluster *= 2;
   const int slice = (vectors + cluster - 1) / cluster;
   const int groups = (slice + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  const int smem = p.n_top > 0 ? groups * kThreads * 4 : 0;
+  const int smem = p.n_top > 0 ? groups * kThreads * 2 : 0;
   const void* fn = reinterpret_cast<const void*>(score_kernel<HALF>);
   static thread_local int allowed = -1;
-  const cudaError_t e = allow_smem(fn, 200 * 1024 - 40 * 1024, &allowed);
+  const cudaError_t e = allow_smem(fn, 64 * 1024, &allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
