@@ -154,6 +154,45 @@ class PagedKV:
         B.dflash_attention_prefix(self.heads(hq), layer, q, b, n, group, causal, scale,
                                   self.struct, ctx_len, prefix_len, out, lse, ws, stream)
 
+    def chunk_workspace(self, n_q_heads: int, batch: int, T: int):
+        """An initialised workspace for attend_chunk (and attention_mass) calls of up to T rows."""
+        size = B.dflash_attention_chunk_bytes(self.heads(n_q_heads), batch, T)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.pool.device)
+        B.dflash_workspace_init(ws)
+        return ws
+
+    def attend_chunk(self, layer: int, q, row_start, ctx_len, out, ws, lse=None, causal=True,
+                     scale=0.0, stream=None):
+        """Attention of the new rows q [T][hq][d] to the cache, rows
+        [row_start[r], row_start[r + 1]) for request r (dflash_attention_chunk)."""
+        T, hq, _ = q.shape
+        B.dflash_attention_chunk(self.heads(hq), layer, q, row_start, ctx_len.shape[0], T, causal, scale,
+                                 self.struct, ctx_len, out, lse, ws, stream)
+
+    def attention_mass(self, layer: int, q, row_start, ctx_len, lse, mass, ws, last=0, causal=True,
+                       scale=0.0, accumulate=True, stream=None):
+        """Add to mass [batch][hkv][positions] the attention weight that each cached key got
+        from the last rows of its request, given attend_chunk's lse (dflash_attention_mass)."""
+        T, hq, _ = q.shape
+        B.dflash_attention_mass(self.heads(hq), layer, q, row_start, ctx_len.shape[0], T, last, causal,
+                                scale, self.struct, ctx_len, lse, mass, accumulate, ws, stream)
+
+    def evict_workspace(self, batch: int):
+        """An initialised workspace for evict_to calls into this cache."""
+        size = B.dflash_kv_evict_bytes(self.heads(self.pool.shape[3]), batch, self.n_pages)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.pool.device)
+        B.dflash_workspace_init(ws)
+        return ws
+
+    def evict_to(self, other, layer: int, ctx_len, keep, mass, kept, ws, sink=0, recent=0, new_len=None,
+                 mass_out=None, stream=None):
+        """Move the keep[r] positions of largest mass of each request and KV head, in order,
+        to positions 0, 1, ... of the cache `other` (dflash_kv_evict); ws from its
+        evict_workspace."""
+        B.dflash_kv_evict(self.heads(self.pool.shape[3]), layer, self.struct, other.struct,
+                          ctx_len.shape[0], ctx_len, keep, sink, recent, mass, kept, new_len, mass_out, ws,
+                          stream)
+
     def read_codes(self, layer: int, req: int, n: int):
         """E4M3 cache: codes [n][2][hkv][d] (uint8) and scales [n][2][hkv] of
         one request's logical positions 0..n-1, on the host."""

@@ -133,6 +133,52 @@ def sample_generate(runner: TargetRunner, prompts: np.ndarray, n_tokens: int, u:
     return res.T.contiguous().cpu().numpy()
 
 
+def score_sequences(runner: TargetRunner, tokens: np.ndarray, n_top=0, temperature=None, chunk=64):
+    """How likely the target finds given sequences (dflash_score_tokens): tokens [batch][n] are
+    fed through the target, at most `chunk` positions a call, and each token after the first
+    is scored by the logits before it.  Returns host arrays logprob, rank and entropy
+    [batch][n - 1] and, with n_top, top_id and top_logprob [batch][n - 1][n_top].  temperature: a
+    number or one per request (None: 1).  An error that the device recorded is raised at the
+    end."""
+    tokens = np.asarray(tokens)
+    if tokens.ndim != 2 or tokens.shape[0] != runner.batch or tokens.shape[1] < 2 or chunk < 1:
+        raise ValueError(f"tokens {tokens.shape}: {runner.batch} sequences of two tokens or more")
+    b, n = tokens.shape
+    if n - 1 > runner.max_len:
+        raise B.DflashError(f"score_sequences ({n} tokens, room for {runner.max_len})", -3)
+    dev, vocab = runner.device, runner.shape.vocab
+    toks = i32(tokens, dev)
+    T = None
+    if temperature is not None:
+        T = torch.as_tensor(np.broadcast_to(np.asarray(temperature), (b,)).copy()).to(dev, torch.float32)
+    step = min(chunk, n - 1)
+    ws = torch.empty(B.dflash_score_tokens_bytes(b * step, vocab, n_top), dtype=torch.uint8, device=dev)
+    B.dflash_workspace_init(ws)
+    logits = torch.empty((b * step, vocab), dtype=torch.float32, device=dev)
+    parts, used = [], set()
+    for at in range(0, n - 1, step):
+        k = min(step, n - 1 - at)
+        z = logits[:b * k]
+        runner.forward(toks[:, at:at + k].contiguous(), i32(np.full(b, at), dev), k, logits=z)
+        used.add(k)
+        res = [torch.empty(b * k, dtype=t, device=dev) for t in (torch.float32, torch.int32, torch.float32)]
+        top = [torch.empty((b * k, n_top), dtype=t, device=dev) if n_top else None
+               for t in (torch.int32, torch.float32)]
+        B.dflash_score_tokens(z, b * k, vocab, T.repeat_interleave(k) if T is not None else None,
+                              toks[:, at + 1:at + 1 + k].reshape(-1).contiguous(), *res, n_top, *top, ws)
+        parts.append([x.view(b, k, *x.shape[1:]) for x in res + top if x is not None])
+    found = [(fn, w, *B.dflash_get_status(w)) for fn, w in
+             [("dflash_target_forward", runner.workspace(k)) for k in sorted(used)] + [("dflash_score_tokens", ws)]]
+    for _, w, status, _ in found:
+        if status != 0:
+            B.dflash_workspace_init(w)   # the runner stays usable
+    for fn, _, status, site in found:
+        if status != 0:
+            raise B.DflashError(f"{fn} (site {site})", status)
+    names = ("logprob", "rank", "entropy", "top_id", "top_logprob")
+    return {k: torch.cat(x, 1).cpu().numpy() for k, x in zip(names, zip(*parts))}
+
+
 class SpecDecoder:
     def __init__(self, target: DeviceModel, drafter: DeviceModel, tap_layers, batch: int,
                  max_len: int, device="cuda"):
