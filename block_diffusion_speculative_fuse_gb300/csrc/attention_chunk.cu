@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 17) tmem_alloc(tmem_slot, 512);
   griddep_wait();
-  griddep_launch_dependents();
   const int worker = blockIdx.x;
   find_range(p, worker, gridDim.x, range, scratch, deal);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();   // (this CTA has its TMEM)
   const uint32_t tmem = *tmem_slot;
 
   // The next piece, for a whole warp; false at the end.  A role that gives up on a

@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
   griddep_wait();
-  griddep_launch_dependents();
   auto request = [&](int r) { return ChunkRequest(p.row_start, p.ctx_len, r, p.T, p.max_pages, p.status, 561); };
   // units of a request and KV head; a length beyond the sums' room counts as that
   auto length = [&](const ChunkRequest& q) { return static_cast<int>(min(static_cast<int64_t>(q.ctx), p.ld_mass)); };
@@ -143,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();   // (this CTA has its TMEM)
   const uint32_t tmem = *tmem_slot;
 
   // The next unit, for a whole warp; false at the end.  A role that gives up on a wait

@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const __gri
   constexpr int AT_ONCE = 32 / VEC;
   const int r = blockIdx.z, h = blockIdx.y, lane = threadIdx.x % 32;
   const int i0 = (blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32) * 32;
+  griddep_wait();
   const Request q(p, r, false);
   if (i0 >= q.keep) return;
-  griddep_wait();
   if (*reinterpret_cast<volatile int*>(p.conflict)) return;
   const int i = i0 + lane;
   const size_t plane = static_cast<size_t>(p.hkv) * 16;      // vectors between planes

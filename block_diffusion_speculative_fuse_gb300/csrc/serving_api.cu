@@ -336,7 +336,7 @@ int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void*
     return DFLASH_ERR_INVALID_ARG;
   const int d = heads->head_dim;
   const int64_t row = static_cast<int64_t>(p.hq) * d;
-  if (ld_q < row || ld_out < row || ld_q % 8 || ld_out % 8 || !scale_of(scale, d, &p.scale_log2))
+  if (q == out || ld_q < row || ld_out < row || ld_q % 8 || ld_out % 8 || !scale_of(scale, d, &p.scale_log2))
     return DFLASH_ERR_INVALID_ARG;
   rc = check_cache(heads, layer, kv);
   if (rc) return rc;
@@ -484,7 +484,7 @@ int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* s
   if (!rc) rc = check_cache(heads, layer, dst);
   if (rc) return rc;
   if (ctx_len == nullptr || keep == nullptr || mass == nullptr || kept == nullptr || batch < 1 || sink < 0 ||
-      recent < 0 || ld_mass < 1 || ld_kept < 1 || mass_out == mass || !aligned(ctx_len, 4) || !aligned(keep, 4) ||
+      recent < 0 || ld_mass < 1 || ld_kept < 1 || mass_out == mass || new_len == ctx_len || new_len == keep || !aligned(ctx_len, 4) || !aligned(keep, 4) ||
       !aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_len, 4) || !aligned(mass_out, 4) ||
       src->dtype != dst->dtype)
     return DFLASH_ERR_INVALID_ARG;

@@ -23,8 +23,8 @@ def lib():
     return B.load()
 
 
-def chunk(lib, hd=None, layer=0, q=P, ldq=512, start=P, batch=4, T=9, causal=1, scale=0.0, kv=None, ctx=P, out=P,
-          ldo=512, lse=P, ws=WS, size=BIG):
+def chunk(lib, hd=None, layer=0, q=P, ldq=512, start=P, batch=4, T=9, causal=1, scale=0.0, kv=None, ctx=P,
+          out=ctypes.c_void_p(0x9000), ldo=512, lse=P, ws=WS, size=BIG):
     hd, kv = hd or heads(), kv or cache()
     return lib.dflash_attention_chunk(ctypes.byref(hd), layer, q, ldq, start, batch, T, causal, scale,
                                       ctypes.byref(kv), ctx, out, ldo, lse, ws, size, None)
@@ -43,7 +43,7 @@ COMMON = [  # shared by the chunk attention and the mass
 
 
 def test_chunk_refuses(lib):
-    for kw, code in COMMON + [(dict(out=None), -1), (dict(out=ODD), -1), (dict(ldo=448), -1), (dict(ldo=516), -1),
+    for kw, code in COMMON + [(dict(out=None), -1), (dict(out=ODD), -1), (dict(out=P), -1), (dict(ldo=448), -1), (dict(ldo=516), -1),
                               (dict(kv=cache(max_pages=1 << 26, n_rows=1 << 20), batch=1 << 20), -2)]:
         assert chunk(lib, **kw) == code, kw
     hd = heads()
@@ -75,7 +75,7 @@ def test_mass_refuses(lib):
 
 
 def evict(lib, hd=None, layer=0, src=None, dst=None, batch=4, ctx=P, keep=P, sink=0, recent=0, sums=P, ldm=64,
-          kept=P, ldk=8, new=P, out=ctypes.c_void_p(0x9000), ws=WS, size=BIG):
+          kept=P, ldk=8, new=ctypes.c_void_p(0x8000), out=ctypes.c_void_p(0x9000), ws=WS, size=BIG):
     hd = hd or heads()
     src, dst = src or cache(), dst or cache()
     return lib.dflash_kv_evict(ctypes.byref(hd), layer, ctypes.byref(src), ctypes.byref(dst), batch, ctx, keep, sink,
@@ -86,7 +86,7 @@ def test_evict_refuses(lib):
     far = cache(pool=0x1000 + 16 * 8)           # inside the first pool
     for kw, code in ((dict(batch=0), -1), (dict(sink=-1), -1), (dict(recent=-1), -1), (dict(ctx=None), -1),
                      (dict(keep=ODDER), -1), (dict(sums=None), -1), (dict(kept=None), -1), (dict(new=ODDER), -1),
-                     (dict(out=P), -1), (dict(ldm=0), -1), (dict(ldk=0), -1), (dict(layer=2), -1),
+                     (dict(out=P), -1), (dict(new=P), -1), (dict(ldm=0), -1), (dict(ldk=0), -1), (dict(layer=2), -1),
                      (dict(dst=cache(n_rows=3)), -3), (dict(src=cache(n_rows=3)), -3), (dict(dst=far), -1),
                      (dict(src=far), -1), (dict(dst=cache(n_pages=7)), -1),                 # one pool, two sizes
                      (dict(dst=cache(pool=1 << 30, dtype=1, scales=0x1000)), -1),
