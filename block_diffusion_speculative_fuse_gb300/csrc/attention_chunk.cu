@@ -205,38 +205,36 @@ __device__ __forceinline__ void store_32(void* dst, const uint32_t* w, bool wide
 // Row `row` of a unit with one tile, whose list[0] pieces lie in the slots list[1 ..]; a warp.
 template <int D>
 __device__ __forceinline__ void join_row(const ChunkParams& p, const int* list, int row, int token0, int kvh) {
-  constexpr int VEC = D / 32, MOST = (kChunkWorkers + 31) / 32;
+  constexpr int VEC = D / 32;
   const int lane = threadIdx.x % 32, parts = list[0];
-  float2 ml[MOST];
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, acc[VEC] = {};
+#pragma unroll 1
+  for (int j = 0; j < parts; j += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (j + lane < parts)
+      ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(list[1 + j + lane]) * p.slot_rows + row);
+    const float mn = fmaxf(m, warp_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn;
+    const float weight = ex2(ml.x - ref), old = ex2(m - ref);
+    l = l * old + warp_sum(ml.y * weight);
 #pragma unroll
-  for (int j = 0; j < MOST; ++j) {
-    ml[j] = make_float2(-INFINITY, 0.f);
-    if (j * 32 + lane < parts)
-      ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(list[1 + j * 32 + lane]) * p.slot_rows + row);
-    m = fmaxf(m, ml[j].x);
-  }
-  m = warp_max(m);
-  float acc[VEC] = {};
-#pragma unroll
-  for (int j = 0; j < MOST; ++j) {
-    const float weight = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - m);
-    l += warp_sum(weight == 0.f ? 0.f : ml[j].y * weight);
-    const int here = min(32, parts - j * 32);
-#pragma unroll 8
+    for (int k = 0; k < VEC; ++k) acc[k] *= old;
+    m = mn;
+    const int here = min(32, parts - j);
+#pragma unroll 4
     for (int i = 0; i < here; ++i) {
       const float wi = __shfl_sync(0xffffffffu, weight, i);
-      const float* src = p.part_o + (static_cast<size_t>(list[1 + j * 32 + i]) * p.slot_rows + row) * D + lane * VEC;
-      float v[VEC];
+      const float* src = p.part_o + (static_cast<size_t>(list[1 + j + i]) * p.slot_rows + row) * D + lane * VEC;
       if constexpr (VEC == 4) {
         const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        acc[0] = fmaf(y.x, wi, acc[0]);
+        acc[1] = fmaf(y.y, wi, acc[1]);
+        acc[2] = fmaf(y.z, wi, acc[2]);
+        acc[3] = fmaf(y.w, wi, acc[3]);
       } else {
         const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-        v[0] = y.x, v[1] = y.y;
+        acc[0] = fmaf(y.x, wi, acc[0]);
+        acc[1] = fmaf(y.y, wi, acc[1]);
       }
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) acc[k] += wi > 0.f ? v[k] * wi : 0.f;
     }
   }
   const bool any = m > -INFINITY;

@@ -158,6 +158,7 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity,
   if (mbar_try_wait(a, parity)) return true;
   const uint64_t t0 = global_ns();
   while (true) {
+#pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(a, parity)) return true;
     if (abort_flag != nullptr && *abort_flag) return false;
