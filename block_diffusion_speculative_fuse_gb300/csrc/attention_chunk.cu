@@ -859,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Deal d = *deal;
             const int end_x = pc.x + Units::unit_cost(pc.keys, true);
             int parts = 0;
+#pragma unroll 1
             for (int w0 = 0; w0 < d.used; w0 += 32) {
               const int w = w0 + lane, x0 = d.start(w), x1 = d.start(w + 1);
               const int lo = x0 <= pc.x ? 0 : Units::cut(x0 - pc.x, pc.all, true);
@@ -871,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) list[0] = parts;
           }
           named_sync(13, 512);
+#pragma unroll 1
           for (int row = warp; row < pc.tokens * p.G; row += 16) join_row<D>(p, list, row, pc.token0, pc.h);
         }
         named_sync(13, 512);

@@ -132,7 +132,7 @@ __device__ __forceinline__ int clean_v(uint8_t* plane, int first, int live) {
   const int lane = threadIdx.x % 32;
   const int i0 = max(first, 0) * PIECES + lane, i1 = min(live, 128) * PIECES;
   bool found = false;
-#pragma unroll 4
+#pragma unroll 2
   for (int i = i0; i < i1; i += 32) found |= bf16_not_finite(*piece(i));
   int bad = 128;
   if (__any_sync(0xffffffffu, found)) {
