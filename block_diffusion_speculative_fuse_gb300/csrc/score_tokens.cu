@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kGroup = 16;         // logits that a thread reads together
-constexpr int kCandidates = 1024;
+constexpr int kCandidates = 1024, kGroups = 512;   // places for candidates, and for groups that hold some
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309f;
 
@@ -95,16 +95,20 @@ struct Row {
   __device__ uint4 load(int v) const {
     const int i = first(v);
     if (i >= 0 && i + PER <= vocab) return __ldg(reinterpret_cast<const uint4*>(base) + v);
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    return edge(v);
+  }
+  // A row's first and last vector.  Out of line: what a row's phases run once has to stay in
+  // the instruction cache beside the pass.
+  __device__ __noinline__ uint4 edge(int v) const {
+    uint32_t w[4] = {};
+    for (int j = 0; j < PER; ++j) {
+      const int i = first(v) + j;
+      const bool in = i >= 0 && i < vocab;
       if (HALF) {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(base) + v * 8 + 2 * j;
-        const uint32_t lo = i + 2 * j >= 0 && i + 2 * j < vocab ? __ldg(h) : 0xFF80u;
-        const uint32_t hi = i + 2 * j + 1 >= 0 && i + 2 * j + 1 < vocab ? __ldg(h + 1) : 0xFF80u;
-        w[j] = lo | hi << 16;
+        const uint32_t x = in ? __ldg(reinterpret_cast<const uint16_t*>(base) + v * 8 + j) : 0xFF80u;
+        w[j / 2] |= x << (j % 2 * 16);
       } else {
-        w[j] = i + j >= 0 && i + j < vocab ? __ldg(reinterpret_cast<const uint32_t*>(base) + v * 4 + j) : 0xFF800000u;
+        w[j % 4] = in ? __ldg(reinterpret_cast<const uint32_t*>(base) + v * 4 + j) : 0xFF800000u;
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   __shared__ float2 best[kMaxCluster * kMaxScoreTop];   // of all slices (rank 0's)
   __shared__ float4 slices[kMaxCluster];                // their statistics (rank 0's)
   __shared__ float thread_max[kThreads];
-  __shared__ int scratch[kThreads / 32], bins[256], count, bound;
+  __shared__ int scratch[kThreads / 32], bins[256], group_list[kGroups], count, reaching, bound;
   __shared__ Stats warps[kThreads / 32];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -242,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       raw[u] = v < v1 ? row.load(v) : R::none();
     }
   };
-  fetch(0);
   int id = p.ids != nullptr ? __ldg(p.ids + r) : -1;
   const bool bad_id = id >= p.vocab;
   if (bad_id || id < 0) id = -1;
@@ -257,11 +260,14 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   // ---- the pass
   Stats st = {-INFINITY, 0.f, 0.f, 0};
 #pragma unroll 1
-  for (int g = 0; g < groups; ++g) {
+  for (int g = -1; g < groups; ++g) {   // (-1: only the first loads)
     float z[kGroup];
+    if (g >= 0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) R::unpack(raw[u], z + u * PER);
+      for (int u = 0; u < kUnroll; ++u) R::unpack(raw[u], z + u * PER);
+    }
     if (g + 1 < groups) fetch(g + 1);
+    if (g < 0) continue;
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) top = fmaxf(top, z[j]);
@@ -296,17 +302,18 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       for (int u = 0; u < kUnroll; ++u) {
         const int v = v0 + (g * kUnroll + u) * kThreads + tid, i = row.first(v);
         if (v >= v1) break;
-        if (i >= 0 && (i + PER <= id || i > id)) {
-          const float border = i > id ? zid : below;
+        // (not the vector that holds the token, nor the one in which the row starts)
+        if (i < 0 || (i <= id && id < i + PER)) continue;
+        const float border = i > id ? zid : below;
 #pragma unroll
-          for (int j = 0; j < PER; ++j) st.better += !(z[u * PER + j] <= border);
-        } else {   // the vector that holds the token, or in which the row starts
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (i + j >= 0 && i + j != id) st.better += !(z[u * PER + j] <= (i + j > id ? zid : below));
-        }
+        for (int j = 0; j < PER; ++j) st.better += !(z[u * PER + j] <= border);
       }
     }
+  }
+  if (id >= 0 && tid < 2 * PER) {   // those two, a logit to a thread
+    const int own = (id + row.shift) / PER, v = tid < PER ? own : 0, i = row.first(v) + tid % PER;
+    if ((tid < PER || (own > 0 && row.shift > 0)) && v >= v0 && v < v1 && i >= 0 && i < row.vocab && i != id)
+      st.better += !(row.at(i) <= (i > id ? zid : below));
   }
   if (p.n_top > 0) thread_max[tid] = st.m;
 
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   }
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     Stats y;
     y.m = __shfl_xor_sync(0xffffffffu, st.m, o);
@@ -325,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     join(st, y, c);
   }
   if (lane == 0) warps[warp] = st;
-  if (tid == 0) count = 0;
+  if (tid == 0) count = reaching = 0;
   __syncthreads();
   if (warp == 0) {
     Stats a = lane < kThreads / 32 ? warps[lane] : Stats{-INFINITY, 0.f, 0.f, 0};
-#pragma unroll
+#pragma unroll 1
     for (int o = 8; o > 0; o >>= 1) {
       Stats y;
       y.m = __shfl_xor_sync(0xffffffffu, a.m, o);
@@ -367,26 +374,28 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     __syncthreads();
     const uint32_t least = static_cast<uint32_t>(bound);
     auto reaches = [&](float z) { return z > -INFINITY && key_of(z) >> 16 >= least; };
+    // the groups that reach it, then their logits, sixteen lanes to a group
 #pragma unroll 1
-    for (int g = 0; g < groups; ++g) {
-      if (group_max[g * kThreads + tid] < least) continue;
-      fetch(g);
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        float z[PER];
-        R::unpack(raw[u], z);
-        const int i = row.first(v0 + (g * kUnroll + u) * kThreads + tid);
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if (reaches(z[j])) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kCandidates) list[at] = make_float2(z[j], __int_as_float(i + j));
-          }
+    for (int g = 0; g < groups; ++g)
+      if (group_max[g * kThreads + tid] >= least) {
+        const int at = atomicAdd(&reaching, 1);
+        if (at < kGroups) group_list[at] = g * kThreads + tid;
       }
+    __syncthreads();
+    const int many = reaching;
+#pragma unroll 1
+    for (int x = warp * 2 + lane / 16; x < min(many, kGroups); x += kThreads / 16) {
+      const int gt = group_list[x], g = gt / kThreads, l = lane % 16;
+      const int v = v0 + (g * kUnroll + l / PER) * kThreads + gt - g * kThreads, i = row.first(v) + l % PER;
+      if (v >= v1 || i < 0 || i >= row.vocab) continue;
+      const float z = row.at(i);
+      if (!reaches(z)) continue;
+      const int at = atomicAdd(&count, 1);
+      if (at < kCandidates) list[at] = make_float2(z, __int_as_float(i));
     }
     __syncthreads();
     int found = count;
-    if (found > kCandidates) found = many_equal<HALF>(row, v0, v1, n, list, scratch, &count, bins);
+    if (found > kCandidates || many > kGroups) found = many_equal<HALF>(row, v0, v1, n, list, scratch, &count, bins);
     // each counts what precedes it
     mine = min(found, n);
     for (int a = tid; a < found; a += kThreads) {
@@ -425,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 
   // ---- the row's results
   Stats a = {-INFINITY, 0.f, 0.f, 0};
+#pragma unroll 1
   for (int k = 0; k < cluster; ++k) {
     const float4 v = slices[k];
     join(a, Stats{v.x, v.y, v.z, __float_as_int(v.w)}, c);
