@@ -97,26 +97,6 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   const int safe0 = p.sink, safe1 = q.ctx - min(p.recent, q.ctx);
   auto key = [&](float m, int j) { return j < safe0 || j >= safe1 ? 0xFFFFFFFFu : key_of(m); };
   const bool fits = j1 - j0 <= cached;
-  // f(key) for the slice's positions of this thread, eight reads at once
-  auto each = [&](auto f) {
-#pragma unroll 1
-    for (int at = tid; at < j1 - j0; at += 8 * kThreads) {
-      uint32_t k[8];
-      if (fits) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = cache[min(at + i * kThreads, j1 - j0 - 1)];
-      } else {
-        float m[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = __ldg(mass + min(j0 + at + i * kThreads, j1 - 1));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = key(m[i], j0 + at + i * kThreads);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (at + i * kThreads < j1 - j0) f(k[i]);
-    }
-  };
   auto sum_of_lower = [&](int v) {   // of the warps before; v: lane w has warp w's
     return static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? v : 0));
   };
@@ -166,17 +146,6 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   int equals = 0;                 // kept of those at the border
   const bool all = q.keep >= q.ctx;
   if (!all) {
-    if (fits) {
-#pragma unroll 1
-      for (int at = tid; at < j1 - j0; at += 8 * kThreads) {
-        float m[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = __ldg(mass + min(j0 + at + i * kThreads, j1 - 1));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (at + i * kThreads < j1 - j0) cache[at + i * kThreads] = key(m[i], j0 + at + i * kThreads);
-      }
-    }
     uint32_t prefix = 0, mask = 0;
     int need = q.keep;            // of the positions with this prefix
 #pragma unroll 1
@@ -185,9 +154,27 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
       uint32_t* mine = bins[pass & 1];
       for (int b = tid; b < kBins; b += kThreads) mine[b] = 0;
       __syncthreads();
-      each([&](uint32_t k) {
-        if ((k & mask) == prefix) atomicAdd(&mine[k >> shift & bits], 1u);
-      });
+      // four positions of a thread at once; the first pass leaves their keys behind
+#pragma unroll 1
+      for (int at = tid; at < j1 - j0; at += 4 * kThreads) {
+        uint32_t k[4];
+        if (pass > 0 && fits) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) k[i] = cache[min(at + i * kThreads, j1 - j0 - 1)];
+        } else {
+          float m[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m[i] = __ldg(mass + min(j0 + at + i * kThreads, j1 - 1));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            k[i] = key(m[i], j0 + at + i * kThreads);
+            if (fits && at + i * kThreads < j1 - j0) cache[at + i * kThreads] = k[i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (at + i * kThreads < j1 - j0 && (k[i] & mask) == prefix) atomicAdd(&mine[k[i] >> shift & bits], 1u);
+      }
       __syncthreads();
       // sums of 32 bins, so that other CTAs' need not all be read: a warp adds up four
 #pragma unroll
@@ -204,6 +191,13 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
       need -= found[1];
       gather(mine + c * 32, 32);
       search(32, need);
+      if (warp == 0) {   // of this slice: what lies above the digit, and at it
+        const uint32_t* co = coarse[pass & 1];
+        int over = (lane > c ? co[lane] : 0) + (lane + 32 > c ? co[lane + 32] : 0);
+        if (lane > found[0]) over += mine[c * 32 + lane];
+        over = __reduce_add_sync(0xffffffffu, over);
+        if (lane == 0) slice_counts = make_int2((pass == 0 ? 0 : slice_counts.x) + over, mine[c * 32 + found[0]]);
+      }
       prefix |= static_cast<uint32_t>(c * 32 + found[0]) << shift;
       mask |= static_cast<uint32_t>(bits) << shift;
       need -= found[1];
@@ -215,24 +209,6 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   // where this slice's kept positions go: count, then number them in order
   int above0 = all ? j0 : 0, equal0 = 0;
   if (!all && cluster > 1) {
-    int above = 0, equal = 0;
-    each([&](uint32_t k) {
-      above += k > border;
-      equal += k == border;
-    });
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    __syncthreads();
-    if (lane == 0) {
-      warps[0][warp] = above;
-      warps[1][warp] = equal;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      above = __reduce_add_sync(0xffffffffu, lane < kWarps ? warps[0][lane] : 0);
-      equal = __reduce_add_sync(0xffffffffu, lane < kWarps ? warps[1][lane] : 0);
-      if (lane == 0) slice_counts = make_int2(above, equal);
-    }
     cluster_sync();
     int2 v[kMaxCluster];
 #pragma unroll
