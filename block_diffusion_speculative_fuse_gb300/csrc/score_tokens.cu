@@ -46,6 +46,12 @@ __device__ __forceinline__ uint32_t key_of(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+// 1 where z <= border does not hold (NaN on either side included), else 0.
+__device__ __forceinline__ float not_at_most(float z, float border) {
+  float r;
+  asm("set.gtu.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(border));
+  return r;
+}
 __device__ __forceinline__ bool before(float za, int ia, float zb, int ib) {
   return za > zb || (za == zb && ia < ib);
 }
@@ -257,8 +263,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   T = bad_T ? 1.f : fminf(fmaxf(T, 1e-30f), 1e30f);
   const float c = kLog2e / T;
 
+  // Groups [whole0, whole1) lie inside the row and the slice for all threads.
+  const int whole0 = v0 == 0 && row.shift > 0 ? 1 : 0;
+  const int whole1 = max(min(v1, (row.shift + row.vocab) / PER) - v0, 0) / (kThreads * kUnroll);
+  auto whole = [&](int g) { return g >= whole0 && g < whole1; };
   // ---- the pass
   Stats st = {-INFINITY, 0.f, 0.f, 0};
+  float better = 0.f;   // (a thread has fewer than 2^24 logits)
 #pragma unroll 1
   for (int g = -1; g < groups; ++g) {   // (-1: only the first loads)
     float z[kGroup];
@@ -266,7 +277,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) R::unpack(raw[u], z + u * PER);
     }
-    if (g + 1 < groups) fetch(g + 1);
+    if (whole(g + 1)) {
+      const uint4* at = reinterpret_cast<const uint4*>(row.base) + v0 + (g + 1) * (kUnroll * kThreads) + tid;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) raw[u] = __ldg(at + u * kThreads);
+    } else if (g + 1 < groups) {
+      fetch(g + 1);
+    }
     if (g < 0) continue;
     float top = -INFINITY;
 #pragma unroll
@@ -298,18 +315,29 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       st.e += e.x + e.y;
     }
     if (id >= 0) {
+      // all of the group before the token or all behind it, or a vector at a time
+      const int i0 = row.first(v0 + g * (kUnroll * kThreads) + tid), i1 = i0 + (kUnroll - 1) * kThreads * PER + PER;
+      if (whole(g) && (i1 <= id || i0 > id)) {
+        const float border = i0 > id ? zid : below;
+        float2 n2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int v = v0 + (g * kUnroll + u) * kThreads + tid, i = row.first(v);
-        if (v >= v1) break;
-        // (not the vector that holds the token, nor the one in which the row starts)
-        if (i < 0 || (i <= id && id < i + PER)) continue;
-        const float border = i > id ? zid : below;
+        for (int j = 0; j < kGroup; j += 2)
+          n2 = add2(n2, make_float2(not_at_most(z[j], border), not_at_most(z[j + 1], border)));
+        better += n2.x + n2.y;
+      } else {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) st.better += !(z[u * PER + j] <= border);
+        for (int u = 0; u < kUnroll; ++u) {
+          const int v = v0 + (g * kUnroll + u) * kThreads + tid, i = row.first(v);
+          // (not the vector that holds the token, nor the one in which the row starts)
+          if (v >= v1 || i < 0 || (i <= id && id < i + PER)) continue;
+          const float border = i > id ? zid : below;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) better += not_at_most(z[u * PER + j], border);
+        }
       }
     }
   }
+  st.better = static_cast<int>(better);
   if (id >= 0 && tid < 2 * PER) {   // those two, a logit to a thread
     const int own = (id + row.shift) / PER, v = tid < PER ? own : 0, i = row.first(v) + tid % PER;
     if ((tid < PER || (own > 0 && row.shift > 0)) && v >= v0 && v < v1 && i >= 0 && i < row.vocab && i != id)
@@ -358,11 +386,20 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   if (n > 0) {
     if (warp == 1) {
       // the n-th largest of the threads' maxima, by the upper 16 bits of its key
-      uint32_t k[kThreads / 32], least = 0;
+      uint32_t k[kThreads / 32], lo = ~0u, hi = 0;
 #pragma unroll
-      for (int j = 0; j < kThreads / 32; ++j) k[j] = key_of(thread_max[j * 32 + lane]) >> 16;
+      for (int j = 0; j < kThreads / 32; ++j) {
+        k[j] = key_of(thread_max[j * 32 + lane]) >> 16;
+        lo = min(lo, k[j]);
+        hi = max(hi, k[j]);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      // (bits above the first in which they differ are all of them's)
+      const int bits = 32 - __clz(lo ^ hi);
+      uint32_t least = hi >> bits << bits;
 #pragma unroll 1
-      for (int b = 15; b >= 0; --b) {
+      for (int b = bits - 1; b >= 0; --b) {
         const uint32_t y = least | 1u << b;
         int many = 0;
 #pragma unroll
