@@ -1,5 +1,49 @@
 // Attention of a ragged batch of new rows (single tokens, chunks of prompts, whole
 // prompts) to the paged cache.
+//
+//   out_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i . k_j
+//
+// A unit is the rows of up to 2 * (128 / G) tokens of a request for one KV head (G query
+// heads to each, so a tile of 128 rows reads a key once for all of them): two tiles of
+// 128 rows, A and B, over the same keys, 128 a chunk.  Per chunk and tile
+//   S = Q K^T   (M = 128, N = 128, K = d)   TMEM, 128 columns
+//   O += P V    (M = 128, N = d, K = 128)   TMEM, d columns
+// in the order S_A S_B | PV_A S_A' PV_B S_B' | ..., so that the tensor pipe has one tile's
+// products while the other's warps form P = exp2(S - m); P replaces S in TMEM (bf16, the A
+// operand of the second product).  A unit whose rows fit one tile (single tokens) takes
+// turns instead: A the even chunks, B the odd ones, over the same Q, joined at its end.
+//
+// Softmax: two threads to a row, 64 keys each, all of them in registers at once.  The
+// row's reference maximum m is raised, and O rescaled, only when a chunk exceeds it by more
+// than 2^8: after the first chunks that is rare, so the two threads' warps exchange a
+// vote per chunk (one barrier with a reduction) and their maxima only when it carries.  P
+// stays below 2^8, and l is summed in fp32 before P is rounded to bf16, the type that the product with
+// bf16 V takes (a second term of P would be half as many products again).
+//
+// Work.  Lengths are on the device, so every CTA (one per SM) adds up the same costs over
+// the requests, in closed form, and takes the range of equal cost that is its own; a planning
+// warp walks it and hands pieces (chunks of a unit) to the others.  A unit that lies in one range
+// is written by its CTA; the pieces of one that was cut leave partial (O, m, l), joined
+// in order by a second kernel or, where rows are few, by the CTA that finishes last.
+//
+// Values that a row must not see.  S is replaced by -inf, and 0 * V must be 0: a warp goes
+// over the planes of V whose keys not all of a unit's rows see, before their product:
+// zeros past the last row's keys, and for what is not finite (the rows that do
+// see it get a NaN by way of l).
+//
+// Bound: with whole units the tensor pipe.  4096 rows of 32 heads behind 12288 keys: 1.64
+// PFLOP/s, 0.86 of the GEMM rate, 0.59 ms; behind 28672 (134 MB of keys, more than L2)
+// 1.36 ms, 1.52 PFLOP/s.  A chunk of both tiles takes 3050 cycles: its products
+// 2048 of the tensor pipe and, at 128 bytes a cycle, 2048 of shared memory (S reads Q and K,
+// P V reads V, the loads write both); a tile's softmax 1100 under the other's products.  For short
+// prompts the units' ends: 8 x 1024 rows take 85 us, 54 of them chunks.  For single tokens
+// the keys' bytes: 32 requests of 3000 to 6200 keys 109 us, 6.1 TB/s; one request of 4096
+// keys 16 us, of which the keys' bytes are 2.5: plan, first loads and join are chains of
+// loads, and code that is not yet in the instruction cache.
+//
+// That cache decides more than arithmetic here.  All roles' code together has to stay
+// in it: with the polls of 20 waits unrolled (172 KB of instructions instead of 77) a
+// unit's end took 5000 cycles instead of 2500 and 8 x 1024 rows 107 us instead of 86.
 #include <climits>
 
 #include "attention_chunk.cuh"
@@ -19,7 +63,8 @@ constexpr int kUnitCost = 10;     // a unit's start and end
 constexpr int kSplitCost = 4;     // of a chunk with one tile: as much as with two, since the
                                   // loads bound it (2, 3, 4: a mixed batch 384, 304, 288 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
-constexpr int kLeast = 4;         // chunks of a piece of a unit
+constexpr int kLeast = 3;         // chunks of a piece of a unit (2, 3, 4: 8 prompts of 1024 rows 88,
+                                  // 85, 85 us, one row of 4096 keys 16.1, 16.4, 17.2)
 
 template <int D>
 struct Cfg {
