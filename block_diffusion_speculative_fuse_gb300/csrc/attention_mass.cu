@@ -16,7 +16,10 @@
 // rows: ranges 50 us, in turn 53); units in a row share Q where there is one tile.  Per tile
 // and plane one D, in two stages each, which the plane's four warps sum up.
 //
-// Bound: with the usual window of rows (32 rows of 4 heads, one tile) K's bytes.
+// Bound: with the usual window of rows (32 rows of 4 heads, one tile) K's bytes: 8
+// requests of 16384 keys 50 us, 5.5 TB/s with 6 us of start-up, 32 of them 182 us, 6.0
+// TB/s; 8 rows take as long as 32.  With many tiles Q's traffic from L2, each tile again
+// for every 256 keys: 512 rows of 8 requests of 16848 keys 624 us, 0.89 PFLOP/s.
 #include <climits>
 
 #include "attention_chunk.cuh"
