@@ -1022,7 +1022,8 @@ cudaError_t launch(const ChunkParams& p, const CUtensorMap& kv_map, const CUtens
   cfg.numAttrs = 1;
   count_launch();
   e = cudaLaunchKernelEx(&cfg, chunk_kernel<D>, kv_map, q_map, p, group0, oob_group);
-  if (e != cudaSuccess || p.fused) return e;
+  // no unit of fewer than 2 * kLeast chunks is cut
+  if (e != cudaSuccess || p.fused || p.max_pages * 16ll <= (2 * kLeast - 1) * kChunk) return e;
   cfg.gridDim = dim3(kChunkWorkers, (p.slot_rows + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;

@@ -322,8 +322,11 @@ int dflash_sample_rows(const float* logits, int32_t n_blocks, int32_t block, int
 /* A decode step over a paged cache for callers that bring their own
  * projections: append rotated K/V (dflash_kv_rope_append), attend to them
  * with a prefix shared by many requests read once (dflash_attention_prefix),
- * draw the next tokens from the logits (dflash_sample_filtered).  None needs a
- * model handle.  They share the conventions above: device pointers, caller's
+ * draw the next tokens from the logits (dflash_sample_filtered).  And a long
+ * prompt through the same cache: attend to it with a ragged batch of chunks
+ * (dflash_attention_chunk), sum up what each cached key was attended to
+ * (dflash_attention_mass), keep the heaviest positions (dflash_kv_evict), score
+ * the prompt's tokens (dflash_score_tokens).  None needs a model handle.  They share the conventions above: device pointers, caller's
  * workspace, asynchronous on `stream`, nothing launched on an argument error.
  * All of a call's device memory belongs to the current device. */
 

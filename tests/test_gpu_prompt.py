@@ -285,6 +285,17 @@ def test_score_extreme_temperatures_and_logits():
     check_scores(z, [1e-35, 1e-3, 1e6, 1e38, 1.0, 1e30], [int(z[0].argmax()), 3, 4, 5, int(z[4].argmax()), 9], 5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_score_rows_at_odd_addresses(dtype):
+    """Rows that start anywhere in a 16-byte vector, and end anywhere."""
+    for off in range(1, 9):
+        z = logits(5, 3001 + off, dtype=dtype, seed=off, pad=3)[:, off:]
+        ids = [0, 1, 3000, 7, -1]
+        check_scores(z, None, ids, 7)
+        tiny = logits(6, 20, dtype=dtype, seed=off)[:, off:off + 1 + off % 3]
+        check_scores(tiny, None, [0] * 6, 2)
+
+
 def test_score_optional_outputs_and_single_rows():
     """Outputs may be left out, and a row's results do not depend on the others."""
     B = B_()
