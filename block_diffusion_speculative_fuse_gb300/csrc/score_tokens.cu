@@ -61,26 +61,23 @@ __device__ __forceinline__ bool before(float za, int ia, float zb, int ib) {
   return za > zb || (za == zb && ia < ib);
 }
 
-// a += b, relative to the larger maximum
-__device__ __forceinline__ void join(Stats& a, const Stats& b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  auto into = [&](const Stats& x, float* s, float* e) {
-    if (x.m == -INFINITY) {   // nothing, or NaN
-      *s = x.s;
-      *e = x.s;
-      return;
-    }
+// x's sums relative to the maximum m >= x.m.
+__device__ __forceinline__ void rebase(Stats& x, float m, float c) {
+  if (x.m == -INFINITY) {   // nothing, or NaN
+    x.e = x.s;
+  } else {
     const float d = (x.m - m) * c, w = ex2(d);
-    *s = x.s * w;
-    *e = w * (x.e + x.s * fmaxf(d, -200.f));
-  };
-  float sa, ea, sb, eb;
-  into(a, &sa, &ea);
-  into(b, &sb, &eb);
-  a.m = m;
-  a.s = sa + sb;
-  a.e = ea + eb;
-  a.better += b.better;
+    x.e = w * (x.e + x.s * fmaxf(d, -200.f));
+    x.s *= w;
+  }
+  x.m = m;
+}
+// The lanes' sums together, to all lanes.
+__device__ __forceinline__ void warp_join(Stats& x, float c) {
+  rebase(x, warp_max(x.m), c);
+  x.s = warp_sum(x.s);
+  x.e = warp_sum(x.e);
+  x.better = __reduce_add_sync(0xffffffffu, x.better);
 }
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
@@ -355,29 +352,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   }
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) {
-    Stats y;
-    y.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    y.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    y.e = __shfl_xor_sync(0xffffffffu, st.e, o);
-    y.better = __shfl_xor_sync(0xffffffffu, st.better, o);
-    join(st, y, c);
-  }
+  warp_join(st, c);
   if (lane == 0) warps[warp] = st;
   if (tid == 0) count = reaching = 0;
   __syncthreads();
   if (warp == 0) {
     Stats a = lane < kThreads / 32 ? warps[lane] : Stats{-INFINITY, 0.f, 0.f, 0};
-#pragma unroll 1
-    for (int o = 8; o > 0; o >>= 1) {
-      Stats y;
-      y.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-      y.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-      y.e = __shfl_xor_sync(0xffffffffu, a.e, o);
-      y.better = __shfl_xor_sync(0xffffffffu, a.better, o);
-      join(a, y, c);
-    }
+    warp_join(a, c);
     if (lane == 0) {
       const float4 v = make_float4(a.m, a.s, a.e, __int_as_float(a.better));
       if (rank == 0) slices[0] = v;
@@ -476,11 +457,11 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 
   // ---- the row's results
   Stats a = {-INFINITY, 0.f, 0.f, 0};
-#pragma unroll 1
-  for (int k = 0; k < cluster; ++k) {
-    const float4 v = slices[k];
-    join(a, Stats{v.x, v.y, v.z, __float_as_int(v.w)}, c);
+  if (lane < cluster) {
+    const float4 v = slices[lane];
+    a = Stats{v.x, v.y, v.z, __float_as_int(v.w)};
   }
+  warp_join(a, c);
   const bool bad = bad_T || a.m == -INFINITY || a.m == INFINITY || !(a.s > 0.f);
   const float nan = __int_as_float(0x7FC00000), ln_s = logf(a.s);
   if (tid == 0) {
