@@ -33,7 +33,7 @@
 //
 // Bound: with whole units the tensor pipe.  4096 rows of 32 heads behind 12288 keys: 1.64
 // PFLOP/s, 0.86 of the GEMM rate, 0.59 ms; behind 28672 (134 MB of keys, more than L2)
-// 1.36 ms, 1.52 PFLOP/s.  A chunk of both tiles takes 3050 cycles: its products
+// 1.29 ms, 1.60 PFLOP/s, in two rounds; behind 126976 5.41 ms, 1.60 PFLOP/s, in eight.  A chunk of both tiles takes 3050 cycles: its products
 // 2048 of the tensor pipe and, at 128 bytes a cycle, 2048 of shared memory (S reads Q and K,
 // P V reads V, the loads write both); a tile's softmax 1100 under the other's products.  For short
 // prompts the units' ends: 8 x 1024 rows take 85 us, 54 of them chunks.  For single tokens
@@ -63,6 +63,13 @@ constexpr int kUnitCost = 10;     // a unit's start and end
 constexpr int kSplitCost = 4;     // of a chunk with one tile: as much as with two, since the
                                   // loads bound it (2, 3, 4: a mixed batch 384, 304, 288 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
+// Keys that several row units read should stay in L2 from one unit to the next.  Where those
+// of all requests do not fit, the workers take the work in rounds (phases), each of fewer
+// heads or requests: the units that run at a time then read the same keys.  One round against
+// up to 8: 4096 rows behind 28672 keys 1.37 -> 1.29 ms, behind 126976 keys 6.24 -> 5.41, 8 x 2048
+// rows behind 15000 3.24 -> 2.88, 1000 rows behind 131072 1.59 -> 1.39.
+constexpr int kResident = 5760;   // in 64 keys of one head of 64: 90 MB
+constexpr int kPhaseCost = 400;   // the least share of a worker in a phase (100, 200, 400: no difference)
 constexpr int kLeast = 3;         // chunks of a piece of a unit (2, 3, 4: 8 prompts of 1024 rows 88,
                                   // 85, 85 us, one row of 4096 keys 16.1, 16.4, 17.2)
 
@@ -75,20 +82,23 @@ struct Cfg {
   static constexpr int SLOTS = D == 128 ? 5 : 10;
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // + 128 * tile
   static constexpr int FIXED = 2 * Q_TILE + SLOTS * PLANE;
-  static constexpr int SMEM = FIXED + 3072;
+  static constexpr int PLAN = (D == 128 ? 3 : 4) * 1024;                  // all else, behind the tiles
+  static constexpr int SMEM = FIXED + PLAN;
 };
 
 // A place in the work: requests, their KV heads, their row units, chunks of keys.
 struct Place {
   int r, h, i, c;
   int x;            // cost of everything before the request's units of this head
-  ChunkRequest q;
 };
 
-// The deal: worker w's range starts at share * w + rest * w / used.
+// The deal: range v, of used * phases, starts at share * v + rest * v / (used * phases);
+// worker w has the ranges w, w + used, ... (one where there is one phase).
 struct Deal {
-  int share, rest, used;
-  __device__ int start(int w) const { return share * w + rest * w / used; }
+  int share, rest, used, phases;
+  int keys;   // in units of 64, of the requests that have several row units
+  ChunkRequest q;   // of the first range's start
+  __device__ int start(int v) const { return share * v + rest * v / (used * phases); }
 };
 
 // Chunks [c0, c0 + n) of a unit, for all warps of the CTA.
@@ -99,10 +109,11 @@ struct Piece {
   int r, h, token0, tokens;  // request, KV head, first row of the call, rows
   int split, begins, ends;   // one tile; the piece is the unit's first, its last
   int x, all;              // of a unit with one tile: cost of everything before it; its chunks
+  int range, first;        // whose piece it is; the range's first
 };
 
-// What a worker leaves for the join.
-struct WorkerRecord {
+// What a range leaves for the join.
+struct RangeRecord {
   int cont, ends;            // its first piece continues a unit; and ends it
   int head;                  // its last piece begins a unit that others continue
   int token0, tokens, kvh;   // that unit's first row of the call, its rows, its head
@@ -162,12 +173,14 @@ __device__ __forceinline__ ChunkRequest request(const ChunkParams& p, int r) {
   return ChunkRequest(p.row_start, p.ctx_len, r, p.T, p.max_pages, p.status, 551);
 }
 
-// Start and end of a worker's range, by all threads of the CTA; ends with a barrier.
+// Start and end of a worker's ranges, by all threads of the CTA; ends with a barrier.
 // scratch: kWarps words.
 __device__ void find_range(const ChunkParams& p, int worker, int workers, Place* out, int* scratch, Deal* deal) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  if (tid < 2) out[tid] = Place{p.batch, 0, 0, 0, 0, ChunkRequest()};
-  int all = 0, used = 0, x0 = 0, x1 = 0;
+  if (tid < 2 * kChunkPhases) out[tid] = Place{p.batch, 0, 0, 0, 0};
+  if (tid == 0) *deal = Deal{0, 0, 0, 1, 0, ChunkRequest()};
+  int all = 0;
+  Deal d{0, 0, 0, 1, 0, ChunkRequest()};
   // a first round adds up the costs, a second finds the boundaries
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
@@ -186,6 +199,7 @@ __device__ void find_range(const ChunkParams& p, int worker, int workers, Place*
       }
       __syncthreads();
       if (lane == 31) scratch[warp] = upto;
+      if (p.phases > 1 && round == 0 && u.tiles > 1) atomicAdd(&deal->keys, q.ctx / 64);
       __syncthreads();
       int at = before + upto - v;
       const int part = lane < kWarps ? scratch[lane] : 0;
@@ -197,18 +211,21 @@ __device__ void find_range(const ChunkParams& p, int worker, int workers, Place*
       }
       if (round == 1) {
         if (base == 0) {
-          used = min(workers, (all + kWorkerCost - 1) / kWorkerCost);
-          if (worker >= used) break;
-          const Deal d{all / used, all % used, used};
-          if (tid == 0) *deal = d;
-          x0 = d.start(worker);
-          x1 = d.start(worker + 1);
+          d.used = min(workers, (all + kWorkerCost - 1) / kWorkerCost);
+          if (worker >= d.used) break;
+          if (d.used == workers)
+            while (d.phases < p.phases && d.phases * kResident <= static_cast<int64_t>(deal->keys) * p.hkv * p.halves &&
+                   all >= 2 * d.phases * workers * kPhaseCost)
+              d.phases *= 2;   // (by twos, so that a phase is whole heads more often)
+          d.share = all / (d.used * d.phases);
+          d.rest = all - d.share * (d.used * d.phases);
         }
 #pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-          const int x = (j == 0 ? x0 : x1) - at;
+        for (int j = 0; j < 2 * d.phases; ++j) {
+          const int x = d.start(worker + j / 2 * d.used + j % 2) - at;
           if (x < 0 || x >= v) continue;
-          Place pl{r, x / one, 0, 0, 0, q};
+          Place pl{r, x / one, 0, 0, 0};
+          if (j == 0) deal->q = q;
           pl.x = at + pl.h * one;
           u.find(x - pl.h * one, &pl.i, &pl.c);
           out[j] = pl;
@@ -216,6 +233,12 @@ __device__ void find_range(const ChunkParams& p, int worker, int workers, Place*
       }
     }
     if (round == 0) all = before;
+  }
+  if (tid == 0) {
+    deal->share = d.share;
+    deal->rest = d.rest;
+    deal->used = d.used;
+    deal->phases = d.phases;
   }
   __syncthreads();
 }
@@ -321,14 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* piece_full = o_full + 1;        // [kPieces]
   uint64_t* piece_free = piece_full + kPieces;
   Piece* pieces = reinterpret_cast<Piece*>(piece_free + kPieces);  // [kPieces]
-  Place* range = reinterpret_cast<Place*>(pieces + kPieces);       // [2]
-  Deal* deal = reinterpret_cast<Deal*>(range + 2);
+  Place* range = reinterpret_cast<Place*>(pieces + kPieces);       // [kChunkPhases][2]
+  Deal* deal = reinterpret_cast<Deal*>(range + 2 * kChunkPhases);
   int* scratch = reinterpret_cast<int*>(deal + 1);                 // [kWarps]
   volatile int* bad = reinterpret_cast<volatile int*>(scratch + kWarps);  // [kPieces] first key with a V that is not finite
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(bad) + kPieces);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(512 * 4 + (3 * SLOTS + 9 + 2 * kPieces) * 8 + kPieces * sizeof(Piece) + 2 * sizeof(Place) + sizeof(Deal) +
-                        (kWarps + kPieces + 2) * 4 <= 3072, "fits");
+  static_assert(512 * 4 + (3 * SLOTS + 9 + 2 * kPieces) * 8 + kPieces * sizeof(Piece) + 2 * kChunkPhases * sizeof(Place) +
+                        sizeof(Deal) +
+                        (kWarps + kPieces + 2) * 4 <= Cfg<D>::PLAN, "fits");
 
   // (one lane's word for it, so that the compiler knows roles and pieces to be the
   // warp's and keeps what depends on them in uniform registers)
@@ -400,11 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 19) {
       // ------------------------------------------------ plan: the worker's range, piece by piece
-      Place at = range[0];
-      const Place end = range[1];
-      ChunkRequest q = at.q;
-      int loaded = at.r, count = 0;
-      bool last = false;
+      Place at = range[0], end = range[1];
+      ChunkRequest q = deal->q;
+      int loaded = at.r, count = 0, phase = 0;
+      bool last = false, first_piece = true;
       while (!last) {
         Piece pc;
         pc.n = -1;
@@ -412,6 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool same = at.r == end.r, there = same && at.h == end.h && at.i == end.i;
           if (at.r >= p.batch || at.r > end.r ||
               (same && (at.h > end.h || (at.h == end.h && (at.i > end.i || (there && at.c >= end.c)))))) {
+            if (++phase < deal->phases) {   // the next range
+              at = range[2 * phase];
+              end = range[2 * phase + 1];
+              loaded = -1;
+              first_piece = true;
+              continue;
+            }
             last = true;
             break;
           }
@@ -448,6 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           pc.ends = c1 == all;
           pc.x = at.x;
           pc.all = all;
+          pc.range = worker + phase * deal->used;
+          pc.first = first_piece;
+          first_piece = false;
           break;
         }
         const int slot = count % kPieces;
@@ -710,12 +743,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = r128 * inv_G >> 16;       // of the tile
     int segs = 0, ns = 0;
     Piece pc;
-    WorkerRecord* rec = reinterpret_cast<WorkerRecord*>(p.records) + worker;
-    if (tid == 0) *rec = WorkerRecord{};
+    RangeRecord* records = reinterpret_cast<RangeRecord*>(p.records);
+    if (tid < p.phases) records[worker + tid * kChunkWorkers] = RangeRecord{};
+    __syncwarp();
     while (next_piece(&pc)) {
       const int n = pc.n;
       if (tid == 0) {
-        if (taken == 0) {
+        RangeRecord* rec = records + pc.range;
+        if (pc.first) {
           rec->cont = !pc.begins;
           rec->ends = !pc.begins && pc.ends;
         }
@@ -833,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = whole ? (m == -INFINITY ? 0.f : 1.f / l) : 1.f;
       const float fa = wa * inv, fb = wb * inv;
       const int row0 = pc.split ? 0 : tile * 128;      // the tile's first in the unit
-      const size_t slot_row = (2 * static_cast<size_t>(worker) + (pc.begins ? 1 : 0)) * p.slot_rows + row0 + r128;
+      const size_t slot_row = (2 * static_cast<size_t>(pc.range) + (pc.begins ? 1 : 0)) * p.slot_rows + row0 + r128;
       const int64_t out_row = (pc.token0 + my_token) * p.ld_out + (pc.h * p.G + r128 - tok * p.G) * D;
       // One tile: a quarter of the columns for each of the four warps of its rows.  16 columns
       // at a time, in few instructions: they are not in the instruction cache when a unit
@@ -895,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int* list = reinterpret_cast<int*>(exch);
           if (warp == 0) {
             // the workers in whose ranges it lies
-            const Deal d = *deal;
+            const Deal d = *deal;   // (one phase: keys are read once)
             const int end_x = pc.x + Units::unit_cost(pc.keys, true);
             int parts = 0;
 #pragma unroll 1
@@ -924,75 +959,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the units that were cut: a CTA takes 32 rows of the unit that
+// Joins the pieces of the units that were cut: a CTA takes 32 rows of the units that
 // worker blockIdx.x began, a warp four of them, whose pieces are read together.
 constexpr int kJoinRows = 32;
 template <int D>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p, int workers) {
-  __shared__ int list[kChunkWorkers + 1], count[8], last;
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ int list[kChunkWorkers * kChunkPhases], count[8], last;
   griddep_wait();
   griddep_launch_dependents();
-  const WorkerRecord* recs = reinterpret_cast<const WorkerRecord*>(p.records);
-  const int w = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const WorkerRecord head = recs[w];
-  int cont = 0, ends = 0;
-  if (tid > w && tid < workers) {
-    cont = recs[tid].cont;
-    ends = recs[tid].ends;
-  }
-  if (!head.head) return;
-  if (tid == 0) {
-    last = workers - 1;
-    list[0] = 2 * w + 1;
-  }
-  __syncthreads();
-  if (cont && ends) atomicMin(&last, tid);
-  __syncthreads();
-  cont = cont && tid <= last;
-  const unsigned votes = __ballot_sync(0xffffffffu, cont);
-  if (lane == 0) count[warp] = __popc(votes);
-  __syncthreads();
-  int parts = 1;
-  for (int j = 0; j < 8; ++j) {
-    if (j == warp && cont) list[parts + __popc(votes & ((1u << lane) - 1))] = 2 * tid;
-    parts += count[j];
-  }
-  __syncthreads();
-  // a warp's four rows, eight lanes to each; a lane has 4 columns of every 32
-  constexpr int COLS = D / 32;
-  const int row = blockIdx.y * kJoinRows + warp * 4 + lane / 8, rt = row % 128, t = rt / p.G;
-  const int token = row / 128 * p.tokens + t;
-  if (row >= p.slot_rows || t >= p.tokens || token >= head.tokens) return;
-  float m = -INFINITY, l = 0.f, acc[COLS][4] = {};
-#pragma unroll 2
-  for (int part = 0; part < parts; ++part) {
-    const size_t at = static_cast<size_t>(list[part]) * p.slot_rows + row;
-    const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
-    float4 v[COLS];
-#pragma unroll
-    for (int i = 0; i < COLS; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + i * 8 + lane % 8);
-    const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), b = ex2(y.x - ref);
-    l = l * a + y.y * b;
-#pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-      acc[i][0] = fmaf(v[i].x, b, acc[i][0] * a);
-      acc[i][1] = fmaf(v[i].y, b, acc[i][1] * a);
-      acc[i][2] = fmaf(v[i].z, b, acc[i][2] * a);
-      acc[i][3] = fmaf(v[i].w, b, acc[i][3] * a);
+  const RangeRecord* recs = reinterpret_cast<const RangeRecord*>(p.records);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int ranges = kChunkWorkers * p.phases, mine = blockIdx.x + lane * kChunkWorkers;
+  unsigned heads = __ballot_sync(0xffffffffu, mine < ranges && recs[mine].head);  // of its ranges
+#pragma unroll 1
+  for (; heads != 0; heads &= heads - 1) {
+    const int w = blockIdx.x + (__ffs(heads) - 1) * kChunkWorkers;
+    const RangeRecord head = recs[w];
+    if (tid == 0) {
+      last = INT_MAX;
+      list[0] = 2 * w + 1;
     }
-    m = mn;
-  }
-  const bool any = m > -INFINITY;
-  const float inv = any ? 1.f / l : 0.f;
-  const int qh = head.kvh * p.G + rt - t * p.G;
-  uint16_t* dst = p.out + static_cast<int64_t>(head.token0 + token) * p.ld_out + qh * D + lane % 8 * 4;
+    int parts = 1;
+    // the ranges that continue the unit, in order, up to the one that ends it
+#pragma unroll 1
+    for (int base = w + 1; base < ranges; base += 256) {
+      const int v = base + tid;
+      bool cont = v < ranges && recs[v].cont;
+      const bool ends = cont && recs[v].ends;
+      __syncthreads();
+      if (ends) atomicMin(&last, v);
+      __syncthreads();
+      cont = cont && v <= last;
+      const unsigned votes = __ballot_sync(0xffffffffu, cont);
+      if (lane == 0) count[warp] = __popc(votes);
+      __syncthreads();
+      for (int j = 0; j < 8; ++j) {
+        if (j == warp && cont) list[parts + __popc(votes & ((1u << lane) - 1))] = 2 * v;
+        parts += count[j];
+      }
+      if (last != INT_MAX) break;
+    }
+    __syncthreads();
+    // a warp's four rows, eight lanes to each; a lane has 4 columns of every 32
+    constexpr int COLS = D / 32;
+    const int row = blockIdx.y * kJoinRows + warp * 4 + lane / 8, rt = row % 128, t = rt / p.G;
+    const int token = row / 128 * p.tokens + t;
+    if (row < p.slot_rows && t < p.tokens && token < head.tokens) {
+      float m = -INFINITY, l = 0.f, acc[COLS][4] = {};
+#pragma unroll 2
+      for (int part = 0; part < parts; ++part) {
+        const size_t at = static_cast<size_t>(list[part]) * p.slot_rows + row;
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at);
+        float4 v[COLS];
 #pragma unroll
-  for (int i = 0; i < COLS; ++i)
-    *reinterpret_cast<uint2*>(dst + i * 32) =
-        make_uint2(bf16x2(acc[i][0] * inv, acc[i][1] * inv), bf16x2(acc[i][2] * inv, acc[i][3] * inv));
-  if (p.lse != nullptr && lane % 8 == 0)
-    p.lse[static_cast<int64_t>(head.token0 + token) * p.hq + qh] =
-        any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+        for (int i = 0; i < COLS; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + i * 8 + lane % 8);
+        const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), b = ex2(y.x - ref);
+        l = l * a + y.y * b;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) {
+          acc[i][0] = fmaf(v[i].x, b, acc[i][0] * a);
+          acc[i][1] = fmaf(v[i].y, b, acc[i][1] * a);
+          acc[i][2] = fmaf(v[i].z, b, acc[i][2] * a);
+          acc[i][3] = fmaf(v[i].w, b, acc[i][3] * a);
+        }
+        m = mn;
+      }
+      const bool any = m > -INFINITY;
+      const float inv = any ? 1.f / l : 0.f;
+      const int qh = head.kvh * p.G + rt - t * p.G;
+      uint16_t* dst = p.out + static_cast<int64_t>(head.token0 + token) * p.ld_out + qh * D + lane % 8 * 4;
+#pragma unroll
+      for (int i = 0; i < COLS; ++i)
+        *reinterpret_cast<uint2*>(dst + i * 32) =
+            make_uint2(bf16x2(acc[i][0] * inv, acc[i][1] * inv), bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+      if (p.lse != nullptr && lane % 8 == 0)
+        p.lse[static_cast<int64_t>(head.token0 + token) * p.hq + qh] =
+            any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+    }
+    __syncthreads();
+  }
 }
 
 template <int D>
@@ -1028,7 +1073,7 @@ cudaError_t launch(const ChunkParams& p, const CUtensorMap& kv_map, const CUtens
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, p, kChunkWorkers);
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, p);
 }
 
 }  // namespace

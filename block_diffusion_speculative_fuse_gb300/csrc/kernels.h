@@ -340,6 +340,7 @@ cudaError_t score_tokens_launch(const ScoreParams& p, bool half, cudaStream_t s)
 
 // Chunk attention (attention_chunk.cu).
 constexpr int kChunkWorkers = 152;  // one CTA per SM
+constexpr int kChunkPhases = 8;     // rounds in which they take the work
 struct ChunkParams {
   const int32_t *row_start, *ctx_len, *page_table;
   int batch, T, hq, hkv, G;
@@ -351,8 +352,10 @@ struct ChunkParams {
   int wide;                    // out's rows start at multiples of 32 bytes
   float* lse;                  // [T][hq] or null
   int slot_rows;               // of a partial
-  float *part_o, *part_ml;     // [2 * workers][slot_rows][d], [..][2]
-  void* records;               // [workers], 32 bytes each
+  int phases;                  // allowed
+  int halves;                  // d / 64
+  float *part_o, *part_ml;     // [2 * workers * phases][slot_rows][d], [..][2]
+  void* records;               // [workers * phases], 32 bytes each
   int fused;                   // units have one tile; the last of a unit's pieces joins them (counters
                                // of batch * hkv units 256 bytes behind the status word, left at 0)
   int* status;

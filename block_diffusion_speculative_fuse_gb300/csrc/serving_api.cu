@@ -105,8 +105,9 @@ size_t layout_chunk(ChunkParams* p, int d, uint8_t* base) {
     off = al256(off + bytes);
     return q;
   };
-  const size_t rows = 2 * static_cast<size_t>(kChunkWorkers) * p->slot_rows;
-  p->records = take(kChunkWorkers * 32);
+  const size_t ranges = kChunkWorkers * static_cast<size_t>(p->phases);
+  const size_t rows = 2 * ranges * p->slot_rows;
+  p->records = take(ranges * 32);
   p->part_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
   p->part_o = reinterpret_cast<float*>(take(rows * d * sizeof(float)));
   return off;
@@ -122,6 +123,10 @@ bool chunk_sizes(const dflash_heads* h, int32_t batch, int32_t T, ChunkParams* p
   p->G = p->hq / p->hkv;
   p->tokens = 128 / p->G;
   p->slot_rows = T <= p->tokens ? T * p->G : 256;
+  // few rows read the keys few times again, and need no workspace for many phases
+  p->phases = 1;
+  while (p->phases < kChunkPhases && p->phases * 8 * p->tokens <= T) p->phases *= 2;
+  p->halves = h->head_dim / 64;
   return true;
 }
 

@@ -461,7 +461,9 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
  * Scores, softmax statistics and accumulators are fp32; probabilities are
  * rounded to bf16 for the product with V.  Deterministic.
  * ws: initialised, dflash_attention_chunk_bytes(heads, batch, T) bytes (0:
- * unsupported sizes); a workspace for larger T serves smaller calls. */
+ * unsupported sizes); a workspace for larger T serves smaller calls.  At most
+ * 41 MB for calls of at most 8 tiles of 128 rows per KV head, 324 MB from 32
+ * tiles on (partial results of the rounds in which long contexts are read). */
 size_t dflash_attention_chunk_bytes(const dflash_heads* heads, int32_t batch, int32_t T);
 int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,
                            const int32_t* row_start, int32_t batch, int32_t T, int32_t causal,
