@@ -20,10 +20,10 @@
 //
 // Rows are a CTA each, two CTAs to an SM; fewer rows than that are cut over clusters.
 //
-// Bound: 2048 fp32 rows of 151936 the loads: 199 us without alternatives, 6.25 TB/s, 223
+// Bound: 2048 fp32 rows of 151936 the loads: 197 us without alternatives, 6.3 TB/s, 221
 // with five: the phases behind a row's pass take its SM 4 us, in which only the other
-// CTA's loads are in flight.  bf16 rows instruction issue, 164 us, 3.8 TB/s.  One row
-// (a cluster of 8) 11.4 us, the latency of five phases.
+// CTA's loads are in flight.  bf16 rows instruction issue, 162 us, 3.8 TB/s.  One row
+// (a cluster of 8) 10.8 us, the latency of five phases.
 #include <cfloat>
 #include <climits>
 

@@ -489,11 +489,12 @@ int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* s
   if (!rc) rc = check_cache(heads, layer, dst);
   if (rc) return rc;
   if (ctx_len == nullptr || keep == nullptr || mass == nullptr || kept == nullptr || batch < 1 || sink < 0 ||
-      recent < 0 || ld_mass < 1 || ld_kept < 1 || mass_out == mass || new_len == ctx_len || new_len == keep || !aligned(ctx_len, 4) || !aligned(keep, 4) ||
-      !aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_len, 4) || !aligned(mass_out, 4) ||
+      recent < 0 || ld_mass < 1 || ld_kept < 1 || mass_out == mass || new_len == ctx_len || new_len == keep ||
+      !aligned(ctx_len, 4) || !aligned(keep, 4) || !aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_len, 4) || !aligned(mass_out, 4) ||
       src->dtype != dst->dtype)
     return DFLASH_ERR_INVALID_ARG;
-  if (batch > 65535 || static_cast<int64_t>(batch) * heads->n_kv_heads > (1 << 26) || ld_mass > (1 << 30) || ld_kept > (1 << 30))
+  if (batch > 65535 || static_cast<int64_t>(batch) * heads->n_kv_heads > (1 << 26) || ld_mass > (1 << 30) ||
+      ld_kept > (1 << 30))
     return DFLASH_ERR_UNSUPPORTED;
   if (batch > src->n_rows || batch > dst->n_rows) return DFLASH_ERR_CAPACITY;
   const int elem = src->dtype == 1 ? 1 : 2, d = heads->head_dim;
