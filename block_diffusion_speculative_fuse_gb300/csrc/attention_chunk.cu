@@ -535,22 +535,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             vb = c / 4;
             vg = kg;
           }
-          const int grp = __shfl_sync(0xffffffffu, is_k ? kg : vg, (c % 4) * 8 + lane % 8);
+          const int grp = is_k || vg == oob_group ? (is_k ? kg : vg) : vg + p.hkv * 2;
+          int y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, grp, (c % 4) * 8 + i);
           const int st = cur.slot;
-          int go = 1;
-          if (lane == 0) {
-            if (at >= SLOTS && !mbar_wait(&empty[st], cur.parity ^ 1, abort_flag)) go = 0;
-            if (go && j == 0 && segs > 0 && !mbar_wait(q_free, (segs - 1) & 1, abort_flag)) go = 0;
-            if (go) mbar_arrive_expect_tx(&full[st], C::PLANE);
-          }
-          if (!__shfl_sync(0xffffffffu, go, 0)) {
+          bool go = mbar_wait(&empty[st], cur.parity ^ 1, abort_flag);   // (the first SLOTS pass)
+          if (j == 0 && segs > 0) go = go && mbar_wait(q_free, (segs - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, go)) {
             give_up(554);
             break;
           }
-          if (lane < 8) {
-            const int y = grp == oob_group || is_k ? grp : grp + p.hkv * 2;
-            tma_load_4d(smem_u32(ring + st * C::PLANE + lane * C::PAGE), &kv_map, y, &full[st], pol);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[st], C::PLANE);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              tma_load_4d(smem_u32(ring + st * C::PLANE + i * C::PAGE), &kv_map, y[i], &full[st], pol);
           }
+          __syncwarp();
           if (j == 0) {  // Q of the piece: [tile][column half], `tokens` rows of G heads each
             if (lane == 0) {
               const int boxes = (pc.split ? 1 : 2) * C::HALVES;
