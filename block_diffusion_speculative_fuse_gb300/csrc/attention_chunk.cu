@@ -60,8 +60,7 @@ constexpr float kRaise = 8.f;     // log2
 constexpr int kPieces = 4;        // planned ahead
 // Costs are counted in 64 keys that one tile of 128 rows goes over (32 bits).
 constexpr int kUnitCost = 10;     // a unit's start and end
-constexpr int kSplitCost = 4;     // of a chunk with one tile: as much as with two, since the
-                                  // loads bound it (2, 3, 4: a mixed batch 384, 304, 288 us)
+constexpr int kSplitCost = 3;     // of a chunk with one tile (2, 3, 4: a mixed batch 238, 235, 254 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
 // Keys that several row units read should stay in L2 from one unit to the next.  Where those
 // of all requests do not fit, the workers take the work in rounds (phases), each of fewer

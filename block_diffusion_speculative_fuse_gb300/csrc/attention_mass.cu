@@ -271,11 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u.load) load_q(u.t0);
 #pragma unroll 1
         for (int k = 0; ok && k < planes; ++k) {
-          const int st = cur.slot, y = grp[k * 8 + lane % 8];
+          const int st = cur.slot;
+          int y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = grp[k * 8 + i];
           if (at >= SLOTS && !wait(&k_free[st], cur.parity ^ 1, 565)) break;
-          if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::PLANE);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&k_full[st], C::PLANE);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              tma_load_4d(smem_u32(ring + st * C::PLANE + i * C::PAGE), &kv_map, y[i], &k_full[st], pol_k);
+          }
           __syncwarp();
-          if (lane < 8) tma_load_4d(smem_u32(ring + st * C::PLANE + lane * C::PAGE), &kv_map, y, &k_full[st], pol_k);
           ++at;
           cur.advance(SLOTS);
         }
