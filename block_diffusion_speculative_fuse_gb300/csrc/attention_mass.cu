@@ -17,9 +17,10 @@
 // and plane one D, in two stages each, which the plane's four warps sum up.
 //
 // Bound: with the usual window of rows (32 rows of 4 heads, one tile) K's bytes: 8
-// requests of 16384 keys 50 us, 5.5 TB/s with 6 us of start-up, 32 of them 182 us, 6.0
-// TB/s; 8 rows take as long as 32.  With many tiles Q's traffic from L2, each tile again
-// for every 256 keys: 512 rows of 8 requests of 16848 keys 624 us, 0.89 PFLOP/s.
+// requests of 16384 keys 46 us, 6.0 TB/s with 6 us of start-up, 32 of them 164 us, 6.7
+// TB/s; 8 rows take as long as 32.  With many tiles the exponentials and Q's traffic
+// from L2, each tile again for every 256 keys: 512 rows of 8 requests of 16848 keys 480 us,
+// 1.16 PFLOP/s.
 #include <climits>
 
 #include "attention_chunk.cuh"
@@ -412,23 +413,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = __all_sync(0xffffffffu, c0 == 0);
         const float2 sc = make_float2(p.scale_log2, p.scale_log2);
         const float4* ls = reinterpret_cast<const float4*>(lse_s + qc.slot * 128);
+        // Whole groups of 32 columns have no tests: as selects in the same loop they cost as
+        // much again as the sums (8 x 16384 keys 50 us instead of 46, all of 512 rows 621
+        // instead of 480).
+        int c = 0;
+        if (whole) {
 #pragma unroll 1
-        for (int c = 0; c < c1; c += 32) {
-          uint32_t x[32];
-          tmem_ld32_nowait(d_addr + stage * 128 + c, x);
-          tmem_wait_ld(x);
+          for (; c + 32 <= c1; c += 32) {
+            uint32_t x[32];
+            tmem_ld32_nowait(d_addr + stage * 128 + c, x);
+            tmem_wait_ld(x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 l4 = ls[c / 4 + j];
-            float2 s0 = fma2(make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), sc, make_float2(l4.x, l4.y));
-            float2 s1 = fma2(make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), sc, make_float2(l4.z, l4.w));
-            if (!whole || c + 32 > c1) {
-              auto seen = [&](int i, float v) { return c + 4 * j + i >= c0 && c + 4 * j + i < c1 ? v : -INFINITY; };
-              s0 = make_float2(seen(0, s0.x), seen(1, s0.y));
-              s1 = make_float2(seen(2, s1.x), seen(3, s1.y));
+            for (int j = 0; j < 8; ++j) {
+              const float4 l4 = ls[c / 4 + j];
+              const float2 s0 = fma2(make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), sc, make_float2(l4.x, l4.y));
+              const float2 s1 = fma2(make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), sc, make_float2(l4.z, l4.w));
+              a0 = add2(a0, make_float2(ex2(s0.x), ex2(s0.y)));
+              a1 = add2(a1, make_float2(ex2(s1.x), ex2(s1.y)));
             }
-            a0 = add2(a0, make_float2(ex2(s0.x), ex2(s0.y)));
-            a1 = add2(a1, make_float2(ex2(s1.x), ex2(s1.y)));
+          }
+        }
+#pragma unroll 1
+        for (; c < c1; c += 16) {
+          uint32_t x[16];
+          tmem_ld16_raw(d_addr + stage * 128 + c, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 l4 = ls[c / 4 + j];
+            const float2 s0 = fma2(make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), sc, make_float2(l4.x, l4.y));
+            const float2 s1 = fma2(make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), sc, make_float2(l4.z, l4.w));
+            auto seen = [&](int i, float v) { return c + 4 * j + i >= c0 && c + 4 * j + i < c1 ? ex2(v) : 0.f; };
+            a0 = add2(a0, make_float2(seen(0, s0.x), seen(1, s0.y)));
+            a1 = add2(a1, make_float2(seen(2, s1.x), seen(3, s1.y)));
           }
         }
         tc_fence_before();
