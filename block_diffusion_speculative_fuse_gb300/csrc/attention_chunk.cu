@@ -31,15 +31,17 @@
 // zeros past the last row's keys, and for what is not finite (the rows that do
 // see it get a NaN by way of l).
 //
-// Bound: with whole units the tensor pipe.  4096 rows of 32 heads behind 12288 keys: 1.64
-// PFLOP/s, 0.86 of the GEMM rate, 0.59 ms; behind 28672 (134 MB of keys, more than L2)
-// 1.29 ms, 1.60 PFLOP/s, in two rounds; behind 126976 5.41 ms, 1.60 PFLOP/s, in eight.  A chunk of both tiles takes 3050 cycles: its products
-// 2048 of the tensor pipe and, at 128 bytes a cycle, 2048 of shared memory (S reads Q and K,
-// P V reads V, the loads write both); a tile's softmax 1100 under the other's products.  For short
-// prompts the units' ends: 8 x 1024 rows take 85 us, 54 of them chunks.  For single tokens
-// the keys' bytes: 32 requests of 3000 to 6200 keys 109 us, 6.1 TB/s; one request of 4096
-// keys 16 us, of which the keys' bytes are 2.5: plan, first loads and join are chains of
-// loads, and code that is not yet in the instruction cache.
+// Bound: with whole units the products and their issue.  4096 rows of 32 heads behind 28672
+// keys (134 MB, more than L2) 1.20 ms, 1.70 PFLOP/s, 0.90 of the GEMM rate, in two rounds;
+// behind 126976 5.15 ms, 1.68 PFLOP/s, in eight.  A chunk of both tiles takes some 2800
+// cycles: its products 2048 of the tensor pipe and, at 128 bytes a cycle, 2048 of shared memory (S
+// reads Q and K, P V reads V, the loads write both); a tile's softmax 1100 under the other's
+// products.  For short prompts the units' ends: 8 x 1024 rows take 82 us, 52 of them chunks.  For
+// single tokens the keys' bytes: 32 requests of 3000 to 6200 keys 106 us, 6.2 TB/s; one
+// request of 4096 keys 16 us, of which the keys' bytes are 2.5: plan, first loads and join are
+// chains of loads, and code that is not yet in the instruction cache.  Beside whole units a CTA
+// with single tokens takes three quarters of a two-tile chunk's time for each of its
+// chunks, by the instructions of the warp that multiplies.
 //
 // That cache decides more than arithmetic here.  All roles' code together has to stay
 // in it: with the polls of 20 waits unrolled (172 KB of instructions instead of 77) a
@@ -65,8 +67,9 @@ constexpr int kWorkerCost = 8;    // the least share of a worker
 // Keys that several row units read should stay in L2 from one unit to the next.  Where those
 // of all requests do not fit, the workers take the work in rounds (phases), each of fewer
 // heads or requests: the units that run at a time then read the same keys.  One round against
-// up to 8: 4096 rows behind 28672 keys 1.37 -> 1.29 ms, behind 126976 keys 6.24 -> 5.41, 8 x 2048
-// rows behind 15000 3.24 -> 2.88, 1000 rows behind 131072 1.59 -> 1.39.
+// up to 8 (before the loads were quicker, which gave both 5 %): 4096 rows behind 28672 keys 1.37 ->
+// 1.29 ms, behind 126976 keys 6.24 -> 5.41, 8 x 2048 rows behind 15000 3.24 -> 2.88, 1000 rows
+// behind 131072 1.59 -> 1.39.
 constexpr int kResident = 5760;   // in 64 keys of one head of 64: 90 MB
 constexpr int kPhaseCost = 400;   // the least share of a worker in a phase (100, 200, 400: no difference)
 constexpr int kLeast = 3;         // chunks of a piece of a unit (2, 3, 4: 8 prompts of 1024 rows 88,
@@ -545,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             give_up(554);
             break;
           }
+          // (eight lanes with a load each take turns, and longer: 1300 cycles a plane, not 700)
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[st], C::PLANE);
 #pragma unroll
