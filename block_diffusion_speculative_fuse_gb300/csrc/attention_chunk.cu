@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;            // [2][2] P of a tile is in TMEM: of each 64 keys the first 32, the others
   uint64_t* q_full = p_full + 4;            // Q of the piece is in shared memory
   uint64_t* q_free = q_full + 1;            // its last S is complete
-  uint64_t* o_full = q_free + 1;            // all of the piece's products are complete; bad
+  uint64_t* o_full = q_free + 1;            // all of the piece's products are complete, bad is written
   uint64_t* piece_full = o_full + 1;        // [kPieces]
   uint64_t* piece_free = piece_full + kPieces;
   Piece* pieces = reinterpret_cast<Piece*>(piece_free + kPieces);  // [kPieces]
@@ -664,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; ok && c < n; ++c) {
           const int t = pc.split ? c & 1 : 0;
           const bool more = c + lead < n && (!pc.split || n > 1);
-          const int iv = take(c >= clean0);
+          // (the last one in any case: what the value warp found in the piece is then written
+          // down before its last product, whose completion is what the softmax waits for)
+          const int iv = take(c >= clean0 || c + 1 == n);
           ok = iv >= 0 && issue_pv(t, iv, pc.split ? c >= 2 : c > 0);
           if (!ok) break;
           if (pc.split) commit(&empty[iv]);
