@@ -187,8 +187,12 @@ class PagedKV:
     def evict_to(self, other, layer: int, ctx_len, keep, mass, kept, ws, sink=0, recent=0, new_len=None,
                  mass_out=None, stream=None):
         """Move the keep[r] positions of largest mass of each request and KV head, in order,
-        to positions 0, 1, ... of the cache `other` (dflash_kv_evict); ws from its
-        evict_workspace."""
+        to positions 0, 1, ... of the cache `other` (dflash_kv_evict), which has this one's
+        layers, planes, heads and dtype; ws from its evict_workspace."""
+        mine, theirs = self.pool.shape, other.pool.shape
+        if self.dtype != other.dtype or mine[0] != theirs[0] or mine[2:] != theirs[2:]:
+            raise ValueError(f"caches of {self.dtype} {tuple(mine)} and {other.dtype} {tuple(theirs)}: they may "
+                             "differ in their pages alone")
         B.dflash_kv_evict(self.heads(self.pool.shape[3]), layer, self.struct, other.struct,
                           ctx_len.shape[0], ctx_len, keep, sink, recent, mass, kept, new_len, mass_out, ws,
                           stream)

@@ -1,0 +1,42 @@
+"""Operators of a long prompt without a GPU: refusals and bounds found by reading."""
+import ctypes
+from types import SimpleNamespace
+
+import numpy as np
+import pytest
+import torch
+
+from block_diffusion_speculative_fuse_gb300 import _build, binding as B
+from block_diffusion_speculative_fuse_gb300.device import PagedKV
+from test_prompt_abi_cpu import chunk, evict, mass
+from test_serving_abi_cpu import cache, heads
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return B.load()
+
+
+# ------------------------------------------------- eviction between two caches
+def paged(n_pages=4, dtype="bf16", **kw):
+    shape = dict(n_layers=2, n_kv_heads=2, head_dim=64, kv_terms=1)
+    shape.update(kw)
+    return PagedKV(SimpleNamespace(**shape), np.zeros((2, 2), np.int32), n_pages, device="cpu", dtype=dtype)
+
+
+def test_evict_to_refuses_caches_of_another_geometry(monkeypatch):
+    """The call has one geometry for both caches: a second one would be written by the first's
+    strides."""
+    calls = []
+    monkeypatch.setattr(B, "dflash_kv_evict", lambda *a: calls.append(a))
+    i, m = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 2, 32)
+    for src, dst in ((dict(), dict(n_layers=1)), (dict(), dict(n_layers=3)), (dict(kv_terms=2), dict()),
+                     (dict(), dict(kv_terms=2)), (dict(), dict(n_kv_heads=1)), (dict(), dict(head_dim=128)),
+                     (dict(head_dim=128), dict()), (dict(), dict(dtype="e4m3")), (dict(dtype="e4m3"), dict())):
+        with pytest.raises(ValueError):
+            paged(**src).evict_to(paged(**dst), 0, i, i, m, i, None)
+    assert not calls
+    for kw in (dict(), dict(kv_terms=2), dict(dtype="e4m3")):     # another number of pages is another cache's right
+        paged(**kw).evict_to(paged(n_pages=9, **kw), 1, i, i, m, i, None)
+    assert len(calls) == 3
