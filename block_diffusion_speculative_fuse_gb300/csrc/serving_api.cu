@@ -476,7 +476,7 @@ int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* 
 }
 
 size_t dflash_kv_evict_bytes(const dflash_heads* heads, int32_t batch, int32_t dst_pages) {
-  if (check_heads(heads) || batch < 1 || batch > 65535 || dst_pages < 1) return 0;
+  if (check_heads(heads) || heads->n_kv_heads > 65535 || batch < 1 || batch > 65535 || dst_pages < 1) return 0;
   return kHeaderBytes + 256 + al256(static_cast<size_t>(dst_pages) * 4);
 }
 
@@ -493,8 +493,9 @@ int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* s
       !aligned(ctx_len, 4) || !aligned(keep, 4) || !aligned(mass, 4) || !aligned(kept, 4) || !aligned(new_len, 4) || !aligned(mass_out, 4) ||
       src->dtype != dst->dtype)
     return DFLASH_ERR_INVALID_ARG;
-  if (batch > 65535 || static_cast<int64_t>(batch) * heads->n_kv_heads > (1 << 26) || ld_mass > (1 << 30) ||
-      ld_kept > (1 << 30))
+  // (heads and requests are rows and layers of the copy's grid)
+  if (batch > 65535 || heads->n_kv_heads > 65535 ||
+      static_cast<int64_t>(batch) * heads->n_kv_heads > (1 << 26) || ld_mass > (1 << 30) || ld_kept > (1 << 30))
     return DFLASH_ERR_UNSUPPORTED;
   if (batch > src->n_rows || batch > dst->n_rows) return DFLASH_ERR_CAPACITY;
   const int elem = src->dtype == 1 ? 1 : 2, d = heads->head_dim;

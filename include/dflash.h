@@ -549,8 +549,9 @@ int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* 
  * ld_mass (site 581) and a keep beyond dst's table or ld_kept (site 582), which
  * count as those; a page id out of range, of dst (site 583: its positions are
  * dropped) or of src (site 585: they read as zeros).
- * batch <= 65535 and <= n_rows of both, batch * n_kv_heads <= 2^26.  Outputs
- * overlap no inputs (new_len is neither ctx_len nor keep, mass_out not mass).
+ * batch <= 65535 and <= n_rows of both, n_kv_heads <= 65535, batch *
+ * n_kv_heads <= 2^26.  Outputs overlap no inputs (new_len is neither ctx_len
+ * nor keep, mass_out not mass).
  * ws: initialised, dflash_kv_evict_bytes(heads, batch, dst->n_pages) bytes. */
 size_t dflash_kv_evict_bytes(const dflash_heads* heads, int32_t batch, int32_t dst_pages);
 int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* src,

@@ -40,3 +40,13 @@ def test_evict_to_refuses_caches_of_another_geometry(monkeypatch):
     for kw in (dict(), dict(kv_terms=2), dict(dtype="e4m3")):     # another number of pages is another cache's right
         paged(**kw).evict_to(paged(n_pages=9, **kw), 1, i, i, m, i, None)
     assert len(calls) == 3
+
+
+def test_evict_refuses_more_heads_than_a_grid_has_rows(lib):
+    """An error launches nothing: one head more than the copy's grid takes is refused before the
+    choice has written its outputs.  (4-byte outputs at their addresses; nothing is read.)"""
+    many = dict(n_q_heads=65536, n_kv_heads=65536)
+    assert evict(lib, hd=heads(**many), dst=cache(pool=1 << 40)) == -2
+    assert evict(lib, hd=heads(n_q_heads=65535, n_kv_heads=65535), dst=cache(pool=1 << 40), size=0) == -3  # (goes on to the workspace)
+    hd = heads(**many)
+    assert lib.dflash_kv_evict_bytes(ctypes.byref(hd), 4, 8) == 0
