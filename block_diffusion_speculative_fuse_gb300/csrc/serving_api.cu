@@ -501,10 +501,14 @@ int dflash_kv_evict(const dflash_heads* heads, int32_t layer, const dflash_kv* s
   const int elem = src->dtype == 1 ? 1 : 2, d = heads->head_dim;
   const size_t src_layer = layer_elems(heads, src) * elem, dst_layer = layer_elems(heads, dst) * elem;
   // two caches are the same pool or apart
-  const auto a = reinterpret_cast<uintptr_t>(src->pool), b = reinterpret_cast<uintptr_t>(dst->pool);
-  const bool same = a == b;
+  const bool same = src->pool == dst->pool;
+  auto meet = [&](const void* x, size_t x_layer, const void* y, size_t y_layer) {
+    const auto a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return a < b + y_layer * heads->n_layers && b < a + x_layer * heads->n_layers;
+  };
   if (same ? src->n_pages != dst->n_pages || src->scales != dst->scales
-           : a < b + dst_layer * heads->n_layers && b < a + src_layer * heads->n_layers)
+           : meet(src->pool, src_layer, dst->pool, dst_layer) ||
+                 (elem == 1 && meet(src->scales, src_layer / d * 4, dst->scales, dst_layer / d * 4)))
     return DFLASH_ERR_INVALID_ARG;
   rc = check_ws(ws, ws_bytes, dflash_kv_evict_bytes(heads, batch, dst->n_pages));
   if (rc) return rc;

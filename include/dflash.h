@@ -542,7 +542,8 @@ int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* 
  * behind it.  ctx_len, keep on the device; mass fp32 [batch][n_kv_heads]
  * [ld_mass].  One layer of caches of one dtype (bf16 with one or two terms, or
  * E4M3 with its scales), vectors copied bit for bit.  dst may be other pages
- * of src's pool (same pool, n_pages and scales), or a pool apart from it.
+ * of src's pool (same pool, n_pages and scales), or a pool (and scales) apart
+ * from it.
  * A page that rows of dst name twice within new_len, or that a kept request of
  * the call reads, is recorded as DFLASH_ERR_INVALID_ARG (site 584) and nothing
  * is copied.  Recorded as DFLASH_ERR_CAPACITY: a ctx_len beyond src's table or

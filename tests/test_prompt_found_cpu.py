@@ -44,9 +44,19 @@ def test_evict_to_refuses_caches_of_another_geometry(monkeypatch):
 
 def test_evict_refuses_more_heads_than_a_grid_has_rows(lib):
     """An error launches nothing: one head more than the copy's grid takes is refused before the
-    choice has written its outputs.  (4-byte outputs at their addresses; nothing is read.)"""
+    choice has written its outputs."""
     many = dict(n_q_heads=65536, n_kv_heads=65536)
     assert evict(lib, hd=heads(**many), dst=cache(pool=1 << 40)) == -2
-    assert evict(lib, hd=heads(n_q_heads=65535, n_kv_heads=65535), dst=cache(pool=1 << 40), size=0) == -3  # (goes on to the workspace)
+    assert evict(lib, hd=heads(n_q_heads=65535, n_kv_heads=65535), dst=cache(pool=1 << 40), size=0) == -3
     hd = heads(**many)
     assert lib.dflash_kv_evict_bytes(ctypes.byref(hd), 4, 8) == 0
+
+
+def test_evict_refuses_two_pools_that_share_their_scales(lib):
+    """E4M3 caches apart from each other have scales apart from each other too (2 layers of 8
+    pages, 2 planes, 2 heads and 16 positions: 4096 bytes)."""
+    src = cache(dtype=1, scales=1 << 30)
+    size = 2 * 8 * 2 * 2 * 16 * 4
+    for at, code in (((1 << 30), -1), ((1 << 30) + size - 16, -1), ((1 << 30) - size + 16, -1),
+                     ((1 << 30) + size, -3), ((1 << 30) - size, -3)):
+        assert evict(lib, src=src, dst=cache(pool=1 << 40, dtype=1, scales=at), size=0) == code, at - (1 << 30)
