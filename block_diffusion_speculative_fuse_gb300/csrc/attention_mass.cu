@@ -399,10 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* out = p.mass + (static_cast<int64_t>(u.r) * p.hkv + u.h) * p.ld_mass + key;
       float old = 0.f;
       if (p.accumulate && key < u.ctx) old = *out;
-      float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+      float sum = 0.f, lost = 0.f;   // of the tiles, and what its last rounding added
 #pragma unroll 1
       for (int t = u.t0; t < u.tiles; ++t) {
         const int stage = dn & 1;
+        float2 a0 = make_float2(0.f, 0.f), a1 = a0;
         if (ok && !held) wait(&l_full[qc.slot], qc.parity, 569);
         if (ok) wait(&d_full[plane * 2 + stage], (dn / 2) & 1, 569);
         tc_fence_after();
@@ -450,6 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_free[plane * 2 + stage]);
+        // A tile's weights add up by themselves, the tiles' sums with their roundings carried along
+        // (Kahan): in one running sum a key that 24576 rows of 16 heads see lost 1.2e-3.
+        const float more = (a0.x + a0.y) + (a1.x + a1.y) - lost, next = sum + more;
+        lost = (next - sum) - more;
+        sum = next;
         ++dn;
         const bool keep = u.tiles == 1 && !u.release;
         held = keep;
@@ -458,10 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           qc.advance(kQ);
         }
       }
-      if (key < u.ctx) {
-        const float sum = (a0.x + a0.y) + (a1.x + a1.y);
-        if (u.tiles > 0 || !p.accumulate) *out = old + sum;
-      }
+      if (key < u.ctx && (u.tiles > 0 || !p.accumulate)) *out = old + sum;
       unit_done();
     }
   }

@@ -520,7 +520,7 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
  * its own position's sum undefined, no other's.
  * A bf16 one-term cache; batch <= 1024 and <= kv->n_rows; batch * n_kv_heads *
  * max_pages below 2^34.  Products, exponents and sums are fp32, the sums in a
- * fixed order.  Deterministic.
+ * fixed order and compensated over the rows.  Deterministic.
  * ws: initialised, dflash_attention_mass_bytes(heads, batch, T) bytes. */
 size_t dflash_attention_mass_bytes(const dflash_heads* heads, int32_t batch, int32_t T);
 int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,

@@ -32,3 +32,30 @@ def test_chunk_pieces_beside_those_whose_v_is_not_finite(d):
         last = torch.tensor([int(s["start"][r]) + 2 for r in range(0, many, 2)], device="cuda")
         assert not torch.isfinite(s["out"][last]).all(-1).any()
         check_chunk(s, 8, d, requests=range(1, many, 2))
+
+
+def test_mass_of_a_key_that_very_many_rows_see():
+    """24576 rows of 16 heads to one: the first half of them gives key 0 about all of their weight,
+    the second half 0.0015 each, less than half a step of the sum that is there by then.
+
+    Tolerance, relative: scores are exact here (one product, scale 1).  The exponent is at most
+    13 (log2 e) from two products rounded to 2^-24 and one sum, its constants to 2^-24: 4 * 19 * 2^-24
+    ln 2 < 53 * 2^-24 of the weight, which exp2 rounds by 2^-22 more.  A tile's 128 weights
+    add up over 34 additions at most, the tiles' sums as if once."""
+    B = B_()
+    n, ctx, G, d = 24576, 256, 16, 64
+    c = Cache(1, 1, d, [ctx], spoil=False)
+    c.pool[0, :, 0] = 0.0
+    c.pool[0, c.ids[0][0], 0, 0, 0, 0] = 1.0             # key 0 is e_0, the others none
+    q = torch.zeros(n, G, d, dtype=torch.bfloat16, device="cuda")
+    q[:n // 2, :, 0], q[n // 2:, :, 0] = 12.0, -0.9609375
+    lse = torch.log(torch.exp(q[:, :, 0].double()) + ctx - 1).float()
+    mass = torch.zeros(1, 1, ctx, device="cuda")
+    hd = heads(1, G, 1, d)
+    ws = workspace(B.dflash_attention_mass_bytes(hd, 1, n))
+    B.dflash_attention_mass(hd, 0, q, i32([0, n]), 1, n, 0, False, 1.0, c.kv, i32([ctx]), lse, mass, False, ws)
+    assert B.dflash_get_status(ws) == (0, 0)
+    want = torch.exp(-lse.double()).sum().expand(ctx).clone()
+    want[0] = torch.exp(q[:, :, 0].double() - lse.double()).sum()
+    err = ((mass[0, 0].double() - want).abs() / want).max()
+    assert float(err) <= (53 + 4 + 34 + 4) * 2.0 ** -24, float(err) * 2.0 ** 24
