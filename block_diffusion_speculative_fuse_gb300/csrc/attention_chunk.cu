@@ -29,7 +29,7 @@
 // Values that a row must not see.  S is replaced by -inf, and 0 * V must be 0: a warp goes
 // over the planes of V whose keys not all of a unit's rows see, before their product:
 // zeros past the last row's keys, and for what is not finite (the rows that do
-// see it get a NaN by way of l).
+// see it get a NaN by way of O's factor; l, and with it lse, does not depend on V).
 //
 // Bound: with whole units the products and their issue.  4096 rows of 32 heads behind 28672
 // keys (134 MB, more than L2) 1.20 ms, 1.70 PFLOP/s, 0.90 of the GEMM rate, in two rounds;
@@ -846,9 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l += (la.x + la.y) + (lb.x + lb.y);
       }
+      bool spoilt = false;   // the row sees a V that is not finite: its result is NaN, its lse is not
       if (n > 0) {
         if (ok && !__all_sync(0xffffffffu, mbar_wait(o_full, segs & 1, abort_flag))) give_up(557);
-        if (lim + half * 64 > bad[taken % kPieces]) l = __int_as_float(0x7FFFFFFF);
+        spoilt = lim + half * 64 > bad[taken % kPieces];
         ++segs;
         tc_fence_after();
       }
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mn;
       }
       const bool whole = pc.begins && pc.ends;
-      const float inv = whole ? (m == -INFINITY ? 0.f : 1.f / l) : 1.f;
+      const float inv = spoilt ? __int_as_float(0x7FFFFFFF) : whole ? (m == -INFINITY ? 0.f : 1.f / l) : 1.f;
       const float fa = wa * inv, fb = wb * inv;
       const int row0 = pc.split ? 0 : tile * 128;      // the tile's first in the unit
       const size_t slot_row = (2 * static_cast<size_t>(pc.range) + (pc.begins ? 1 : 0)) * p.slot_rows + row0 + r128;

@@ -453,7 +453,8 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
  * Row ranges of one call must not overlap; out must not overlap q.
  * Pages and values that a row does not see never reach it, whatever they hold;
  * q, and K and V of what a row sees, must be finite (else that row, no other,
- * is undefined: a V that is not finite makes the rows that see it NaN).
+ * is undefined: a V that is not finite makes the results of the rows that see
+ * it infinite or NaN and leaves their lse as it is).
  * Row strides are multiples of 8 elements, base pointers 16-byte aligned.
  * batch <= kv->n_rows, T <= 2^30; a call whose work may pass n_kv_heads *
  * (T / 16 + batch) * max_pages = 2^30 is DFLASH_ERR_UNSUPPORTED (some larger

@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_prompt import B_, Cache, PAGE, built, check_chunk, chunk_case, heads, i32, workspace  # noqa: F401
+from test_gpu_prompt import (PAGE, B_, Cache, built, check_chunk, chunk_case, heads, i32, mass_case,  # noqa: F401
+                             workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +60,28 @@ def test_mass_of_a_key_that_very_many_rows_see():
     want[0] = torch.exp(q[:, :, 0].double() - lse.double()).sum()
     err = ((mass[0, 0].double() - want).abs() / want).max()
     assert float(err) <= (53 + 4 + 34 + 4) * 2.0 ** -24, float(err) * 2.0 ** 24
+
+
+@pytest.mark.parametrize("ns,ctx,hq,hkv,d", [([5, 40, 3], [165, 300, 30], 8, 2, 64), ([300], [300], 2, 2, 128),
+                                             ([33, 1], [4000, 2500], 4, 1, 128), ([1], [3001], 8, 1, 64)])
+def test_lse_and_masses_do_not_depend_on_v(ns, ctx, hq, hkv, d):
+    """A V that is not finite makes the rows that see it NaN and leaves their lse, and all
+    masses, as they are, wherever the position is."""
+    B = B_()
+    s = mass_case(ns, ctx, hq, hkv, d, seed=4)
+    lse, mass = s["lse"].clone(), s["mass"].clone()
+    for r, (n, m) in enumerate(zip(ns, ctx)):
+        for pos in sorted({m - n // 2 - 1, m - 1, m // 3}):
+            page, slot = divmod(pos, PAGE)
+            at = s["c"].pool[0, s["c"].ids[r][page], 1, :, slot]
+            before = at.clone()
+            at.fill_(math.nan if pos % 2 else math.inf)
+            s["out"].fill_(7.0)
+            B.dflash_attention_chunk(*s["args"])
+            B.dflash_attention_mass(*s["mass_args"])
+            a = int(s["start"][r])
+            first = max(0, pos - (m - n))               # the first row that sees it
+            assert not torch.isfinite(s["out"][a + first:a + n]).any(), (r, pos)
+            assert torch.isfinite(s["out"][a:a + first]).all(), (r, pos)
+            assert torch.equal(s["lse"], lse) and torch.equal(s["mass"], mass), (r, pos)
+            at.copy_(before)
