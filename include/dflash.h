@@ -517,8 +517,10 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
  * [ld_mass].  A request without rows gets sums of 0 (unchanged when
  * accumulating).  Bad row ranges, lengths and pages are treated and recorded
  * as there (sites 561, 562, 563); a ctx_len above ld_mass is recorded (site
- * 564) and the positions beyond are dropped.  A K that is not finite makes
- * its own position's sum undefined, no other's.
+ * 564) and the positions beyond are dropped.  By finite lse a K that is not
+ * finite makes its own position's sum undefined, no other's.  The lse that
+ * dflash_attention_chunk leaves for a row that sees such a K is undefined, and
+ * makes so the sums of all positions that this row sees, in its KV head.
  * A bf16 one-term cache; batch <= 1024 and <= kv->n_rows; batch * n_kv_heads *
  * max_pages below 2^34.  Products, exponents and sums are fp32, the sums in a
  * fixed order and compensated over the rows.  Deterministic.

@@ -85,3 +85,26 @@ def test_lse_and_masses_do_not_depend_on_v(ns, ctx, hq, hkv, d):
             assert torch.isfinite(s["out"][a:a + first]).all(), (r, pos)
             assert torch.equal(s["lse"], lse) and torch.equal(s["mass"], mass), (r, pos)
             at.copy_(before)
+
+
+def test_masses_by_the_lse_of_rows_that_saw_a_bad_key():
+    """A K that is not finite spoils its own mass alone by a finite lse.  The one that the
+    attention leaves for the rows that see it spoils those of the whole head, none of another."""
+    B = B_()
+    s = mass_case([5, 40, 3], [165, 300, 30], 8, 2, 64, seed=4)
+    pool, lse, mass = s["c"].pool.clone(), s["lse"].clone(), s["mass"].clone()
+    for bad in (math.nan, math.inf):
+        s["c"].pool.copy_(pool)
+        s["c"].pool[0, s["c"].ids[1][3], 0, 1, 7] = bad          # position 55, which all 40 rows see
+        B.dflash_attention_chunk(*s["args"])
+        B.dflash_attention_mass(*s["mass_args"])
+        spoilt = torch.zeros_like(mass, dtype=torch.bool)
+        spoilt[1, 1, :300] = True
+        assert torch.isnan(s["mass"][spoilt]).all()
+        assert torch.equal(s["mass"][~spoilt], mass[~spoilt])
+        args = list(s["mass_args"])
+        args[11] = lse
+        B.dflash_attention_mass(*args)
+        other = torch.ones_like(spoilt)
+        other[1, 1, 55] = False
+        assert torch.equal(s["mass"][other], mass[other])
