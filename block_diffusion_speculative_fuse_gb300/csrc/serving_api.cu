@@ -351,15 +351,15 @@ int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void*
   const uint64_t layer_groups = static_cast<uint64_t>(kv->n_pages) * 2 * heads->n_kv_heads * 2;
   const uint64_t groups = layer_groups * heads->n_layers;
   if (groups >= (1ull << 31) - 2 || T > (1 << 30) || ld_q >= (1ll << 38)) return DFLASH_ERR_UNSUPPORTED;
+  p.max_pages = kv->max_pages;
+  if (!attention_chunk_fits(p)) return DFLASH_ERR_UNSUPPORTED;
   rc = check_ws(ws, ws_bytes, layout_chunk(&p, d, static_cast<uint8_t*>(ws)));
   if (rc) return rc;
   p.row_start = row_start;
   p.ctx_len = ctx_len;
   p.page_table = kv->page_table;
   p.causal = causal;
-  p.max_pages = kv->max_pages;
   p.n_pages = kv->n_pages;
-  if (!attention_chunk_fits(p)) return DFLASH_ERR_UNSUPPORTED;
   // A unit's last piece can join them all where units have one tile and, on average, few
   // rows; that saves a kernel, but one CTA reads all of a unit's partials.  With and
   // without: a row of 4096 keys 18.6 and 23.3 us, of 30000 35.0 and 41.9, 8 rows 23.3 and

@@ -456,14 +456,14 @@ int dflash_attention_prefix(const dflash_heads* heads, int32_t layer, const void
  * is undefined: a V that is not finite makes the results of the rows that see
  * it infinite or NaN and leaves their lse as it is).
  * Row strides are multiples of 8 elements, base pointers 16-byte aligned.
- * batch <= kv->n_rows, T <= 2^30; a call whose work may pass n_kv_heads *
- * (T / 16 + batch) * max_pages = 2^30 is DFLASH_ERR_UNSUPPORTED (some larger
- * ones with fewer than 16 query heads to a KV head are not).
+ * batch <= kv->n_rows, T <= 2^30; a call with n_kv_heads * (T / (2 * (128 / G))
+ * + batch) * (max_pages / 2 + 11) >= 2^30, G query heads to a KV head (the first
+ * two quotients whole numbers), is DFLASH_ERR_UNSUPPORTED.
  * Scores, softmax statistics and accumulators are fp32; probabilities are
  * rounded to bf16 for the product with V.  Deterministic.
  * ws: initialised, dflash_attention_chunk_bytes(heads, batch, T) bytes (0:
  * unsupported sizes); a workspace for larger T serves smaller calls.  At most
- * 41 MB for calls of at most 8 tiles of 128 rows per KV head, 324 MB from 32
+ * 41 MB for calls of fewer than 8 tiles (128 / G rows each), 324 MB from 32
  * tiles on (partial results of the rounds in which long contexts are read). */
 size_t dflash_attention_chunk_bytes(const dflash_heads* heads, int32_t batch, int32_t T);
 int dflash_attention_chunk(const dflash_heads* heads, int32_t layer, const void* q, int64_t ld_q,
@@ -522,7 +522,7 @@ int dflash_sample_filtered(const float* logits, int64_t ld, int32_t rows, int32_
  * dflash_attention_chunk leaves for a row that sees such a K is undefined, and
  * makes so the sums of all positions that this row sees, in its KV head.
  * A bf16 one-term cache; batch <= 1024 and <= kv->n_rows; batch * n_kv_heads *
- * max_pages below 2^34.  Products, exponents and sums are fp32, the sums in a
+ * (max_pages / 16 + 1) below 2^30 (a whole quotient).  Products, exponents and sums are fp32, the sums in a
  * fixed order and compensated over the rows.  Deterministic.
  * ws: initialised, dflash_attention_mass_bytes(heads, batch, T) bytes. */
 size_t dflash_attention_mass_bytes(const dflash_heads* heads, int32_t batch, int32_t T);

@@ -60,3 +60,41 @@ def test_evict_refuses_two_pools_that_share_their_scales(lib):
     for at, code in (((1 << 30), -1), ((1 << 30) + size - 16, -1), ((1 << 30) - size + 16, -1),
                      ((1 << 30) + size, -3), ((1 << 30) - size, -3)):
         assert evict(lib, src=src, dst=cache(pool=1 << 40, dtype=1, scales=at), size=0) == code, at - (1 << 30)
+
+
+# ------------------------------------------------------- bounds that the header states
+def test_chunk_workspace_by_tiles(lib):
+    """At most 41 MB for fewer than 8 tiles of rows, 324 MB from 32 tiles on."""
+    for hq, hkv, d in ((32, 8, 128), (15, 3, 128), (2, 2, 128), (16, 1, 64)):
+        hd = heads(n_q_heads=hq, n_kv_heads=hkv, head_dim=d)
+        tokens = 128 // (hq // hkv)
+        size = lambda T: lib.dflash_attention_chunk_bytes(ctypes.byref(hd), 3, T)  # noqa: E731
+        assert size(8 * tokens - 1) <= 41e6
+        for tiles, phases in ((1, 1), (8, 2), (16, 4), (32, 8), (1000, 8)):
+            # two slots of 256 rows, or of a single tile's, for each of 152 workers and round
+            rows = 2 * 152 * phases * (256 if tiles > 1 else tokens * (hq // hkv))
+            assert rows * (d + 2) * 4 <= size(tiles * tokens) - (1 << 16) <= rows * (d + 2) * 4 + 4 * 8 * 152 * 32
+        assert size(32 * tokens - 1) < size(32 * tokens) == size(10000 * tokens) <= 324e6
+
+
+def test_chunk_refuses_work_by_the_stated_formula(lib):
+    """(T / (2 * (128 / G)) + batch) * n_kv_heads * (max_pages / 2 + 11) = 2^30, short tables too."""
+    for max_pages, batch, hq, hkv in ((1, 4, 1024, 1024), (10, 5, 64, 64), (21, 100, 24, 8), (1 << 20, 3, 32, 8), (1 << 26, 7, 3, 1)):
+        G = hq // hkv
+        units = int((1 << 30) // (hkv * (max_pages / 2 + 11)))      # the largest count below the bound
+        units -= units * hkv * (max_pages / 2 + 11) >= 1 << 30
+        if units < batch:
+            T, codes = 1, (-2, -2)
+        else:
+            T, codes = (units - batch + 1) * 2 * (128 // G) - 1, (-3, -2)   # the last row count with these units
+        for t, code in zip((T, T + 1), codes):
+            hd, kv = heads(n_q_heads=hq, n_kv_heads=hkv), cache(max_pages=max_pages, n_rows=batch)
+            assert chunk(lib, hd=hd, kv=kv, batch=batch, T=t, ldq=hq * 64, ldo=hq * 64, size=0) == code, (max_pages, t)
+
+
+def test_mass_refuses_work_by_the_stated_formula(lib):
+    """batch * n_kv_heads * (max_pages / 16 + 1) = 2^30."""
+    hd = heads(n_q_heads=65536, n_kv_heads=65536)
+    for max_pages, code in ((239, -3), (240, -2)):
+        kv = cache(max_pages=max_pages, n_rows=1024)
+        assert mass(lib, hd=hd, kv=kv, batch=1024, ldq=65536 * 64, size=0) == code, max_pages
