@@ -7,8 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_prompt import (PAGE, B_, Cache, built, check_chunk, chunk_case, heads, i32, mass_case,  # noqa: F401
-                             workspace)
+from test_gpu_prompt import (PAGE, B_, Cache, built, check_chunk, chunk_case, heads, i32, logits,  # noqa: F401
+                             mass_case, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,19 @@ def test_masses_by_the_lse_of_rows_that_saw_a_bad_key():
         other = torch.ones_like(spoilt)
         other[1, 1, 55] = False
         assert torch.equal(s["mass"][other], mass[other])
+
+
+def test_score_records_which_of_the_two_it_was():
+    """Ids beyond the vocabulary alone are site 572, bad rows alone 571; with both, one of them."""
+    B = B_()
+    ws = workspace()
+    lp = torch.zeros(3, device="cuda")
+    for ids, bad, sites in (([1, 300, 2], False, (572,)), ([2 ** 31 - 1, 1, 1], False, (572,)), ([1, 2, 3], True, (571,)),
+                            ([1, 300, 2], True, (571, 572))):
+        z = logits(3, 300)
+        if bad:
+            z[2, 7] = math.nan
+        B.dflash_workspace_init(ws)
+        B.dflash_score_tokens(z, 3, 300, None, i32(ids), lp, None, None, 0, None, None, ws)
+        status, site = B.dflash_get_status(ws)
+        assert status == -1 and site in sites, (ids, bad, site)
