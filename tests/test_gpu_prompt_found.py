@@ -124,3 +124,31 @@ def test_score_records_which_of_the_two_it_was():
         B.dflash_score_tokens(z, 3, 300, None, i32(ids), lp, None, None, 0, None, None, ws)
         status, site = B.dflash_get_status(ws)
         assert status == -1 and site in sites, (ids, bad, site)
+
+
+def test_calls_at_once_on_two_streams():
+    """Each with a workspace of its own: the same bits as one after the other."""
+    B = B_()
+    cases = [mass_case(ns, ctx, 8, 2, d, seed=d) for ns, ctx, d in
+             (([300, 1, 45], [4000, 900, 45], 64), ([1, 70], [9000, 300], 128))]
+    z = logits(40, 50000)
+    ids, wss = i32(np.arange(40) * 7), [workspace(), workspace()]
+    lps = [torch.zeros(40, device="cuda") for _ in range(2)]
+
+    def call(i, stream=None):
+        B.dflash_attention_chunk(*cases[i]["args"], stream=stream)
+        B.dflash_attention_mass(*cases[i]["mass_args"], stream=stream)
+        B.dflash_score_tokens(z, 40, 50000, None, ids, lps[i], None, None, 0, None, None, wss[i], stream=stream)
+    for i in range(2):
+        call(i)
+    torch.cuda.synchronize()
+    want = [[cases[i][k].clone() for k in ("out", "lse", "mass")] + [lps[i].clone()] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i in range(2):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in zip([cases[i][k] for k in ("out", "lse", "mass")] + [lps[i]], want[i]):
+            assert torch.equal(a, b), i
+        assert all(B.dflash_get_status(ws) == (0, 0) for ws in (cases[i]["ws"], wss[i], cases[i]["mass_args"][-1]))
