@@ -188,7 +188,9 @@ class PagedKV:
                  mass_out=None, stream=None):
         """Move the keep[r] positions of largest mass of each request and KV head, in order,
         to positions 0, 1, ... of the cache `other` (dflash_kv_evict), which has this one's
-        layers, planes, heads and dtype; ws from its evict_workspace."""
+        layers, planes, heads and dtype; ws from its evict_workspace.  New rows are
+        turned by their place in the whole sequence and appended behind new_len without a
+        rotation."""
         mine, theirs = self.pool.shape, other.pool.shape
         if self.dtype != other.dtype or mine[0] != theirs[0] or mine[2:] != theirs[2:]:
             raise ValueError(f"caches of {self.dtype} {tuple(mine)} and {other.dtype} {tuple(theirs)}: they may "

@@ -536,8 +536,14 @@ int dflash_attention_mass(const dflash_heads* heads, int32_t layer, const void* 
  * with the largest mass are kept and moved together, in their order, to
  * positions 0, 1, ... of row r of dst; the first `sink` and the last `recent`
  * positions count as heavier than all others, equals go to the lower
- * position, NaN comes last.  (Keys keep the rotation of the position at which
- * they were appended; new rows go on from the old positions' angles.)
+ * position, NaN comes last.
+ * Keys keep the rotation of the position at which they were appended, so new
+ * rows turn by their place in the whole sequence and are stored behind
+ * new_len.  dflash_kv_rope_append stores at the position that it turns by:
+ * their q and k are turned first (by the caller, or as the q rows of an append
+ * into a scratch cache), then appended with rot_dim 0.  The calls that bring
+ * their own projections (dflash_target_forward, dflash_draft_block) turn by the
+ * cache's positions and cannot go on from an evicted cache.
  *   kept int32 [batch][n_kv_heads][ld_kept]: the positions, ascending
  *   new_len int32 [batch] or NULL: how many
  *   mass_out fp32, as mass, or NULL: their masses, in the same order

@@ -152,3 +152,62 @@ def test_calls_at_once_on_two_streams():
         for a, b in zip([cases[i][k] for k in ("out", "lse", "mass")] + [lps[i]], want[i]):
             assert torch.equal(a, b), i
         assert all(B.dflash_get_status(ws) == (0, 0) for ws in (cases[i]["ws"], wss[i], cases[i]["mass_args"][-1]))
+
+
+def test_decoding_on_from_an_evicted_cache():
+    """New rows go on from the old length's angles and behind the positions that are left, on the
+    device throughout: q and k are rotated as the q heads of an append into a scratch cache (a
+    page per request, which every entry of its table names), and stored by one without a
+    rotation.  Against rows rotated in 64 bits (an angle to 2^-19 of the pair, k's and q's
+    rounding to bf16 2^-8)."""
+    B = B_()
+    from oracle import serving as O
+    from types import SimpleNamespace
+    from block_diffusion_speculative_fuse_gb300.device import PagedKV
+    hq, hkv, d, batch, layer = 8, 2, 64, 2, 1
+    shape = SimpleNamespace(n_layers=2, n_kv_heads=hkv, head_dim=d, kv_terms=1)
+    lens, keep, steps = [150, 61], [48, 40], 5
+    big = PagedKV(shape, np.random.default_rng(0).permutation(20).reshape(2, 10), 20)
+    small = PagedKV(shape, np.arange(8).reshape(2, 4), 8)
+    scratch = PagedKV(SimpleNamespace(n_layers=1, n_kv_heads=hkv, head_dim=d, kv_terms=1),
+                      np.repeat([[0], [1]], 10, 1), 2)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rope, none = B.dflash_rope_init(d, base=1e4), B.dflash_rope_init(0)
+    f, mag = O.rope_freqs(d, 1e4)
+    ws = big.chunk_workspace(hq, batch, 256)
+    seq = [torch.randn(n + steps, hq + 2 * hkv, d, generator=g, device="cuda").to(torch.bfloat16) for n in lens]
+    for r, n in enumerate(lens):
+        x = seq[r][:n]
+        big.append_rotated(rope, layer, None, x[:, hq:hq + hkv].contiguous(), x[:, hq + hkv:].contiguous(), i32([r] * n),
+                           i32(np.arange(n)), ws)
+    mass = torch.rand(batch, hkv, 160, generator=g, device="cuda")
+    kept, new_len = torch.zeros(batch, hkv, 48, dtype=torch.int32, device="cuda"), i32([0, 0])
+    big.evict_to(small, layer, i32(lens), i32(keep), mass, kept, small.evict_workspace(batch), new_len=new_len)
+    pos, req, start = i32(lens), i32([0, 1]), i32([0, 1, 2])
+    for i in range(steps):
+        x = torch.stack([seq[r][lens[r] + i] for r in range(batch)])
+        q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:].contiguous()
+        qk = torch.empty(batch, hq + hkv, d, dtype=torch.bfloat16, device="cuda")
+        scratch.append_rotated(rope, 0, x[:, :hq + hkv], k, v, req, pos, ws, q_out=qk)
+        small.append_rotated(none, layer, None, qk[:, hq:], v, req, new_len, ws)
+        new_len += 1
+        pos += 1
+        out = torch.zeros(batch, hq, d, dtype=torch.bfloat16, device="cuda")
+        small.attend_chunk(layer, qk[:, :hq], start, new_len, out, ws)
+        at = [lens[r] + i for r in range(batch)]
+        qr, kr = (O.rotate(t.double().cpu().numpy(), at, f, mag, False) for t in (q, k))
+        size = math.sqrt(2) * max(float(q.abs().max()), float(k.abs().max()))
+        assert np.all(np.abs(qk[:, :hq].double().cpu().numpy() - qr) <= 2.0 ** -8 * np.abs(qr) + 2.0 ** -18 * size)
+        for r in range(batch):
+            kk, vv = (t.double().cpu().numpy() for t in small.read_logical(layer, r, keep[r] + i + 1))
+            assert np.all(np.abs(kk[-1] - kr[r]) <= 2.0 ** -8 * np.abs(kr[r]) + 2.0 ** -18 * size)
+            assert np.array_equal(vv[-1], v[r].double().cpu().numpy())
+            o, _, mag_v = O.attend(qk[r:r + 1, :hq].double().cpu().numpy(), kk, vv, 0.125, [keep[r] + i + 1])
+            assert np.all(np.abs(out[r:r + 1].double().cpu().numpy() - o) <= 2.0 ** -7 * (mag_v + np.abs(o)) + 1e-6)
+    # what was kept lies before them as it lay in the old cache
+    for r in range(batch):
+        old, left = big.read_logical(layer, r, lens[r]), small.read_logical(layer, r, keep[r])
+        for h in range(hkv):
+            for a, b in zip(old, left):
+                assert torch.equal(b[:, h].cpu(), a[kept[r, h, :keep[r]].long().cpu(), h].cpu())
+    assert B.dflash_get_status(ws) == (0, 0)
