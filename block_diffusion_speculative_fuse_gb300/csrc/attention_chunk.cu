@@ -31,17 +31,20 @@
 // zeros past the last row's keys, and for what is not finite (the rows that do
 // see it get a NaN by way of O's factor; l, and with it lse, does not depend on V).
 //
-// Bound: with whole units the products and their issue.  4096 rows of 32 heads behind 28672
-// keys (134 MB, more than L2) 1.20 ms, 1.70 PFLOP/s, 0.90 of the GEMM rate, in two rounds;
-// behind 126976 5.15 ms, 1.68 PFLOP/s, in eight.  A chunk of both tiles takes some 2800
+// Bound (times with inputs that change from call to call): with whole units the products and
+// their issue.  4096 rows of 32 heads behind 28672 keys (134 MB, more than L2) 1.19 to 1.28 ms by
+// box and clock, 1.73 to 1.61 PFLOP/s, in two rounds; behind 126976 5.18 ms, 1.67 PFLOP/s,
+// in eight.  A chunk of both tiles takes some 2800
 // cycles: its products 2048 of the tensor pipe and, at 128 bytes a cycle, 2048 of shared memory (S
 // reads Q and K, P V reads V, the loads write both); a tile's softmax 1100 under the other's
-// products.  For short prompts the units' ends: 8 x 1024 rows take 82 us, 52 of them chunks.  For
-// single tokens the keys' bytes: 32 requests of 3000 to 6200 keys 106 us, 6.2 TB/s; one
+// products.  For short prompts the units' ends: 8 x 1024 rows take 84 us, 52 of them chunks; the
+// softmax warps read and store O themselves, and the next unit's P waits for them.  For
+// single tokens the keys' bytes: 32 requests of 3100 to 6200 keys 96 us, 6.1 TB/s; one
 // request of 4096 keys 16 us, of which the keys' bytes are 2.5: plan, first loads and join are
 // chains of loads, and code that is not yet in the instruction cache.  Beside whole units a CTA
 // with single tokens takes 1800 cycles for each of its chunks (77 GB/s an SM; with d = 64
-// as many): the chain of S, softmax and P V, and their issue.
+// as many): the chain of S, softmax and P V, and their issue.  That softmax goes over all 128
+// rows of the tile, though only G of them are a token's.
 //
 // That cache decides more than arithmetic here.  All roles' code together has to stay
 // in it: with the polls of 20 waits unrolled (172 KB of instructions instead of 77) a
@@ -62,12 +65,12 @@ constexpr float kRaise = 8.f;     // log2
 constexpr int kPieces = 4;        // planned ahead
 // Costs are counted in 64 keys that one tile of 128 rows goes over (32 bits).
 constexpr int kUnitCost = 10;     // a unit's start and end
-constexpr int kSplitCost = 3;     // of a chunk with one tile (2, 3, 4: a mixed batch 238, 235, 254 us)
+constexpr int kSplitCost = 3;     // of a chunk with one tile (2, 3, 4: a mixed batch, same inputs again, 238, 235, 254 us)
 constexpr int kWorkerCost = 8;    // the least share of a worker
 // Keys that several row units read should stay in L2 from one unit to the next.  Where those
 // of all requests do not fit, the workers take the work in rounds (phases), each of fewer
 // heads or requests: the units that run at a time then read the same keys.  One round against
-// up to 8 (before the loads were quicker, which gave both 5 %): 4096 rows behind 28672 keys 1.37 ->
+// up to 8 (same inputs again, before the loads were quicker, which gave both 5 %): 4096 rows behind 28672 keys 1.37 ->
 // 1.29 ms, behind 126976 keys 6.24 -> 5.41, 8 x 2048 rows behind 15000 3.24 -> 2.88, 1000 rows
 // behind 131072 1.59 -> 1.39.
 constexpr int kResident = 5760;   // in 64 keys of one head of 64: 90 MB

@@ -17,10 +17,11 @@
 // and plane one D, in two stages each, which the plane's four warps sum up.
 //
 // Bound: with the usual window of rows (32 rows of 4 heads, one tile) K's bytes: 8
-// requests of 16384 keys 46 us, 6.0 TB/s with 6 us of start-up, 32 of them 164 us, 6.7
-// TB/s; 8 rows take as long as 32.  With many tiles the exponentials and Q's traffic
-// from L2, each tile again for every 256 keys: 512 rows of 8 requests of 16848 keys 480 us,
-// 1.16 PFLOP/s.
+// requests of 16384 keys 46 us, 5.9 TB/s with 6 us of start-up, 32 of them 176 us, 6.2
+// TB/s (169 with the same inputs again); 8 rows take as long as 32.  With many tiles 512 rows
+// of 8 requests of 16848 keys 488 us, 1.14 PFLOP/s: a warp waits for each 32 columns of D before
+// it works on them, with two warps to a scheduler, and Q comes from L2 again for every 256 keys (2.2
+// GB, 4.6 TB/s); which of the two it is has not been measured.
 #include <climits>
 
 #include "attention_chunk.cuh"
@@ -415,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 sc = make_float2(p.scale_log2, p.scale_log2);
         const float4* ls = reinterpret_cast<const float4*>(lse_s + qc.slot * 128);
         // Whole groups of 32 columns have no tests: as selects in the same loop they cost as
-        // much again as the sums (8 x 16384 keys 50 us instead of 46, all of 512 rows 621
-        // instead of 480).
+        // much again as the sums (same inputs again, 8 x 16384 keys 50 us instead of 46, all of
+        // 512 rows 621 instead of 480).
         int c = 0;
         if (whole) {
 #pragma unroll 1

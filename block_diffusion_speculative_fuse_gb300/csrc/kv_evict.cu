@@ -11,8 +11,8 @@
 // copies whole vectors.
 //
 // Bound: the copy's bytes where there are many requests: 32 x 8192 positions to 2048 in
-// 105 us, of which the copy is 83, 6.4 TB/s.  For one request the choice: 98304
-// positions of 8 heads take 39 us, 20 of them for three digits (each a pass over 6144
+// 111 us, of which the copy is 83, 6.4 TB/s.  For one request the choice: 98304
+// positions of 8 heads take 46 us (40 with the same inputs again), 20 of them for three digits (each a pass over 6144
 // positions a CTA, a barrier of 16 CTAs and an exchange of 96 counts) and the numbering.
 #include <climits>
 

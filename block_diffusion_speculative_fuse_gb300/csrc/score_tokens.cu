@@ -22,7 +22,8 @@
 //
 // Bound: 2048 fp32 rows of 151936 the loads: 197 us without alternatives, 6.3 TB/s, 221
 // with five: the phases behind a row's pass take its SM 4 us, in which only the other
-// CTA's loads are in flight.  bf16 rows instruction issue, 162 us, 3.8 TB/s.  One row
+// CTA's loads are in flight.  bf16 rows instruction issue, 162 us, 3.8 TB/s (without
+// alternatives 139, 4.5).  One row
 // (a cluster of 8) 10.8 us, the latency of five phases.
 #include <cfloat>
 #include <climits>
